@@ -398,6 +398,176 @@ MUON_API void muon_graph_destroy(muon_graph* graph);
  * plan needs more than MUON_NOALLOC_MAX_BYTES), SHAPE, HIP. */
 MUON_API muon_status muon_step_noalloc(const muon_plan* plan, const muon_step_config* config, void* stream);
 
+/* ---- routed experts: routing, grouped rows, 8-bit products ------------------------------- */
+
+/* The layer whose matrices a step updates: every token is routed to top_k of n_experts, its
+ * activations and the experts' weights are multiplied in 8 bits, and the products of the
+ * backward pass are the gradients that a plan's step reads (the pages: one shared and the
+ * top 7 of 512 routed experts, 8-bit compute with block scales; "Frontier Pre-training at
+ * Microsoft AI", setup sections 2 and 4).  These calls need no plan: all their state is in
+ * their arguments, they never allocate or synchronise, and they can be captured.  Calls on
+ * different streams may overlap unless they share a written buffer or a workspace.
+ * Device pointers are 16-byte aligned; where a size is 0 nothing is launched and the
+ * pointers are not looked at.  Outputs must not overlap inputs unless stated. */
+
+#define MUON_MAX_EXPERTS 1024
+#define MUON_MAX_TOP_K 64
+
+#define MUON_SCORE_SOFTMAX 0
+#define MUON_SCORE_SIGMOID 1
+
+typedef struct muon_route_config {
+    int64_t tokens;      /* rows of logits                                                   */
+    int64_t ld;          /* row stride of logits in elements, >= n_experts                   */
+    int32_t n_experts;   /* 1..MUON_MAX_EXPERTS                                              */
+    int32_t top_k;       /* 1..min(n_experts, MUON_MAX_TOP_K)                                */
+    int32_t dtype;       /* of logits (and of their gradient): MUON_DTYPE_*                  */
+    int32_t score;       /* MUON_SCORE_*                                                     */
+    int32_t n_groups;    /* consecutive equal groups of experts; 1: no groups; at most 64    */
+    int32_t top_groups;  /* groups that a token may use, 1..n_groups                         */
+    int32_t renormalize; /* 1: weights divided by the sum of the chosen scores               */
+    float scale;         /* factor of every weight (finite)                                  */
+} muon_route_config;
+
+/* Routing.  Scores s of a token's logits x: softmax over its experts, or sigmoid.  An expert
+ * whose logit is -inf or NaN is out for that token (score 0, never chosen, left out of the
+ * softmax); +inf counts as the largest finite value.  The choice goes by the key s + bias (bias:
+ * n_experts floats; an expert with a NaN key is out), or by x itself where bias is NULL.
+ * With n_groups > 1 only the experts of the top_groups groups stay whose two largest s + bias
+ * add up to the most (a group without an expert comes last).  experts (tokens x top_k) gets
+ * the experts of the top_k largest keys in falling order, equal keys (and equal groups) by
+ * lowest index, and -1 where a token has no further expert; weights (tokens x top_k,
+ * float32) gets scale * s without the bias, divided by the sum of the chosen s with
+ * renormalize (0 where that sum underflows), and 0 beside -1.  Scores and keys are
+ * formed in float64 where bias or groups make the choice depend on them, so that near ties fall as the
+ * formulas say; weights are rounded to float32 once.
+ * Errors: INVALID_ARG (NULL, enum, n_groups not a divisor of n_experts or above 64,
+ * top_groups, non-finite scale), SHAPE (tokens < 0, n_experts, top_k, ld), ALIGNMENT, HIP. */
+MUON_API muon_status muon_route(const muon_route_config* config, const void* logits, const float* bias,
+                                int32_t* experts, float* weights, void* stream);
+
+/* The gradient of the weights with respect to the logits, the choice held fixed: grad_logits
+ * (row stride ld_grad, logits' dtype) gets sum_j grad_weights[t][j] * d weights[t][j] / d x,
+ * whole rows, zeros where nothing flows.  experts is muon_route's; entries outside
+ * [0, n_experts) and entries whose logit is -inf or NaN pass nothing on, equal entries of a
+ * row add up.  bias, n_groups and top_groups take no part.  Errors: as muon_route. */
+MUON_API muon_status muon_route_backward(const muon_route_config* config, const void* logits,
+                                         const int32_t* experts, const float* grad_weights, void* grad_logits,
+                                         int64_t ld_grad, void* stream);
+
+/* Device workspace of muon_group_rows in bytes (0 for few rows).  Errors: INVALID_ARG, SHAPE. */
+MUON_API muon_status muon_group_rows_workspace(int64_t n, int32_t n_experts, uint64_t* bytes);
+
+/* Rows of `rows` below: n, plus what the padding may add. */
+MUON_API muon_status muon_group_rows_capacity(int64_t n, int32_t n_experts, int32_t align, int64_t* rows);
+
+/* Groups n choices of experts (muon_route's experts, n = tokens * top_k; entries outside [0, n_experts)
+ * go nowhere) by expert, in stable order: counts[e] (n_experts) choices of expert e sit in segment
+ * [offsets[e], offsets[e + 1]) (n_experts + 1), which is padded to a multiple of `align`
+ * (1, 2, 4, ..., 128; 128 is what MUON_PRODUCT_DEPTH needs).  rows[r] (muon_group_rows_capacity
+ * entries, all written) is the index of the choice in row r, so rows[r] / top_k is its token,
+ * or -1 in the padding and behind the last segment; position[i] (n) is the row of choice i, or
+ * -1.  The same on every run.  Errors: INVALID_ARG, SHAPE (n, n_experts, or a capacity of
+ * 2^31 or more), ALIGNMENT, WORKSPACE_TOO_SMALL, HIP. */
+MUON_API muon_status muon_group_rows(const int32_t* experts, int64_t n, int32_t n_experts, int32_t align,
+                                     int32_t* counts, int32_t* offsets, int32_t* rows, int32_t* position,
+                                     void* workspace, uint64_t workspace_bytes, void* stream);
+
+/* The step of the selection bias, which no gradient reaches: bias_out[e] = bias[e] + rate *
+ * sign(mean of counts - counts[e]) in float32, the sign exact.  bias_out may be bias.
+ * Errors: INVALID_ARG (NULL, non-finite rate), SHAPE (n_experts), ALIGNMENT, HIP. */
+MUON_API muon_status muon_balance_step(const float* bias, const int32_t* counts, int32_t n_experts, float rate,
+                                       float* bias_out, void* stream);
+
+/* 8-bit matrices: one byte per value (e4m3 or e5m2) and one scale byte per block of 128 values
+ * of a row, or per 128 x 128 square.  Scale byte b stands for 2^(b - 127).  A power of two changes no
+ * value's significand, so a code is its value rounded once, and the matrix instructions take
+ * the scales as they are.  A matrix of rows x cols has rows of round_up(cols, 128) codes and
+ * scale rows of round_up(ceil(cols / 128), 4) bytes, one per row or per 128 rows (square);
+ * codes and scales outside cols are zero bytes. */
+#define MUON_FP8_E4M3 0
+#define MUON_FP8_E5M2 1
+
+typedef struct muon_fp8_quantize_config {
+    const void* src;          /* batch matrices of float32 or bfloat16                      */
+    int32_t src_dtype;        /* MUON_DTYPE_*                                               */
+    int32_t format;           /* MUON_FP8_*                                                 */
+    int32_t square;           /* 0: a scale per 128 values of a row; 1: per 128 x 128       */
+    int32_t per;              /* with gather: choices per source row (top_k), >= 1          */
+    int64_t batch;
+    int64_t rows, cols;       /* of each quantised matrix                                   */
+    int64_t ld;               /* row stride of src in elements, >= cols                     */
+    int64_t batch_stride;     /* between src's matrices, in elements                        */
+    /* Device, nullable (batch 1): quantised row r is source row gather[r] / per, or zero where
+     * that is outside [0, src_rows). */
+    const int32_t* gather;
+    int64_t src_rows;
+    /* Device, nullable (batch 1, square 0): one int32; rows from *limit on are left as they
+     * were (of the transposed copy, the blocks of 128 that begin there), and those of a
+     * transposed block that *limit cuts are zero. */
+    const int32_t* limit;
+    uint8_t* codes;           /* nullable: batch x rows x round_up(cols, 128)               */
+    uint8_t* scales;
+    /* nullable: the transposed matrix (cols x rows) in the same layout, its blocks along rows:
+     * batch x cols x round_up(rows, 128). */
+    uint8_t* codes_t;
+    uint8_t* scales_t;
+} muon_fp8_quantize_config;
+
+/* Quantises, and quantises the transpose, in one pass over src.  A block's scale is 2^e with the
+ * least e in [-127, 127] for which its largest finite magnitude is at most 448 * 2^e (e4m3)
+ * or 57344 * 2^e (e5m2), -127 for a block of zeros; a code is the value * 2^-e rounded to
+ * nearest even.  An infinity or NaN becomes a NaN code and has no part in its block's scale.
+ * Errors: INVALID_ARG (NULL, enum, no output, one of a codes / scales pair NULL, gather or
+ * limit with batch > 1 or limit with square, per < 1, an output that overlaps src),
+ * SHAPE (sizes, strides), ALIGNMENT, HIP. */
+MUON_API muon_status muon_fp8_quantize(const muon_fp8_quantize_config* config, void* stream);
+
+typedef struct muon_fp8_operand {
+    const void* codes;
+    const void* scales;
+    int64_t ld;            /* row stride of codes in bytes, a multiple of 16                */
+    int64_t ld_scales;     /* row stride of scales in bytes, a multiple of 4                */
+    int64_t stride;        /* b of MUON_PRODUCT_ROWS: bytes between the groups' codes (multiple of 16) */
+    int64_t stride_scales; /* and scales (multiple of 4)                                    */
+    int32_t format;        /* MUON_FP8_*; b: e4m3                                           */
+    int32_t square;        /* 1: a scale row per 128 rows                                   */
+} muon_fp8_operand;
+
+/* out = a b^T for a (m x k) and b (n x k): one product. */
+#define MUON_PRODUCT_DENSE 0
+/* Rows of a grouped: rows [offsets[g], offsets[g + 1]) of out are those of a by the transpose of group g's b
+ * (outputs and input gradients of experts); rows outside every segment are left as they were. */
+#define MUON_PRODUCT_ROWS 1
+/* Depth grouped: a (m x k) and b (n x k) are transposed copies whose columns hold segments, and
+ * out[g] (m x n) = a b^T over columns [offsets[g], offsets[g + 1]) only, zeros where that is
+ * empty (weight gradients).  offsets are multiples of 128 (muon_group_rows with align 128):
+ * a segment's blocks of 128 must be its own.  Others are rounded down. */
+#define MUON_PRODUCT_DEPTH 2
+
+typedef struct muon_fp8_product_config {
+    int32_t mode;             /* MUON_PRODUCT_*                                             */
+    int32_t groups;           /* 1 for MUON_PRODUCT_DENSE; at most MUON_MAX_EXPERTS         */
+    int64_t m, n, k;
+    muon_fp8_operand a, b;
+    const int32_t* offsets;   /* device, groups + 1, not falling (NULL for DENSE); values outside the
+                                 operand are clamped to it                                  */
+    void* out;                /* rows of n                                                  */
+    int64_t ld_out;           /* in elements, >= n                                          */
+    int64_t out_stride;       /* MUON_PRODUCT_DEPTH: elements between groups                */
+    int32_t out_dtype;        /* MUON_DTYPE_*                                               */
+    int32_t accumulate;       /* 1: added to out (float32 only)                             */
+} muon_fp8_product_config;
+
+/* 8-bit product on the matrix cores, sums in float32, one rounding to out's type.  For a
+ * bfloat16 out the 8-bit matrix instruction forms the sums: within each 8 neighbouring
+ * products it drops what is below 2^-13 of the largest, about 1.4e-5 of a sum.  For a float32
+ * out the codes go through the bfloat16 instruction, at half its rate, and the sums
+ * are full float32 sums (values below 2^-126 count as zero).
+ * Errors: INVALID_ARG (NULL, enum, groups, accumulate into bfloat16, out overlapping an
+ * operand), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
+MUON_API muon_status muon_fp8_product(const muon_fp8_product_config* config, void* stream);
+
 /* ---- per-kernel timing (HIP events on the launching stream) --------------------------- */
 
 #define MUON_KERNEL_MOMENTUM 0

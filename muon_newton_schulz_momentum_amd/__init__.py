@@ -3,12 +3,13 @@ Newton–Schulz -> FP32 apply with decoupled weight decay) on one AMD Instinct M
 
 The compute path is the C-ABI library libmuon.so (hand-written HIP for gfx950), declared
 in include/muon.h.  `muon_newton_schulz_momentum_amd.binding` is its ctypes binding
-(argument marshalling only) and `harness` builds torch-owned tensors around it.
+(argument marshalling only), `harness` builds torch-owned tensors around the optimizer step and
+`experts` around the routed-expert operators.
 Importing the package itself loads nothing native; importing `binding` fails loudly when
 the shared library has not been built.
 """
 
-__all__ = ["workloads", "binding", "harness", "build"]
+__all__ = ["workloads", "binding", "harness", "experts", "build"]
 
 
 def __getattr__(name):

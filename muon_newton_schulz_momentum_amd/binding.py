@@ -65,6 +65,19 @@ MUON_SCALE_NONE = 0
 MUON_SCALE_ASPECT = 1
 MUON_SCALE_RMS_MATCH = 2
 
+MUON_MAX_EXPERTS = 1024
+MUON_MAX_TOP_K = 64
+
+MUON_SCORE_SOFTMAX = 0
+MUON_SCORE_SIGMOID = 1
+
+MUON_FP8_E4M3 = 0
+MUON_FP8_E5M2 = 1
+
+MUON_PRODUCT_DENSE = 0
+MUON_PRODUCT_ROWS = 1
+MUON_PRODUCT_DEPTH = 2
+
 
 class muon_param_desc(C.Structure):
     _fields_ = [("ndim", C.c_int32), ("grad_dtype", C.c_int32), ("rows", C.c_int64),
@@ -104,6 +117,30 @@ class muon_param_info(C.Structure):
     _fields_ = [("included", C.c_int32), ("chunk", C.c_int32), ("slot", C.c_int64),
                 ("transposed", C.c_int32), ("scale", C.c_float),
                 ("output_offset", C.c_uint64), ("ld", C.c_int64)]
+
+
+class muon_route_config(C.Structure):
+    _fields_ = [("tokens", C.c_int64), ("ld", C.c_int64), ("n_experts", C.c_int32), ("top_k", C.c_int32),
+                ("dtype", C.c_int32), ("score", C.c_int32), ("n_groups", C.c_int32), ("top_groups", C.c_int32),
+                ("renormalize", C.c_int32), ("scale", C.c_float)]
+
+
+class muon_fp8_quantize_config(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("src_dtype", C.c_int32), ("format", C.c_int32), ("square", C.c_int32),
+                ("per", C.c_int32), ("batch", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64), ("ld", C.c_int64),
+                ("batch_stride", C.c_int64), ("gather", C.c_void_p), ("src_rows", C.c_int64), ("limit", C.c_void_p),
+                ("codes", C.c_void_p), ("scales", C.c_void_p), ("codes_t", C.c_void_p), ("scales_t", C.c_void_p)]
+
+
+class muon_fp8_operand(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("ld", C.c_int64), ("ld_scales", C.c_int64),
+                ("stride", C.c_int64), ("stride_scales", C.c_int64), ("format", C.c_int32), ("square", C.c_int32)]
+
+
+class muon_fp8_product_config(C.Structure):
+    _fields_ = [("mode", C.c_int32), ("groups", C.c_int32), ("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64),
+                ("a", muon_fp8_operand), ("b", muon_fp8_operand), ("offsets", C.c_void_p), ("out", C.c_void_p),
+                ("ld_out", C.c_int64), ("out_stride", C.c_int64), ("out_dtype", C.c_int32), ("accumulate", C.c_int32)]
 
 
 _P = C.c_void_p  # muon_plan*
@@ -148,6 +185,21 @@ muon_graph_capture_ex = _fn("muon_graph_capture_ex", C.c_int32, [_P, C.POINTER(m
 muon_graph_launch = _fn("muon_graph_launch", C.c_int32, [_G, C.c_void_p])
 muon_graph_node_count = _fn("muon_graph_node_count", C.c_int32, [_G, C.POINTER(C.c_int64)])
 muon_graph_destroy = _fn("muon_graph_destroy", None, [_G])
+muon_route = _fn("muon_route", C.c_int32, [C.POINTER(muon_route_config), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                          C.c_void_p])
+muon_route_backward = _fn("muon_route_backward", C.c_int32,
+                          [C.POINTER(muon_route_config), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64,
+                           C.c_void_p])
+muon_group_rows_workspace = _fn("muon_group_rows_workspace", C.c_int32, [C.c_int64, C.c_int32, C.POINTER(C.c_uint64)])
+muon_group_rows_capacity = _fn("muon_group_rows_capacity", C.c_int32,
+                               [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_int64)])
+muon_group_rows = _fn("muon_group_rows", C.c_int32,
+                      [C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                       C.c_void_p, C.c_uint64, C.c_void_p])
+muon_balance_step = _fn("muon_balance_step", C.c_int32,
+                        [C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_void_p, C.c_void_p])
+muon_fp8_quantize = _fn("muon_fp8_quantize", C.c_int32, [C.POINTER(muon_fp8_quantize_config), C.c_void_p])
+muon_fp8_product = _fn("muon_fp8_product", C.c_int32, [C.POINTER(muon_fp8_product_config), C.c_void_p])
 muon_timing_enable = _fn("muon_timing_enable", C.c_int32, [_P, C.c_int32])
 muon_timing_read = _fn("muon_timing_read", C.c_int32,
                        [_P, C.c_int32, C.POINTER(C.c_double), C.POINTER(C.c_int64), C.POINTER(C.c_double)])
@@ -163,7 +215,9 @@ EXPORTED = [
     "muon_ns_batched", "muon_ns_batched_schedule", "muon_apply", "muon_adamw_step", "muon_plan_adamw_counts",
     "muon_step", "muon_step_ex", "muon_step_noalloc",
     "muon_graph_capture", "muon_graph_capture_ex", "muon_graph_launch",
-    "muon_graph_node_count", "muon_graph_destroy", "muon_timing_enable", "muon_timing_read",
+    "muon_graph_node_count", "muon_graph_destroy", "muon_route", "muon_route_backward",
+    "muon_group_rows_workspace", "muon_group_rows_capacity", "muon_group_rows", "muon_balance_step",
+    "muon_fp8_quantize", "muon_fp8_product", "muon_timing_enable", "muon_timing_read",
     "muon_timing_reset", "muon_kernel_name", "muon_plan_destroy", "muon_status_string",
     "muon_last_error",
 ]

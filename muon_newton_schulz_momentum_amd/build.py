@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 
-HIP_SOURCES = ["api.hip", "elementwise.hip", "ns_gemm.hip", "ns_small.hip"]
+HIP_SOURCES = ["api.hip", "elementwise.hip", "ns_gemm.hip", "ns_small.hip",
+               "experts_api.hip", "route.hip", "fp8_quantize.hip", "fp8_product.hip"]
 CXX_SOURCES = ["plan.cpp"]
 ARCH = "gfx950"
 

@@ -1,0 +1,338 @@
+"""Torch-side wrapper of the routed-expert operators of libmuon: routing, grouping rows by expert, 8-bit
+block quantisation and 8-bit products.
+
+One layer's matrices in a training step, with the optimizer's `harness.Plan` at its end:
+
+    chosen, weights = route(logits, top_k, bias=bias, score="sigmoid")
+    g = group_rows(chosen, n_experts, align=128)
+    w, w_t = quantize(W, block="square", transpose=True)             # after each step: W (experts, out, in)
+    x, x_t = quantize(tokens, rows=g.rows, per=top_k, limit=g.limit, transpose=True)
+    y = product(x, w, offsets=g.offsets, group="rows")               # rows of g, each by its expert
+    ...
+    dy, dy_t = quantize(grad_y, limit=g.limit, transpose=True)
+    dx = product(dy, w_t, offsets=g.offsets, group="rows")
+    product(dy_t, x_t, offsets=g.offsets, group="depth", out=G)      # the gradients that the plan reads
+    bias = balance_step(bias, g.counts, rate)
+
+Every operator runs in libmuon's HIP kernels on the current stream of its tensors' device (or on
+`stream`); this module checks tensors, allocates outputs and marshals arguments.  Sizes that only the
+device knows (segments, the number of grouped rows) are never read back.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import binding as L
+
+BLOCK = 128
+_SCORES = {"softmax": L.MUON_SCORE_SOFTMAX, "sigmoid": L.MUON_SCORE_SIGMOID}
+_FORMATS = {"e4m3": (L.MUON_FP8_E4M3, torch.float8_e4m3fn), "e5m2": (L.MUON_FP8_E5M2, torch.float8_e5m2)}
+_GROUPS = {None: L.MUON_PRODUCT_DENSE, "rows": L.MUON_PRODUCT_ROWS, "depth": L.MUON_PRODUCT_DEPTH}
+_DTYPES = {torch.float32: L.MUON_DTYPE_F32, torch.bfloat16: L.MUON_DTYPE_BF16}
+
+
+def _up(v: int, step: int) -> int:
+    return -(-v // step) * step
+
+
+@contextlib.contextmanager
+def _switched(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
+    """The device of t, and the stream if one is given, made current: outputs are then allocated for the
+    stream that the kernels run on."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _switched(t.device, stream)
+
+
+def _stream_ptr() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _tensor(name: str, t: torch.Tensor, like: torch.Tensor, dtype, shape=None, contiguous=True) -> torch.Tensor:
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.dtype not in (dtype if isinstance(dtype, (tuple, dict)) else (dtype,)):
+        raise ValueError(f"{name} has dtype {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _rows(name: str, t: torch.Tensor) -> int:
+    """Row stride of a matrix whose rows are contiguous and do not overlap."""
+    cols = t.shape[-1]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    ld = t.stride(-2) if t.shape[-2] > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows overlap")
+    return ld
+
+
+def _route_config(logits, top_k, score, groups, top_groups, renormalize, scale):
+    if logits.dim() != 2 or logits.dtype not in _DTYPES:
+        raise ValueError("logits must be a float32 or bfloat16 matrix (tokens, experts)")
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {', '.join(_SCORES)}")
+    tokens, n = logits.shape
+    return L.muon_route_config(tokens, _rows("logits", logits), n, top_k, _DTYPES[logits.dtype], _SCORES[score],
+                               groups, top_groups, 1 if renormalize else 0, scale)
+
+
+def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+          groups: int = 1, top_groups: int = 1, renormalize: bool = True, scale: float = 1.0, stream=None):
+    """The top_k experts of each token and their weights: (int32, float32) of (tokens, top_k).
+
+    muon_route: an expert with a logit of -inf or NaN is out; the bias moves the choice and not the weights; a
+    token with fewer experts gets -1 and weight 0 in the remaining places.
+    """
+    k = _route_config(logits, top_k, score, groups, top_groups, renormalize, scale)
+    with _on(logits, stream):
+        if bias is not None:
+            _tensor("bias", bias, logits, torch.float32, (logits.shape[1],))
+        size = (k.tokens, max(int(top_k), 0))
+        experts = torch.empty(size, dtype=torch.int32, device=logits.device)
+        weights = torch.empty(size, dtype=torch.float32, device=logits.device)
+        L.check(L.muon_route(C.byref(k), logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                             experts.data_ptr(), weights.data_ptr(), _stream_ptr()), "muon_route")
+    return experts, weights
+
+
+def route_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor, *,
+                   score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of `route`'s weights with respect to the logits (in `out` if given), the choice held fixed."""
+    if experts.dim() != 2:
+        raise ValueError("experts must be route's (tokens, top_k)")
+    k = _route_config(logits, experts.shape[1], score, 1, 1, renormalize, scale)
+    with _on(logits, stream):
+        size = (k.tokens, k.top_k)
+        _tensor("experts", experts, logits, torch.int32, size)
+        _tensor("grad_weights", grad_weights, logits, torch.float32, size)
+        if out is None:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        else:
+            _tensor("out", out, logits, logits.dtype, logits.shape, contiguous=False)
+        L.check(L.muon_route_backward(C.byref(k), logits.data_ptr(), experts.data_ptr(), grad_weights.data_ptr(),
+                                      out.data_ptr(), _rows("out", out), _stream_ptr()), "muon_route_backward")
+    return out
+
+
+@dataclass
+class Groups:
+    """Choices grouped by expert (muon_group_rows)."""
+    counts: torch.Tensor     # (experts,) choices of each expert
+    offsets: torch.Tensor    # (experts + 1,) segments of the grouped rows, padded to `align`
+    rows: torch.Tensor       # (capacity,) choice in each grouped row, -1 in padding
+    position: torch.Tensor   # grouped row of each choice, -1 where it has no expert
+
+    @property
+    def limit(self) -> torch.Tensor:
+        """How many grouped rows there are, on the device."""
+        return self.offsets[-1:]
+
+
+def group_rows(experts: torch.Tensor, n_experts: int, *, align: int = 1, stream=None) -> Groups:
+    """Groups route's choices (any shape) by expert in stable order, each segment padded to a multiple of align."""
+    with _on(experts, stream):
+        _tensor("experts", experts, experts, torch.int32)
+        n, dev = experts.numel(), experts.device
+        cap, ws = C.c_int64(), C.c_uint64()
+        L.check(L.muon_group_rows_capacity(n, n_experts, align, C.byref(cap)), "muon_group_rows_capacity")
+        L.check(L.muon_group_rows_workspace(n, n_experts, C.byref(ws)), "muon_group_rows_workspace")
+        g = Groups(torch.empty(n_experts, dtype=torch.int32, device=dev),
+                   torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
+                   torch.empty(cap.value, dtype=torch.int32, device=dev), torch.empty_like(experts))
+        work = torch.empty(ws.value, dtype=torch.uint8, device=dev)
+        L.check(L.muon_group_rows(experts.data_ptr(), n, n_experts, align, g.counts.data_ptr(), g.offsets.data_ptr(),
+                                  g.rows.data_ptr(), g.position.data_ptr(), work.data_ptr(), ws.value, _stream_ptr()),
+                "muon_group_rows")
+    return g
+
+
+def balance_step(bias: torch.Tensor, counts: torch.Tensor, rate: float, *, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """The selection bias after one step: + rate where an expert had fewer choices than the mean, - rate where
+    more.  `out` may be `bias`."""
+    with _on(bias, stream):
+        if bias.dim() != 1:
+            raise ValueError("bias must be (experts,)")
+        _tensor("bias", bias, bias, torch.float32)
+        _tensor("counts", counts, bias, torch.int32, bias.shape)
+        if out is None:
+            out = torch.empty_like(bias)
+        else:
+            _tensor("out", out, bias, torch.float32, bias.shape)
+        L.check(L.muon_balance_step(bias.data_ptr(), counts.data_ptr(), bias.numel(), rate, out.data_ptr(),
+                                    _stream_ptr()), "muon_balance_step")
+    return out
+
+
+@dataclass
+class Fp8:
+    """An 8-bit matrix, or a stack of them: codes (.., rows, cols rounded up to 128) and the power-of-two scales
+    (.., rows or ceil(rows / 128) if square, blocks rounded up to 4)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+    square: bool
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+    @staticmethod
+    def empty(rows: int, cols: int, *, format: str = "e4m3", square: bool = False, stack: Optional[int] = None,
+              device="cuda") -> "Fp8":
+        lead = () if stack is None else (stack,)
+        srows = -(-rows // BLOCK) if square else rows
+        return Fp8(torch.empty(*lead, rows, _up(cols, BLOCK), dtype=_FORMATS[format][1], device=device),
+                   torch.empty(*lead, srows, _up(-(-cols // BLOCK), 4), dtype=torch.float8_e8m0fnu, device=device),
+                   cols, square)
+
+    def dequantize(self) -> torch.Tensor:
+        """The float32 values (with torch operations; for looking at them)."""
+        kb = self.codes.shape[-1] // BLOCK
+        s = self.scales[..., :kb].float()
+        if self.square:
+            s = s.repeat_interleave(BLOCK, dim=-2)[..., :self.rows, :]
+        v = self.codes.float().unflatten(-1, (kb, BLOCK)) * s.unsqueeze(-1)
+        return v.flatten(-2)[..., :self.cols]
+
+
+def _check_fp8(name: str, q: Fp8, like: torch.Tensor, dims: int, formats) -> None:
+    _tensor(f"{name}.codes", q.codes, like, formats, contiguous=False)
+    _tensor(f"{name}.scales", q.scales, like, torch.float8_e8m0fnu, contiguous=False)
+    if q.codes.dim() != dims or q.scales.dim() != dims or q.codes.shape[:-2] != q.scales.shape[:-2]:
+        raise ValueError(f"{name} must have {dims} dimensions, the same in codes and scales")
+    kb = -(-q.cols // BLOCK)
+    srows = -(-q.rows // BLOCK) if q.square else q.rows
+    if q.cols < 0 or q.codes.shape[-1] != kb * BLOCK or tuple(q.scales.shape[-2:]) != (srows, _up(kb, 4)):
+        raise ValueError(f"{name}: codes {tuple(q.codes.shape)} and scales {tuple(q.scales.shape)} are not those of "
+                         f"{q.cols} columns, square={q.square}")
+
+
+def quantize(src: torch.Tensor, *, block: str = "row", format: str = "e4m3", transpose: bool = False,
+             rows: Optional[torch.Tensor] = None, per: int = 1, limit: Optional[torch.Tensor] = None, out=None,
+             stream=None):
+    """8-bit copy of a float32 or bfloat16 matrix (or stack of them): an Fp8, or with `transpose` the pair of
+    it and the Fp8 of the transposed matrix, from one pass over src (muon_fp8_quantize).
+
+    block "row": a scale per 128 values of a row; "square": per 128 x 128.  With `rows` (int32), quantised row
+    r is src row rows[r] // per, or zeros for -1.  `limit` (one int32 on the device): rows from there on are
+    left as they were.  `out`: an Fp8, or with transpose a pair, to write into.
+    """
+    if block not in ("row", "square"):
+        raise ValueError("block must be 'row' or 'square'")
+    if format not in _FORMATS:
+        raise ValueError(f"format must be one of {', '.join(_FORMATS)}")
+    if src.dim() not in (2, 3) or src.dtype not in _DTYPES:
+        raise ValueError("src must be a float32 or bfloat16 matrix or stack of matrices")
+    square, (fmt, ftype) = block == "square", _FORMATS[format]
+    stack = src.shape[0] if src.dim() == 3 else None
+    if rows is not None and stack is not None:
+        raise ValueError("rows goes with one matrix")
+    cols, n = src.shape[-1], src.shape[-2] if rows is None else rows.numel()
+    with _on(src, stream):
+        if rows is not None:
+            _tensor("rows", rows, src, torch.int32, (n,))
+        if limit is not None:
+            _tensor("limit", limit, src, torch.int32, (1,))
+        want = [(n, cols)] + ([(cols, n)] if transpose else [])
+        if out is None:
+            got = [Fp8.empty(r, c, format=format, square=square, stack=stack, device=src.device) for r, c in want]
+        else:
+            got = list(out) if isinstance(out, (tuple, list)) else [out]
+            if len(got) != len(want):
+                raise ValueError("out must be an Fp8, or with transpose a pair of them")
+            for name, q, (r, c) in zip(("out", "transposed out"), got, want):
+                _check_fp8(name, q, src, src.dim(), ftype)
+                if (q.rows, q.cols, q.square) != (r, c, square) or (stack is not None and q.codes.shape[0] != stack):
+                    raise ValueError(f"{name} must hold {(r, c)}, square={square}")
+                if not q.codes.is_contiguous() or not q.scales.is_contiguous():
+                    raise ValueError(f"{name} must be contiguous")
+        k = L.muon_fp8_quantize_config()
+        k.src, k.src_dtype, k.format, k.square = src.data_ptr(), _DTYPES[src.dtype], fmt, 1 if square else 0
+        k.batch, k.rows, k.cols, k.ld = 1 if stack is None else stack, n, cols, _rows("src", src)
+        k.batch_stride = src.stride(0) if stack is not None and stack > 1 else 0
+        if rows is not None:
+            k.gather, k.per, k.src_rows = rows.data_ptr(), per, src.shape[0]
+        if limit is not None:
+            k.limit = limit.data_ptr()
+        k.codes, k.scales = got[0].codes.data_ptr(), got[0].scales.data_ptr()
+        if transpose:
+            k.codes_t, k.scales_t = got[1].codes.data_ptr(), got[1].scales.data_ptr()
+        # without rows there is nothing to write (and torch gives an empty tensor no address)
+        if n > 0 and k.batch > 0:
+            L.check(L.muon_fp8_quantize(C.byref(k), _stream_ptr()), "muon_fp8_quantize")
+    return (got[0], got[1]) if transpose else got[0]
+
+
+def _operand(q: Fp8, stacked: bool) -> L.muon_fp8_operand:
+    o = L.muon_fp8_operand()
+    o.codes, o.scales = q.codes.data_ptr(), q.scales.data_ptr()
+    o.ld, o.ld_scales = _rows("codes", q.codes), _rows("scales", q.scales)
+    if stacked:
+        o.stride, o.stride_scales = q.codes.stride(0), q.scales.stride(0)
+    o.format = L.MUON_FP8_E4M3 if q.codes.dtype == torch.float8_e4m3fn else L.MUON_FP8_E5M2
+    o.square = 1 if q.square else 0
+    return o
+
+
+def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Optional[str] = None,
+            out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16, accumulate: bool = False,
+            stream=None) -> torch.Tensor:
+    """a times the transpose of b in 8 bits with float32 sums (muon_fp8_product).
+
+    group None: (m, n) of a (m, k) and b (n, k).  "rows": b is a stack (groups, n, k), and the rows offsets[g] to
+    offsets[g + 1] of a go by b[g]; rows outside every segment are not written.
+    "depth": out (groups, m, n), group g's over columns offsets[g] to offsets[g + 1] (multiples of 128) of both;
+    with `accumulate` added to a float32 `out`.  a is e4m3 or e5m2, b e4m3.
+    """
+    if group not in _GROUPS:
+        raise ValueError("group must be None, 'rows' or 'depth'")
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    with _on(a.codes, stream):
+        _check_fp8("a", a, a.codes, 2, (torch.float8_e4m3fn, torch.float8_e5m2))
+        _check_fp8("b", b, a.codes, 3 if group == "rows" else 2, torch.float8_e4m3fn)
+        if a.cols != b.cols:
+            raise ValueError(f"a has {a.cols} columns, b {b.cols}")
+        k = L.muon_fp8_product_config()
+        k.mode, k.m, k.n, k.k = _GROUPS[group], a.rows, b.rows, a.cols
+        k.groups = 1
+        if (group is None) != (offsets is None):
+            raise ValueError("offsets go with group 'rows' or 'depth'")
+        if offsets is not None:
+            _tensor("offsets", offsets, a.codes, torch.int32)
+            k.groups, k.offsets = offsets.numel() - 1, offsets.data_ptr()
+            if offsets.dim() != 1 or (group == "rows" and b.codes.shape[0] != k.groups):
+                raise ValueError("offsets must be (groups + 1,)")
+        shape = (k.groups, k.m, k.n) if group == "depth" else (k.m, k.n)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=a.codes.device)
+        else:
+            _tensor("out", out, a.codes, _DTYPES, shape, contiguous=False)
+        k.a, k.b = _operand(a, False), _operand(b, group == "rows" and k.groups > 1)
+        k.out, k.out_dtype, k.ld_out = out.data_ptr(), _DTYPES[out.dtype], _rows("out", out)
+        if group == "depth":
+            k.out_stride = out.stride(0) if k.groups > 1 else k.m * k.ld_out
+        k.accumulate = 1 if accumulate else 0
+        L.check(L.muon_fp8_product(C.byref(k), _stream_ptr()), "muon_fp8_product")
+    return out
