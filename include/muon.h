@@ -526,8 +526,8 @@ MUON_API muon_status muon_fp8_quantize(const muon_fp8_quantize_config* config, v
 typedef struct muon_fp8_operand {
     const void* codes;
     const void* scales;
-    int64_t ld;            /* row stride of codes in bytes, a multiple of 16                */
-    int64_t ld_scales;     /* row stride of scales in bytes, a multiple of 4                */
+    int64_t ld;            /* row stride of codes in bytes, a multiple of 16, below 2^23    */
+    int64_t ld_scales;     /* row stride of scales in bytes, a multiple of 4, below 2^23    */
     int64_t stride;        /* b of MUON_PRODUCT_ROWS: bytes between the groups' codes (multiple of 16) */
     int64_t stride_scales; /* and scales (multiple of 4)                                    */
     int32_t format;        /* MUON_FP8_*; b: e4m3                                           */

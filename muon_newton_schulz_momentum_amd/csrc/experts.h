@@ -66,7 +66,7 @@ struct ProductArgs {
     int64_t ld_out, out_stride;
     int64_t m, n, k;
     int32_t groups, mode, accumulate;
-    int32_t tiles_m, tiles_n;  // MUON_PRODUCT_ROWS: tiles_m is an upper bound
+    int32_t tiles_m, tiles_n, tiles;
     int32_t vec;               // out rows are 16-byte aligned
 };
 

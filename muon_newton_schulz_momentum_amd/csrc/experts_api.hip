@@ -14,6 +14,7 @@ using namespace muon;
 namespace {
 
 constexpr int64_t MAX_I32 = 0x7fffffff;
+constexpr int64_t MAX_LD = 1 << 23;       // of an operand of a product
 
 muon_status fail(muon_status s, const char* who, const char* what) {
     return set_error(s, std::string(who) + ": " + what);
@@ -78,10 +79,12 @@ muon_status check_operand(const muon_fp8_operand& o, int64_t rows, int64_t k, in
     if (o.square != 0 && o.square != 1) return fail(MUON_ERR_INVALID_ARG, who, "square must be 0 or 1");
     if (misaligned(o.codes) || misaligned(o.scales))
         return fail(MUON_ERR_ALIGNMENT, who, "codes and scales must be 16-byte aligned");
-    if (o.ld % 16 != 0 || o.ld < round_up(k, 128) || o.ld > MAX_I32)
-        return fail(MUON_ERR_SHAPE, who, "ld must be a multiple of 16, at least round_up(k, 128) and below 2^31");
-    if (o.ld_scales % 4 != 0 || o.ld_scales < round_up(ceil_div(k, 128), 4) || o.ld_scales > MAX_I32)
-        return fail(MUON_ERR_SHAPE, who, "ld_scales must be a multiple of 4 and at least round_up(ceil(k / 128), 4)");
+    // a tile's 256 rows lie within 2^31 bytes of its first
+    if (o.ld % 16 != 0 || o.ld < round_up(k, 128) || o.ld >= MAX_LD)
+        return fail(MUON_ERR_SHAPE, who, "ld must be a multiple of 16, at least round_up(k, 128) and below 2^23");
+    if (o.ld_scales % 4 != 0 || o.ld_scales < round_up(ceil_div(k, 128), 4) || o.ld_scales >= MAX_LD)
+        return fail(MUON_ERR_SHAPE, who,
+                    "ld_scales must be a multiple of 4, at least round_up(ceil(k / 128), 4) and below 2^23");
     if (groups > 1) {
         const int64_t srows = o.square ? ceil_div(rows, 128) : rows;
         if (o.stride % 16 != 0 || o.stride_scales % 4 != 0 || o.stride < 0 || o.stride_scales < 0 ||

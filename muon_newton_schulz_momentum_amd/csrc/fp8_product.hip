@@ -2,23 +2,21 @@
 //
 //     out[i][j] = sum over blocks kb of 2^(ea[i][kb] + eb[j][kb]) * sum over k in kb of a[i][k] b[j][k].
 //
-// v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 rows by 16 rows over 128 values of k, one
+// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 rows by 32 rows over 64 values of k, half a
 // block, and takes both scale exponents as bytes, so scaling costs no instruction and the
 // sum over blocks stays in the float32 accumulators.  A lane supplies 32 values of one row and that
-// row's scale; which 32 of the 128 is free as long as both operands agree, as all of them share the scale.
-// b's rows are the instruction's first operand: a lane then holds 4 consecutive columns
+// row's scale; which 32 of the 64 is free as long as both operands agree, as all of them share the scale.
+// b's rows are the instruction's first operand: a lane then holds runs of 4 consecutive columns
 // of one row of out.
 //
 // That instruction adds 8 products at a time after shifting them to the largest one's exponent, and drops
 // what falls below 2^-13 of it (measured: 256 * 256 - 256 * 256 + 1 is 0 within such a group and 1 across
 // groups): 1.4e-5 of a sum of normal values.  A bfloat16 out (half step 3.9e-3) does not see it.  A float32
 // out is asked for where sums go on being added up, so there the codes become bfloat16
-// values (exact, the scale included) and v_mfma_f32_16x16x32_bf16 keeps full float32 sums, at half the rate.
-//
-// 128 x 128 output tiles, 4 waves of 64 x 64.  Operand tiles of 128 bytes a row go from global
-// memory straight to LDS, the next step's while this one is multiplied.  Row r's 16-byte
-// chunk c is at c ^ ((r >> 1) & 7): the 16 rows that a fragment read touches then fall on 16
-// different 16-byte slots of the 256 bytes that LDS serves at once.
+// values (exact, the scale included) and v_mfma_f32_32x32x16_bf16 keeps full float32 sums, at half the rate.
+#include <algorithm>
+#include <type_traits>
+
 #include "device_common.h"
 #include "experts.h"
 
@@ -28,28 +26,39 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int NUM_XCD = 8;
-constexpr int TILE = 128, KB = 128;
-
-// Consecutive tiles on one XCD (workgroups are dealt to the XCDs in turn).
-__device__ __forceinline__ int xcd_remap(int b, int g) {
-    const int xcd = b % NUM_XCD, local = b / NUM_XCD;
-    const int q = g / NUM_XCD, r = g % NUM_XCD;
-    return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
-}
-
-// 16 bytes a lane from global memory to lds_base + 16 * lane.  The compiler does not track the load;
-// it is waited for with vmcnt before the barrier that publishes the stage.
-__device__ __forceinline__ void load_to_lds(const uint8_t* src, const uint8_t* lds_base) {
-    const uint32_t base = __builtin_amdgcn_readfirstlane(
-        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)lds_base);
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(src), "s"(base) : "memory", "m0");
-}
-
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 8 codes (two dwords) times 2^(byte - 127) as bfloat16.
+constexpr int NUM_XCD = 8, CUS = 256;
+constexpr int KB = 128;                   // values that share a scale
+
+// Bands of BAND tile rows, each walked column by column: the tiles an XCD runs at once share panels.
+constexpr int BAND = 8;
+__device__ __forceinline__ void band_decode(int t, int tm, int tn, int& ti, int& tj) {
+    const int band = t / (BAND * tn);
+    const int r0 = band * BAND;
+    const int rows = min(BAND, tm - r0);
+    const int w = t - band * BAND * tn;
+    tj = w / rows;
+    ti = r0 + (w - tj * rows);
+}
+
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint8_t*)(((uint64_t)hi << 32) | lo);
+}
+
+// 4 bytes a lane from the buffer at offset + soffset to lds_base + 4 * lane; past the buffer's end zeros arrive.
+// The compiler does not track the load; loads end in order, so waiting for a later one covers it.
+__device__ __forceinline__ void load_dword_to_lds(__amdgpu_buffer_rsrc_t buf, int offset, int soffset, const uint32_t* lds_base) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint32_t*)lds_base);
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+                 : : "v"(offset), "s"(buf), "s"(soffset), "s"(base) : "memory", "m0");
+}
+
+// 8 codes (two dwords) times the scale as bfloat16.
 template <int FMT>
 __device__ __forceinline__ bf16x8 widen(int lo, int hi, float scale) {
     if constexpr (FMT == MUON_FP8_E4M3) {
@@ -67,194 +76,413 @@ __device__ __forceinline__ bf16x8 widen(int lo, int hi, float scale) {
     }
 }
 
-// The segment of tile row `tile` of a rows-grouped launch: segments take ceil(length / TILE) tile
-// rows each, in order.  False past the last one.  Run by the whole workgroup.
-__device__ __forceinline__ bool find_segment(const ProductArgs& p, int tile, int& group, int64_t& lo, int64_t& hi) {
-    __shared__ int wave_tot[4], found[2];
+// Keeps the matrix instructions that have written acc so far in front of what follows: the compiler would
+// move them past a branch to where their results are used.
+template <int FM, int FN>
+__device__ __forceinline__ void pin(f32x16 (&acc)[FM][FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
+
+// Tiles of 256 x 256, one workgroup of 8 waves per CU that goes through its share of them.  Wave (h, c) of 2 x 4 takes the 32
+// row blocks 2 i + h and columns 64 c .. 64 c + 63, so that a tile with fewer rows (a segment's end) leaves both
+// wave rows half of what there is: a wave runs its first NB of 4 row blocks.
+constexpr int TILE = 256, WAVES = 8, THREADS = 64 * WAVES;
+constexpr int FM = 4, FN = 2;                             // 32 x 32 blocks of a wave
+
+struct Tile {
+    int64_t m0, n0;            // first row of a, of b
+    int rows_a, rows_b;        // rows of either inside the tile
+    int group, kb0, kb1;       // blocks of k [kb0, kb1)
+};
+
+// The segments' bounds, clamped to the operand, and (rows-grouped) how many tile rows lie before each segment, into
+// LDS, by the whole workgroup.
+__device__ __forceinline__ void read_segments(const ProductArgs& p, int* bounds, int* ends, int64_t* wave_tot) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int g0 = 0; g0 < p.groups; g0 += 256) {
+    const int64_t limit = p.mode == MUON_PRODUCT_ROWS ? p.m : (p.k + KB - 1) / KB * KB;
+    for (int g = tid; g <= p.groups; g += THREADS) bounds[g] = (int)min(max((int64_t)p.offsets[g], (int64_t)0), limit);
+    if (tid == 0) ends[0] = 0;
+    __syncthreads();
+    if (p.mode != MUON_PRODUCT_ROWS) return;
+    // sums in 64 bits and capped: falling offsets, which are not allowed, must not lead outside the operand either
+    int64_t before = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += THREADS) {
         const int g = g0 + tid;
-        int tiles = 0;
-        if (g < p.groups) {
-            const int64_t s = min(max((int64_t)p.offsets[g], (int64_t)0), p.m);
-            const int64_t e = min(max((int64_t)p.offsets[g + 1], s), p.m);
-            tiles = (int)((e - s + TILE - 1) / TILE);
-        }
-        int inc = tiles;
+        int64_t inc = g < p.groups ? (max(bounds[g + 1] - bounds[g], 0) + TILE - 1) / TILE : 0;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
-            const int o = __shfl_up(inc, off, 64);
+            const int64_t o = __shfl_up(inc, off, 64);
             if (lane >= off) inc += o;
         }
         if (lane == 63) wave_tot[wave] = inc;
         __syncthreads();
-        int total = 0;
-        for (int w = 0; w < 4; ++w) {
+        int64_t total = 0;
+        for (int w = 0; w < WAVES; ++w) {
             if (w < wave) inc += wave_tot[w];
             total += wave_tot[w];
         }
-        if (tile < total) {
-            if (tile < inc && tile >= inc - tiles) { found[0] = g; found[1] = tile - (inc - tiles); }
-            __syncthreads();
-            group = found[0];
-            const int64_t s = min(max((int64_t)p.offsets[group], (int64_t)0), p.m);
-            hi = min(max((int64_t)p.offsets[group + 1], s), p.m);
-            lo = s + (int64_t)found[1] * TILE;
-            return true;
-        }
-        tile -= total;
+        if (g < p.groups) ends[g + 1] = (int)min(before + inc, (int64_t)1 << 30);
+        before += total;
         __syncthreads();
     }
-    return false;
+}
+
+// Tile t of the launch.
+__device__ __forceinline__ Tile decode(const ProductArgs& p, int t, const int* bounds, const int* ends) {
+    auto at = [](const int* v) { return __builtin_amdgcn_readfirstlane(*v); };
+    Tile r;
+    r.group = 0;
+    r.kb0 = 0;
+    r.kb1 = (int)((p.k + KB - 1) / KB);
+    int64_t m1 = p.m;
+    int tm, tn;
+    if (p.mode == MUON_PRODUCT_ROWS) {
+        tm = t / p.tiles_n;
+        tn = t - tm * p.tiles_n;
+        int lo = 0, hi = p.groups;                         // the last g with ends[g] <= tm
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (at(ends + mid) <= tm) lo = mid;
+            else hi = mid;
+        }
+        r.group = lo;
+        r.m0 = at(bounds + lo) + (int64_t)(tm - at(ends + lo)) * TILE;
+        m1 = at(bounds + lo + 1);
+    } else {
+        if (p.mode == MUON_PRODUCT_DEPTH) {
+            const int per = p.tiles_m * p.tiles_n;
+            r.group = t / per;
+            t -= r.group * per;
+            r.kb0 = at(bounds + r.group) / KB;
+            r.kb1 = max(at(bounds + r.group + 1) / KB, r.kb0);
+        }
+        band_decode(t, p.tiles_m, p.tiles_n, tm, tn);
+        r.m0 = (int64_t)tm * TILE;
+    }
+    r.n0 = (int64_t)tn * TILE;
+    r.rows_a = (int)min(m1 - r.m0, (int64_t)TILE);
+    r.rows_b = (int)min(p.n - r.n0, (int64_t)TILE);
+    return r;
+}
+
+template <int N>
+using ic = std::integral_constant<int, N>;
+
+// A step is one block of k.  Operands go global -> VGPR -> LDS: while a step is multiplied from one of two LDS
+// stages, the next one's registers are stored to the other stage and at once loaded again for the
+// step after it.  (A lone 256 x 256 tile of depth 16384 takes 133 us this way and 152
+// with loads straight to LDS; the matrix instructions alone would take 121.)
+// Rows are 144 bytes apart in LDS: the 16 rows that a fragment read touches fall on 16 different 16-byte slots of the
+// 256 bytes that LDS serves at once, and every read is one address plus a constant.
+//
+// A step has two sub-steps of 64 values.  Its one barrier comes in the middle of the second, whose fragments are then in
+// registers: past it the next stage is complete and this one may be overwritten.  The matrix instructions
+// before it cover the fragment reads that it waits for, those behind it the next stage's first reads.
+template <int AFMT, class OUT>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_kernel(ProductArgs p) {
+    constexpr bool PRECISE = sizeof(OUT) == 4;
+    constexpr int LA = TILE / 64, NLOAD = 2 * LA;          // load instructions of a step: 64 rows each
+    constexpr int ROW = 144, PANEL = TILE * ROW, STAGE = 2 * PANEL;
+    constexpr int EPL = 16 / sizeof(OUT);                  // values of out in 16 bytes
+    constexpr int OROW = 64 * sizeof(OUT) + 16;            // a row of out in LDS
+    static_assert(WAVES * 32 * OROW <= STAGE, "out goes through one stage");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
+    __shared__ __attribute__((aligned(1024))) uint32_t scale_words[2][2 * TILE];
+    __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
+    __shared__ int64_t wave_tot[WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wh = wave >> 2, wn = (wave & 3) * 64;        // wave row; first column
+    const int fr = lane & 31, fk = lane >> 5;
+    const int kp = (int)((p.k + KB - 1) / KB) * KB, sp = (kp / KB + 3) / 4 * 4;
+
+    // Each XCD takes a contiguous share of the tiles (workgroups are dealt to the XCDs in turn) and its
+    // workgroups walk it together, so that the tiles that run at once share operand panels in its L2.
+    int total = p.tiles;
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments(p, bounds, ends, wave_tot);
+    if (p.mode == MUON_PRODUCT_ROWS)
+        total = (int)min((int64_t)__builtin_amdgcn_readfirstlane(ends[p.groups]) * p.tiles_n, (int64_t)p.tiles);
+    const int xcd = blockIdx.x % NUM_XCD, stride = gridDim.x / NUM_XCD;
+    const int share = total / NUM_XCD, rest = total % NUM_XCD;
+    const int first = xcd * share + min(xcd, rest), last_tile = first + share + (xcd < rest ? 1 : 0);
+    int t = first + blockIdx.x / NUM_XCD;
+    if (t >= last_tile) return;
+
+    // staging: load d of wave w brings rows 8 w + 64 i + lane / 8 of an operand
+    const int lrow = 8 * wave + (lane >> 3), lchunk = lane & 7;
+    const int va = lrow * (int)p.lda + 16 * lchunk, vb = lrow * (int)p.ldb + 16 * lchunk;
+    const int wst = lrow * ROW + 16 * lchunk;
+
+    const uint8_t *abase, *bbase, *scale_base;
+    int bytes_a, bytes_b, scale_bytes, vs, s0, s1;
+    i32x4 staged[NLOAD];
+    // Chunk d of a step into its register.  keep is -1, or 0 past the last step: then from an empty buffer, which
+    // fetches nothing (a branch in the main loop would let the compiler move the matrix instructions behind it).
+    auto load = [&](int d, int step, int keep) {
+        const int i = d < LA ? d : d - LA;
+        const int at = (step * KB + i * 64 * (int)(d < LA ? p.lda : p.ldb)) & keep;
+        const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(d < LA ? abase : bbase), 0, (d < LA ? bytes_a : bytes_b) & keep, 0x00020000);
+        staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, d < LA ? va : vb, at, 0);
+    };
+    auto mask = [](bool valid) {
+        int keep = __builtin_amdgcn_readfirstlane(valid ? -1 : 0);
+        asm volatile("" : "+s"(keep));
+        return keep;
+    };
+    auto store = [&](int d, int st) {
+        const int i = d < LA ? d : d - LA;
+        *reinterpret_cast<i32x4*>(smem + st * STAGE + (d < LA ? 0 : PANEL) + 64 * ROW * i + wst) = staged[d];
+    };
+    // Scales, a word of 4 blocks' bytes per row of the tile (a's rows, then b's; wave w brings 64 of them), go through
+    // LDS, two groups of 4 blocks in turn.
+    auto load_scales = [&](int g, bool valid) {
+        load_dword_to_lds(__builtin_amdgcn_make_buffer_rsrc((void*)scale_base, 0, valid ? scale_bytes : 0, 0x00020000), vs,
+                          valid ? 4 * g : 0, &scale_words[g & 1][64 * wave]);
+    };
+    uint32_t ea[FM], eb[FN];
+    auto read_scales = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) ea[i] = scale_words[g & 1][64 * i + 32 * wh + fr];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) eb[j] = scale_words[g & 1][TILE + wn + 32 * j + fr];
+    };
+    // The tile's operands, and the first loads of them.
+    auto begin = [&](const Tile& x) {
+        int ln = lane;
+        asm volatile("" : "+v"(ln));                       // as in write
+        const bool per_group = p.mode == MUON_PRODUCT_ROWS;
+        abase = p.a + x.m0 * p.lda;
+        bbase = p.b + (per_group ? x.group * p.stride_b : 0) + x.n0 * p.ldb;
+        bytes_a = (int)((x.rows_a - 1) * p.lda + kp);
+        bytes_b = (int)((x.rows_b - 1) * p.ldb + kp);
+        const bool is_a = wave < WAVES / 2;
+        const int64_t r0 = is_a ? x.m0 : x.n0, sh = is_a ? p.shift_a : p.shift_b;
+        const int ld = (int)(is_a ? p.ldas : p.ldbs), last = (is_a ? x.rows_a : x.rows_b) - 1;
+        const int64_t base = r0 >> sh;
+        vs = (int)(((r0 + min((64 * wave) % TILE + ln, last)) >> sh) - base) * ld;
+        scale_bytes = __builtin_amdgcn_readfirstlane((int)(((r0 + last) >> sh) - base) * ld + sp);
+        scale_base = uniform((is_a ? p.as : p.bs + (per_group ? x.group * p.stride_bs : 0)) + base * ld);
+        s0 = __builtin_amdgcn_readfirstlane(x.kb0);
+        s1 = __builtin_amdgcn_readfirstlane(x.kb1);
+        load_scales(x.kb0 >> 2, s0 < s1);
+        load_scales((x.kb0 >> 2) + 1, ((x.kb0 >> 2) + 1) * 4 < x.kb1);
+#pragma unroll
+        for (int d = 0; d < NLOAD; ++d) load(d, s0, mask(s0 < s1));
+    };
+
+    // fragments of sub-step kk: 32 codes of a row
+    auto fragment = [&](const uint8_t* row, int kk) {
+        const i32x4 lo = *reinterpret_cast<const i32x4*>(row + 64 * kk);
+        const i32x4 hi = *reinterpret_cast<const i32x4*>(row + 64 * kk + 16);
+        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    const int ra = (32 * wh + fr) * ROW + 32 * fk, rb = PANEL + (wn + fr) * ROW + 32 * fk;
+    auto read_a = [&](int i, int st, int kk) { return fragment(smem + st * STAGE + ra + 64 * i * ROW, kk); };
+    auto read_b = [&](int j, int st, int kk) { return fragment(smem + st * STAGE + rb + 32 * j * ROW, kk); };
+
+    f32x16 acc[FM][FN];
+    // The steps of a tile for a wave with NB row blocks.
+    auto multiply = [&](auto nb_) {
+        constexpr int NB = decltype(nb_)::value;
+        // slots of a sub-step: groups of matrix instructions that staging and reads go behind; the barrier comes
+        // before slot BAR of the second
+        constexpr int SLOTS = PRECISE ? 4 * NB : NB * FN, BAR = PRECISE ? 2 * NB : NB / 2 * FN, HALF = NB / 2;
+        read_scales(s0 >> 2);
+        i32x8 fa[NB], fb[2][FN];                           // a's are refilled in place, b's alternate
+#pragma unroll
+        for (int i = 0; i < NB; ++i) fa[i] = read_a(i, 0, 0);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) fb[0][j] = read_b(j, 0, 0);
+        for (int step = s0; step < s1; ++step) {
+            const int ahead = mask(step + 2 < s1);
+            const int st = (step - s0) & 1, st_next = st ^ 1;
+            const int sh = 8 * (step & 3);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const int cur = kk, nxt = kk ^ 1;
+                const bool last = kk == 1;
+                const int rst = last ? st_next : st;
+                auto turn = [&]() {                          // the barrier of a step, and the scales of the next
+                    pin(acc);
+                    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                    __builtin_amdgcn_s_barrier();
+                    asm volatile("" ::: "memory");
+                    if (((step + 1) & 3) == 0) {
+                        // this sub-step has its exponents, and the words of the group before last are free
+                        const int g = (step + 1) >> 2;
+                        read_scales(g);
+                        load_scales(g + 1, (g + 1) * 4 < s1);
+                    }
+                };
+                auto stage = [&](int f) {                    // this slot's share of the staging, before the barrier
+                    constexpr int ALL = SLOTS + BAR;
+                    if (last && f >= BAR) return;
+                    const int g = kk * SLOTS + f;
+#pragma unroll
+                    for (int d = g * NLOAD / ALL; d < (g + 1) * NLOAD / ALL; ++d) {
+                        store(d, st_next);
+                        load(d, step + 2, ahead);
+                    }
+                };
+                if constexpr (PRECISE) {
+                    float xa[NB], xb[FN];
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) xa[i] = __uint_as_float(((ea[i] >> sh) & 255u) << 23);
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) xb[j] = __uint_as_float(((eb[j] >> sh) & 255u) << 23);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (last && q == 2) turn();
+                        bf16x8 wb[FN];
+#pragma unroll
+                        for (int j = 0; j < FN; ++j)
+                            wb[j] = widen<MUON_FP8_E4M3>(fb[cur][j][2 * q], fb[cur][j][2 * q + 1], xb[j]);
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const bf16x8 wa = widen<AFMT>(fa[i][2 * q], fa[i][2 * q + 1], xa[i]);
+                            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                            for (int j = 0; j < FN; ++j)
+                                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa, acc[i][j], 0, 0, 0);
+                            __builtin_amdgcn_sched_barrier(0);
+                            stage(q * NB + i);
+                            if (q == 2 && i == 0)
+#pragma unroll
+                                for (int j = 0; j < FN; ++j) fb[nxt][j] = read_b(j, rst, nxt);
+                            if (q == 3) fa[i] = read_a(i, rst, nxt);
+                        }
+                    }
+                } else {
+                    int xa[NB], xb[FN];
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) xa[i] = (int)(ea[i] >> sh);
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) xb[j] = (int)(eb[j] >> sh);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        if (last && i == HALF) turn();
+#pragma unroll
+                        for (int j = 0; j < FN; ++j) {
+                            __builtin_amdgcn_sched_barrier(0);
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[cur][j], fa[i], acc[i][j], 0, AFMT, 0,
+                                                                                        xb[j], 0, xa[i]);
+                            __builtin_amdgcn_sched_barrier(0);
+                            stage(i * FN + j);
+                            if (i == (last ? HALF : 0)) {
+                                fb[nxt][j] = read_b(j, rst, nxt);
+                                if (last && j < HALF) fa[j] = read_a(j, rst, nxt);
+                            }
+                            if (j == FN - 1 && (!last || i >= HALF)) fa[i] = read_a(i, rst, nxt);
+                        }
+                    }
+                }
+            }
+        }
+    };
+
+    // The first step into LDS, the second into the registers.
+    auto fill = [&]() {
+        if (s0 >= s1) return;
+#pragma unroll
+        for (int d = 0; d < NLOAD; ++d) {
+            store(d, 0);
+            load(d, s0 + 1, mask(s0 + 1 < s1));
+        }
+    };
+    // Row block i of out: 32 rows x 64 columns of the wave through its part of the second stage (which nobody reads
+    // between a tile's last barrier and the next one's first step), then in 16-byte stores along the rows.
+    OUT* out;
+    Tile done;
+    auto write = [&](int i) {
+        // opaque, so that the addresses are worked out per tile instead of being kept through the main loop
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        uint8_t* mine = smem + STAGE + wave * 32 * OROW;
+        const int r0 = 64 * i + 32 * wh;
+        if (r0 >= done.rows_a) return;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint8_t* o = mine + (ln & 31) * OROW + (32 * j + 8 * q + 4 * (ln >> 5)) * sizeof(OUT);
+                const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                if constexpr (PRECISE) *reinterpret_cast<f32x4*>(o) = v;
+                else *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int LPR = 64 / EPL, RPS = 64 / LPR;      // lanes per row, rows per store
+        const int col = ln % LPR * EPL, row = ln / LPR;
+        const int64_t left = p.n - done.n0 - wn - col;     // columns of out from the lane's first
+        OUT* o = out + (done.m0 + r0 + row) * p.ld_out + done.n0 + wn + col;
+#pragma unroll
+        for (int q = 0; q < 32 / RPS; ++q, o += RPS * p.ld_out) {
+            const uint4 w = *reinterpret_cast<const uint4*>(mine + (q * RPS + row) * OROW + col * sizeof(OUT));
+            if (r0 + q * RPS + row >= done.rows_a) continue;
+            if (p.vec && EPL <= left) {
+                if constexpr (PRECISE) {
+                    f32x4 v = __builtin_bit_cast(f32x4, w);
+                    if (p.accumulate) v += *reinterpret_cast<const f32x4*>(o);
+                    *reinterpret_cast<f32x4*>(o) = v;
+                } else {
+                    *reinterpret_cast<uint4*>(o) = w;
+                }
+            } else {
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < EPL; ++e) {
+                    if (e >= left) continue;
+                    if constexpr (PRECISE) o[e] = p.accumulate ? o[e] + __uint_as_float(u[e]) : __uint_as_float(u[e]);
+                    else o[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+
+    Tile x = decode(p, t, bounds, ends);
+    begin(x);
+    fill();
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+        if (s0 < s1) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const int blocks = (x.rows_a - 32 * wh + 63) / 64;
+            if (blocks >= 4) multiply(ic<4>{});
+            else if (blocks == 3) multiply(ic<3>{});
+            else if (blocks == 2) multiply(ic<2>{});
+            else multiply(ic<1>{});
+        }
+        done = x;
+        out = static_cast<OUT*>(p.out) + (p.mode == MUON_PRODUCT_DEPTH ? done.group * p.out_stride : 0);
+        t += stride;
+        const bool more = t < last_tile;
+        // the next tile's first loads run beside this one's stores
+        if (more) {
+            x = decode(p, t, bounds, ends);
+            begin(x);
+        }
+        write(0);
+        write(1);
+        if (more) fill();
+        write(2);
+        write(3);
+        if (!more) break;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the scale words' loads write LDS
 }
 
 template <int AFMT, class OUT>
-__global__ __launch_bounds__(256) void product_kernel(ProductArgs p) {
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2][2][TILE * KB];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-    const int b = xcd_remap(blockIdx.x, gridDim.x);
-
-    // the tile: rows [m0, m1) of a, from n0 of b, blocks [kb0, kb1)
-    int group = 0;
-    int64_t m0, m1 = p.m;
-    int kb0 = 0, kb1 = (int)((p.k + KB - 1) / KB);
-    const int tn = b % p.tiles_n;
-    int tm = b / p.tiles_n;
-    if (p.mode == MUON_PRODUCT_ROWS) {
-        if (!find_segment(p, tm, group, m0, m1)) return;
-    } else {
-        if (p.mode == MUON_PRODUCT_DEPTH) {
-            group = tm / p.tiles_m;
-            tm -= group * p.tiles_m;
-            const int64_t all = (int64_t)kb1 * KB;
-            const int64_t s = min(max((int64_t)p.offsets[group], (int64_t)0), all);
-            const int64_t e = min(max((int64_t)p.offsets[group + 1], s), all);
-            kb0 = (int)(s / KB);
-            kb1 = (int)(e / KB);
-        }
-        m0 = (int64_t)tm * TILE;
-    }
-    const int64_t n0 = (int64_t)tn * TILE;
-    const bool per_group = p.mode == MUON_PRODUCT_ROWS;
-    const uint8_t* bq = p.b + (per_group ? group * p.stride_b : 0);
-    const uint8_t* bs = p.bs + (per_group ? group * p.stride_bs : 0);
-
-    // staging: wave w loads 8 rows a time, rows 8 (w + 4 i) of either tile; rows past the end repeat the last
-    const uint8_t *ga[4], *gb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 8 * (wave + 4 * i) + (lane >> 3);
-        const int chunk = (lane & 7) ^ ((row >> 1) & 7);
-        ga[i] = p.a + min(m0 + row, m1 - 1) * p.lda + 16 * chunk;
-        gb[i] = bq + min(n0 + row, p.n - 1) * p.ldb + 16 * chunk;
-    }
-    auto stage = [&](int kb, int st) {
-        const int64_t k = (int64_t)kb * KB;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            load_to_lds(ga[i] + k, &smem[st][0][1024 * (wave + 4 * i)]);
-            load_to_lds(gb[i] + k, &smem[st][1][1024 * (wave + 4 * i)]);
-        }
-    };
-    // scales of the fragments' rows
-    const int fr = lane & 15, fk = lane >> 4;
-    const uint8_t *sa[4], *sb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sa[i] = p.as + (min(m0 + wm + 16 * i + fr, m1 - 1) >> p.shift_a) * p.ldas;
-        sb[i] = bs + (min(n0 + wn + 16 * i + fr, p.n - 1) >> p.shift_b) * p.ldbs;
-    }
-    // fragment: 32 of a row's 128 bytes, chunks 2 fk and 2 fk + 1
-    auto fragment = [&](const uint8_t* tile, int row) {
-        const int sw = (row >> 1) & 7;
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(tile + row * KB + 16 * ((2 * fk) ^ sw));
-        const i32x4 hi = *reinterpret_cast<const i32x4*>(tile + row * KB + 16 * ((2 * fk + 1) ^ sw));
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-
-    f32x4 acc[4][4];                                       // [fragment of m][fragment of n]
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-    if (kb0 < kb1) stage(kb0, 0);
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int st = (kb - kb0) & 1;
-        int ea[4], eb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ea[i] = sa[i][kb];
-            eb[i] = sb[i][kb];
-        }
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __syncthreads();                                   // this stage is in; the other is no longer read
-        if (kb + 1 < kb1) stage(kb + 1, st ^ 1);
-        i32x8 fa[4], fb[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            fa[i] = fragment(smem[st][0], wm + 16 * i + fr);
-            fb[i] = fragment(smem[st][1], wn + 16 * i + fr);
-        }
-        if constexpr (sizeof(OUT) == 4) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                bf16x8 wa[4], wb[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    wa[i] = widen<AFMT>(fa[i][2 * q], fa[i][2 * q + 1], __uint_as_float((uint32_t)ea[i] << 23));
-                    wb[i] = widen<MUON_FP8_E4M3>(fb[i][2 * q], fb[i][2 * q + 1], __uint_as_float((uint32_t)eb[i] << 23));
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        fb[j], fa[i], acc[i][j], 0, AFMT, 0, eb[j], 0, ea[i]);
-        }
-    }
-
-    OUT* out = static_cast<OUT*>(p.out) + (p.mode == MUON_PRODUCT_DEPTH ? group * p.out_stride : 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t r = m0 + wm + 16 * i + fr;
-        if (r >= m1) continue;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = n0 + wn + 16 * j + 4 * fk;
-            OUT* o = out + r * p.ld_out + c;
-            f32x4 v = acc[i][j];
-            if (p.vec && c + 4 <= p.n) {
-                if constexpr (sizeof(OUT) == 4) {
-                    f32x4* o4 = reinterpret_cast<f32x4*>(o);
-                    if (p.accumulate) v += *o4;
-                    *o4 = v;
-                } else {
-                    *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
-                }
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (c + q >= p.n) continue;
-                    if constexpr (sizeof(OUT) == 4) o[q] = p.accumulate ? o[q] + v[q] : v[q];
-                    else o[q] = dev::f32_to_bf16(v[q]);
-                }
-            }
-        }
-    }
-}
-
-}  // namespace
-
-hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, hipStream_t s) {
+hipError_t product_as(ProductArgs a, hipStream_t s) {
     a.tiles_n = (int32_t)((a.n + TILE - 1) / TILE);
     a.tiles_m = (int32_t)((a.m + TILE - 1) / TILE);
     // every segment may end inside a tile, but not more of them than there are rows
@@ -264,16 +492,18 @@ hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, hi
     const int64_t total = rows * a.tiles_n;
     if (total >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
     if (total == 0) return hipSuccess;
-    const dim3 grid((unsigned)total), block(256);
-    const bool f32 = out_dtype == MUON_DTYPE_F32;
-    if (a_format == MUON_FP8_E4M3) {
-        if (f32) hipLaunchKernelGGL((product_kernel<0, float>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((product_kernel<0, uint16_t>), grid, block, 0, s, a);
-    } else {
-        if (f32) hipLaunchKernelGGL((product_kernel<1, float>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((product_kernel<1, uint16_t>), grid, block, 0, s, a);
-    }
+    a.tiles = (int32_t)total;
+    const unsigned grid = (unsigned)std::min<int64_t>((total + NUM_XCD - 1) / NUM_XCD * NUM_XCD, CUS);
+    hipLaunchKernelGGL((product_kernel<AFMT, OUT>), dim3(grid), dim3(THREADS), 0, s, a);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, hipStream_t s) {
+    const bool f32 = out_dtype == MUON_DTYPE_F32;
+    if (a_format == MUON_FP8_E4M3) return f32 ? product_as<0, float>(a, s) : product_as<0, uint16_t>(a, s);
+    return f32 ? product_as<1, float>(a, s) : product_as<1, uint16_t>(a, s);
 }
 
 }  // namespace muon

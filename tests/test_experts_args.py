@@ -171,6 +171,7 @@ def _product(mode=0, **kw):
     (0, dict(a__codes=None), L.MUON_ERR_INVALID_ARG), (0, dict(b__scales=None), L.MUON_ERR_INVALID_ARG),
     (0, dict(a__codes=A + 8), L.MUON_ERR_ALIGNMENT), (0, dict(b__scales=T + 4), L.MUON_ERR_ALIGNMENT),
     (0, dict(a__ld=255), L.MUON_ERR_SHAPE), (0, dict(a__ld=240), L.MUON_ERR_SHAPE), (0, dict(b__ld_scales=6), L.MUON_ERR_SHAPE),
+    (0, dict(a__ld=1 << 23), L.MUON_ERR_SHAPE), (0, dict(b__ld_scales=1 << 23), L.MUON_ERR_SHAPE),
     (0, dict(k=600, a__ld=640, b__ld=640), L.MUON_ERR_SHAPE), (0, dict(a__square=2), L.MUON_ERR_INVALID_ARG),
     (1, dict(b__stride=200 * 256 - 16), L.MUON_ERR_SHAPE), (1, dict(b__stride_scales=200 * 4 - 4), L.MUON_ERR_SHAPE),
     (1, dict(b__stride=-16), L.MUON_ERR_SHAPE), (0, dict(out=A), L.MUON_ERR_INVALID_ARG),
