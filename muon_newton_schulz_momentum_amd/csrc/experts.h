@@ -31,7 +31,7 @@ struct RouteBackwardArgs {
 
 // Choices that one workgroup groups in a single launch, and that a workgroup takes of more.
 constexpr int64_t GROUP_SINGLE_MAX = 8192;
-constexpr int64_t GROUP_CHUNK = 4096;
+constexpr int64_t GROUP_CHUNK = 2048;
 
 struct GroupRowsArgs {
     const int32_t* experts;

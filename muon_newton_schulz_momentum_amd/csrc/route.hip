@@ -4,8 +4,7 @@
 //     s_e = exp(x_e - max x) / sum_i exp(x_i - max x)   or   1 / (1 + exp(-x_e)),
 //     key_e = s_e + b_e   (x_e itself without a bias),
 //     the top_k largest keys (of the best groups), w_j = scale * s_j / (sum of the chosen s).
-// One wave takes one token and keeps its E values in registers (expert lane + 64 i in
-// register i).  The scores and keys are float64: two experts' keys that differ in float64 but not in
+// The choice is that of float64 scores and keys: two experts' keys that differ in float64 but not in
 // float32 would otherwise be taken in the order of their rounding errors.
 //
 // Backward, with g_j the weights' gradients times scale and w'_j the weights before scale:
@@ -44,21 +43,64 @@ __device__ __forceinline__ float wave_sum32(float v) {
     return v;
 }
 
-// The largest key of a wave and its index, the lowest index among equal keys; every lane gets it.
-__device__ __forceinline__ void wave_best(double& key, int& idx) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-        const double k = __shfl_xor(key, off, 64);
-        const int i = __shfl_xor(idx, off, 64);
-        if (k > key || (k == key && i < idx)) { key = k; idx = i; }
-    }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dppf(float v) { return __uint_as_float(dpp<CTRL>(__float_as_uint(v))); }
+
+// Exchanges that, one after another, spread over 2, 4, 8 and 16 lanes: neighbours, pairs, halves of 8, halves of 16.
+constexpr int XCHG_1 = 0xb1, XCHG_2 = 0x4e, XCHG_4 = 0x141, XCHG_8 = 0x140;
+
+__device__ __forceinline__ uint32_t row_value(uint32_t v, int row) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * row); }
+
+template <int CTRL>
+__device__ __forceinline__ double dppd(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)u) | ((uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32));
+}
+__device__ __forceinline__ double row_valued(double v, int row) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)row_value((uint32_t)u, row) | ((uint64_t)row_value((uint32_t)(u >> 32), row) << 32));
 }
 
+// The largest key of a wave and its index, the lowest index among equal keys; every lane gets it.
+__device__ __forceinline__ void wave_best(double& key, int& idx) {
+    auto better = [&](double k, int i) {
+        if (k > key || (k == key && i < idx)) { key = k; idx = i; }
+    };
+    better(dppd<XCHG_1>(key), (int)dpp<XCHG_1>((uint32_t)idx));
+    better(dppd<XCHG_2>(key), (int)dpp<XCHG_2>((uint32_t)idx));
+    better(dppd<XCHG_4>(key), (int)dpp<XCHG_4>((uint32_t)idx));
+    better(dppd<XCHG_8>(key), (int)dpp<XCHG_8>((uint32_t)idx));
+    const double k = key;
+    const int i = idx;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) better(row_valued(k, r), (int)row_value((uint32_t)i, r));
+}
+
+// The two largest keys of a wave.
+__device__ __forceinline__ void wave_best2(double& k1, double& k2) {
+    auto merge = [&](double o1, double o2) {
+        k2 = fmax(fmin(k1, o1), fmax(k2, o2));
+        k1 = fmax(k1, o1);
+    };
+    merge(dppd<XCHG_1>(k1), dppd<XCHG_1>(k2));
+    merge(dppd<XCHG_2>(k1), dppd<XCHG_2>(k2));
+    merge(dppd<XCHG_4>(k1), dppd<XCHG_4>(k2));
+    merge(dppd<XCHG_8>(k1), dppd<XCHG_8>(k2));
+    const double r1 = k1, r2 = k2;
+    k1 = row_valued(r1, 0);
+    k2 = row_valued(r2, 0);
+#pragma unroll
+    for (int r = 1; r < 4; ++r) merge(row_valued(r1, r), row_valued(r2, r));
+}
+
+// One token by one wave in float64: expert lane + 64 i in register i.
 template <class T, int V>
-__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p) {
+__device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6);
-    if (t >= p.tokens) return;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     float x[V];
 #pragma unroll
@@ -110,13 +152,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p) {
                 if (k > k1) { k2 = k1; k1 = k; }
                 else if (k > k2) k2 = k;
             }
-#pragma unroll
-            for (int off = 32; off > 0; off >>= 1) {
-                const double o1 = __shfl_xor(k1, off, 64), o2 = __shfl_xor(k2, off, 64);
-                const double lo = fmin(k1, o1);
-                k1 = fmax(k1, o1);
-                k2 = fmax(lo, fmax(k2, o2));
-            }
+            wave_best2(k1, k2);
             if (lane == g) worth = k1 == -INFINITY ? -INFINITY : k1 + (k2 == -INFINITY ? 0.0 : k2);
         }
         int before = 0;
@@ -161,7 +197,467 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p) {
 }
 
 template <class T, int V>
-__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteBackwardArgs p) {
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_exact_kernel(RouteArgs p) {
+    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6);
+    if (t < p.tokens) route_exact<T, V>(p, t);
+}
+
+// ---- 16 or 64 lanes a token -----------------------------------------------------------------
+//
+// Lane l of LT takes experts 4 LT c + 4 l + v (c < C, v < 4).  Scores and keys are float32, as ordered integers
+// whose last 6 bits give way to the expert's place in its lane.  Each lane sorts out its 4 largest (a maximum
+// and three medians per value; again when they are used up), and top_k + 1 rounds take the largest of all lanes.
+// What float32 cannot decide is found by looking at what was taken: two neighbours nearer than the keys' error,
+// or two lanes at once.  Neighbours (with a bias, in one token of forty at 512 experts) are settled by
+// taking on to 16 experts and ranking those by their float64 keys, unless those need the whole row (softmax plus
+// bias); whatever else is left is done again by the whole wave in float64.  So the choice is always the
+// float64 one.
+constexpr int FAST_MAX_K = 15;
+constexpr int64_t WIDE_MAX_TOKENS = 2048;
+
+// Over the LT lanes of a token, to all of them.
+template <int LT>
+__device__ __forceinline__ uint32_t token_max(uint32_t v) {
+    v = max(v, dpp<XCHG_1>(v));
+    v = max(v, dpp<XCHG_2>(v));
+    v = max(v, dpp<XCHG_4>(v));
+    v = max(v, dpp<XCHG_8>(v));
+    if (LT == 64) v = max(max(row_value(v, 0), row_value(v, 1)), max(row_value(v, 2), row_value(v, 3)));
+    return v;
+}
+template <int LT>
+__device__ __forceinline__ float token_maxf(float v) {
+    v = fmaxf(v, dppf<XCHG_1>(v));
+    v = fmaxf(v, dppf<XCHG_2>(v));
+    v = fmaxf(v, dppf<XCHG_4>(v));
+    v = fmaxf(v, dppf<XCHG_8>(v));
+    if (LT == 64) {
+        const uint32_t u = __float_as_uint(v);
+        v = fmaxf(fmaxf(__uint_as_float(row_value(u, 0)), __uint_as_float(row_value(u, 1))),
+                  fmaxf(__uint_as_float(row_value(u, 2)), __uint_as_float(row_value(u, 3))));
+    }
+    return v;
+}
+template <int LT>
+__device__ __forceinline__ float token_sum(float v) {
+    v += dppf<XCHG_1>(v);
+    v += dppf<XCHG_2>(v);
+    v += dppf<XCHG_4>(v);
+    v += dppf<XCHG_8>(v);
+    if (LT == 64) {
+        const uint32_t u = __float_as_uint(v);
+        v = (__uint_as_float(row_value(u, 0)) + __uint_as_float(row_value(u, 1))) +
+            (__uint_as_float(row_value(u, 2)) + __uint_as_float(row_value(u, 3)));
+    }
+    return v;
+}
+
+// Order-preserving bits of a float32 and back.
+__device__ __forceinline__ uint32_t ordered(float f) {
+    const uint32_t u = __float_as_uint(f);
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+    return __uint_as_float(u ^ (((u >> 31) - 1u) | 0x80000000u));
+}
+
+__device__ __forceinline__ uint32_t med3(uint32_t a, uint32_t b, uint32_t c) {
+    return max(min(a, b), min(max(a, b), c));
+}
+
+// Two largest of two pairs, each in falling order.
+__device__ __forceinline__ void merge2(float& a1, float& a2, float b1, float b2) {
+    a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+    a1 = fmaxf(a1, b1);
+}
+
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+}
+
+// Two keys (a above b) that float32 tells apart: scores are off by less than 2^-21, and the place has taken 2^-17 of
+// the size away.
+__device__ __forceinline__ bool apart(float a, float b) { return a - b > 0x1p-16f * fmaxf(1.f, fabsf(a)); }
+
+// GROUPS: n_groups > 1 (16 lanes only).
+template <class T, int LT, int C, bool GROUPS>
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, int vec) {
+    constexpr int PT = 64 / LT;                            // tokens a wave
+    static_assert(!GROUPS || LT == 16, "groups lie in 16 lanes");
+    const int lane = threadIdx.x & 63, l = lane & (LT - 1);
+    const int64_t t0 = ((int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6)) * PT;
+    if (t0 >= p.tokens) return;
+    const int64_t t = t0 + lane / LT;
+    const bool live = t < p.tokens;
+    const T* row = static_cast<const T*>(p.logits) + (live ? t : t0) * p.ld;
+    auto expert = [&](int c, int v) { return 4 * LT * c + 4 * l + v; };
+    float x[C][4];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int e = expert(c, 0);
+        if (vec) {
+            if (e < p.n_experts) load4(row + e, x[c]);
+            else x[c][0] = x[c][1] = x[c][2] = x[c][3] = -INFINITY;
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x[c][v] = e + v < p.n_experts ? load_logit(row + e + v) : -INFINITY;
+        }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            x[c][v] = clean_logit(x[c][v]);
+            top = fmaxf(top, x[c][v]);
+        }
+    top = token_maxf<LT>(top);
+    const bool any = top > -INFINITY;
+    const bool softmax = p.score == MUON_SCORE_SOFTMAX;
+    const bool scored = p.bias || GROUPS;                  // the choice goes by scores
+    // key[c][v]: the score plus bias; and the softmax's sum
+    float z = 0.f, key[C][4];
+    if (softmax && (scored || !p.renormalize)) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                key[c][v] = any ? __expf(x[c][v] - top) : 0.f;
+                z += key[c][v];
+            }
+        z = token_sum<LT>(z);
+        const float inv = any ? 1.f / z : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) key[c][v] *= inv;
+    } else if (scored) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) key[c][v] = __builtin_amdgcn_rcpf(1.f + __expf(-x[c][v]));
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) key[c][v] += expert(c, v) < p.n_experts ? p.bias[expert(c, v)] : 0.f;
+    }
+    bool again = false;                                    // for the whole wave in float64
+    uint64_t kept = ~0ull;                                 // groups that stay
+    const int per = GROUPS ? p.n_experts / p.n_groups : 1;
+    if constexpr (GROUPS) {
+        // per is 16, 32 or a multiple of 64: a group is 4, 8 or 16 lanes of one c, or several c's
+        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // lane l: groups l + 16 i
+        float m1 = -INFINITY, m2 = -INFINITY;
+        int begun = 0;                                     // c's of the group under way
+        float score[C];                                    // this lane's group of row c: its two largest, added up
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float a1 = -INFINITY, a2 = -INFINITY;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float k = x[c][v] > -INFINITY ? key[c][v] : -INFINITY;
+                a2 = fmaxf(fminf(a1, k), a2);
+                a1 = fmaxf(a1, k);
+            }
+            merge2(a1, a2, dppf<XCHG_1>(a1), dppf<XCHG_1>(a2));
+            merge2(a1, a2, dppf<XCHG_2>(a1), dppf<XCHG_2>(a2));
+            if (per >= 32) merge2(a1, a2, dppf<XCHG_4>(a1), dppf<XCHG_4>(a2));
+            if (per >= 64) merge2(a1, a2, dppf<XCHG_8>(a1), dppf<XCHG_8>(a2));
+            // a group of several c's: the running pair, complete at its last c
+            if (begun == 0) { m1 = -INFINITY; m2 = -INFINITY; }
+            merge2(m1, m2, a1, a2);
+            if (++begun * 64 >= per) begun = 0;
+            score[c] = m1 == -INFINITY ? -INFINITY : m1 + (m2 == -INFINITY ? 0.f : m2);
+        }
+        kept = 0;
+        for (int g = 0; g < p.n_groups; ++g) {
+            // group g's sum, from the lane and row that hold it
+            const int first = g * per, c0 = (first + per - 1) / 64, src = (first % 64) / 4;
+            float w = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (c == c0) w = score[c];
+            w = __shfl(w, (lane & 48) + src, 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (l + 16 * i == g) best[i] = w;
+        }
+        // the largest top_groups of them, and one more to see how near it comes
+        float border = INFINITY;
+        for (int r = 0; r <= p.top_groups && r < p.n_groups; ++r) {
+            const float w = token_maxf<LT>(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])));
+            if (r == p.top_groups && w > -INFINITY) again |= !(border - w > 0x1p-19f * fmaxf(1.f, fabsf(border)));
+            border = w;
+            if (r == p.top_groups) break;
+            // which group it is (of two with the same sum either: that token is done again)
+            uint32_t at = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (best[i] == w && l + 16 * i < p.n_groups && !((kept >> (l + 16 * i)) & 1)) at = max(at, (uint32_t)(64 - (l + 16 * i)));
+            at = token_max<LT>(at);
+            const int g = 64 - (int)at;
+            if (at != 0) kept |= 1ull << g;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (l + 16 * i == g) best[i] = -INFINITY;
+        }
+    }
+    // Each lane's 4 largest keys, ordered, the place in the lane in the last 6 bits (larger: lower expert).  bfloat16
+    // logits are decided by 16 bits: there the expert itself fits behind them, and equal logits need no second look.
+    const bool whole = sizeof(T) == 2 && !p.bias;
+    uint32_t bits[C][4];
+    int group = 0, rows = 0;                               // of groups of several c's: which, and its c's so far
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        bool stays = true;
+        if constexpr (GROUPS) {
+            stays = (kept >> (per == 16 ? expert(c, 0) >> 4 : per == 32 ? expert(c, 0) >> 5 : group)) & 1;
+            if (++rows * 64 >= per) { rows = 0; ++group; }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const float k = p.bias ? key[c][v] : x[c][v];
+            const bool in = stays && x[c][v] > -INFINITY && k > -INFINITY;
+            const uint32_t o = ordered(k);
+            const uint32_t kv = whole ? (o & 0xffff0000u) | (uint32_t)(1023 - expert(c, v)) : (o & ~63u) | (uint32_t)(63 - (4 * c + v));
+            bits[c][v] = in ? kv : 0u;
+        }
+    }
+    uint32_t k0, k1, k2, k3;                               // the 4 largest below `below`
+    int had = 0;                                           // of them taken
+    auto sort_out = [&](uint32_t below, bool me) {
+        uint32_t a0 = 0, a1 = 0, a2 = 0, a3 = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const uint32_t u = bits[c][v] < below ? bits[c][v] : 0u;
+                a3 = med3(a2, a3, u);
+                a2 = med3(a1, a2, u);
+                a1 = med3(a0, a1, u);
+                a0 = max(a0, u);
+            }
+        if (me) { k0 = a0; k1 = a1; k2 = a2; k3 = a3; had = 0; }
+    };
+    sort_out(0xffffffffu, true);
+    int taken = 0, mine = -1;                              // keys this lane gave; lane j: the j-th expert taken
+    auto take = [&](uint32_t w, int j) {
+        const bool won = w != 0 && k0 == w;
+        // the winner's expert to every lane of the token
+        const int place = 63 - (int)(w & 63u);
+        const int here = whole ? 1023 - (int)(w & 1023u) : 4 * LT * (place >> 2) + 4 * l + (place & 3);
+        const int e = (int)token_max<LT>(won ? (uint32_t)here + 1u : 0u) - 1;
+        if (l == j) mine = e;
+        if (won) {
+            k0 = k1;
+            k1 = k2;
+            k2 = k3;
+            k3 = 0;
+            ++taken;
+            ++had;
+        }
+        if (__ballot(had == 4)) sort_out(w, had == 4);
+    };
+    // whether float32 decides that a (larger bits) comes before b
+    auto tell = [&](uint32_t a, uint32_t b) {
+        return p.bias ? apart(unordered(a), unordered(b)) : whole || a >> 6 != b >> 6;
+    };
+    bool close = false;                                    // two neighbours, or the border, that it does not
+    uint32_t before = 0, w = token_max<LT>(k0);
+    for (int j = 0; j < p.top_k; ++j) {
+        take(w, j);
+        before = w;
+        w = token_max<LT>(k0);
+        if (w != 0) close |= !tell(before, w);
+    }
+    // two lanes with the same bits leave together
+    again |= token_sum<LT>((float)taken) != token_sum<LT>(mine >= 0 ? 1.f : 0.f);
+
+    int slot = l;                                          // where this lane's expert goes
+    const bool local = !(p.bias && softmax);               // a key is that of its logit alone
+    if (local && __ballot(close && !again)) {
+        // The keys of the 16 first, one a lane, ranked in float64.  Whoever was not taken is below the 16th; so the
+        // ranking holds if the 16th is apart from the last chosen.
+        const uint32_t last = before;
+        for (int j = p.top_k; j < 16; ++j) {
+            take(w, j);
+            before = w;
+            w = token_max<LT>(k0);
+        }
+        const bool two = token_sum<LT>((float)taken) != token_sum<LT>(mine >= 0 ? 1.f : 0.f);
+        if (close) again |= two || (before != 0 && !tell(last, before));
+        double k64 = -INFINITY;
+        if (mine >= 0) {
+            k64 = (double)clean_logit(load_logit(row + mine));
+            if (p.bias) k64 = sigmoid64(k64) + (double)p.bias[mine];
+        }
+        int rank = 0;
+        for (int j = 0; j < 16; ++j) {
+            const double other = __shfl(k64, (lane & ~(LT - 1)) + j, 64);
+            const int e = __shfl(mine, (lane & ~(LT - 1)) + j, 64);
+            if (other > k64 || (other == k64 && e >= 0 && e < mine)) ++rank;
+        }
+        if (close) {
+            slot = mine >= 0 ? rank : l;
+            if (slot >= p.top_k) mine = -1;
+        } else if (l >= p.top_k) {
+            mine = -1;
+        }
+    } else if (close) {
+        again = true;
+    }
+
+    float s = 0.f;
+    if (mine >= 0) {
+        const float xj = clean_logit(load_logit(row + mine));
+        s = softmax ? expf(xj - top) : 1.f / (1.f + expf(-xj));
+    }
+    float weight = s;
+    if (p.renormalize) {
+        const float total = token_sum<LT>(s);
+        again |= token_max<LT>(mine >= 0 ? 1u : 0u) != 0 && !(total > 1e-12f);   // its terms may have lost digits
+        weight = total > 0.f ? s / total : 0.f;
+    } else if (softmax) {
+        weight = any ? s / z : 0.f;
+    }
+    if (live && !again && slot < p.top_k && (mine >= 0 || slot == l)) {
+        p.experts[t * p.top_k + slot] = mine;
+        p.weights[t * p.top_k + slot] = weight * p.scale;
+    }
+    uint64_t left = __ballot(live && again && l == 0);
+    while (left) {
+        const int g = __builtin_ctzll(left);
+        left &= left - 1;
+        route_exact<T, LT * C / 16>(p, t0 + g / LT);
+    }
+}
+
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) { *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+}
+
+__device__ __forceinline__ double token_sum16(double v) {
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// Backward for up to 16 slots: 16 lanes a token as in route_kernel, lane j also slot j.
+template <class T, int C>
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteBackwardArgs p, int vec) {
+    const int lane = threadIdx.x & 63, l = lane & 15;
+    const int64_t t0 = ((int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6)) * 4;
+    if (t0 >= p.tokens) return;
+    const bool live = t0 + (lane >> 4) < p.tokens;
+    const int64_t t = live ? t0 + (lane >> 4) : t0;
+    const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+    T* grad = static_cast<T*>(p.grad_logits) + t * p.ld_grad;
+    int e = -1;
+    float xj = -INFINITY, g = 0.f;
+    if (l < p.top_k) {
+        e = p.experts[t * p.top_k + l];
+        if (e < 0 || e >= p.n_experts) e = -1;
+        if (e >= 0) xj = clean_logit(load_logit(row + e));
+        if (!(xj > -INFINITY)) e = -1;
+        if (e >= 0) g = p.grad_weights[t * p.top_k + l] * p.scale;
+    }
+    float out[C][4];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) out[c][v] = 0.f;
+    float dx;                                              // what slot l adds to its expert
+    if (p.score == MUON_SCORE_SIGMOID) {
+        const double ex = exp(-fabs((double)xj));          // s and 1 - s without cancellation
+        const double big = 1.0 / (1.0 + ex), small = ex * big;
+        const double s = e < 0 ? 0.0 : xj >= 0.f ? big : small, rest = xj >= 0.f ? small : big;
+        if (p.renormalize) {
+            const double total = token_sum16(s);
+            const double w = total > 0.0 ? s / total : 0.0;
+            const double mean = token_sum16((double)g * w);
+            dx = e >= 0 ? (float)(w * rest * ((double)g - mean)) : 0.f;
+        } else {
+            dx = e >= 0 ? (float)((double)g * s * rest) : 0.f;
+        }
+    } else if (p.renormalize) {
+        const float top = token_maxf<16>(xj);
+        const double ex = e >= 0 ? exp((double)xj - (double)top) : 0.0;
+        const double total = token_sum16(ex);
+        const double w = total > 0.0 ? ex / total : 0.0;
+        const double mean = token_sum16((double)g * w);
+        dx = e >= 0 ? (float)(w * ((double)g - mean)) : 0.f;
+    } else {
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int ei = 64 * c + 4 * l;
+            if (vec) {
+                if (ei < p.n_experts) load4(row + ei, out[c]);
+                else out[c][0] = out[c][1] = out[c][2] = out[c][3] = -INFINITY;
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) out[c][v] = ei + v < p.n_experts ? load_logit(row + ei + v) : -INFINITY;
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                out[c][v] = clean_logit(out[c][v]);
+                top = fmaxf(top, out[c][v]);
+            }
+        }
+        top = token_maxf<16>(top);
+        float z = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                out[c][v] = out[c][v] > -INFINITY ? __expf(out[c][v] - top) : 0.f;
+                z += out[c][v];
+            }
+        z = token_sum<16>(z);
+        const float inv = z > 0.f ? 1.f / z : 0.f;
+        const float pj = e >= 0 ? __expf(xj - top) * inv : 0.f;
+        dx = e >= 0 ? g * pj : 0.f;
+        const float mean = token_sum<16>(dx) * -inv;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) out[c][v] *= mean;
+    }
+    for (int j = 0; j < p.top_k; ++j) {
+        const int ej = __shfl(e, (lane & 48) + j, 64);
+        const float dj = __shfl(dx, (lane & 48) + j, 64);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (ej == 64 * c + 4 * l + v) out[c][v] += dj;
+    }
+    if (!live) return;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int ei = 64 * c + 4 * l;
+        if (vec) {
+            if (ei < p.n_experts) store4(grad + ei, out[c]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (ei + v < p.n_experts) store_logit(grad + ei + v, out[c][v]);
+        }
+    }
+}
+
+// Backward for any number of slots: a wave a token.
+template <class T, int V>
+__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(RouteBackwardArgs p) {
     const int lane = threadIdx.x & 63;
     const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6);
     if (t >= p.tokens) return;
@@ -361,50 +857,56 @@ __global__ __launch_bounds__(GROUP_THREADS) void group_count_kernel(GroupRowsArg
     }
 }
 
-// partial[chunk][e] becomes the row where the chunk's first choice of expert e goes.
-__global__ __launch_bounds__(GROUP_THREADS) void group_scan_kernel(GroupRowsArgs p) {
+// partial[chunk][e] becomes the number of the expert's choices in earlier chunks, and counts[e] all of them: a wave
+// for each expert, a lane for each of 64 chunks at a time.
+__global__ __launch_bounds__(256) void group_prefix_kernel(GroupRowsArgs p) {
+    const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (e >= p.n_experts) return;
+    int before = 0;
+    for (int64_t b0 = 0; b0 < p.chunks; b0 += 64) {
+        const int64_t b = b0 + lane;
+        const int h = b < p.chunks ? p.partial[b * p.n_experts + e] : 0;
+        int inc = h;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int o = __shfl_up(inc, off, 64);
+            if (lane >= off) inc += o;
+        }
+        if (b < p.chunks) p.partial[b * p.n_experts + e] = before + inc - h;
+        before += __shfl(inc, 63, 64);
+    }
+    if (lane == 0) p.counts[e] = before;
+}
+
+// Every workgroup works the offsets out from the counts; the first writes them down.
+__global__ __launch_bounds__(GROUP_THREADS) void group_place_kernel(GroupRowsArgs p) {
+    extern __shared__ int lds[];
     __shared__ int wave_tot[GROUP_WAVES];
+    const int64_t lo = blockIdx.x * GROUP_CHUNK, hi = min(p.n, lo + GROUP_CHUNK);
+    count(p, lo, hi, GROUP_CHUNK / GROUP_WAVES, lds);
     const int e = threadIdx.x;
-    int c = 0;
-    if (e < p.n_experts)
-        for (int64_t b = 0; b < p.chunks; ++b) c += p.partial[b * p.n_experts + e];
+    const int c = e < p.n_experts ? p.counts[e] : 0;
     const int padded = (c + p.align - 1) / p.align * p.align;
     int total;
     const int start = block_prefix(padded, wave_tot, total);
     if (e < p.n_experts) {
-        int at = start;
-        for (int64_t b = 0; b < p.chunks; ++b) {
-            const int h = p.partial[b * p.n_experts + e];
-            p.partial[b * p.n_experts + e] = at;
-            at += h;
-        }
-        p.counts[e] = c;
-        p.offsets[e] = start;
-    }
-    if (threadIdx.x == 0) p.offsets[p.n_experts] = total;
-}
-
-__global__ __launch_bounds__(GROUP_THREADS) void group_place_kernel(GroupRowsArgs p) {
-    extern __shared__ int lds[];
-    const int64_t lo = blockIdx.x * GROUP_CHUNK, hi = min(p.n, lo + GROUP_CHUNK);
-    count(p, lo, hi, GROUP_CHUNK / GROUP_WAVES, lds);
-    for (int e = threadIdx.x; e < p.n_experts; e += GROUP_THREADS) {
-        int at = p.partial[blockIdx.x * (int64_t)p.n_experts + e];
+        int at = start + p.partial[blockIdx.x * (int64_t)p.n_experts + e];
         for (int w = 0; w < GROUP_WAVES; ++w) {
             const int h = lds[w * p.n_experts + e];
             lds[w * p.n_experts + e] = at;
             at += h;
         }
+        if (blockIdx.x == 0) p.offsets[e] = start;
+        // a segment's padding
+        if (e % gridDim.x == blockIdx.x)
+            for (int r = start + c; r < start + padded; ++r) p.rows[r] = -1;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.n_experts] = total;
     __syncthreads();
     place(p, lo, hi, GROUP_CHUNK / GROUP_WAVES, lds);
-    // the padding of segments, and what lies behind the last one
-    for (int64_t e = blockIdx.x; e < p.n_experts; e += gridDim.x)
-        for (int64_t r = (int64_t)p.offsets[e] + p.counts[e] + threadIdx.x; r < p.offsets[e + 1]; r += GROUP_THREADS)
-            p.rows[r] = -1;
+    // what lies behind the last segment
     const int64_t step = (int64_t)gridDim.x * GROUP_THREADS;
-    for (int64_t r = p.offsets[p.n_experts] + blockIdx.x * (int64_t)GROUP_THREADS + threadIdx.x; r < p.capacity; r += step)
-        p.rows[r] = -1;
+    for (int64_t r = total + blockIdx.x * (int64_t)GROUP_THREADS + threadIdx.x; r < p.capacity; r += step) p.rows[r] = -1;
 }
 
 __global__ __launch_bounds__(GROUP_THREADS) void balance_kernel(const float* bias, const int32_t* counts, int32_t n,
@@ -424,21 +926,54 @@ __global__ __launch_bounds__(GROUP_THREADS) void balance_kernel(const float* bia
     out[e] = d > 0 ? bias[e] + rate : d < 0 ? bias[e] - rate : bias[e];
 }
 
+// Variants, by what the sizes allow and what they measured (7 of 512 experts):
+//   * 16 lanes a token from 2048 tokens on (65536 tokens, softmax: 37 us, a wave a token in float64: 200 us), and for
+//     groups of 16, 32 or multiples of 64, which lie in a row of lanes;
+//   * 64 lanes below (16 tokens: 5.6 us against 8.4), where a wave's own time counts, and above 512 experts, whose
+//     values 16 lanes cannot hold;
+//   * the float64 wave for what neither covers: more than 15 choices, other groups.
 template <class T>
 hipError_t route_by_width(const RouteArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.tokens + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(64 * ROUTE_WAVES);
-    if (a.n_experts <= 128) hipLaunchKernelGGL((route_kernel<T, 2>), grid, block, 0, s, a);
-    else if (a.n_experts <= 512) hipLaunchKernelGGL((route_kernel<T, 8>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((route_kernel<T, 16>), grid, block, 0, s, a);
+    const int per = a.n_experts / a.n_groups;
+    const bool few = a.top_k <= FAST_MAX_K, flat = a.n_groups == 1;
+    const bool wide = few && flat && (a.tokens < WIDE_MAX_TOKENS || a.n_experts > 512);
+    const bool narrow = few && !wide && a.n_experts <= 512 && (flat || per == 16 || per == 32 || per % 64 == 0);
+    const int64_t per_block = ROUTE_WAVES * (narrow ? 4 : 1);
+    const dim3 grid((unsigned)((a.tokens + per_block - 1) / per_block)), block(64 * ROUTE_WAVES);
+    const int vec = a.ld % 4 == 0 && a.n_experts % 4 == 0;
+    if (wide) {
+        if (a.n_experts <= 256) hipLaunchKernelGGL((route_kernel<T, 64, 1, false>), grid, block, 0, s, a, vec);
+        else if (a.n_experts <= 512) hipLaunchKernelGGL((route_kernel<T, 64, 2, false>), grid, block, 0, s, a, vec);
+        else hipLaunchKernelGGL((route_kernel<T, 64, 4, false>), grid, block, 0, s, a, vec);
+    } else if (narrow && flat) {
+        if (a.n_experts <= 128) hipLaunchKernelGGL((route_kernel<T, 16, 2, false>), grid, block, 0, s, a, vec);
+        else hipLaunchKernelGGL((route_kernel<T, 16, 8, false>), grid, block, 0, s, a, vec);
+    } else if (narrow) {
+        if (a.n_experts <= 128) hipLaunchKernelGGL((route_kernel<T, 16, 2, true>), grid, block, 0, s, a, vec);
+        else hipLaunchKernelGGL((route_kernel<T, 16, 8, true>), grid, block, 0, s, a, vec);
+    } else {
+        if (a.n_experts <= 128) hipLaunchKernelGGL((route_exact_kernel<T, 2>), grid, block, 0, s, a);
+        else if (a.n_experts <= 512) hipLaunchKernelGGL((route_exact_kernel<T, 8>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((route_exact_kernel<T, 16>), grid, block, 0, s, a);
+    }
     return hipGetLastError();
 }
 
 template <class T>
 hipError_t backward_by_width(const RouteBackwardArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.tokens + ROUTE_WAVES - 1) / ROUTE_WAVES)), block(64 * ROUTE_WAVES);
-    if (a.n_experts <= 128) hipLaunchKernelGGL((route_backward_kernel<T, 2>), grid, block, 0, s, a);
-    else if (a.n_experts <= 512) hipLaunchKernelGGL((route_backward_kernel<T, 8>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((route_backward_kernel<T, 16>), grid, block, 0, s, a);
+    const bool fast = a.top_k <= 16;
+    const int64_t per_block = ROUTE_WAVES * (fast ? 4 : 1);
+    const dim3 grid((unsigned)((a.tokens + per_block - 1) / per_block)), block(64 * ROUTE_WAVES);
+    const int vec = a.ld % 4 == 0 && a.ld_grad % 4 == 0 && a.n_experts % 4 == 0;
+    if (fast) {
+        if (a.n_experts <= 128) hipLaunchKernelGGL((route_backward_kernel<T, 2>), grid, block, 0, s, a, vec);
+        else if (a.n_experts <= 512) hipLaunchKernelGGL((route_backward_kernel<T, 8>), grid, block, 0, s, a, vec);
+        else hipLaunchKernelGGL((route_backward_kernel<T, 16>), grid, block, 0, s, a, vec);
+    } else {
+        if (a.n_experts <= 128) hipLaunchKernelGGL((route_backward_wave_kernel<T, 2>), grid, block, 0, s, a);
+        else if (a.n_experts <= 512) hipLaunchKernelGGL((route_backward_wave_kernel<T, 8>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((route_backward_wave_kernel<T, 16>), grid, block, 0, s, a);
+    }
     return hipGetLastError();
 }
 
@@ -461,7 +996,7 @@ hipError_t launch_group_rows(const GroupRowsArgs& a, hipStream_t s) {
     }
     const dim3 grid((unsigned)a.chunks);
     hipLaunchKernelGGL(group_count_kernel, grid, block, lds, s, a);
-    hipLaunchKernelGGL(group_scan_kernel, dim3(1), block, 0, s, a);
+    hipLaunchKernelGGL(group_prefix_kernel, dim3((unsigned)((a.n_experts + 3) / 4)), dim3(256), 0, s, a);
     hipLaunchKernelGGL(group_place_kernel, grid, block, lds, s, a);
     return hipGetLastError();
 }

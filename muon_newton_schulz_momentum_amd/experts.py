@@ -40,6 +40,9 @@ def _up(v: int, step: int) -> int:
     return -(-v // step) * step
 
 
+_AS_IT_IS = contextlib.nullcontext()
+
+
 @contextlib.contextmanager
 def _switched(device: torch.device, stream: Optional[torch.cuda.Stream]):
     with torch.cuda.device(device), torch.cuda.stream(stream):
@@ -51,13 +54,14 @@ def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
     stream that the kernels run on."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+    if stream is None and t.device.index == torch._C._cuda_getDevice():
+        return _AS_IT_IS
     return _switched(t.device, stream)
 
 
-def _stream_ptr() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _stream_ptr(t: torch.Tensor) -> int:
+    # the current stream of t's device, without the Stream object that torch.cuda.current_stream makes (7 us)
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _tensor(name: str, t: torch.Tensor, like: torch.Tensor, dtype, shape=None, contiguous=True) -> torch.Tensor:
@@ -108,7 +112,7 @@ def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = No
         experts = torch.empty(size, dtype=torch.int32, device=logits.device)
         weights = torch.empty(size, dtype=torch.float32, device=logits.device)
         L.check(L.muon_route(C.byref(k), logits.data_ptr(), None if bias is None else bias.data_ptr(),
-                             experts.data_ptr(), weights.data_ptr(), _stream_ptr()), "muon_route")
+                             experts.data_ptr(), weights.data_ptr(), _stream_ptr(logits)), "muon_route")
     return experts, weights
 
 
@@ -128,7 +132,7 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weights: to
         else:
             _tensor("out", out, logits, logits.dtype, logits.shape, contiguous=False)
         L.check(L.muon_route_backward(C.byref(k), logits.data_ptr(), experts.data_ptr(), grad_weights.data_ptr(),
-                                      out.data_ptr(), _rows("out", out), _stream_ptr()), "muon_route_backward")
+                                      out.data_ptr(), _rows("out", out), _stream_ptr(logits)), "muon_route_backward")
     return out
 
 
@@ -159,7 +163,7 @@ def group_rows(experts: torch.Tensor, n_experts: int, *, align: int = 1, stream=
                    torch.empty(cap.value, dtype=torch.int32, device=dev), torch.empty_like(experts))
         work = torch.empty(ws.value, dtype=torch.uint8, device=dev)
         L.check(L.muon_group_rows(experts.data_ptr(), n, n_experts, align, g.counts.data_ptr(), g.offsets.data_ptr(),
-                                  g.rows.data_ptr(), g.position.data_ptr(), work.data_ptr(), ws.value, _stream_ptr()),
+                                  g.rows.data_ptr(), g.position.data_ptr(), work.data_ptr(), ws.value, _stream_ptr(experts)),
                 "muon_group_rows")
     return g
 
@@ -178,7 +182,7 @@ def balance_step(bias: torch.Tensor, counts: torch.Tensor, rate: float, *, out: 
         else:
             _tensor("out", out, bias, torch.float32, bias.shape)
         L.check(L.muon_balance_step(bias.data_ptr(), counts.data_ptr(), bias.numel(), rate, out.data_ptr(),
-                                    _stream_ptr()), "muon_balance_step")
+                                    _stream_ptr(bias)), "muon_balance_step")
     return out
 
 
@@ -278,7 +282,7 @@ def quantize(src: torch.Tensor, *, block: str = "row", format: str = "e4m3", tra
             k.codes_t, k.scales_t = got[1].codes.data_ptr(), got[1].scales.data_ptr()
         # without rows there is nothing to write (and torch gives an empty tensor no address)
         if n > 0 and k.batch > 0:
-            L.check(L.muon_fp8_quantize(C.byref(k), _stream_ptr()), "muon_fp8_quantize")
+            L.check(L.muon_fp8_quantize(C.byref(k), _stream_ptr(src)), "muon_fp8_quantize")
     return (got[0], got[1]) if transpose else got[0]
 
 
@@ -334,5 +338,5 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
         if group == "depth":
             k.out_stride = out.stride(0) if k.groups > 1 else k.m * k.ld_out
         k.accumulate = 1 if accumulate else 0
-        L.check(L.muon_fp8_product(C.byref(k), _stream_ptr()), "muon_fp8_product")
+        L.check(L.muon_fp8_product(C.byref(k), _stream_ptr(a.codes)), "muon_fp8_product")
     return out

@@ -2,7 +2,9 @@
 
 Tolerances.  u = 2^-24 is float32's half step, 2^-8 bfloat16's.
   * choices, groups, scales and codes are compared for equality;
-  * weights are float64 values rounded once: u, and half of float32's least denormal;
+  * sigmoid weights: expf is off by 4 u at most, 1 + e and the quotient by u, a sum of 64 and its quotient by 65 u: 80 u;
+    softmax weights: the argument's rounding (|x - max| <= 40 here) 40 u, twice for the chosen and the sum, the sum's
+    1024 terms in 16 lanes 68 u and its exponentials' 62 u: 256 u; beside 1e-32 where terms are denormal;
   * the routing gradient is off by the rounding of g = grad * scale (u each, in the terms g and mean of
     at most max|g|, with their products: 8 u B, B = (weight or score) * max|g|) and its own
     rounding; the unnormalised softmax works in float32: its exponent's argument (|x - max| <= 40 here)
@@ -68,7 +70,7 @@ def _check_route(x, experts, weights, want, k):
     e_ref, w_ref = want
     assert np.array_equal(experts.cpu().numpy(), e_ref)
     w = _np(weights)
-    assert (np.abs(w - w_ref) <= U * (1 + 1e-6) * np.abs(w_ref) + 2.0 ** -150).all()
+    assert (np.abs(w - w_ref) <= 256 * U * np.abs(w_ref) + 1e-32).all()
 
 
 ROUTES = [
@@ -88,6 +90,20 @@ ROUTES = [
     (6, 1024, 64, torch.float32, "plain", dict(score="softmax", bias=True, renormalize=False)),
     (6, 96, 5, torch.float32, "plain", dict(score="sigmoid", groups=96 // 3 // 2, top_groups=3)),
     (4, 256, 3, torch.float32, "lowest", dict(score="sigmoid")),
+    (1003, 512, 7, torch.float32, "plain", dict(score="sigmoid", bias=True)),
+    (1003, 512, 8, torch.bfloat16, "ties", dict(score="softmax")),
+    (301, 512, 8, torch.float32, "ties", dict(score="softmax", groups=8, top_groups=4)),
+    (301, 256, 8, torch.bfloat16, "ties", dict(score="sigmoid", groups=8, top_groups=4, bias=True)),
+    (65, 256, 15, torch.float32, "masked", dict(score="softmax", groups=4, top_groups=2, bias=True)),
+    (65, 160, 6, torch.float32, "plain", dict(score="softmax", groups=10, top_groups=3)),
+    (65, 1024, 6, torch.bfloat16, "masked", dict(score="sigmoid", groups=4, top_groups=1)),
+    (65, 1024, 9, torch.float32, "plain", dict(score="softmax", groups=64, top_groups=5, bias=True)),
+    (5, 100, 15, torch.float32, "masked", dict(score="sigmoid", bias=True)),
+    (2051, 300, 7, torch.bfloat16, "masked", dict(score="sigmoid", bias=True)),
+    (2051, 512, 15, torch.float32, "ties", dict(score="softmax", renormalize=False)),
+    (2050, 65, 4, torch.bfloat16, "lowest", dict(score="softmax", bias=True)),
+    (2048, 128, 8, torch.float32, "wild", dict(score="softmax")),
+    (7, 20, 15, torch.bfloat16, "wild", dict(score="softmax")),
 ]
 
 
@@ -133,6 +149,36 @@ def test_route_keeps_near_ties_apart():
     assert experts.cpu().tolist() == [[40, 0]]
     s = torch.sigmoid(x)
     assert s[0, 40] == s[0, 0]            # which is why float32 keys would not do
+
+
+def test_route_low_scores_and_crowded_lanes():
+    """Scores that underflow in float32, and the chosen experts side by side (one lane's)."""
+    x = torch.randn(40, 512, device="cuda", generator=_gen(2)) - 120.0
+    for kw in (dict(score="sigmoid"), dict(score="sigmoid", renormalize=False), dict(score="softmax")):
+        experts, weights = X().route(x, 6, **kw)
+        e_ref, w_ref = orc.route(_np(x), 6, **kw)
+        assert np.array_equal(experts.cpu().numpy(), e_ref)
+        # e^-120 is below float32's normal range: half its least denormal, 2^-150
+        assert (np.abs(_np(weights) - w_ref) <= 256 * U * w_ref + 2.0 ** -149).all()
+    x = torch.randn(40, 512, device="cuda", generator=_gen(3))
+    x[:, 4:8] += 20.0
+    x[:, 68:72] += 18.0
+    for bias in (None, torch.zeros(512, device="cuda")):
+        for dtype in (torch.float32, torch.bfloat16):
+            y = x.to(dtype)
+            experts, weights = X().route(y, 7, bias=bias)
+            _check_route(y, experts, weights, orc.route(_np(y), 7, None if bias is None else _np(bias)), 7)
+
+
+def test_route_bias_infinite_and_nan():
+    x = torch.randn(9, 64, device="cuda", generator=_gen(4))
+    bias = torch.zeros(64, device="cuda")
+    bias[3], bias[5], bias[7] = float("inf"), -float("inf"), float("nan")
+    for groups, top in ((1, 1), (2, 1), (4, 2)):
+        kw = dict(groups=groups, top_groups=top, score="sigmoid")
+        experts, weights = X().route(x, 4, bias=bias, **kw)
+        _check_route(x, experts, weights, orc.route(_np(x), 4, _np(bias), **kw), 4)
+        assert (experts[:, 0] == 3).all() and not ((experts == 5) | (experts == 7)).any()
 
 
 def test_route_strided_and_large_rows():
