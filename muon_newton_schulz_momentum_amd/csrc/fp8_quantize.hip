@@ -2,8 +2,8 @@
 //
 // For a block of values with the largest finite magnitude amax, e is the least exponent with
 // amax <= MAX * 2^e (MAX = 1.75 * 2^8 for e4m3, 1.75 * 2^15 for e5m2): with amax = f * 2^E, 1 <= f
-// < 2, that is E - 8 (or E - 15), and one more where f > 1.75.  The code is v * 2^-e, an exact product
-// of float32 values, rounded once by the conversion instruction; it never exceeds MAX.
+// < 2, that is E - 8 (or E - 15), and one more where f > 1.75.  The code is v * 2^-e, which never exceeds MAX, rounded
+// once by the scaling conversion instruction.
 //
 // One workgroup takes a 128 x 128 tile, 8 x 8 values a thread: src is read once whatever is
 // written, a row's block and (in the transposed copy) a column's block lie inside the tile, and a thread's
@@ -22,53 +22,174 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     const int e = (int)(amax >> 23) - (FMT == MUON_FP8_E4M3 ? 8 : 15) + ((amax & 0x7fffffu) > 0x600000u ? 1 : 0);
     return (uint32_t)max(e, 0);
 }
-__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// The byte as the conversions take it.
+__device__ __forceinline__ float scale_operand(uint32_t byte) { return __uint_as_float(byte << 23); }
 
-// Magnitude bits of a finite value, 0 for an infinity or NaN.
-__device__ __forceinline__ uint32_t finite_bits(float v) {
-    const uint32_t u = __float_as_uint(v) & 0x7fffffffu;
-    return u < 0x7f800000u ? u : 0u;
+constexpr uint32_t INF_BITS = 0x7f800000u;
+
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Over the 16 lanes of a row, to all of them.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, false));    // neighbours
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, false));    // pairs
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, false));   // halves of 8
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, false));  // halves of 16
+}
+// Over the same lane of the wave's four rows, to all of them.
+__device__ __forceinline__ uint32_t max_rows(uint32_t v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max((uint32_t)a[0], (uint32_t)a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max((uint32_t)b[0], (uint32_t)b[1]);
 }
 
-template <int FMT>
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-    int w = 0;
-    if (FMT == MUON_FP8_E4M3) {
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-    } else {
-        w = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, w, false);
-        w = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
-    }
-    return (uint32_t)w;
+// Two values over 2^(byte - 127) as codes in the low or high half of a word: one instruction each, rounding to nearest
+// even; scale carries the byte in its exponent.
+template <int FMT, bool HIGH>
+__device__ __forceinline__ s16x2 convert2(s16x2 old, float a, float b, float scale) {
+    if constexpr (FMT == MUON_FP8_E4M3) return __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(old, a, b, scale, HIGH);
+    else return __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(old, a, b, scale, HIGH);
+}
+template <int FMT, bool HIGH>
+__device__ __forceinline__ s16x2 convert2(s16x2 old, uint32_t pair, float scale) {
+    const bf16x2 v = __builtin_bit_cast(bf16x2, pair);
+    if constexpr (FMT == MUON_FP8_E4M3) return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(old, v, scale, HIGH);
+    else return __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(old, v, scale, HIGH);
 }
 
-// v * s, with a NaN for an infinity.
-__device__ __forceinline__ float scaled(float v, float s) {
-    return fabsf(v) < INFINITY ? v * s : __uint_as_float(0x7fc00000u);
-}
+// A thread's 8 x 8 values as they are in memory.
+template <class T>
+struct Block;
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+template <>
+struct Block<float> {
+    float v[8][8];
+    __device__ __forceinline__ void clear(int i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
     }
-}
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return dev::bf16_to_f32(*p); }
+    __device__ __forceinline__ void load(int i, const float* p) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
+        v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
+    }
+    __device__ __forceinline__ void set(int i, int j, float x) { v[i][j] = x; }
+    // Largest magnitude bits of each row and column; with FINITE infinities and NaN count as zeros.
+    template <bool FINITE>
+    __device__ __forceinline__ void maxima(uint32_t (&row)[8], uint32_t (&col)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[i] = col[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t u = __float_as_uint(v[i][j]) & 0x7fffffffu;
+                if (FINITE && u >= INF_BITS) u = 0;
+                row[i] = max(row[i], u);
+                col[j] = max(col[j], u);
+            }
+    }
+    __device__ __forceinline__ void infinities_to_nan() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if ((__float_as_uint(v[i][j]) & 0x7fffffffu) == INF_BITS) v[i][j] = __uint_as_float(0x7fc00000u);
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2 row_codes(int i, float scale) const {
+        s16x2 a = {0, 0}, b = {0, 0};
+        a = convert2<FMT, false>(a, v[i][0], v[i][1], scale);
+        a = convert2<FMT, true>(a, v[i][2], v[i][3], scale);
+        b = convert2<FMT, false>(b, v[i][4], v[i][5], scale);
+        b = convert2<FMT, true>(b, v[i][6], v[i][7], scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2 col_codes(int j, float scale) const {
+        s16x2 a = {0, 0}, b = {0, 0};
+        a = convert2<FMT, false>(a, v[0][j], v[1][j], scale);
+        a = convert2<FMT, true>(a, v[2][j], v[3][j], scale);
+        b = convert2<FMT, false>(b, v[4][j], v[5][j], scale);
+        b = convert2<FMT, true>(b, v[6][j], v[7][j], scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    }
+};
+
+template <>
+struct Block<uint16_t> {
+    uint32_t w[8][4];          // two values a word
+    __device__ __forceinline__ void clear(int i) { w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0; }
+    __device__ __forceinline__ void load(int i, const uint16_t* p) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
+    }
+    __device__ __forceinline__ void set(int i, int j, uint16_t x) { w[i][j >> 1] |= (uint32_t)x << (16 * (j & 1)); }
+    template <bool FINITE>
+    __device__ __forceinline__ void maxima(uint32_t (&row)[8], uint32_t (&col)[8]) const {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = u16x2{0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            u16x2 r = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t u = w[i][k] & 0x7fff7fffu;
+                if (FINITE && (u & 0xffffu) >= 0x7f80u) u &= 0xffff0000u;
+                if (FINITE && u >= INF_BITS) u &= 0xffffu;
+                const u16x2 h = __builtin_bit_cast(u16x2, u);
+                r = __builtin_elementwise_max(r, h);
+                c[k] = __builtin_elementwise_max(c[k], h);
+            }
+            row[i] = (uint32_t)max(r[0], r[1]) << 16;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            col[2 * k] = (uint32_t)c[k][0] << 16;
+            col[2 * k + 1] = (uint32_t)c[k][1] << 16;
+        }
+    }
+    __device__ __forceinline__ void infinities_to_nan() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if ((w[i][k] & 0x7fffu) == 0x7f80u) w[i][k] |= 0x40u;
+                if ((w[i][k] & 0x7fff0000u) == INF_BITS) w[i][k] |= 0x400000u;
+            }
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2 row_codes(int i, float scale) const {
+        s16x2 a = {0, 0}, b = {0, 0};
+        a = convert2<FMT, false>(a, w[i][0], scale);
+        a = convert2<FMT, true>(a, w[i][1], scale);
+        b = convert2<FMT, false>(b, w[i][2], scale);
+        b = convert2<FMT, true>(b, w[i][3], scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    }
+    // values (i, j) and (i + 1, j) in one word
+    __device__ __forceinline__ uint32_t pair(int i, int j) const {
+        return __builtin_amdgcn_perm(w[i + 1][j >> 1], w[i][j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+    }
+    template <int FMT>
+    __device__ __forceinline__ uint2 col_codes(int j, float scale) const {
+        s16x2 a = {0, 0}, b = {0, 0};
+        a = convert2<FMT, false>(a, pair(0, j), scale);
+        a = convert2<FMT, true>(a, pair(2, j), scale);
+        b = convert2<FMT, false>(b, pair(4, j), scale);
+        b = convert2<FMT, true>(b, pair(6, j), scale);
+        return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+    }
+};
 
 template <class T, int FMT, bool SQUARE>
 __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) {
     __shared__ __attribute__((aligned(16))) uint8_t lds_t[QT * QT];
-    __shared__ uint32_t col_amax[4][QT];
+    __shared__ __attribute__((aligned(16))) uint32_t col_amax[4][QT];
     __shared__ uint32_t tile_amax[4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int cg = tid & 15, rg = tid >> 4;
@@ -82,11 +203,10 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) 
 
     const T* src = static_cast<const T*>(p.src) + mat * p.batch_stride;
     const int64_t c = c0 + 8 * cg;
-    float v[8][8];
+    Block<T> v;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        v.clear(i);
         const int64_t r = r0 + 8 * rg + i;
         if (r >= end) continue;
         int64_t sr = r;
@@ -98,28 +218,32 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) 
         }
         const T* row = src + sr * p.ld;
         if (vec && c + 8 <= p.cols) {
-            load8(row + c, v[i]);
+            v.load(i, row + c);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (c + j < p.cols) v[i][j] = load1(row + c + j);
+                if (c + j < p.cols) v.set(i, j, row[c + j]);
         }
     }
 
-    uint32_t all = 0;
+    uint32_t row_max[8], col_max[8], all = 0;
+    v.template maxima<false>(row_max, col_max);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all = max(all, row_max[i]);
+    if (__ballot(all >= INF_BITS)) {                       // an infinity or NaN among the wave's values
+        v.infinities_to_nan();
+        v.template maxima<true>(row_max, col_max);
+        all = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all = max(all, row_max[i]);
+    }
     if (SQUARE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) all = max(all, finite_bits(v[i][j]));
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) all = max(all, (uint32_t)__shfl_xor((int)all, off, 64));
+        all = max_rows(max16(all));
         if (lane == 0) tile_amax[wave] = all;
         __syncthreads();
         all = max(max(tile_amax[0], tile_amax[1]), max(tile_amax[2], tile_amax[3]));
     }
     const uint32_t tile_byte = scale_byte<FMT>(all);
-    const float tile_inv = inverse_scale(tile_byte);
 
     if (p.codes) {
         uint8_t* codes = p.codes + mat * p.rows * p.kp;
@@ -127,22 +251,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 8 * rg + i;
-            uint32_t byte = tile_byte;
-            float inv = tile_inv;
-            if (!SQUARE) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) m = max(m, finite_bits(v[i][j]));
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, off, 64));
-                byte = scale_byte<FMT>(m);
-                inv = inverse_scale(byte);
-            }
+            const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(max16(row_max[i]));
             if (r < end) {
-                uint2 w;
-                w.x = codes4<FMT>(scaled(v[i][0], inv), scaled(v[i][1], inv), scaled(v[i][2], inv), scaled(v[i][3], inv));
-                w.y = codes4<FMT>(scaled(v[i][4], inv), scaled(v[i][5], inv), scaled(v[i][6], inv), scaled(v[i][7], inv));
-                *reinterpret_cast<uint2*>(codes + r * p.kp + c) = w;
+                *reinterpret_cast<uint2*>(codes + r * p.kp + c) = v.template row_codes<FMT>(i, scale_operand(byte));
                 if (!SQUARE) {
                     if (cg == 0) scales[r * p.sp + tc] = (uint8_t)byte;
                     else if (tc + 1 == p.tiles_c && tc + cg < p.sp) scales[r * p.sp + tc + cg] = 0;
@@ -154,33 +265,26 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) 
     }
 
     if (p.codes_t) {
-        // lane of columns 8 cg .. 8 cg + 7: column amax over the wave's four row groups, then over the waves
-        float inv[8];
+        // columns 8 cg .. 8 cg + 7: over the wave's four row groups, then over the waves
         if (!SQUARE) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) m = max(m, finite_bits(v[i][j]));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-                if (lane < 16) col_amax[wave][8 * cg + j] = m;
+            for (int j = 0; j < 8; ++j) col_max[j] = max_rows(col_max[j]);
+            if (lane < 16) {
+                uint4* to = reinterpret_cast<uint4*>(col_amax[wave] + 8 * cg);
+                to[0] = make_uint4(col_max[0], col_max[1], col_max[2], col_max[3]);
+                to[1] = make_uint4(col_max[4], col_max[5], col_max[6], col_max[7]);
             }
             __syncthreads();
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) col_max[j] = max(col_max[j], col_amax[w][8 * cg + j]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int col = 8 * cg + j;
-            inv[j] = tile_inv;
-            if (!SQUARE) {
-                const uint32_t m = max(max(col_amax[0][col], col_amax[1][col]), max(col_amax[2][col], col_amax[3][col]));
-                inv[j] = inverse_scale(scale_byte<FMT>(m));
-            }
-            uint2 w;
-            w.x = codes4<FMT>(scaled(v[0][j], inv[j]), scaled(v[1][j], inv[j]), scaled(v[2][j], inv[j]), scaled(v[3][j], inv[j]));
-            w.y = codes4<FMT>(scaled(v[4][j], inv[j]), scaled(v[5][j], inv[j]), scaled(v[6][j], inv[j]), scaled(v[7][j], inv[j]));
+            const uint32_t byte = SQUARE ? tile_byte : scale_byte<FMT>(col_max[j]);
             // 8-byte granule rg of transposed row col, at granule rg ^ cg: the 16 lanes of a row group hit 16 granules
-            *reinterpret_cast<uint2*>(lds_t + col * QT + 8 * (rg ^ cg)) = w;
+            *reinterpret_cast<uint2*>(lds_t + (8 * cg + j) * QT + 8 * (rg ^ cg)) = v.template col_codes<FMT>(j, scale_operand(byte));
         }
         __syncthreads();
         uint8_t* codes = p.codes_t + mat * p.cols * p.kp_t;
