@@ -15,6 +15,7 @@
 // out is asked for where sums go on being added up, so there the codes become bfloat16
 // values (exact, the scale included) and v_mfma_f32_32x32x16_bf16 keeps full float32 sums, at half the rate.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "device_common.h"
@@ -86,11 +87,7 @@ __device__ __forceinline__ void pin(f32x16 (&acc)[FM][FN]) {
         for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
 }
 
-// Tiles of 256 x 256, one workgroup of 8 waves per CU that goes through its share of them.  Wave (h, c) of 2 x 4 takes the 32
-// row blocks 2 i + h and columns 64 c .. 64 c + 63, so that a tile with fewer rows (a segment's end) leaves both
-// wave rows half of what there is: a wave runs its first NB of 4 row blocks.
-constexpr int TILE = 256, WAVES = 8, THREADS = 64 * WAVES;
-constexpr int FM = 4, FN = 2;                             // 32 x 32 blocks of a wave
+constexpr int WAVES = 8, THREADS = 64 * WAVES;
 
 struct Tile {
     int64_t m0, n0;            // first row of a, of b
@@ -100,7 +97,7 @@ struct Tile {
 
 // The segments' bounds, clamped to the operand, and (rows-grouped) how many tile rows lie before each segment, into
 // LDS, by the whole workgroup.
-__device__ __forceinline__ void read_segments(const ProductArgs& p, int* bounds, int* ends, int64_t* wave_tot) {
+__device__ __forceinline__ void read_segments(const ProductArgs& p, int tile_rows, int* bounds, int* ends, int64_t* wave_tot) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t limit = p.mode == MUON_PRODUCT_ROWS ? p.m : (p.k + KB - 1) / KB * KB;
     for (int g = tid; g <= p.groups; g += THREADS) bounds[g] = (int)min(max((int64_t)p.offsets[g], (int64_t)0), limit);
@@ -111,7 +108,7 @@ __device__ __forceinline__ void read_segments(const ProductArgs& p, int* bounds,
     int64_t before = 0;
     for (int g0 = 0; g0 < p.groups; g0 += THREADS) {
         const int g = g0 + tid;
-        int64_t inc = g < p.groups ? (max(bounds[g + 1] - bounds[g], 0) + TILE - 1) / TILE : 0;
+        int64_t inc = g < p.groups ? ((int64_t)max(bounds[g + 1] - bounds[g], 0) + tile_rows - 1) / tile_rows : 0;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
             const int64_t o = __shfl_up(inc, off, 64);
@@ -130,8 +127,9 @@ __device__ __forceinline__ void read_segments(const ProductArgs& p, int* bounds,
     }
 }
 
-// Tile t of the launch.
-__device__ __forceinline__ Tile decode(const ProductArgs& p, int t, const int* bounds, const int* ends) {
+// Tile t of the launch, of up to tile_rows x tile_cols.
+__device__ __forceinline__ Tile decode(const ProductArgs& p, int t, int tile_rows, int tile_cols, const int* bounds,
+                                       const int* ends) {
     auto at = [](const int* v) { return __builtin_amdgcn_readfirstlane(*v); };
     Tile r;
     r.group = 0;
@@ -149,7 +147,7 @@ __device__ __forceinline__ Tile decode(const ProductArgs& p, int t, const int* b
             else hi = mid;
         }
         r.group = lo;
-        r.m0 = at(bounds + lo) + (int64_t)(tm - at(ends + lo)) * TILE;
+        r.m0 = at(bounds + lo) + (int64_t)(tm - at(ends + lo)) * tile_rows;
         m1 = at(bounds + lo + 1);
     } else {
         if (p.mode == MUON_PRODUCT_DEPTH) {
@@ -160,13 +158,36 @@ __device__ __forceinline__ Tile decode(const ProductArgs& p, int t, const int* b
             r.kb1 = max(at(bounds + r.group + 1) / KB, r.kb0);
         }
         band_decode(t, p.tiles_m, p.tiles_n, tm, tn);
-        r.m0 = (int64_t)tm * TILE;
+        r.m0 = (int64_t)tm * tile_rows;
     }
-    r.n0 = (int64_t)tn * TILE;
-    r.rows_a = (int)min(m1 - r.m0, (int64_t)TILE);
-    r.rows_b = (int)min(p.n - r.n0, (int64_t)TILE);
+    r.n0 = (int64_t)tn * tile_cols;
+    r.rows_a = (int)min(m1 - r.m0, (int64_t)tile_rows);
+    r.rows_b = (int)min(p.n - r.n0, (int64_t)tile_cols);
     return r;
 }
+
+// A workgroup's tiles: each XCD takes a contiguous share of them (workgroups are dealt to the XCDs in turn) and its
+// workgroups walk it together, so that the tiles that run at once share operand panels in its L2.
+struct Walk {
+    int t, last, stride;       // first tile, end of the XCD's share, step
+};
+__device__ __forceinline__ Walk walk(const ProductArgs& p, const int* ends) {
+    int total = p.tiles;
+    if (p.mode == MUON_PRODUCT_ROWS)
+        total = (int)min((int64_t)__builtin_amdgcn_readfirstlane(ends[p.groups]) * p.tiles_n, (int64_t)p.tiles);
+    const int xcd = blockIdx.x % NUM_XCD;
+    const int share = total / NUM_XCD, rest = total % NUM_XCD;
+    const int first = xcd * share + min(xcd, rest);
+    return {first + (int)blockIdx.x / NUM_XCD, first + share + (xcd < rest ? 1 : 0), (int)gridDim.x / NUM_XCD};
+}
+
+// ---- 256 x 256 tiles ----------------------------------------------------------------------
+//
+// One workgroup of 8 waves per CU that goes through its share of the tiles.  Wave (h, c) of 2 x 4 takes the 32-row
+// blocks 2 i + h and columns 64 c .. 64 c + 63, so that a tile with fewer rows (a segment's end) leaves both
+// wave rows half of what there is: a wave runs its first NB of 4 row blocks.
+constexpr int TILE = 256;
+constexpr int FM = 4, FN = 2;                             // 32 x 32 blocks of a wave
 
 template <int N>
 using ic = std::integral_constant<int, N>;
@@ -198,17 +219,10 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const int fr = lane & 31, fk = lane >> 5;
     const int kp = (int)((p.k + KB - 1) / KB) * KB, sp = (kp / KB + 3) / 4 * 4;
 
-    // Each XCD takes a contiguous share of the tiles (workgroups are dealt to the XCDs in turn) and its
-    // workgroups walk it together, so that the tiles that run at once share operand panels in its L2.
-    int total = p.tiles;
-    if (p.mode != MUON_PRODUCT_DENSE) read_segments(p, bounds, ends, wave_tot);
-    if (p.mode == MUON_PRODUCT_ROWS)
-        total = (int)min((int64_t)__builtin_amdgcn_readfirstlane(ends[p.groups]) * p.tiles_n, (int64_t)p.tiles);
-    const int xcd = blockIdx.x % NUM_XCD, stride = gridDim.x / NUM_XCD;
-    const int share = total / NUM_XCD, rest = total % NUM_XCD;
-    const int first = xcd * share + min(xcd, rest), last_tile = first + share + (xcd < rest ? 1 : 0);
-    int t = first + blockIdx.x / NUM_XCD;
-    if (t >= last_tile) return;
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments(p, TILE, bounds, ends, wave_tot);
+    const Walk my = walk(p, ends);
+    int t = my.t;
+    if (t >= my.last) return;
 
     // staging: load d of wave w brings rows 8 w + 64 i + lane / 8 of an operand
     const int lrow = 8 * wave + (lane >> 3), lchunk = lane & 7;
@@ -444,7 +458,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         __builtin_amdgcn_wave_barrier();
     };
 
-    Tile x = decode(p, t, bounds, ends);
+    Tile x = decode(p, t, TILE, TILE, bounds, ends);
     begin(x);
     fill();
     for (;;) {
@@ -464,11 +478,11 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         }
         done = x;
         out = static_cast<OUT*>(p.out) + (p.mode == MUON_PRODUCT_DEPTH ? done.group * p.out_stride : 0);
-        t += stride;
-        const bool more = t < last_tile;
+        t += my.stride;
+        const bool more = t < my.last;
         // the next tile's first loads run beside this one's stores
         if (more) {
-            x = decode(p, t, bounds, ends);
+            x = decode(p, t, TILE, TILE, bounds, ends);
             begin(x);
         }
         write(0);
@@ -481,20 +495,180 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the scale words' loads write LDS
 }
 
-template <int AFMT, class OUT>
-hipError_t product_as(ProductArgs a, hipStream_t s) {
-    a.tiles_n = (int32_t)((a.n + TILE - 1) / TILE);
-    a.tiles_m = (int32_t)((a.m + TILE - 1) / TILE);
+// ---- few tiles: 32 x 64 or 32 x 16, depth split over the waves ---------------------------------
+//
+// Where 256 x 256 tiles would leave most of the chip idle.  Each of 8 waves takes every eighth block of k of a tile of
+// 32 rows of a by 16 NB rows of b, its fragments (v_mfma_scale_f32_16x16x128_f8f6f4: a block at once) straight from
+// memory into registers, AHEAD blocks at a time, so that a tile's loads are under way together; the waves' sums are
+// added up through LDS in the order of the waves.
+constexpr int FEW_ROWS = 32;
+
+template <int AFMT, class OUT, int NB, int AHEAD>
+__global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
+    constexpr bool PRECISE = sizeof(OUT) == 4;
+    constexpr int COLS = 16 * NB, SUMS = COLS + 4;         // columns of a tile; a row of sums in LDS
+    __shared__ __attribute__((aligned(16))) float sums[WAVES][FEW_ROWS * SUMS];
+    __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
+    __shared__ int64_t wave_tot[WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int fr = lane & 15, fk = lane >> 4;
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments(p, FEW_ROWS, bounds, ends, wave_tot);
+    const Walk my = walk(p, ends);
+    for (int t = my.t; t < my.last; t += my.stride) {
+        const Tile x = decode(p, t, FEW_ROWS, COLS, bounds, ends);
+        const bool per_group = p.mode == MUON_PRODUCT_ROWS;
+        // offsets of the lane's rows from the tile's first; rows past the end repeat the last: their sums are not stored
+        const uint8_t* abase = p.a + x.m0 * p.lda;
+        const uint8_t* bbase = p.b + (per_group ? x.group * p.stride_b : 0) + x.n0 * p.ldb;
+        const int64_t sa0 = x.m0 >> p.shift_a, sb0 = x.n0 >> p.shift_b;
+        const uint8_t* as = p.as + sa0 * p.ldas;
+        const uint8_t* bs = p.bs + (per_group ? x.group * p.stride_bs : 0) + sb0 * p.ldbs;
+        uint32_t oa[2], sa[2], ob[NB], sb[NB];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = min(16 * i + fr, x.rows_a - 1);
+            oa[i] = (uint32_t)r * (uint32_t)p.lda + 32 * fk;
+            sa[i] = (uint32_t)(((x.m0 + r) >> p.shift_a) - sa0) * (uint32_t)p.ldas;
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int r = min(16 * j + fr, x.rows_b - 1);
+            ob[j] = (uint32_t)r * (uint32_t)p.ldb + 32 * fk;
+            sb[j] = (uint32_t)(((x.n0 + r) >> p.shift_b) - sb0) * (uint32_t)p.ldbs;
+        }
+        auto codes = [](const uint8_t* at) {
+            const i32x4 lo = *reinterpret_cast<const i32x4*>(at), hi = *reinterpret_cast<const i32x4*>(at + 16);
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        f32x4 acc[2][NB];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        // U blocks from kb0 on, all of them there
+        auto blocks = [&](auto u_, int kb0) {
+            constexpr int U = decltype(u_)::value;
+            i32x8 fa[U][2], fb[U][NB];
+            int ea[U][2], eb[U][NB];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int kb = kb0 + u * WAVES;
+                const int64_t k = (int64_t)kb * KB;
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    fb[u][j] = codes(bbase + k + ob[j]);
+                    eb[u][j] = bs[sb[j] + kb];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    fa[u][i] = codes(abase + k + oa[i]);
+                    ea[u][i] = as[sa[i] + kb];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if constexpr (PRECISE) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        bf16x8 wa[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            wa[i] = widen<AFMT>(fa[u][i][2 * q], fa[u][i][2 * q + 1], __uint_as_float((uint32_t)ea[u][i] << 23));
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) {
+                            const bf16x8 wb = widen<MUON_FP8_E4M3>(fb[u][j][2 * q], fb[u][j][2 * q + 1], __uint_as_float((uint32_t)eb[u][j] << 23));
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, wa[i], acc[i][j], 0, 0, 0);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[u][j], fa[u][i], acc[i][j], 0, AFMT, 0, eb[u][j], 0, ea[u][i]);
+                }
+            }
+        };
+        int kb = x.kb0 + wave;
+        for (; kb + (AHEAD - 1) * WAVES < x.kb1; kb += AHEAD * WAVES) blocks(ic<AHEAD>{}, kb);
+        for (; kb < x.kb1; kb += WAVES) blocks(ic<1>{}, kb);
+        // a lane's sums are rows 16 i + fr, columns 16 j + 4 fk + (0 .. 3)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) *reinterpret_cast<f32x4*>(&sums[wave][(16 * i + fr) * SUMS + 16 * j + 4 * fk]) = acc[i][j];
+        __syncthreads();
+        if (tid < FEW_ROWS * COLS / 4) {
+            const int row = tid / (COLS / 4), col = 4 * (tid % (COLS / 4));
+            f32x4 v = *reinterpret_cast<const f32x4*>(&sums[0][row * SUMS + col]);
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) v += *reinterpret_cast<const f32x4*>(&sums[w][row * SUMS + col]);
+            if (row < x.rows_a) {
+                OUT* o = static_cast<OUT*>(p.out) + (p.mode == MUON_PRODUCT_DEPTH ? x.group * p.out_stride : 0) +
+                         (x.m0 + row) * p.ld_out + x.n0 + col;
+                const int64_t left = p.n - x.n0 - col;
+                if (p.vec && left >= 4) {
+                    if constexpr (PRECISE) {
+                        f32x4* o4 = reinterpret_cast<f32x4*>(o);
+                        if (p.accumulate) v += *o4;
+                        *o4 = v;
+                    } else {
+                        *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e >= left) continue;
+                        if constexpr (PRECISE) o[e] = p.accumulate ? o[e] + v[e] : v[e];
+                        else o[e] = dev::f32_to_bf16(v[e]);
+                    }
+                }
+            }
+        }
+        __syncthreads();                                   // the sums are read
+    }
+}
+
+// Tiles of a launch, at most; -1 for too many.
+int64_t count_tiles(ProductArgs& a, int tile_rows, int tile_cols) {
+    a.tiles_n = (int32_t)((a.n + tile_cols - 1) / tile_cols);
+    a.tiles_m = (int32_t)((a.m + tile_rows - 1) / tile_rows);
     // every segment may end inside a tile, but not more of them than there are rows
     int64_t rows = a.tiles_m;
-    if (a.mode == MUON_PRODUCT_ROWS) rows = a.m / TILE + (a.m < a.groups ? a.m : (int64_t)a.groups);
+    if (a.mode == MUON_PRODUCT_ROWS) rows = a.m / tile_rows + (a.m < a.groups ? a.m : (int64_t)a.groups);
     if (a.mode == MUON_PRODUCT_DEPTH) rows *= a.groups;
     const int64_t total = rows * a.tiles_n;
-    if (total >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;
-    if (total == 0) return hipSuccess;
+    if (total >= (int64_t)1 << 31) return -1;
     a.tiles = (int32_t)total;
-    const unsigned grid = (unsigned)std::min<int64_t>((total + NUM_XCD - 1) / NUM_XCD * NUM_XCD, CUS);
-    hipLaunchKernelGGL((product_kernel<AFMT, OUT>), dim3(grid), dim3(THREADS), 0, s, a);
+    return total;
+}
+
+template <int AFMT, class OUT>
+hipError_t product_as(ProductArgs a, hipStream_t s) {
+    ProductArgs few = a, thin = a;
+    const int64_t n_big = count_tiles(a, TILE, TILE), n_few = count_tiles(few, FEW_ROWS, 64), n_thin = count_tiles(thin, FEW_ROWS, 16);
+    if (n_big < 0) return hipErrorInvalidConfiguration;
+    if (n_big == 0) return hipSuccess;
+    // What each would take, in us, from what they measured: big tiles by the round of 256 (256 x 4096 x 4096: 38 us in
+    // bfloat16, 76 in float32), the others by the depth of a wave where there are few tiles and by the blocks of all
+    // tiles where there are many.  1 row by 4096 x 4096: 26 us in big tiles, 12 in 32 x 64, 6 in 32 x 16; 256 rows: 38,
+    // 30, 61; 512 rows: 40, 55, 118; 256 x 256 x 16384: 128, 52, 31; 112 rows of 512 experts, 1024 x 4096: 94, 104, 115.
+    const double kb = (double)((a.k + KB - 1) / KB) / (a.mode == MUON_PRODUCT_DEPTH ? a.groups : 1);
+    // (a big tile runs as many of its 4 row blocks as it has rows for: of its 64 rows each)
+    const int64_t rows = a.mode == MUON_PRODUCT_ROWS ? a.m / std::min<int64_t>(a.m, a.groups) : a.m;
+    const double more = (double)std::min<int64_t>((std::min<int64_t>(rows, TILE) + 63) / 64 - 1, 3) / 3.0;
+    const double step = sizeof(OUT) == 4 ? 1.0 + 1.2 * more : 0.66 + 0.39 * more;
+    const double t_big = std::ceil((double)n_big / CUS) * (5.0 + kb * step);
+    const double t_few = n_few < 0 ? 1e30 : 5.0 + std::max(kb / WAVES * 2.5, (double)n_few * kb / 590.0);
+    const double t_thin = n_thin < 0 ? 1e30 : 4.0 + std::max(kb / WAVES * 1.6, (double)n_thin * kb / 1150.0);
+    const int pick = t_big <= std::min(t_few, t_thin) ? 0 : t_few <= t_thin ? 1 : 2;
+    const int64_t total = pick == 0 ? n_big : pick == 1 ? n_few : n_thin;
+    const int64_t most = pick == 0 ? CUS : 2 * CUS;        // workgroups that run at once
+    const dim3 grid((unsigned)std::min<int64_t>((total + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)), block(THREADS);
+    if (pick == 0) hipLaunchKernelGGL((product_kernel<AFMT, OUT>), grid, block, 0, s, a);
+    else if (pick == 1) hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, 4, 2>), grid, block, 0, s, few);
+    else hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, 1, 4>), grid, block, 0, s, thin);
     return hipGetLastError();
 }
 

@@ -218,16 +218,19 @@ class Fp8:
         return v.flatten(-2)[..., :self.cols]
 
 
-def _check_fp8(name: str, q: Fp8, like: torch.Tensor, dims: int, formats) -> None:
-    _tensor(f"{name}.codes", q.codes, like, formats, contiguous=False)
-    _tensor(f"{name}.scales", q.scales, like, torch.float8_e8m0fnu, contiguous=False)
-    if q.codes.dim() != dims or q.scales.dim() != dims or q.codes.shape[:-2] != q.scales.shape[:-2]:
-        raise ValueError(f"{name} must have {dims} dimensions, the same in codes and scales")
+def _layout(name: str, q: Fp8):
+    """The shape and strides of q's codes and the strides of its scales, after checking that the two go together."""
+    shape, strides, sshape, sstrides = q.codes.shape, q.codes.stride(), q.scales.shape, q.scales.stride()
     kb = -(-q.cols // BLOCK)
-    srows = -(-q.rows // BLOCK) if q.square else q.rows
-    if q.cols < 0 or q.codes.shape[-1] != kb * BLOCK or tuple(q.scales.shape[-2:]) != (srows, _up(kb, 4)):
-        raise ValueError(f"{name}: codes {tuple(q.codes.shape)} and scales {tuple(q.scales.shape)} are not those of "
-                         f"{q.cols} columns, square={q.square}")
+    srows = -(-shape[-2] // BLOCK) if q.square else shape[-2]
+    if q.cols < 0 or shape[-1] != kb * BLOCK or sshape[-1] != -(-kb // 4) * 4 or sshape[-2] != srows or shape[:-2] != sshape[:-2]:
+        raise ValueError(f"{name}: codes {tuple(shape)} and scales {tuple(sshape)} are not those of {q.cols} columns, "
+                         f"square={q.square}")
+    if q.codes.device != q.scales.device or q.scales.dtype != torch.float8_e8m0fnu:
+        raise ValueError(f"{name}.scales must be float8_e8m0fnu on the codes' device")
+    if kb and (strides[-1] != 1 or sstrides[-1] != 1):
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return shape, strides, sshape, sstrides
 
 
 def quantize(src: torch.Tensor, *, block: str = "row", format: str = "e4m3", transpose: bool = False,
@@ -264,7 +267,9 @@ def quantize(src: torch.Tensor, *, block: str = "row", format: str = "e4m3", tra
             if len(got) != len(want):
                 raise ValueError("out must be an Fp8, or with transpose a pair of them")
             for name, q, (r, c) in zip(("out", "transposed out"), got, want):
-                _check_fp8(name, q, src, src.dim(), ftype)
+                if q.codes.device != src.device or q.codes.dtype != ftype or q.codes.dim() != src.dim():
+                    raise ValueError(f"{name} must be {ftype} with {src.dim()} dimensions on {src.device}")
+                _layout(name, q)
                 if (q.rows, q.cols, q.square) != (r, c, square) or (stack is not None and q.codes.shape[0] != stack):
                     raise ValueError(f"{name} must hold {(r, c)}, square={square}")
                 if not q.codes.is_contiguous() or not q.scales.is_contiguous():
@@ -286,15 +291,22 @@ def quantize(src: torch.Tensor, *, block: str = "row", format: str = "e4m3", tra
     return (got[0], got[1]) if transpose else got[0]
 
 
-def _operand(q: Fp8, stacked: bool) -> L.muon_fp8_operand:
-    o = L.muon_fp8_operand()
-    o.codes, o.scales = q.codes.data_ptr(), q.scales.data_ptr()
-    o.ld, o.ld_scales = _rows("codes", q.codes), _rows("scales", q.scales)
-    if stacked:
-        o.stride, o.stride_scales = q.codes.stride(0), q.scales.stride(0)
-    o.format = L.MUON_FP8_E4M3 if q.codes.dtype == torch.float8_e4m3fn else L.MUON_FP8_E5M2
-    o.square = 1 if q.square else 0
-    return o
+def _operand(o: L.muon_fp8_operand, name: str, q: Fp8, stacked: bool) -> torch.Size:
+    """Fills o with q, checked; the shape of its codes."""
+    shape, strides, sshape, sstrides = _layout(name, q)
+    dtype = q.codes.dtype
+    if len(shape) != (3 if stacked else 2):
+        raise ValueError(f"{name} must be {'a stack of matrices' if stacked else 'one matrix'}")
+    if dtype == torch.float8_e5m2:
+        o.format = L.MUON_FP8_E5M2
+    elif dtype != torch.float8_e4m3fn:
+        raise ValueError(f"{name} has dtype {dtype}")
+    o.codes, o.scales, o.square = q.codes.data_ptr(), q.scales.data_ptr(), 1 if q.square else 0
+    o.ld = strides[-2] if shape[-2] > 1 else shape[-1]
+    o.ld_scales = sstrides[-2] if sshape[-2] > 1 else sshape[-1]
+    if stacked and shape[0] > 1:
+        o.stride, o.stride_scales = strides[0], sstrides[0]
+    return shape
 
 
 def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Optional[str] = None,
@@ -309,34 +321,35 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
     """
     if group not in _GROUPS:
         raise ValueError("group must be None, 'rows' or 'depth'")
-    if dtype not in _DTYPES:
-        raise ValueError("dtype must be float32 or bfloat16")
+    if (group is None) != (offsets is None):
+        raise ValueError("offsets go with group 'rows' or 'depth'")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    with _on(a.codes, stream):
-        _check_fp8("a", a, a.codes, 2, (torch.float8_e4m3fn, torch.float8_e5m2))
-        _check_fp8("b", b, a.codes, 3 if group == "rows" else 2, torch.float8_e4m3fn)
+    codes = a.codes
+    with _on(codes, stream):
+        k = L.muon_fp8_product_config()
+        k.mode, k.groups = _GROUPS[group], 1
+        (m, _), (*stack, n, _) = _operand(k.a, "a", a, False), _operand(k.b, "b", b, group == "rows")
+        if b.codes.device != codes.device or b.codes.dtype != torch.float8_e4m3fn:
+            raise ValueError(f"b must have dtype float8_e4m3fn on {codes.device}")
         if a.cols != b.cols:
             raise ValueError(f"a has {a.cols} columns, b {b.cols}")
-        k = L.muon_fp8_product_config()
-        k.mode, k.m, k.n, k.k = _GROUPS[group], a.rows, b.rows, a.cols
-        k.groups = 1
-        if (group is None) != (offsets is None):
-            raise ValueError("offsets go with group 'rows' or 'depth'")
+        k.m, k.n, k.k = m, n, a.cols
         if offsets is not None:
-            _tensor("offsets", offsets, a.codes, torch.int32)
+            _tensor("offsets", offsets, codes, torch.int32)
             k.groups, k.offsets = offsets.numel() - 1, offsets.data_ptr()
-            if offsets.dim() != 1 or (group == "rows" and b.codes.shape[0] != k.groups):
+            if offsets.dim() != 1 or (stack and stack[0] != k.groups):
                 raise ValueError("offsets must be (groups + 1,)")
-        shape = (k.groups, k.m, k.n) if group == "depth" else (k.m, k.n)
+        shape = (k.groups, m, n) if group == "depth" else (m, n)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=a.codes.device)
+            if dtype not in _DTYPES:
+                raise ValueError("dtype must be float32 or bfloat16")
+            out = torch.empty(shape, dtype=dtype, device=codes.device)
+            k.ld_out, k.out_stride = n, m * n
         else:
-            _tensor("out", out, a.codes, _DTYPES, shape, contiguous=False)
-        k.a, k.b = _operand(a, False), _operand(b, group == "rows" and k.groups > 1)
-        k.out, k.out_dtype, k.ld_out = out.data_ptr(), _DTYPES[out.dtype], _rows("out", out)
-        if group == "depth":
-            k.out_stride = out.stride(0) if k.groups > 1 else k.m * k.ld_out
-        k.accumulate = 1 if accumulate else 0
-        L.check(L.muon_fp8_product(C.byref(k), _stream_ptr(a.codes)), "muon_fp8_product")
+            _tensor("out", out, codes, _DTYPES, shape, contiguous=False)
+            k.ld_out = _rows("out", out)
+            k.out_stride = out.stride(0) if group == "depth" and k.groups > 1 else m * k.ld_out
+        k.out, k.out_dtype, k.accumulate = out.data_ptr(), _DTYPES[out.dtype], 1 if accumulate else 0
+        L.check(L.muon_fp8_product(C.byref(k), _stream_ptr(codes)), "muon_fp8_product")
     return out
