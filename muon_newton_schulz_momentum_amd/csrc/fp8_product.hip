@@ -660,8 +660,8 @@ hipError_t product_as(ProductArgs a, hipStream_t s) {
     const double more = (double)std::min<int64_t>((std::min<int64_t>(rows, TILE) + 63) / 64 - 1, 3) / 3.0;
     const double step = sizeof(OUT) == 4 ? 1.0 + 1.2 * more : 0.66 + 0.39 * more;
     const double t_big = std::ceil((double)n_big / CUS) * (5.0 + kb * step);
-    const double t_few = n_few < 0 ? 1e30 : 5.0 + std::max(kb / WAVES * 2.5, (double)n_few * kb / 590.0);
-    const double t_thin = n_thin < 0 ? 1e30 : 4.0 + std::max(kb / WAVES * 1.6, (double)n_thin * kb / 1150.0);
+    const double t_few = n_few < 0 ? 1e30 : 5.0 + std::max(kb / WAVES * 2.5, (double)n_few * (kb + 2.0) / 590.0);
+    const double t_thin = n_thin < 0 ? 1e30 : 4.0 + std::max(kb / WAVES * 1.6, (double)n_thin * (kb + 1.5) / 1150.0);
     const int pick = t_big <= std::min(t_few, t_thin) ? 0 : t_few <= t_thin ? 1 : 2;
     const int64_t total = pick == 0 ? n_big : pick == 1 ? n_few : n_thin;
     const int64_t most = pick == 0 ? CUS : 2 * CUS;        // workgroups that run at once

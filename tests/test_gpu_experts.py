@@ -411,6 +411,8 @@ def _check_product(out, a, b, k, rows=slice(None), before=0.0):
 
 SIZES = [(1, 1, 1), (1, 128, 128), (16, 16, 256), (17, 100, 300), (128, 128, 128), (129, 255, 1000), (300, 513, 640),
          (5, 2000, 130), (257, 129, 2048)]
+# enough tiles for the 256 x 256 kernel; last tiles of 5, 100 and 190 rows, and more tiles than workgroups
+SIZES += [(2053, 1100, 640), (2148, 1280, 1), (2238, 1025, 129), (4500, 4300, 400)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
@@ -439,6 +441,10 @@ GROUPS = [
     ([2, 40, 17, 64, 33, 8, 100, 0], 256, 1000),
     ([0] * 600 + [7] + [0] * 300 + [20], 33, 130),
     ([600, 500], 257, 256),
+    # enough tiles for the 256 x 256 kernel: segments of every number of row blocks, some empty
+    ([(37 * i * i) % 290 if i % 7 else 0 for i in range(40)], 1000, 400),
+    ([300, 0, 513, 64, 65, 1000, 1, 129, 192, 193, 255, 256], 2100, 900),
+    ([20] * 150 + [0] * 50 + [21] * 100, 2060, 300),
 ]
 
 
@@ -463,7 +469,8 @@ def test_product_rows(sizes, n, k, fmt, dtype):
     assert torch.equal(again, out)
 
 
-@pytest.mark.parametrize("sizes,m,n", [([3], 20, 30), ([0, 128, 5, 0], 130, 128), ([300, 1, 256], 100, 515), ([0, 0], 8, 8)])
+@pytest.mark.parametrize("sizes,m,n", [([3], 20, 30), ([0, 128, 5, 0], 130, 128), ([300, 1, 256], 100, 515), ([0, 0], 8, 8),
+                                       ([600, 0, 1, 128, 300, 0], 700, 1100), ([130, 0, 0, 0, 20, 1, 513, 128, 0], 1030, 2060)])
 @pytest.mark.parametrize("fmt,dtype", [("e4m3", torch.float32), ("e5m2", torch.bfloat16)])
 def test_product_depth(sizes, m, n, fmt, dtype):
     ends = np.concatenate([[0], np.cumsum([-(-s // 128) * 128 for s in sizes])])
