@@ -252,9 +252,9 @@ __device__ __forceinline__ float token_sum(float v) {
     return v;
 }
 
-// Order-preserving bits of a float32 and back.
+// Order-preserving bits of a float32 and back; the zeros are equal (-0 + 0 is 0).
 __device__ __forceinline__ uint32_t ordered(float f) {
-    const uint32_t u = __float_as_uint(f);
+    const uint32_t u = __float_as_uint(f + 0.f);
     return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t u) {

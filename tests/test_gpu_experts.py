@@ -170,6 +170,19 @@ def test_route_low_scores_and_crowded_lanes():
             _check_route(y, experts, weights, orc.route(_np(y), 7, None if bias is None else _np(bias)), 7)
 
 
+@pytest.mark.parametrize("T", [5, 2050])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_zeros_of_both_signs_are_equal(T, dtype):
+    x = torch.zeros(T, 64, device="cuda")
+    x[:, 1::3] = -0.0
+    x[:, ::2] *= -1.0
+    x[:, 5] = -1.0
+    x = x.to(dtype)
+    for kw in (dict(score="softmax"), dict(score="sigmoid"), dict(score="sigmoid", groups=4, top_groups=2)):
+        experts, weights = X().route(x, 6, **kw)
+        _check_route(x, experts, weights, orc.route(_np(x), 6, **kw), 6)
+
+
 def test_route_bias_infinite_and_nan():
     x = torch.randn(9, 64, device="cuda", generator=_gen(4))
     bias = torch.zeros(64, device="cuda")
