@@ -417,7 +417,7 @@ MUON_API muon_status muon_step_noalloc(const muon_plan* plan, const muon_step_co
 #define MUON_SCORE_SIGMOID 1
 
 typedef struct muon_route_config {
-    int64_t tokens;      /* rows of logits                                                   */
+    int64_t tokens;      /* rows of logits, below 2^26                                       */
     int64_t ld;          /* row stride of logits in elements, >= n_experts                   */
     int32_t n_experts;   /* 1..MUON_MAX_EXPERTS                                              */
     int32_t top_k;       /* 1..min(n_experts, MUON_MAX_TOP_K)                                */
@@ -450,7 +450,8 @@ MUON_API muon_status muon_route(const muon_route_config* config, const void* log
  * (row stride ld_grad, logits' dtype) gets sum_j grad_weights[t][j] * d weights[t][j] / d x,
  * whole rows, zeros where nothing flows.  experts is muon_route's; entries outside
  * [0, n_experts) and entries whose logit is -inf or NaN pass nothing on, equal entries of a
- * row add up.  bias, n_groups and top_groups take no part.  Errors: as muon_route. */
+ * row add up.  bias, n_groups and top_groups take no part.  grad_logits may be logits, with
+ * the same ld.  Errors: as muon_route. */
 MUON_API muon_status muon_route_backward(const muon_route_config* config, const void* logits,
                                          const int32_t* experts, const float* grad_weights, void* grad_logits,
                                          int64_t ld_grad, void* stream);
@@ -494,7 +495,7 @@ typedef struct muon_fp8_quantize_config {
     int32_t format;           /* MUON_FP8_*                                                 */
     int32_t square;           /* 0: a scale per 128 values of a row; 1: per 128 x 128       */
     int32_t per;              /* with gather: choices per source row (top_k), >= 1          */
-    int64_t batch;
+    int64_t batch;            /* fewer than 2^24 tiles of 128 x 128 in all                  */
     int64_t rows, cols;       /* of each quantised matrix                                   */
     int64_t ld;               /* row stride of src in elements, >= cols                     */
     int64_t batch_stride;     /* between src's matrices, in elements                        */

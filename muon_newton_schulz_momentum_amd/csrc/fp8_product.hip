@@ -639,7 +639,7 @@ int64_t count_tiles(ProductArgs& a, int tile_rows, int tile_cols) {
     if (a.mode == MUON_PRODUCT_ROWS) rows = a.m / tile_rows + (a.m < a.groups ? a.m : (int64_t)a.groups);
     if (a.mode == MUON_PRODUCT_DEPTH) rows *= a.groups;
     const int64_t total = rows * a.tiles_n;
-    if (total >= (int64_t)1 << 31) return -1;
+    if (total >= ((int64_t)1 << 31) - 2 * CUS) return -1;   // a workgroup's step past its last tile stays an int
     a.tiles = (int32_t)total;
     return total;
 }

@@ -54,8 +54,11 @@ def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
     stream that the kernels run on."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
-    if stream is None and t.device.index == torch._C._cuda_getDevice():
-        return _AS_IT_IS
+    if stream is None:
+        if t.device.index == torch._C._cuda_getDevice():
+            return _AS_IT_IS
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, expected {t.device}")
     return _switched(t.device, stream)
 
 
@@ -119,7 +122,8 @@ def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = No
 def route_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weights: torch.Tensor, *,
                    score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The gradient of `route`'s weights with respect to the logits (in `out` if given), the choice held fixed."""
+    """The gradient of `route`'s weights with respect to the logits (in `out` if given, which may be `logits`), the
+    choice held fixed."""
     if experts.dim() != 2:
         raise ValueError("experts must be route's (tokens, top_k)")
     k = _route_config(logits, experts.shape[1], score, 1, 1, renormalize, scale)

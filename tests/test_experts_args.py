@@ -25,7 +25,7 @@ def _route(**kw):
     (dict(n_experts=0), L.MUON_ERR_SHAPE), (dict(n_experts=1025, ld=2000), L.MUON_ERR_SHAPE),
     (dict(top_k=0), L.MUON_ERR_SHAPE), (dict(top_k=9), L.MUON_ERR_SHAPE),
     (dict(n_experts=100, ld=100, top_k=65), L.MUON_ERR_SHAPE), (dict(tokens=-1), L.MUON_ERR_SHAPE),
-    (dict(tokens=1 << 31), L.MUON_ERR_SHAPE), (dict(tokens=1 << 30), L.MUON_ERR_SHAPE), (dict(ld=7), L.MUON_ERR_SHAPE),
+    (dict(tokens=1 << 31), L.MUON_ERR_SHAPE), (dict(tokens=1 << 26, top_k=1), L.MUON_ERR_SHAPE), (dict(tokens=1 << 30), L.MUON_ERR_SHAPE), (dict(ld=7), L.MUON_ERR_SHAPE),
     (dict(dtype=2), L.MUON_ERR_INVALID_ARG), (dict(score=2), L.MUON_ERR_INVALID_ARG),
     (dict(n_groups=3), L.MUON_ERR_INVALID_ARG), (dict(n_groups=0), L.MUON_ERR_INVALID_ARG),
     (dict(n_experts=130, ld=130, n_groups=65), L.MUON_ERR_INVALID_ARG),
@@ -129,6 +129,7 @@ def _quant(**kw):
     (dict(gather=W + 4, src_rows=4), L.MUON_ERR_ALIGNMENT), (dict(limit=W + 2), L.MUON_ERR_ALIGNMENT),
     (dict(codes=A + 1024), L.MUON_ERR_INVALID_ARG), (dict(codes_t=A - 256), L.MUON_ERR_INVALID_ARG),
     (dict(rows=(1 << 31) - 128, cols=(1 << 31) - 128, ld=(1 << 31) - 128), L.MUON_ERR_SHAPE),
+    (dict(batch=1 << 24, rows=1, cols=1, batch_stride=1), L.MUON_ERR_SHAPE),
 ])
 def test_quantize_refuses(kw, status):
     c = _quant(**kw)
@@ -176,6 +177,7 @@ def _product(mode=0, **kw):
     (1, dict(b__stride=200 * 256 - 16), L.MUON_ERR_SHAPE), (1, dict(b__stride_scales=200 * 4 - 4), L.MUON_ERR_SHAPE),
     (1, dict(b__stride=-16), L.MUON_ERR_SHAPE), (0, dict(out=A), L.MUON_ERR_INVALID_ARG),
     (1, dict(out=B + 2 * 200 * 256), L.MUON_ERR_INVALID_ARG),
+    (2, dict(groups=1024, m=1 << 17, n=1 << 20, ld_out=1 << 20, out_stride=1 << 37, offsets=W), L.MUON_ERR_SHAPE),
 ])
 def test_product_refuses(mode, kw, status):
     c = _product(mode, **kw)

@@ -222,6 +222,17 @@ def test_route_backward_repeated_and_foreign_experts():
             _check_backward(x, experts.cpu().numpy(), grad, X().route_backward(x, experts, grad, **bk), bk)
 
 
+@pytest.mark.parametrize("E,k", [(40, 4), (512, 7), (300, 20), (1024, 8)])
+@pytest.mark.parametrize("kw", [dict(score="softmax"), dict(score="softmax", renormalize=False), dict(score="sigmoid")])
+def test_route_backward_in_place(E, k, kw):
+    x = torch.randn(67, E, device="cuda", generator=_gen(11))
+    experts, _ = X().route(x, k, **kw)
+    grad = torch.randn(67, k, device="cuda", generator=_gen(12))
+    want = X().route_backward(x, experts, grad, **kw)
+    assert X().route_backward(x, experts, grad, out=x, **kw) is x
+    assert torch.equal(x, want)
+
+
 def test_route_gradient_is_the_difference_quotient():
     """d sum(w * grad) / dx by central differences of the kernel's own weights (float32: the quotient of
     weights rounded at 2^-24 over 2 * 2^-6 is off by k * 2^-24 * 2^5, the third derivative adds h^2)."""
@@ -394,6 +405,30 @@ def test_quantize_empty_rows():
     assert (none.codes.view(torch.uint8) == 0).all()
 
 
+def test_route_and_quantize_beyond_32_bits():
+    """Logits, sources and copies of more than 2^32 bytes: the last rows are those of a call on them alone."""
+    x = torch.empty(4_300_000, 512, dtype=torch.bfloat16, device="cuda").normal_(generator=_gen(1))
+    tail = x[-2051:]
+    for got, want in zip(X().route(x, 7, score="sigmoid"), X().route(tail, 7, score="sigmoid")):
+        assert torch.equal(got[-2051:], want)
+    experts, _ = X().route(tail, 7)
+    grad = torch.randn(len(x), 7, device="cuda", generator=_gen(2))
+    every = torch.zeros(len(x), 7, dtype=torch.int32, device="cuda")
+    every[-2051:] = experts
+    want = X().route_backward(tail, experts, grad[-2051:].clone())
+    assert torch.equal(X().route_backward(x, every, grad, out=x)[-2051:], want)
+    del every, grad
+    x.normal_(generator=_gen(3))
+    x = x.view(-1, 4096)                                     # 537500 rows, not a multiple of 128
+    cut = 537500 // 128 * 128
+    q, qt = X().quantize(x[:, :4090], transpose=True)
+    part, part_t = X().quantize(x[cut:, :4090], transpose=True)
+    assert torch.equal(q.codes[cut:].view(torch.uint8), part.codes.view(torch.uint8))
+    assert torch.equal(q.scales[cut:].view(torch.uint8), part.scales.view(torch.uint8))
+    assert torch.equal(qt.codes[:, cut:].view(torch.uint8), part_t.codes.view(torch.uint8))
+    assert torch.equal(qt.scales[:, cut // 128].view(torch.uint8), part_t.scales[:, 0].view(torch.uint8))
+
+
 # ---- products ---------------------------------------------------------------------------------
 
 def _random_fp8(rows, cols, fmt, square, seed, stack=None):
@@ -525,6 +560,96 @@ def test_product_offsets_are_clamped():
     vt = _np(t.dequantize())
     _check_product(out[0], vt[:, :128], vt[:, :128], 128)
     _check_product(out[1], vt[:, 128:], vt[:, 128:], 128)
+
+
+def test_product_large_with_bad_offsets_and_odd_rows():
+    """256 x 256 tiles: offsets outside the operand, rows of out that are not 16-byte aligned, sums onto out."""
+    m, n, k, E = 3001, 2045, 300, 4
+    a, b = _random_fp8(m, k, "e4m3", False, 5), _random_fp8(n, k, "e4m3", True, 6, stack=E)
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    offsets = torch.tensor([-7, 1000, 1000, 2500, 1 << 30], dtype=torch.int32, device="cuda")
+    ends = [0, 1000, 1000, 2500, m]
+    for accumulate in (False, True):
+        wide = torch.randn(m + 5, n + 2, device="cuda", generator=_gen(7))   # rows of 8188 bytes
+        before = wide.clone()
+        X().product(a, b, offsets=offsets, group="rows", out=wide[:m, :n], accumulate=accumulate)
+        for g in range(E):
+            s = slice(ends[g], ends[g + 1])
+            if s.stop > s.start:
+                _check_product(wide[s, :n], va[s], vb[g], k, before=_np(before[s, :n]) if accumulate else 0.0)
+        assert torch.equal(wide[m:], before[m:]) and torch.equal(wide[:, n:], before[:, n:])
+    half = torch.full((m, n + 1), 3.0, dtype=torch.bfloat16, device="cuda")
+    X().product(a, b, offsets=offsets, group="rows", out=half[:, :n])
+    for g in (0, 2, 3):
+        s = slice(ends[g], ends[g + 1])
+        _check_product(half[s, :n], va[s], vb[g], k)
+    assert (half[:, n] == 3.0).all()
+    # depth: bounds below, between blocks (rounded down) and behind the operand
+    xa, xb = (torch.randn(1024, c, device="cuda", generator=_gen(c)) for c in (1500, 2000))
+    ta, tb = X().quantize(xa, transpose=True)[1], X().quantize(xb, transpose=True)[1]
+    out = X().product(ta, tb, offsets=torch.tensor([-1, 300, 640, 640, 9999], dtype=torch.int32, device="cuda"),
+                      group="depth", dtype=torch.float32)
+    va, vb = _np(ta.dequantize()), _np(tb.dequantize())
+    for g, (lo, hi) in enumerate([(0, 256), (256, 640), (640, 640), (640, 1024)]):
+        _check_product(out[g], va[:, lo:hi], vb[:, lo:hi], hi - lo)
+
+
+def test_product_beyond_32_bits():
+    """Operands and results of more than 2^32 bytes: their last rows and groups."""
+    def random_fp8(rows, cols, stack=None):
+        q = X().Fp8.empty(rows, cols, stack=stack)
+        q.codes.view(torch.uint8).random_(0, 0x78, generator=_gen(rows))             # finite
+        q.scales.view(torch.uint8).random_(120, 130, generator=_gen(cols))
+        return q
+
+    def last(q, n):
+        return X().Fp8(q.codes[..., -n:, :], q.scales[..., -n:, :], q.cols, q.square)
+
+    a, b = random_fp8(1_100_000, 4096), random_fp8(2100, 4096)
+    out = X().product(a, b)                                   # 4.5 and 4.6 GB
+    _check_product(out[-300:], _np(last(a, 300).dequantize()), _np(b.dequantize()), 4096)
+    del out
+    b = random_fp8(2048, 4096, stack=520)                     # 4.4 GB
+    offsets = torch.arange(521, dtype=torch.int32, device="cuda") * 2
+    a = last(a, 1040)
+    one = X().Fp8(b.codes[519], b.scales[519], 4096, False)
+    _check_product(X().product(a, b, offsets=offsets, group="rows")[-2:], _np(last(a, 2).dequantize()),
+                   _np(one.dequantize()), 4096)
+    del b
+    a, b = random_fp8(4096, 8192), random_fp8(4300, 8192)
+    offsets = torch.arange(65, dtype=torch.int32, device="cuda") * 128
+    out = X().product(a, b, offsets=offsets, group="depth", dtype=torch.float32)     # 4.5 GB
+    _check_product(out[63][:, -300:], _np(a.dequantize())[:, -128:], _np(last(b, 300).dequantize())[:, -128:], 128)
+
+
+def test_product_large_captured_and_replayed():
+    """Rows-grouped and depth-grouped products in 256 x 256 tiles, their offsets changed between replays."""
+    E, n, k = 5, 1300, 512
+    a, b = _random_fp8(2560, k, "e4m3", False, 1), _random_fp8(n, k, "e4m3", True, 2, stack=E)
+    ta, tb = _random_fp8(1000, 2560, "e4m3", False, 3), _random_fp8(n, 2560, "e4m3", False, 4)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    y = torch.zeros(2560, n, dtype=torch.bfloat16, device="cuda")
+    dw = torch.zeros(E, 1000, n, device="cuda")
+
+    def run(y, dw):
+        X().product(a, b, offsets=offsets, group="rows", out=y)
+        X().product(ta, tb, offsets=offsets, group="depth", out=dw)
+
+    run(y, dw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(y, dw)
+    for bounds in ([0, 512, 512, 1024, 2432, 2560], [0, 0, 0, 0, 0, 128], [0, 128, 1280, 1408, 1536, 2304]):
+        offsets.copy_(torch.tensor(bounds, dtype=torch.int32))
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        y2, dw2 = torch.zeros_like(y), torch.zeros_like(dw)
+        run(y2, dw2)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(dw, dw2)
+        assert (y[bounds[-1]:] == 0).all()
 
 
 def test_product_no_depth():
@@ -711,6 +836,13 @@ def test_two_streams_at_once():
     for i in range(2):
         for (name, a), (_, b) in zip(_flat(got[i]), _flat(want[i])):
             assert torch.equal(a, b), name
+
+
+def test_stream_of_another_device_is_refused():
+    class Elsewhere:
+        device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="stream is on"):
+        X().route(torch.zeros(4, 8, device="cuda"), 2, stream=Elsewhere())
 
 
 def test_stream_argument():
