@@ -540,9 +540,14 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
     }
 }
 
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) { *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+// Stores that do not stay in the caches (65536 rows of 512 float32: 27 us against 33).
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(p));
+}
 __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+    const uint2 w = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+    __builtin_nontemporal_store(__builtin_bit_cast(uint64_t, w), reinterpret_cast<uint64_t*>(p));
 }
 
 __device__ __forceinline__ double token_sum16(double v) {
