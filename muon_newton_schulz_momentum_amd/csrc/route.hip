@@ -80,63 +80,75 @@ __device__ __forceinline__ void wave_best(double& key, int& idx) {
     for (int r = 0; r < 4; ++r) better(row_valued(k, r), (int)row_value((uint32_t)i, r));
 }
 
-// The two largest keys of a wave.
+// The two largest keys of 16 lanes, and of a wave.
+__device__ __forceinline__ void merge2(double& k1, double& k2, double o1, double o2) {
+    k2 = fmax(fmin(k1, o1), fmax(k2, o2));
+    k1 = fmax(k1, o1);
+}
+__device__ __forceinline__ void row_best2(double& k1, double& k2) {
+    merge2(k1, k2, dppd<XCHG_1>(k1), dppd<XCHG_1>(k2));
+    merge2(k1, k2, dppd<XCHG_2>(k1), dppd<XCHG_2>(k2));
+    merge2(k1, k2, dppd<XCHG_4>(k1), dppd<XCHG_4>(k2));
+    merge2(k1, k2, dppd<XCHG_8>(k1), dppd<XCHG_8>(k2));
+}
 __device__ __forceinline__ void wave_best2(double& k1, double& k2) {
-    auto merge = [&](double o1, double o2) {
-        k2 = fmax(fmin(k1, o1), fmax(k2, o2));
-        k1 = fmax(k1, o1);
-    };
-    merge(dppd<XCHG_1>(k1), dppd<XCHG_1>(k2));
-    merge(dppd<XCHG_2>(k1), dppd<XCHG_2>(k2));
-    merge(dppd<XCHG_4>(k1), dppd<XCHG_4>(k2));
-    merge(dppd<XCHG_8>(k1), dppd<XCHG_8>(k2));
+    row_best2(k1, k2);
     const double r1 = k1, r2 = k2;
     k1 = row_valued(r1, 0);
     k2 = row_valued(r2, 0);
 #pragma unroll
-    for (int r = 1; r < 4; ++r) merge(row_valued(r1, r), row_valued(r2, r));
+    for (int r = 1; r < 4; ++r) merge2(k1, k2, row_valued(r1, r), row_valued(r2, r));
+}
+// A group's worth by its two largest keys (-inf: none).
+__device__ __forceinline__ double worth_of(double k1, double k2) {
+    return k1 == -INFINITY ? -INFINITY : k1 + (k2 == -INFINITY ? 0.0 : k2);
 }
 
-// One token by one wave in float64: expert lane + 64 i in register i.
+// One token by one wave in float64, expert lane + 64 i in the lane's i-th place of x and key (LDS).  route_kernel comes
+// here for the odd token, with the code not in the instruction cache: so the loops with exponentials are not
+// unrolled (16 KiB of unrolled code for 512 experts took 13 us for one token).
 template <class T, int V>
-__device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t) {
+__device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, float* x, double* key) {
     const int lane = threadIdx.x & 63;
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-    float x[V];
+    const bool softmax = p.score == MUON_SCORE_SOFTMAX;
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane + 64 * i;
-        x[i] = e < p.n_experts ? clean_logit(load_logit(row + e)) : -INFINITY;
+        const float v = e < p.n_experts ? clean_logit(load_logit(row + e)) : -INFINITY;
+        x[e] = v;
+        top = fmaxf(top, v);
     }
-    double s[V], key[V];
-    if (p.score == MUON_SCORE_SOFTMAX) {
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < V; ++i) top = fmaxf(top, x[i]);
-        top = wave_max(top);
-        double z = 0.0;
-#pragma unroll
+    top = wave_max(top);
+    // the sigmoid, or the softmax before its division by z
+    auto raw = [&](float v) {
+        const double ex = exp(softmax ? (double)v - (double)top : -(double)v);
+        return softmax ? ex : 1.0 / (1.0 + ex);
+    };
+    const bool scored = p.bias || p.n_groups > 1;
+    double z = 1.0;
+    if (scored || (softmax && !p.renormalize)) {           // otherwise z cancels
+        z = 0.0;
+#pragma unroll 1
         for (int i = 0; i < V; ++i) {
-            s[i] = x[i] > -INFINITY ? exp((double)x[i] - (double)top) : 0.0;
-            z += s[i];
+            const float v = x[lane + 64 * i];
+            const double s = v > -INFINITY ? raw(v) : 0.0;
+            key[lane + 64 * i] = s;
+            z += s;
         }
-        z = dev::wave_sum(z);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = z > 0.0 ? s[i] / z : 0.0;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = x[i] > -INFINITY ? sigmoid64((double)x[i]) : 0.0;
+        z = softmax ? dev::wave_sum(z) : 1.0;
     }
     // keys; -inf marks an expert that is out (a NaN key puts it out too)
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < V; ++i) {
         const int e = lane + 64 * i;
-        double k = (double)x[i];
-        if ((p.bias || p.n_groups > 1) && x[i] > -INFINITY) {
-            k = s[i] + (p.bias ? (double)p.bias[e] : 0.0);
+        double k = (double)x[e];
+        if (scored && x[e] > -INFINITY) {
+            k = key[e] / z + (p.bias ? (double)p.bias[e] : 0.0);
             if (!(k > -INFINITY)) k = -INFINITY;
         }
-        key[i] = k;
+        key[e] = k;
     }
     if (p.n_groups > 1) {
         // each group's two largest keys, then the groups by rank: a group stays when fewer than
@@ -145,15 +157,14 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t) {
         double worth = -INFINITY;                          // lane g: group g's
         for (int g = 0; g < p.n_groups; ++g) {
             double k1 = -INFINITY, k2 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
+            for (int i = g * per / 64; i <= ((g + 1) * per - 1) / 64; ++i) {
                 const int e = lane + 64 * i;
-                const double k = e >= g * per && e < (g + 1) * per ? key[i] : -INFINITY;
+                const double k = e >= g * per && e < (g + 1) * per ? key[e] : -INFINITY;
                 if (k > k1) { k2 = k1; k1 = k; }
                 else if (k > k2) k2 = k;
             }
             wave_best2(k1, k2);
-            if (lane == g) worth = k1 == -INFINITY ? -INFINITY : k1 + (k2 == -INFINITY ? 0.0 : k2);
+            if (lane == g) worth = worth_of(k1, k2);
         }
         int before = 0;
         for (int g = 0; g < p.n_groups; ++g) {
@@ -161,30 +172,30 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t) {
             if (w > worth || (w == worth && g < lane)) ++before;
         }
         const uint64_t kept = __ballot(lane < p.n_groups && before < p.top_groups);
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < V; ++i) {
             const int e = lane + 64 * i;
-            if (e < p.n_experts && !((kept >> (e / per)) & 1)) key[i] = -INFINITY;
-            else if (!p.bias) key[i] = (double)x[i];
+            if (e < p.n_experts && !((kept >> (e / per)) & 1)) key[e] = -INFINITY;
+            else if (!p.bias) key[e] = (double)x[e];
         }
     }
     int my_expert = -1;
-    double my_score = 0.0;
     for (int j = 0; j < p.top_k; ++j) {
         double best = -INFINITY;
         int at = 1 << 20;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (key[i] > best) { best = key[i]; at = lane + 64 * i; }
+        for (int i = 0; i < V; ++i) {
+            const double k = key[lane + 64 * i];
+            if (k > best) { best = k; at = lane + 64 * i; }
+        }
         wave_best(best, at);
         if (best == -INFINITY) break;
-        double sc = 0.0;
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (at == lane + 64 * i) { sc = s[i]; key[i] = -INFINITY; }
-        sc = __shfl(sc, at & 63, 64);
-        if (lane == j) { my_expert = at; my_score = sc; }
+        if ((at & 63) == lane) key[at] = -INFINITY;
+        if (lane == j) my_expert = at;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // other lanes' places of x
+    __builtin_amdgcn_wave_barrier();
+    const double my_score = my_expert >= 0 ? raw(x[my_expert]) / z : 0.0;
     double w = my_score;
     if (p.renormalize) {
         const double total = dev::wave_sum(my_score);
@@ -194,12 +205,17 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t) {
         p.experts[t * p.top_k + lane] = my_expert;
         p.weights[t * p.top_k + lane] = (float)(w * (double)p.scale);
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the next token's come after
+    __builtin_amdgcn_wave_barrier();
 }
 
 template <class T, int V>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_exact_kernel(RouteArgs p) {
-    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6);
-    if (t < p.tokens) route_exact<T, V>(p, t);
+    __shared__ double key[ROUTE_WAVES][64 * V];
+    __shared__ float x[ROUTE_WAVES][64 * V];
+    const int wave = threadIdx.x >> 6;
+    const int64_t t = (int64_t)blockIdx.x * ROUTE_WAVES + wave;
+    if (t < p.tokens) route_exact<T, V>(p, t, x[wave], key[wave]);
 }
 
 // ---- 16 or 64 lanes a token -----------------------------------------------------------------
@@ -207,11 +223,10 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_exact_kernel(RouteArgs
 // Lane l of LT takes experts 4 LT c + 4 l + v (c < C, v < 4).  Scores and keys are float32, as ordered integers
 // whose last 6 bits give way to the expert's place in its lane.  Each lane sorts out its 4 largest (a maximum
 // and three medians per value; again when they are used up), and top_k + 1 rounds take the largest of all lanes.
-// What float32 cannot decide is found by looking at what was taken: two neighbours nearer than the keys' error,
-// or two lanes at once.  Neighbours (with a bias, in one token of forty at 512 experts) are settled by
-// taking on to 16 experts and ranking those by their float64 keys, unless those need the whole row (softmax plus
-// bias); whatever else is left is done again by the whole wave in float64.  So the choice is always the
-// float64 one.
+// What float32 cannot decide is found by looking at what was taken: two neighbours nearer than the keys' error.
+// They (with a bias, in one token of forty at 512 experts) are settled by
+// taking on to 16 experts and ranking those by their float64 keys, and two groups at the border by their float64 sums;
+// whatever is left is done again by the whole wave in float64.  So the choice is always the float64 one.
 constexpr int FAST_MAX_K = 15;
 constexpr int64_t WIDE_MAX_TOKENS = 2048;
 
@@ -290,6 +305,9 @@ template <class T, int LT, int C, bool GROUPS>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, int vec) {
     constexpr int PT = 64 / LT;                            // tokens a wave
     static_assert(!GROUPS || LT == 16, "groups lie in 16 lanes");
+    constexpr int V = LT * C / 16;
+    __shared__ double exact_key[ROUTE_WAVES][64 * V];
+    __shared__ float exact_x[ROUTE_WAVES][64 * V];
     const int lane = threadIdx.x & 63, l = lane & (LT - 1);
     const int64_t t0 = ((int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6)) * PT;
     if (t0 >= p.tokens) return;
@@ -363,7 +381,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
             float a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const float k = x[c][v] > -INFINITY ? key[c][v] : -INFINITY;
+                const float k = x[c][v] > -INFINITY && key[c][v] > -INFINITY ? key[c][v] : -INFINITY;   // NaN: out
                 a2 = fmaxf(fminf(a1, k), a2);
                 a1 = fmaxf(a1, k);
             }
@@ -390,24 +408,61 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
             for (int i = 0; i < 4; ++i)
                 if (l + 16 * i == g) best[i] = w;
         }
-        // the largest top_groups of them, and one more to see how near it comes
-        float border = INFINITY;
-        for (int r = 0; r <= p.top_groups && r < p.n_groups; ++r) {
+        // the largest top_groups of them; how near the next one comes, and those on either side of the two
+        float prev = INFINITY;
+        bool near_in = false, near = false, near_out = false;
+        int last_in = 0, first_out = 0;
+        for (int r = 0; r < min(p.top_groups + 2, p.n_groups); ++r) {
             const float w = token_maxf<LT>(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])));
-            if (r == p.top_groups && w > -INFINITY) again |= !(border - w > 0x1p-19f * fmaxf(1.f, fabsf(border)));
-            border = w;
-            if (r == p.top_groups) break;
-            // which group it is (of two with the same sum either: that token is done again)
+            const bool here = r > 0 && w > -INFINITY && !(prev - w > 0x1p-19f * fmaxf(1.f, fabsf(prev)));
+            if (r == p.top_groups - 1) near_in = here;
+            if (r == p.top_groups) near = here;
+            if (r == p.top_groups + 1) {
+                near_out = here;
+                break;
+            }
+            prev = w;
+            // which group it is; of equal sums the lowest
             uint32_t at = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (best[i] == w && l + 16 * i < p.n_groups && !((kept >> (l + 16 * i)) & 1)) at = max(at, (uint32_t)(64 - (l + 16 * i)));
             at = token_max<LT>(at);
             const int g = 64 - (int)at;
-            if (at != 0) kept |= 1ull << g;
+            if (r < p.top_groups) {
+                if (at != 0) kept |= 1ull << g;
+                last_in = g;
+            } else {
+                first_out = g;
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (l + 16 * i == g) best[i] = -INFINITY;
+        }
+        if (__ballot(near)) {
+            // those two groups alone in float64, unless their scores need the whole row's sum
+            again |= near && (near_in || near_out || (softmax && p.bias));
+            double worth[2];
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side) {
+                double k1 = -INFINITY, k2 = -INFINITY;
+                const int g0 = (side == 0 ? last_in : first_out) * per;
+#pragma unroll 1
+                for (int e0 = 4 * l; e0 < per; e0 += 64)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        if (!near) continue;
+                        const float xv = clean_logit(load_logit(row + g0 + e0 + v));
+                        const double ex = exp(softmax ? (double)xv - (double)top : -(double)xv);
+                        double k = (softmax ? ex : 1.0 / (1.0 + ex)) + (p.bias ? (double)p.bias[g0 + e0 + v] : 0.0);
+                        if (!(xv > -INFINITY && k > -INFINITY)) k = -INFINITY;
+                        merge2(k1, k2, k, -INFINITY);
+                    }
+                row_best2(k1, k2);
+                worth[side] = worth_of(k1, k2);
+            }
+            if (near && (worth[1] > worth[0] || (worth[1] == worth[0] && first_out < last_in)))
+                kept ^= 1ull << last_in | 1ull << first_out;
         }
     }
     // Each lane's 4 largest keys, ordered, the place in the lane in the last 6 bits (larger: lower expert).  bfloat16
@@ -448,20 +503,19 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
         if (me) { k0 = a0; k1 = a1; k2 = a2; k3 = a3; had = 0; }
     };
     sort_out(0xffffffffu, true);
-    int taken = 0, mine = -1;                              // keys this lane gave; lane j: the j-th expert taken
+    int mine = -1;                                         // lane j: the j-th expert taken
     auto take = [&](uint32_t w, int j) {
-        const bool won = w != 0 && k0 == w;
-        // the winner's expert to every lane of the token
+        // the winner's expert to every lane of the token; the lowest of equal bits
         const int place = 63 - (int)(w & 63u);
         const int here = whole ? 1023 - (int)(w & 1023u) : 4 * LT * (place >> 2) + 4 * l + (place & 3);
-        const int e = (int)token_max<LT>(won ? (uint32_t)here + 1u : 0u) - 1;
-        if (l == j) mine = e;
+        const int e = 1024 - (int)token_max<LT>(w != 0 && k0 == w ? (uint32_t)(1024 - here) : 0u);
+        const bool won = w != 0 && k0 == w && here == e;
+        if (l == j && w != 0) mine = e;
         if (won) {
             k0 = k1;
             k1 = k2;
             k2 = k3;
             k3 = 0;
-            ++taken;
             ++had;
         }
         if (__ballot(had == 4)) sort_out(w, had == 4);
@@ -478,12 +532,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
         w = token_max<LT>(k0);
         if (w != 0) close |= !tell(before, w);
     }
-    // two lanes with the same bits leave together
-    again |= token_sum<LT>((float)taken) != token_sum<LT>(mine >= 0 ? 1.f : 0.f);
 
     int slot = l;                                          // where this lane's expert goes
-    const bool local = !(p.bias && softmax);               // a key is that of its logit alone
-    if (local && __ballot(close && !again)) {
+    if (__ballot(close && !again)) {
         // The keys of the 16 first, one a lane, ranked in float64.  Whoever was not taken is below the 16th; so the
         // ranking holds if the 16th is apart from the last chosen.
         const uint32_t last = before;
@@ -492,27 +543,38 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
             before = w;
             w = token_max<LT>(k0);
         }
-        const bool two = token_sum<LT>((float)taken) != token_sum<LT>(mine >= 0 ? 1.f : 0.f);
-        if (close) again |= two || (before != 0 && !tell(last, before));
-        double k64 = -INFINITY;
+        if (close) again |= before != 0 && !tell(last, before);
+        double k64 = -INFINITY, s64 = 0.0;
         if (mine >= 0) {
-            k64 = (double)clean_logit(load_logit(row + mine));
-            if (p.bias) k64 = sigmoid64(k64) + (double)p.bias[mine];
+            const float xj = clean_logit(load_logit(row + mine));
+            k64 = (double)xj;
+            if (p.bias) {
+                const double ex = exp(softmax ? (double)xj - (double)top : -(double)xj);
+                s64 = softmax ? ex / (double)z : 1.0 / (1.0 + ex);
+                k64 = s64 + (double)p.bias[mine];
+            }
         }
+        // The softmax's sum is float32's, off by less than 2^-18 of itself: which moves the difference of two keys
+        // by no more than that part of the difference of their scores.
+        const bool rough = p.bias && softmax;
         int rank = 0;
+        bool open = false;
         for (int j = 0; j < 16; ++j) {
             const double other = __shfl(k64, (lane & ~(LT - 1)) + j, 64);
             const int e = __shfl(mine, (lane & ~(LT - 1)) + j, 64);
             if (other > k64 || (other == k64 && e >= 0 && e < mine)) ++rank;
+            if (rough) {
+                const double d = fabs(__shfl(s64, (lane & ~(LT - 1)) + j, 64) - s64);
+                open |= mine >= 0 && e >= 0 && d > 0.0 && !(fabs(other - k64) > 0x1p-18 * d);
+            }
         }
         if (close) {
+            if (rough) again |= token_max<LT>(open ? 1u : 0u) != 0;
             slot = mine >= 0 ? rank : l;
             if (slot >= p.top_k) mine = -1;
         } else if (l >= p.top_k) {
             mine = -1;
         }
-    } else if (close) {
-        again = true;
     }
 
     float s = 0.f;
@@ -536,7 +598,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
     while (left) {
         const int g = __builtin_ctzll(left);
         left &= left - 1;
-        route_exact<T, LT * C / 16>(p, t0 + g / LT);
+        route_exact<T, V>(p, t0 + g / LT, exact_x[threadIdx.x >> 6], exact_key[threadIdx.x >> 6]);
     }
 }
 

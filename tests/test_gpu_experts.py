@@ -183,6 +183,54 @@ def test_route_zeros_of_both_signs_are_equal(T, dtype):
         _check_route(x, experts, weights, orc.route(_np(x), 6, **kw), 6)
 
 
+@pytest.mark.parametrize("T", [300, 2100])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_near_ties_with_bias(T, score):
+    """Keys that agree to 1e-7 and to 1e-5 in some of the chosen: float64 decides, for 16 experts or for the row."""
+    E, k = 512, 7
+    base = torch.randn(1, E, device="cuda", generator=_gen(21))
+    x = base + 1e-6 * torch.randn(T, E, device="cuda", generator=_gen(22))
+    s = torch.from_numpy(orc.scores(_np(base), score)[0][0]).cuda()
+    for near, spread in ((10, 1e-7), (10, 1e-5), (10, 0.0), (500, 1e-7)):
+        bias = torch.randn(E, device="cuda", generator=_gen(23)).double().abs() * -0.1
+        at = torch.randperm(E, device="cuda", generator=_gen(24))[:near]
+        bias[at] = 0.5 + spread * torch.randn(near, device="cuda", generator=_gen(25)).double()
+        bias = (bias - s).float()
+        experts, weights = X().route(x, k, bias=bias, score=score)
+        _check_route(x, experts, weights, orc.route(_np(x), k, _np(bias), score=score), k)
+
+
+@pytest.mark.parametrize("E,groups,top", [(512, 8, 4), (256, 16, 3), (512, 16, 15), (512, 4, 1), (512, 2, 1), (128, 4, 4)])
+@pytest.mark.parametrize("score,biased", [("sigmoid", False), ("softmax", False), ("sigmoid", True), ("softmax", True)])
+def test_route_groups_at_the_border(E, groups, top, score, biased):
+    """Group sums that are equal (coarse logits) or agree to 1e-7 (two groups alike but for their noise)."""
+    T, k, per = 2100, 5, E // groups
+    coarse = ((torch.randn(T, E, device="cuda", generator=_gen(31)) * 4).round() / 4).bfloat16()
+    alike = torch.randn(T, per, device="cuda", generator=_gen(32)).repeat(1, groups)
+    alike = alike + 1e-6 * torch.randn(T, E, device="cuda", generator=_gen(33))
+    alike[:, per:2 * per] += 1.0
+    if groups > 3:
+        alike[:, 3 * per:] -= 1.0
+    bias = None
+    if biased:
+        bias = (torch.randn(per, device="cuda", generator=_gen(34)) * 0.1).repeat(groups)
+    for x in (coarse, alike):
+        kw = dict(score=score, groups=groups, top_groups=top)
+        experts, weights = X().route(x, k, bias=bias, **kw)
+        _check_route(x, experts, weights, orc.route(_np(x), k, None if bias is None else _np(bias), **kw), k)
+
+
+def test_route_nan_bias_counts_in_no_group():
+    x = torch.randn(2100, 128, device="cuda", generator=_gen(41))
+    bias = torch.zeros(128, device="cuda")
+    bias[40::3] = float("nan")
+    bias[20:32] = -float("inf")
+    for groups in (8, 4, 2):
+        kw = dict(groups=groups, top_groups=1, score="sigmoid")
+        experts, weights = X().route(x, 4, bias=bias, **kw)
+        _check_route(x, experts, weights, orc.route(_np(x), 4, _np(bias), **kw), 4)
+
+
 def test_route_bias_infinite_and_nan():
     x = torch.randn(9, 64, device="cuda", generator=_gen(4))
     bias = torch.zeros(64, device="cuda")
