@@ -228,7 +228,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_exact_kernel(RouteArgs
 // taking on to 16 experts and ranking those by their float64 keys, and two groups at the border by their float64 sums;
 // whatever is left is done again by the whole wave in float64.  So the choice is always the float64 one.
 constexpr int FAST_MAX_K = 15;
-constexpr int64_t WIDE_MAX_TOKENS = 2048;
+constexpr int64_t WIDE_MAX_TOKENS = 4096;
 
 // Over the LT lanes of a token, to all of them.
 template <int LT>
@@ -993,12 +993,13 @@ __global__ __launch_bounds__(GROUP_THREADS) void balance_kernel(const float* bia
     out[e] = d > 0 ? bias[e] + rate : d < 0 ? bias[e] - rate : bias[e];
 }
 
-// Variants, by what the sizes allow and what they measured (7 of 512 experts):
-//   * 16 lanes a token from 2048 tokens on (65536 tokens, softmax: 37 us, a wave a token in float64: 200 us), and for
-//     groups of 16, 32 or multiples of 64, which lie in a row of lanes;
-//   * 64 lanes below (16 tokens: 5.6 us against 8.4), where a wave's own time counts, and above 512 experts, whose
-//     values 16 lanes cannot hold;
-//   * the float64 wave for what neither covers: more than 15 choices, other groups.
+// Variants, by what the sizes allow and what they measured (of 512 experts, times of whole calls back to back, which
+// take 9.5 us at least):
+//   * 16 lanes a token from 4096 tokens on (65536 tokens, 7 by softmax: 38 us, by sigmoid and bias 64; 64 lanes: 57 and
+//     78), and for groups of 16, 32 or multiples of 64, which lie in a row of lanes;
+//   * 64 lanes below (2048 tokens by sigmoid and bias: 11.1 us against 14.2), where a wave's own time counts, and above
+//     512 experts, whose values 16 lanes cannot hold;
+//   * the float64 wave for what neither covers: more than 15 choices, other groups (65536 tokens, 20 choices: 284 us).
 template <class T>
 hipError_t route_by_width(const RouteArgs& a, hipStream_t s) {
     const int per = a.n_experts / a.n_groups;
