@@ -670,6 +670,21 @@ def test_product_beyond_32_bits():
     _check_product(out[63][:, -300:], _np(a.dequantize())[:, -128:], _np(last(b, 300).dequantize())[:, -128:], 128)
 
 
+@pytest.mark.parametrize("m,n,groups,dtype", [(1100, 3400, 9, torch.float32), (2048, 2048, 20, torch.bfloat16), (2000, 2050, 300, torch.bfloat16)])
+def test_product_depth_groups_of_many_tiles(m, n, groups, dtype):
+    """Groups whose tiles are dealt to all XCDs, deepest first (or, from 257 groups on, as they come)."""
+    blocks = [(5 * g * g + 3 * g) % 4 for g in range(groups)]
+    ends = np.concatenate([[0], np.cumsum(blocks)]) * 128
+    a, b = _random_fp8(m, int(ends[-1]), "e4m3", False, m), _random_fp8(n, int(ends[-1]), "e4m3", False, n)
+    out = torch.full((groups, m, n), float("nan"), dtype=dtype, device="cuda")
+    X().product(a, b, offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"), group="depth", out=out)
+    assert not torch.isnan(out).any()
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    for g in range(groups) if groups < 10 else (0, 1, 2, groups // 2, groups - 2, groups - 1):
+        s = slice(ends[g], ends[g + 1])
+        _check_product(out[g], va[:, s], vb[:, s], ends[g + 1] - ends[g])
+
+
 def test_product_large_captured_and_replayed():
     """Rows-grouped and depth-grouped products in 256 x 256 tiles, their offsets changed between replays."""
     E, n, k = 5, 1300, 512
