@@ -252,6 +252,10 @@ using ic = std::integral_constant<int, N>;
 // A step has two sub-steps of 64 values.  Its one barrier comes in the middle of the second, whose fragments are then in
 // registers: past it the next stage is complete and this one may be overwritten.  The matrix instructions
 // before it cover the fragment reads that it waits for, those behind it the next stage's first reads.
+//
+// 16381 x 5632 x 2048 in bfloat16: 170 us, 2.2 PFLOP/s; 8192 x 8192 x 8320: 2.5.  57344 rows of 128 experts, 1024 x 4096:
+// 278 us.  Weight gradients of 64 experts, 1024 x 4096 in float32 over 28672 rows: 399 us, about 140 of products and
+// 200 of stores (1.07 GB), one after the other: a wave's loads and stores retire in order.
 template <int AFMT, class OUT>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_kernel(ProductArgs p) {
     constexpr bool PRECISE = sizeof(OUT) == 4;
@@ -551,7 +555,8 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // Where 256 x 256 tiles would leave most of the chip idle.  Each of 8 waves takes every eighth block of k of a tile of
 // 32 rows of a by 16 NB rows of b, its fragments (v_mfma_scale_f32_16x16x128_f8f6f4: a block at once) straight from
 // memory into registers, AHEAD blocks at a time, so that a tile's loads are under way together; the waves' sums are
-// added up through LDS in the order of the waves.
+// added up through LDS in the order of the waves.  Bound by the loads' latency, then by L2 (16 rows by 4096 x 4096: 6 us
+// of kernel; 256 rows: 30 us).
 constexpr int FEW_ROWS = 32;
 
 template <int AFMT, class OUT, int NB, int AHEAD>
