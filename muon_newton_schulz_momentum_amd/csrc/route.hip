@@ -365,9 +365,18 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
     }
     if (p.bias) {
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c) {
+            float b[4] = {0.f, 0.f, 0.f, 0.f};
+            if (p.n_experts % 4 == 0) {
+                if (expert(c, 0) < p.n_experts) load4(p.bias + expert(c, 0), b);
+            } else {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) key[c][v] += expert(c, v) < p.n_experts ? p.bias[expert(c, v)] : 0.f;
+                for (int v = 0; v < 4; ++v)
+                    if (expert(c, v) < p.n_experts) b[v] = p.bias[expert(c, v)];
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) key[c][v] += b[v];
+        }
     }
     bool again = false;                                    // for the whole wave in float64
     uint64_t kept = ~0ull;                                 // groups that stay
@@ -398,17 +407,16 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, in
             score[c] = m1 == -INFINITY ? -INFINITY : m1 + (m2 == -INFINITY ? 0.f : m2);
         }
         kept = 0;
-        for (int g = 0; g < p.n_groups; ++g) {
-            // group g's sum, from the lane and row that hold it
-            const int first = g * per, c0 = (first + per - 1) / 64, src = (first % 64) / 4;
-            float w = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (c == c0) w = score[c];
-            w = __shfl(w, (lane & 48) + src, 64);
+        for (int i = 0; i < 4; ++i) {
+            if (16 * i >= p.n_groups) break;
+            // group l + 16 i's sum, from the lane and row that hold it
+            const int g = l + 16 * i, first = g * per, c0 = (first + per - 1) / 64, src = (first % 64) / 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (l + 16 * i == g) best[i] = w;
+            for (int c = 0; c < C; ++c) {
+                const float w = __shfl(score[c], (lane & 48) + src, 64);
+                if (g < p.n_groups && c == c0) best[i] = w;
+            }
         }
         // the largest top_groups of them; how near the next one comes, and those on either side of the two
         float prev = INFINITY;
@@ -809,7 +817,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
 // a run of those, so that positions follow from counts: choices of an expert in earlier
 // runs, then in the earlier waves of this one, then in the earlier lanes of the wave, found
 // by matching the bits of the expert across the wave with ballots.  458759 choices of 512 experts: counts 3.2 us, prefix
-// 5.6, placement 11.3 (4-byte stores to all segments; the bytes alone would take 1.2); 112 in one workgroup: 3.8 us.
+// 4.6, placement 10.4 (4-byte stores to all segments; the bytes alone would take 1.2); 112 in one workgroup: 3.8 us.
 
 constexpr int GROUP_WAVES = 16;
 constexpr int GROUP_THREADS = 64 * GROUP_WAVES;
@@ -854,46 +862,56 @@ __device__ __forceinline__ int block_prefix(int v, int* wave_tot, int& total) {
     return before + inc - v;
 }
 
-// Places the choices [lo, hi): cursor[w][e] is where wave w's first choice of expert e goes.
-__device__ __forceinline__ void place(const GroupRowsArgs& p, int64_t lo, int64_t hi, int64_t per_wave, int* cursor) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t w0 = lo + wave * per_wave, w1 = min(hi, w0 + per_wave);
-    int* mine = cursor + wave * p.n_experts;
-    for (int64_t i0 = w0; i0 < w1; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const int e = load_choice(p, i, w1);
-        const uint64_t same = match_lanes(e);
-        int at = -1;
-        if (e >= 0) at = mine[e] + __popcll(same & ((1ull << lane) - 1));
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the reads come before the write
-        __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && (same >> lane) == 1) mine[e] = at + 1;   // the last lane of the expert
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        if (i < w1) p.position[i] = at;
-        if (e >= 0) p.rows[at] = (int32_t)i;
+// A workgroup's choices from lo on: wave w has 64 per consecutive ones (per <= PER), lane l every 64th of them.
+template <int PER>
+struct Run {
+    int64_t first;             // the lane's first choice
+    int per;
+    int e[PER];                // experts, -1 for none
+    __device__ __forceinline__ Run(const GroupRowsArgs& p, int64_t lo, int per_) : per(per_) {
+        first = lo + (int64_t)(threadIdx.x >> 6) * 64 * per + (threadIdx.x & 63);
+#pragma unroll
+        for (int k = 0; k < PER; ++k) e[k] = load_choice(p, first + 64 * k, k < per ? p.n : 0);
     }
-}
-
-// hist[w][e]: choices of expert e in wave w's run of [lo, hi).
-__device__ __forceinline__ void count(const GroupRowsArgs& p, int64_t lo, int64_t hi, int64_t per_wave, int* hist) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = threadIdx.x; i < GROUP_WAVES * p.n_experts; i += GROUP_THREADS) hist[i] = 0;
-    __syncthreads();
-    const int64_t w0 = lo + wave * per_wave, w1 = min(hi, w0 + per_wave);
-    for (int64_t i = w0 + lane; i < w1; i += 64) {
-        const int e = load_choice(p, i, w1);
-        if (e >= 0) atomicAdd(&hist[wave * p.n_experts + e], 1);   // a count: the order does not matter
+    // hist[w][e]: choices of expert e in wave w's run.
+    __device__ __forceinline__ void count(int n_experts, int* hist) const {
+        for (int i = threadIdx.x; i < GROUP_WAVES * n_experts; i += GROUP_THREADS) hist[i] = 0;
+        __syncthreads();
+        int* mine = hist + (threadIdx.x >> 6) * n_experts;
+#pragma unroll
+        for (int k = 0; k < PER; ++k)
+            if (e[k] >= 0) atomicAdd(&mine[e[k]], 1);      // a count: the order does not matter
+        __syncthreads();
     }
-    __syncthreads();
-}
+    // cursor[w][e] is where wave w's first choice of expert e goes.
+    __device__ __forceinline__ void place(const GroupRowsArgs& p, int* cursor) const {
+        const int lane = threadIdx.x & 63;
+        int* mine = cursor + (threadIdx.x >> 6) * p.n_experts;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int64_t i = first + 64 * k;
+            if (k >= per || i - lane >= p.n) break;
+            const uint64_t same = match_lanes(e[k]);
+            int at = -1;
+            if (e[k] >= 0) at = mine[e[k]] + __popcll(same & ((1ull << lane) - 1));
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the reads come before the write
+            __builtin_amdgcn_wave_barrier();
+            if (e[k] >= 0 && (same >> lane) == 1) mine[e[k]] = at + 1;   // the last lane of the expert
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            if (i < p.n) p.position[i] = at;
+            if (e[k] >= 0) p.rows[at] = (int32_t)i;
+        }
+    }
+};
+constexpr int SINGLE_PER = GROUP_SINGLE_MAX / GROUP_THREADS, CHUNK_PER = GROUP_CHUNK / GROUP_THREADS;
 
 // All of a small call in one workgroup.
 __global__ __launch_bounds__(GROUP_THREADS) void group_single_kernel(GroupRowsArgs p) {
     extern __shared__ int lds[];
     __shared__ int wave_tot[GROUP_WAVES];
-    const int64_t per_wave = ((p.n + GROUP_WAVES - 1) / GROUP_WAVES + 63) / 64 * 64;
-    count(p, 0, p.n, per_wave, lds);
+    const Run<SINGLE_PER> run(p, 0, (int)((p.n + GROUP_THREADS - 1) / GROUP_THREADS));
+    run.count(p.n_experts, lds);
     const int e = threadIdx.x;
     int c = 0;
     if (e < p.n_experts)
@@ -915,13 +933,13 @@ __global__ __launch_bounds__(GROUP_THREADS) void group_single_kernel(GroupRowsAr
     if (threadIdx.x == 0) p.offsets[p.n_experts] = total;
     for (int64_t r = total + threadIdx.x; r < p.capacity; r += GROUP_THREADS) p.rows[r] = -1;
     __syncthreads();
-    place(p, 0, p.n, per_wave, lds);
+    run.place(p, lds);
 }
 
 __global__ __launch_bounds__(GROUP_THREADS) void group_count_kernel(GroupRowsArgs p) {
     extern __shared__ int lds[];
-    const int64_t lo = blockIdx.x * GROUP_CHUNK, hi = min(p.n, lo + GROUP_CHUNK);
-    count(p, lo, hi, GROUP_CHUNK / GROUP_WAVES, lds);
+    const Run<CHUNK_PER> run(p, blockIdx.x * (int64_t)GROUP_CHUNK, CHUNK_PER);
+    run.count(p.n_experts, lds);
     for (int e = threadIdx.x; e < p.n_experts; e += GROUP_THREADS) {
         int c = 0;
         for (int w = 0; w < GROUP_WAVES; ++w) c += lds[w * p.n_experts + e];
@@ -930,22 +948,31 @@ __global__ __launch_bounds__(GROUP_THREADS) void group_count_kernel(GroupRowsArg
 }
 
 // partial[chunk][e] becomes the number of the expert's choices in earlier chunks, and counts[e] all of them: a wave
-// for each expert, a lane for each of 64 chunks at a time.
+// for each expert, a lane for each of 64 chunks at a time, the loads of 256 chunks together.
+constexpr int PREFIX_AHEAD = 4;
 __global__ __launch_bounds__(256) void group_prefix_kernel(GroupRowsArgs p) {
     const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
     if (e >= p.n_experts) return;
     int before = 0;
-    for (int64_t b0 = 0; b0 < p.chunks; b0 += 64) {
-        const int64_t b = b0 + lane;
-        const int h = b < p.chunks ? p.partial[b * p.n_experts + e] : 0;
-        int inc = h;
+    for (int64_t b0 = 0; b0 < p.chunks; b0 += 64 * PREFIX_AHEAD) {
+        int h[PREFIX_AHEAD];
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int o = __shfl_up(inc, off, 64);
-            if (lane >= off) inc += o;
+        for (int k = 0; k < PREFIX_AHEAD; ++k) {
+            const int64_t b = b0 + 64 * k + lane;
+            h[k] = b < p.chunks ? p.partial[b * p.n_experts + e] : 0;
         }
-        if (b < p.chunks) p.partial[b * p.n_experts + e] = before + inc - h;
-        before += __shfl(inc, 63, 64);
+#pragma unroll
+        for (int k = 0; k < PREFIX_AHEAD; ++k) {
+            const int64_t b = b0 + 64 * k + lane;
+            int inc = h[k];
+#pragma unroll
+            for (int off = 1; off < 64; off <<= 1) {
+                const int o = __shfl_up(inc, off, 64);
+                if (lane >= off) inc += o;
+            }
+            if (b < p.chunks) p.partial[b * p.n_experts + e] = before + inc - h[k];
+            before += __shfl(inc, 63, 64);
+        }
     }
     if (lane == 0) p.counts[e] = before;
 }
@@ -954,15 +981,16 @@ __global__ __launch_bounds__(256) void group_prefix_kernel(GroupRowsArgs p) {
 __global__ __launch_bounds__(GROUP_THREADS) void group_place_kernel(GroupRowsArgs p) {
     extern __shared__ int lds[];
     __shared__ int wave_tot[GROUP_WAVES];
-    const int64_t lo = blockIdx.x * GROUP_CHUNK, hi = min(p.n, lo + GROUP_CHUNK);
-    count(p, lo, hi, GROUP_CHUNK / GROUP_WAVES, lds);
+    const Run<CHUNK_PER> run(p, blockIdx.x * (int64_t)GROUP_CHUNK, CHUNK_PER);
     const int e = threadIdx.x;
     const int c = e < p.n_experts ? p.counts[e] : 0;
+    const int earlier = e < p.n_experts ? p.partial[blockIdx.x * (int64_t)p.n_experts + e] : 0;
+    run.count(p.n_experts, lds);
     const int padded = (c + p.align - 1) / p.align * p.align;
     int total;
     const int start = block_prefix(padded, wave_tot, total);
     if (e < p.n_experts) {
-        int at = start + p.partial[blockIdx.x * (int64_t)p.n_experts + e];
+        int at = start + earlier;
         for (int w = 0; w < GROUP_WAVES; ++w) {
             const int h = lds[w * p.n_experts + e];
             lds[w * p.n_experts + e] = at;
@@ -975,7 +1003,7 @@ __global__ __launch_bounds__(GROUP_THREADS) void group_place_kernel(GroupRowsArg
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.n_experts] = total;
     __syncthreads();
-    place(p, lo, hi, GROUP_CHUNK / GROUP_WAVES, lds);
+    run.place(p, lds);
     // what lies behind the last segment
     const int64_t step = (int64_t)gridDim.x * GROUP_THREADS;
     for (int64_t r = total + blockIdx.x * (int64_t)GROUP_THREADS + threadIdx.x; r < p.capacity; r += step) p.rows[r] = -1;
