@@ -228,7 +228,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_exact_kernel(RouteArgs
 // taking on to 16 experts and ranking those by their float64 keys, and two groups at the border by their float64 sums;
 // whatever is left is done again by the whole wave in float64.  So the choice is always the float64 one.
 // 65537 tokens of 512 float32 logits, 7 by softmax: 40 us, 3.4 TB/s, the sorting's vector instructions; 8192 in 8 groups by
-// sigmoid and bias, bfloat16: 21 us, two waves a SIMD, each a chain of reductions.
+// sigmoid and bias, bfloat16: 20 us, two waves a SIMD, each a chain of reductions.
 constexpr int FAST_MAX_K = 15;
 constexpr int64_t WIDE_MAX_TOKENS = 4096;
 
@@ -302,9 +302,10 @@ __device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
 // the size away.
 __device__ __forceinline__ bool apart(float a, float b) { return a - b > 0x1p-16f * fmaxf(1.f, fabsf(a)); }
 
-// GROUPS: n_groups > 1 (16 lanes only).
+// GROUPS: n_groups > 1 (16 lanes only).  Four waves a SIMD at least: at three, which the widest form would have, 65536 tokens
+// in 8 groups take 93 us instead of 78.
 template <class T, int LT, int C, bool GROUPS>
-__global__ __launch_bounds__(64 * ROUTE_WAVES) void route_kernel(RouteArgs p, int vec) {
+__global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_eu(4))) void route_kernel(RouteArgs p, int vec) {
     constexpr int PT = 64 / LT;                            // tokens a wave
     static_assert(!GROUPS || LT == 16, "groups lie in 16 lanes");
     constexpr int V = LT * C / 16;
@@ -1028,7 +1029,7 @@ __global__ __launch_bounds__(GROUP_THREADS) void balance_kernel(const float* bia
 
 // Variants, by what the sizes allow and what they measured (of 512 experts, times of whole calls back to back, which
 // take 9.5 us at least):
-//   * 16 lanes a token from 4096 tokens on (65536 tokens, 7 by softmax: 38 us, by sigmoid and bias 64; 64 lanes: 57 and
+//   * 16 lanes a token from 4096 tokens on (65536 tokens, 7 by softmax: 38 us, by sigmoid and bias 55; 64 lanes: 57 and
 //     78), and for groups of 16, 32 or multiples of 64, which lie in a row of lanes;
 //   * 64 lanes below (2048 tokens by sigmoid and bias: 11.1 us against 14.2), where a wave's own time counts, and above
 //     512 experts, whose values 16 lanes cannot hold;

@@ -670,10 +670,13 @@ def test_product_beyond_32_bits():
     _check_product(out[63][:, -300:], _np(a.dequantize())[:, -128:], _np(last(b, 300).dequantize())[:, -128:], 128)
 
 
-@pytest.mark.parametrize("m,n,groups,dtype", [(1100, 3400, 9, torch.float32), (2048, 2048, 20, torch.bfloat16), (2000, 2050, 300, torch.bfloat16)])
-def test_product_depth_groups_of_many_tiles(m, n, groups, dtype):
+@pytest.mark.parametrize("m,n,groups,dtype,deep", [
+    (1100, 3400, 9, torch.float32, 1), (2048, 2048, 20, torch.bfloat16, 1), (2000, 2050, 300, torch.bfloat16, 1),
+    (2048, 64, 9, torch.float32, 6),                           # 32 x 64 tiles
+])
+def test_product_depth_groups_of_many_tiles(m, n, groups, dtype, deep):
     """Groups whose tiles are dealt to all XCDs, deepest first (or, from 257 groups on, as they come)."""
-    blocks = [(5 * g * g + 3 * g) % 4 for g in range(groups)]
+    blocks = [(5 * g * g + 3 * g) % 4 * deep for g in range(groups)]
     ends = np.concatenate([[0], np.cumsum(blocks)]) * 128
     a, b = _random_fp8(m, int(ends[-1]), "e4m3", False, m), _random_fp8(n, int(ends[-1]), "e4m3", False, n)
     out = torch.full((groups, m, n), float("nan"), dtype=dtype, device="cuda")
