@@ -165,9 +165,10 @@ def group_rows(experts: torch.Tensor, n_experts: int, *, align: int = 1, stream=
         g = Groups(torch.empty(n_experts, dtype=torch.int32, device=dev),
                    torch.empty(n_experts + 1, dtype=torch.int32, device=dev),
                    torch.empty(cap.value, dtype=torch.int32, device=dev), torch.empty_like(experts))
-        work = torch.empty(ws.value, dtype=torch.uint8, device=dev)
+        work = torch.empty(ws.value, dtype=torch.uint8, device=dev) if ws.value else None
         L.check(L.muon_group_rows(experts.data_ptr(), n, n_experts, align, g.counts.data_ptr(), g.offsets.data_ptr(),
-                                  g.rows.data_ptr(), g.position.data_ptr(), work.data_ptr(), ws.value, _stream_ptr(experts)),
+                                  g.rows.data_ptr(), g.position.data_ptr(), None if work is None else work.data_ptr(), ws.value,
+                                  _stream_ptr(experts)),
                 "muon_group_rows")
     return g
 
