@@ -29,6 +29,10 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// in rows of out that need not begin on a 16-byte boundary
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(2)));
+typedef uint2 uint2_any __attribute__((aligned(2)));
 
 constexpr int NUM_XCD = 8, CUS = 256;
 constexpr int KB = 128;                   // values that share a scale
@@ -491,13 +495,15 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         for (int q = 0; q < 32 / RPS; ++q, o += RPS * p.ld_out) {
             const uint4 w = *reinterpret_cast<const uint4*>(mine + (q * RPS + row) * OROW + col * sizeof(OUT));
             if (r0 + q * RPS + row >= done.rows_a) continue;
-            if (p.vec && EPL <= left) {
+            if (EPL <= left) {
                 if constexpr (PRECISE) {
                     f32x4 v = __builtin_bit_cast(f32x4, w);
-                    if (p.accumulate) v += *reinterpret_cast<const f32x4*>(o);
-                    __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(o));
+                    if (p.accumulate) v += *reinterpret_cast<const f32x4_any*>(o);
+                    if (p.vec) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(o));
+                    else *reinterpret_cast<f32x4_any*>(o) = v;
                 } else {
-                    __builtin_nontemporal_store(__builtin_bit_cast(i32x4, w), reinterpret_cast<i32x4*>(o));
+                    if (p.vec) __builtin_nontemporal_store(__builtin_bit_cast(i32x4, w), reinterpret_cast<i32x4*>(o));
+                    else *reinterpret_cast<i32x4_any*>(o) = __builtin_bit_cast(i32x4, w);
                 }
             } else {
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -664,13 +670,13 @@ __global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
                 OUT* o = static_cast<OUT*>(p.out) + (p.mode == MUON_PRODUCT_DEPTH ? x.group * p.out_stride : 0) +
                          (x.m0 + row) * p.ld_out + x.n0 + col;
                 const int64_t left = p.n - x.n0 - col;
-                if (p.vec && left >= 4) {
+                if (left >= 4) {
                     if constexpr (PRECISE) {
-                        f32x4* o4 = reinterpret_cast<f32x4*>(o);
+                        f32x4_any* o4 = reinterpret_cast<f32x4_any*>(o);
                         if (p.accumulate) v += *o4;
                         *o4 = v;
                     } else {
-                        *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+                        *reinterpret_cast<uint2_any*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
                     }
                 } else {
 #pragma unroll

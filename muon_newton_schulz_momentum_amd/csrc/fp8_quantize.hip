@@ -73,6 +73,10 @@ __device__ __forceinline__ void store_once(uint8_t* p, uint4 v) {
     __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p));
 }
 
+// Rows of src need not begin on a 16-byte boundary.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // A thread's 8 x 8 values as they are in memory.
 template <class T>
 struct Block;
@@ -85,7 +89,7 @@ struct Block<float> {
         for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
     }
     __device__ __forceinline__ void load(int i, const float* p) {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        const f32x4_any a = *reinterpret_cast<const f32x4_any*>(p), b = *reinterpret_cast<const f32x4_any*>(p + 4);
         v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
         v[i][4] = b.x; v[i][5] = b.y; v[i][6] = b.z; v[i][7] = b.w;
     }
@@ -137,7 +141,7 @@ struct Block<uint16_t> {
     uint32_t w[8][4];          // two values a word
     __device__ __forceinline__ void clear(int i) { w[i][0] = w[i][1] = w[i][2] = w[i][3] = 0; }
     __device__ __forceinline__ void load(int i, const uint16_t* p) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        const u32x4_any u = *reinterpret_cast<const u32x4_any*>(p);
         w[i][0] = u.x; w[i][1] = u.y; w[i][2] = u.z; w[i][3] = u.w;
     }
     __device__ __forceinline__ void set(int i, int j, uint16_t x) { w[i][j >> 1] |= (uint32_t)x << (16 * (j & 1)); }
@@ -201,7 +205,7 @@ struct Block<uint16_t> {
 };
 
 template <class T, int FMT, bool SQUARE>
-__global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) {
+__global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t lds_t[QT * QT];
     __shared__ __attribute__((aligned(16))) uint32_t col_amax[4][QT];
     __shared__ uint32_t tile_amax[4];
@@ -231,7 +235,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) 
             if (sr >= p.src_rows) continue;
         }
         const T* row = src + sr * p.ld;
-        if (vec && c + 8 <= p.cols) {
+        if (c + 8 <= p.cols) {
             v.load(i, row + c);
         } else {
 #pragma unroll
@@ -327,12 +331,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs p, int vec) 
 
 template <class T, int FMT>
 void quantize_as(const QuantizeArgs& a, int32_t square, hipStream_t s) {
-    // 16-byte loads where every row of src begins on one
-    const int64_t size = sizeof(T);
-    const int vec = a.ld * size % 16 == 0 && a.batch_stride * size % 16 == 0;
     const dim3 grid((unsigned)a.tiles);
-    if (square) hipLaunchKernelGGL((quantize_kernel<T, FMT, true>), grid, dim3(256), 0, s, a, vec);
-    else hipLaunchKernelGGL((quantize_kernel<T, FMT, false>), grid, dim3(256), 0, s, a, vec);
+    if (square) hipLaunchKernelGGL((quantize_kernel<T, FMT, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((quantize_kernel<T, FMT, false>), grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
