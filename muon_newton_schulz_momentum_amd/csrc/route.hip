@@ -309,8 +309,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
     constexpr int PT = 64 / LT;                            // tokens a wave
     static_assert(!GROUPS || LT == 16, "groups lie in 16 lanes");
     constexpr int V = LT * C / 16;
-    __shared__ double exact_key[ROUTE_WAVES][64 * V];
-    __shared__ float exact_x[ROUTE_WAVES][64 * V];
+    // of a wave: its four tokens' keys while their groups are chosen, later the token done again (keys, logits)
+    constexpr int KEYS = 66 * C + 1, DOUBLES = std::max(64 * V + 32 * V, GROUPS ? 2 * KEYS : 0);
+    __shared__ double room[ROUTE_WAVES][DOUBLES];
     const int lane = threadIdx.x & 63, l = lane & (LT - 1);
     const int64_t t0 = ((int64_t)blockIdx.x * ROUTE_WAVES + (threadIdx.x >> 6)) * PT;
     if (t0 >= p.tokens) return;
@@ -381,43 +382,41 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
     }
     bool again = false;                                    // for the whole wave in float64
     uint64_t kept = ~0ull;                                 // groups that stay
+    float* keys = reinterpret_cast<float*>(room[threadIdx.x >> 6]) + (GROUPS ? (lane >> 4) * KEYS : 0);
     const int per = GROUPS ? p.n_experts / p.n_groups : 1;
     if constexpr (GROUPS) {
-        // per is 16, 32 or a multiple of 64: a group is 4, 8 or 16 lanes of one c, or several c's
-        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // lane l: groups l + 16 i
-        float m1 = -INFINITY, m2 = -INFINITY;
-        int begun = 0;                                     // c's of the group under way
-        float score[C];                                    // this lane's group of row c: its two largest, added up
+        // Through LDS, expert e at e + e / 32 (and tokens 66 C + 1 apart), so that groups begin on different banks.  Up to
+        // 16 groups: 2^share lanes each; more: a lane takes every 16th.
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            float a1 = -INFINITY, a2 = -INFINITY;
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const float k = x[c][v] > -INFINITY && key[c][v] > -INFINITY ? key[c][v] : -INFINITY;   // NaN: out
-                a2 = fmaxf(fminf(a1, k), a2);
-                a1 = fmaxf(a1, k);
-            }
-            merge2(a1, a2, dppf<XCHG_1>(a1), dppf<XCHG_1>(a2));
-            merge2(a1, a2, dppf<XCHG_2>(a1), dppf<XCHG_2>(a2));
-            if (per >= 32) merge2(a1, a2, dppf<XCHG_4>(a1), dppf<XCHG_4>(a2));
-            if (per >= 64) merge2(a1, a2, dppf<XCHG_8>(a1), dppf<XCHG_8>(a2));
-            // a group of several c's: the running pair, complete at its last c
-            if (begun == 0) { m1 = -INFINITY; m2 = -INFINITY; }
-            merge2(m1, m2, a1, a2);
-            if (++begun * 64 >= per) begun = 0;
-            score[c] = m1 == -INFINITY ? -INFINITY : m1 + (m2 == -INFINITY ? 0.f : m2);
-        }
+            for (int v = 0; v < 4; ++v)                    // a NaN key is out
+                keys[66 * c + 4 * l + (l >> 3) + v] = x[c][v] > -INFINITY && key[c][v] > -INFINITY ? key[c][v] : -INFINITY;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int share = p.n_groups <= 2 ? 3 : p.n_groups <= 4 ? 2 : p.n_groups <= 8 ? 1 : 0, step = 1 << share;
+        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // lane l: groups l + 16 i, their two largest added up
         kept = 0;
+#pragma unroll 1
+        for (int i = 0; 16 * i < p.n_groups; ++i) {
+            const int g = (l >> share) + 16 * i, first = g * per, end = g < p.n_groups ? first + per : first;
+            float m1 = -INFINITY, m2 = -INFINITY;
+            for (int e0 = first + (l & (step - 1)); e0 < end; e0 += 8 * step)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (16 * i >= p.n_groups) break;
-            // group l + 16 i's sum, from the lane and row that hold it
-            const int g = l + 16 * i, first = g * per, c0 = (first + per - 1) / 64, src = (first % 64) / 4;
+                for (int j = 0; j < 8; ++j) {
+                    const int e = e0 + j * step;
+                    const float k = e < end ? keys[e + (e >> 5)] : -INFINITY;
+                    m2 = fmaxf(fminf(m1, k), m2);
+                    m1 = fmaxf(m1, k);
+                }
+            if (share >= 1) merge2(m1, m2, dppf<XCHG_1>(m1), dppf<XCHG_1>(m2));
+            if (share >= 2) merge2(m1, m2, dppf<XCHG_2>(m1), dppf<XCHG_2>(m2));
+            if (share >= 3) merge2(m1, m2, dppf<XCHG_4>(m1), dppf<XCHG_4>(m2));
+            const float w = m1 == -INFINITY ? -INFINITY : m1 + (m2 == -INFINITY ? 0.f : m2);
+            const float mine = __shfl(w, (lane & 48) + ((l << share) & 15), 64);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const float w = __shfl(score[c], (lane & 48) + src, 64);
-                if (g < p.n_groups && c == c0) best[i] = w;
-            }
+            for (int q = 0; q < 4; ++q)
+                if (q == i && l + 16 * i < p.n_groups) best[q] = mine;
         }
         // the largest top_groups of them; how near the next one comes, and those on either side of the two
         float prev = INFINITY;
@@ -462,7 +461,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
                 for (int e0 = 4 * l; e0 < per; e0 += 64)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
-                        if (!near) continue;
+                        if (!near || e0 + v >= per) continue;
                         const float xv = clean_logit(load_logit(row + g0 + e0 + v));
                         const double ex = exp(softmax ? (double)xv - (double)top : -(double)xv);
                         double k = (softmax ? ex : 1.0 / (1.0 + ex)) + (p.bias ? (double)p.bias[g0 + e0 + v] : 0.0);
@@ -480,17 +479,14 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
     // logits are decided by 16 bits: there the expert itself fits behind them, and equal logits need no second look.
     const bool whole = sizeof(T) == 2 && !p.bias;
     uint32_t bits[C][4];
-    int group = 0, rows = 0;                               // of groups of several c's: which, and its c's so far
+    const uint32_t inv = GROUPS ? (1u << 20) / (uint32_t)per + 1 : 0;   // e / per is e * inv >> 20 for e * per < 2^20
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        bool stays = true;
-        if constexpr (GROUPS) {
-            stays = (kept >> (per == 16 ? expert(c, 0) >> 4 : per == 32 ? expert(c, 0) >> 5 : group)) & 1;
-            if (++rows * 64 >= per) { rows = 0; ++group; }
-        }
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-            const float k = p.bias ? key[c][v] : x[c][v];
+            const bool stays = !GROUPS || (kept >> (((uint32_t)expert(c, v) * inv >> 20) & 63u)) & 1;
+            // (from LDS where it is there: fewer registers while the groups are chosen)
+            const float k = !p.bias ? x[c][v] : GROUPS ? keys[66 * c + 4 * l + (l >> 3) + v] : key[c][v];
             const bool in = stays && x[c][v] > -INFINITY && k > -INFINITY;
             const uint32_t o = ordered(k);
             const uint32_t kv = whole ? (o & 0xffff0000u) | (uint32_t)(1023 - expert(c, v)) : (o & ~63u) | (uint32_t)(63 - (4 * c + v));
@@ -606,10 +602,13 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
         p.weights[t * p.top_k + slot] = weight * p.scale;
     }
     uint64_t left = __ballot(live && again && l == 0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the groups' keys have been read
+    __builtin_amdgcn_wave_barrier();
     while (left) {
         const int g = __builtin_ctzll(left);
         left &= left - 1;
-        route_exact<T, V>(p, t0 + g / LT, exact_x[threadIdx.x >> 6], exact_key[threadIdx.x >> 6]);
+        double* mine = room[threadIdx.x >> 6];
+        route_exact<T, V>(p, t0 + g / LT, reinterpret_cast<float*>(mine + 64 * V), mine);
     }
 }
 
@@ -1030,16 +1029,16 @@ __global__ __launch_bounds__(GROUP_THREADS) void balance_kernel(const float* bia
 // Variants, by what the sizes allow and what they measured (of 512 experts, times of whole calls back to back, which
 // take 9.5 us at least):
 //   * 16 lanes a token from 4096 tokens on (65536 tokens, 7 by softmax: 38 us, by sigmoid and bias 55; 64 lanes: 57 and
-//     78), and for groups of 16, 32 or multiples of 64, which lie in a row of lanes;
+//     78), and for groups of up to 512 experts;
 //   * 64 lanes below (2048 tokens by sigmoid and bias: 11.1 us against 14.2), where a wave's own time counts, and above
 //     512 experts, whose values 16 lanes cannot hold;
-//   * the float64 wave for what neither covers: more than 15 choices, other groups (65536 tokens, 20 choices: 284 us).
+//   * the float64 wave for what neither covers: more than 15 choices (65536 tokens, 20 choices: 284 us), groups of more
+//     than 512 experts.
 template <class T>
 hipError_t route_by_width(const RouteArgs& a, hipStream_t s) {
-    const int per = a.n_experts / a.n_groups;
     const bool few = a.top_k <= FAST_MAX_K, flat = a.n_groups == 1;
     const bool wide = few && flat && (a.tokens < WIDE_MAX_TOKENS || a.n_experts > 512);
-    const bool narrow = few && !wide && a.n_experts <= 512 && (flat || per == 16 || per == 32 || per % 64 == 0);
+    const bool narrow = few && !wide && a.n_experts <= 512;
     const int64_t per_block = ROUTE_WAVES * (narrow ? 4 : 1);
     const dim3 grid((unsigned)((a.tokens + per_block - 1) / per_block)), block(64 * ROUTE_WAVES);
     const int vec = a.ld % 4 == 0 && a.n_experts % 4 == 0;

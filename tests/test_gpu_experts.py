@@ -17,6 +17,7 @@ Tolerances.  u = 2^-24 is float32's half step, 2^-8 bfloat16's.
     at most 7 * 2^-13 of its largest product.
 """
 import ctypes as C
+import itertools
 
 import numpy as np
 import pytest
@@ -200,7 +201,8 @@ def test_route_near_ties_with_bias(T, score):
         _check_route(x, experts, weights, orc.route(_np(x), k, _np(bias), score=score), k)
 
 
-@pytest.mark.parametrize("E,groups,top", [(512, 8, 4), (256, 16, 3), (512, 16, 15), (512, 4, 1), (512, 2, 1), (128, 4, 4)])
+@pytest.mark.parametrize("E,groups,top", [(512, 8, 4), (256, 16, 3), (512, 16, 15), (512, 4, 1), (512, 2, 1), (128, 4, 4),
+                                          (304, 8, 5), (160, 2, 1), (22, 2, 1), (60, 20, 7), (64, 64, 9), (512, 64, 20), (350, 50, 33)])
 @pytest.mark.parametrize("score,biased", [("sigmoid", False), ("softmax", False), ("sigmoid", True), ("softmax", True)])
 def test_route_groups_at_the_border(E, groups, top, score, biased):
     """Group sums that are equal (coarse logits) or agree to 1e-7 (two groups alike but for their noise)."""
@@ -217,7 +219,33 @@ def test_route_groups_at_the_border(E, groups, top, score, biased):
     for x in (coarse, alike):
         kw = dict(score=score, groups=groups, top_groups=top)
         experts, weights = X().route(x, k, bias=bias, **kw)
-        _check_route(x, experts, weights, orc.route(_np(x), k, None if bias is None else _np(bias), **kw), k)
+        e_ref, w_ref = orc.route(_np(x), k, None if bias is None else _np(bias), **kw)
+        got = experts.cpu().numpy()
+        for t in np.nonzero((got != e_ref).any(axis=1))[0]:
+            assert biased
+            e_ref[t], w_ref[t] = _either_group(_np(x[t:t + 1]), got[t], _np(bias), score, groups, top)
+        _check_route(x, experts, weights, (e_ref, w_ref), k)
+
+
+def _either_group(x, got, bias, score, groups, top):
+    """got, if it is the choice for some order of the groups whose sums are equal but for rounding.
+
+    Coarse logits and a bias that repeats give groups like (s_a + b_0) + (s_c + b_1) and (s_c + b_0) + (s_a + b_1): equal in
+    exact arithmetic, and in float64 off by their roundings.  Those are at most 2^-53 for each of the three
+    sums (of at most 1) and, for either score, 2^-52 of exp and 2^-53 of the quotient (what the softmax's sum is off
+    by is a factor common to both): below 2^-50 in all."""
+    s = orc.scores(x, score)[0][0]
+    key, per = s + bias, len(bias) // groups
+    worth = np.array([np.sort(key[g * per:(g + 1) * per])[-2:].sum() for g in range(groups)])
+    border = np.sort(worth)[::-1][top - 1]
+    sure = [g for g in range(groups) if worth[g] > border + 2.0 ** -50]
+    level = [g for g in range(groups) if abs(worth[g] - border) <= 2.0 ** -50]
+    for some in itertools.combinations(level, top - len(sure)):
+        kept = set(sure) | set(some)
+        order = sorted((e for e in range(len(bias)) if e // per in kept), key=lambda e: (-key[e], e))[:len(got)]
+        if list(got) == order:
+            return np.array(order), s[order] / s[order].sum()
+    raise AssertionError((got, worth))
 
 
 def test_route_nan_bias_counts_in_no_group():
