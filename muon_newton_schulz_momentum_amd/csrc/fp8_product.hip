@@ -258,7 +258,7 @@ using ic = std::integral_constant<int, N>;
 // before it cover the fragment reads that it waits for, those behind it the next stage's first reads.
 //
 // 16381 x 5632 x 2048 in bfloat16: 170 us, 2.2 PFLOP/s; 8192 x 8192 x 8320: 2.5.  57344 rows of 128 experts, 1024 x 4096:
-// 278 us.  Weight gradients of 64 experts, 1024 x 4096 in float32 over 28672 rows: 399 us, about 140 of products and
+// 274-282 us.  Weight gradients of 64 experts, 1024 x 4096 in float32 over 28672 rows: 398 us, about 140 of products and
 // 200 of stores (1.07 GB), one after the other: a wave's loads and stores retire in order.
 template <int AFMT, class OUT>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_kernel(ProductArgs p) {
