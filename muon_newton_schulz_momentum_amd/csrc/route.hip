@@ -412,7 +412,8 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
             if (share >= 1) merge2(m1, m2, dppf<XCHG_1>(m1), dppf<XCHG_1>(m2));
             if (share >= 2) merge2(m1, m2, dppf<XCHG_2>(m1), dppf<XCHG_2>(m2));
             if (share >= 3) merge2(m1, m2, dppf<XCHG_4>(m1), dppf<XCHG_4>(m2));
-            const float w = m1 == -INFINITY ? -INFINITY : m1 + (m2 == -INFINITY ? 0.f : m2);
+            // (two of the lowest value stay above a group without an expert)
+            const float w = m1 == -INFINITY ? -INFINITY : fmaxf(m1 + (m2 == -INFINITY ? 0.f : m2), -F32_MAX);
             const float mine = __shfl(w, (lane & 48) + ((l << share) & 15), 64);
 #pragma unroll
             for (int q = 0; q < 4; ++q)

@@ -259,6 +259,30 @@ def test_route_nan_bias_counts_in_no_group():
         _check_route(x, experts, weights, orc.route(_np(x), 4, _np(bias), **kw), 4)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_lowest_bias_and_empty_groups(score):
+    """A bias of float32's lowest value leaves its experts in, behind all others; groups without an expert come last."""
+    T, E, groups = 2100, 64, 8
+    x = torch.randn(T, E, device="cuda", generator=_gen(51))
+    x[:, :8] = -float("inf")                                   # group 0: nobody
+    x[::2, 16:24] = float("nan")
+    bias = torch.full((E,), torch.finfo(torch.float32).min, device="cuda")
+    bias[60:] = 0.1
+    bias[40] = 0.2                                             # one such expert in its group
+    for top in (1, 2, 3, 7, 8):
+        kw = dict(score=score, groups=groups, top_groups=top)
+        experts, weights = X().route(x, 12, bias=bias, **kw)
+        _check_route(x, experts, weights, orc.route(_np(x), 12, _np(bias), **kw), 12)
+    experts, weights = X().route(x, 9, bias=bias, score=score)
+    _check_route(x, experts, weights, orc.route(_np(x), 9, _np(bias), score=score), 9)
+    x, bias = x[:, 6:22].clone(), bias[48:].clone()            # pairs: one empty, six of the lowest value, one above them
+    bias[:-2] = torch.finfo(torch.float32).min
+    for top in (1, 2, 3):
+        kw = dict(score=score, groups=8, top_groups=top)
+        experts, weights = X().route(x, 6, bias=bias, **kw)
+        _check_route(x, experts, weights, orc.route(_np(x), 6, _np(bias), **kw), 6)
+
+
 def test_route_bias_infinite_and_nan():
     x = torch.randn(9, 64, device="cuda", generator=_gen(4))
     bias = torch.zeros(64, device="cuda")
