@@ -20,6 +20,7 @@
 
 #include "device_common.h"
 #include "experts.h"
+#include "fp8_panel.h"
 
 namespace muon {
 namespace {
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 
     // staging: load d of wave w brings rows 8 w + 64 i + lane / 8 of an operand
     const int lrow = 8 * wave + (lane >> 3), lchunk = lane & 7;
-    const int va = lrow * (int)p.lda + 16 * lchunk, vb = lrow * (int)p.ldb + 16 * lchunk;
+    const int32_t va = Panel::lane(lrow, lchunk, (int)p.lda), vb = Panel::lane(lrow, lchunk, (int)p.ldb);
     const int wst = lrow * ROW + 16 * lchunk;
 
     const uint8_t *abase, *bbase, *scale_base;
@@ -294,10 +295,13 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     // fetches nothing (a branch in the main loop would let the compiler move the matrix instructions behind it).
     auto load = [&](int d, int step, int keep) {
         const int i = d < LA ? d : d - LA;
-        const int at = (step * KB + i * 64 * (int)(d < LA ? p.lda : p.ldb)) & keep;
+        int32_t rows_on = Panel::rows(64 * i, (int)(d < LA ? p.lda : p.ldb));
+        asm volatile("" : "+s"(rows_on));                  // added here, or the sums of all d stay in registers
+        const int32_t of_row = (d < LA ? va : vb) + rows_on;
+        const int32_t of_block = Panel::block(step) & keep;
         const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(
             (void*)(d < LA ? abase : bbase), 0, (d < LA ? bytes_a : bytes_b) & keep, 0x00020000);
-        staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, d < LA ? va : vb, at, 0);
+        staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, of_row, of_block, 0);
     };
     auto mask = [](bool valid) {
         int keep = __builtin_amdgcn_readfirstlane(valid ? -1 : 0);
@@ -328,8 +332,8 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         const bool per_group = p.mode == MUON_PRODUCT_ROWS;
         abase = p.a + x.m0 * p.lda;
         bbase = p.b + (per_group ? x.group * p.stride_b : 0) + x.n0 * p.ldb;
-        bytes_a = (int)((x.rows_a - 1) * p.lda + kp);
-        bytes_b = (int)((x.rows_b - 1) * p.ldb + kp);
+        bytes_a = Panel::bytes(x.rows_a, (int)p.lda, kp);
+        bytes_b = Panel::bytes(x.rows_b, (int)p.ldb, kp);
         const bool is_a = wave < WAVES / 2;
         const int64_t r0 = is_a ? x.m0 : x.n0, sh = is_a ? p.shift_a : p.shift_b;
         const int ld = (int)(is_a ? p.ldas : p.ldbs), last = (is_a ? x.rows_a : x.rows_b) - 1;
