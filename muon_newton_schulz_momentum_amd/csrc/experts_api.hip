@@ -64,7 +64,8 @@ muon_status check_group(int64_t n, int32_t n_experts, int32_t align, const char*
         return fail(MUON_ERR_SHAPE, who, "n_experts must be in [1, 1024]");
     if (align < 1 || align > 128 || (align & (align - 1)) != 0)
         return fail(MUON_ERR_INVALID_ARG, who, "align must be 1, 2, 4, ..., 128");
-    if (n < 0 || n + (int64_t)n_experts * 128 > MAX_I32)
+    // the capacity, n + n_experts * 127 rounded up to 128 at most, is an int32 (as a difference: no sum that could overflow)
+    if (n < 0 || n > MAX_I32 - 127 - (int64_t)n_experts * 128)
         return fail(MUON_ERR_SHAPE, who, "n must be at least 0 and the padded rows below 2^31");
     return MUON_OK;
 }

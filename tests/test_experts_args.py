@@ -262,3 +262,20 @@ def test_oracle_route_gradient_is_the_difference_quotient(score, renormalize):
             dn[t, e] -= 1e-6
             # central difference: error of order 1e-12 * third derivative + 1e-16 / 1e-6
             assert abs((loss(up) - loss(dn)) / 2e-6 - dx[t, e]) < 1e-8
+
+
+# ---- sizes near the ends of their types --------------------------------------------------------
+
+@pytest.mark.parametrize("n", [(1 << 63) - 1, (1 << 63) - 512, 1 << 62, (1 << 31) - 1 - 4 * 128])
+def test_group_rows_refuses_a_capacity_that_is_no_int32(n):
+    rows, ws = C.c_int64(), C.c_uint64()
+    assert L.muon_group_rows_capacity(n, 4, 128, C.byref(rows)) == L.MUON_ERR_SHAPE
+    assert L.muon_group_rows_workspace(n, 4, C.byref(ws)) == L.MUON_ERR_SHAPE
+    assert L.muon_group_rows(A, n, 4, 128, B, S, T, O, W, (1 << 64) - 1, None) == L.MUON_ERR_SHAPE
+
+
+def test_group_rows_takes_the_largest_size():
+    rows = C.c_int64()
+    n = (1 << 31) - 1 - 127 - 4 * 128
+    assert L.muon_group_rows_capacity(n, 4, 128, C.byref(rows)) == L.MUON_OK
+    assert n <= rows.value < 1 << 31
