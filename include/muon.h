@@ -417,7 +417,7 @@ MUON_API muon_status muon_step_noalloc(const muon_plan* plan, const muon_step_co
 #define MUON_SCORE_SIGMOID 1
 
 typedef struct muon_route_config {
-    int64_t tokens;      /* rows of logits, below 2^26                                       */
+    int64_t tokens;      /* rows of logits, at most 2^26 - 4; tokens * top_k below 2^31      */
     int64_t ld;          /* row stride of logits in elements, >= n_experts                   */
     int32_t n_experts;   /* 1..MUON_MAX_EXPERTS                                              */
     int32_t top_k;       /* 1..min(n_experts, MUON_MAX_TOP_K)                                */

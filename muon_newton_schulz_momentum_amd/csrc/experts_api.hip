@@ -15,8 +15,8 @@ namespace {
 
 constexpr int64_t MAX_I32 = 0x7fffffff;
 constexpr int64_t MAX_LD = 1 << 23;       // of an operand of a product
-// a launch holds fewer than 2^32 threads: up to 64 a token, 256 a tile
-constexpr int64_t MAX_TOKENS = 1 << 26, MAX_QUANTIZE_TILES = 1 << 24;
+// a launch holds fewer than 2^32 threads: up to 64 a token in workgroups of 256, 256 a tile
+constexpr int64_t MAX_TOKENS = (1 << 26) - 4, MAX_QUANTIZE_TILES = 1 << 24;
 
 muon_status fail(muon_status s, const char* who, const char* what) {
     return set_error(s, std::string(who) + ": " + what);
@@ -43,8 +43,8 @@ muon_status check_route(const muon_route_config* c, const char* who) {
         return fail(MUON_ERR_SHAPE, who, "n_experts must be in [1, 1024]");
     if (c->top_k < 1 || c->top_k > c->n_experts || c->top_k > MUON_MAX_TOP_K)
         return fail(MUON_ERR_SHAPE, who, "top_k must be in [1, min(n_experts, 64)]");
-    if (c->tokens < 0 || c->tokens >= MAX_TOKENS || c->tokens * c->top_k > MAX_I32)
-        return fail(MUON_ERR_SHAPE, who, "tokens must be in [0, 2^26) and tokens * top_k below 2^31");
+    if (c->tokens < 0 || c->tokens > MAX_TOKENS || c->tokens * c->top_k > MAX_I32)
+        return fail(MUON_ERR_SHAPE, who, "tokens must be in [0, 2^26 - 4] and tokens * top_k below 2^31");
     if (c->ld < c->n_experts || c->ld > MAX_I32) return fail(MUON_ERR_SHAPE, who, "ld must be in [n_experts, 2^31)");
     if (!is_dtype(c->dtype)) return fail(MUON_ERR_INVALID_ARG, who, "dtype must be F32 or BF16");
     if (c->score != MUON_SCORE_SOFTMAX && c->score != MUON_SCORE_SIGMOID)

@@ -279,3 +279,16 @@ def test_group_rows_takes_the_largest_size():
     n = (1 << 31) - 1 - 127 - 4 * 128
     assert L.muon_group_rows_capacity(n, 4, 128, C.byref(rows)) == L.MUON_OK
     assert n <= rows.value < 1 << 31
+
+
+def test_route_launches_stay_below_2_32_threads():
+    """64 lanes a token, 4 tokens a workgroup: 2^26 - 3 tokens would be 2^24 workgroups of 256."""
+    for tokens in ((1 << 26) - 3, (1 << 26) - 1):
+        c = _route(tokens=tokens, top_k=1)
+        assert L.muon_route(C.byref(c), A, None, B, S, None) == L.MUON_ERR_SHAPE
+        assert L.muon_route_backward(C.byref(c), A, B, S, O, 8, None) == L.MUON_ERR_SHAPE
+    # the last size that is taken: refused for a buffer only
+    c = _route(tokens=(1 << 26) - 4, top_k=1)
+    assert -(-c.tokens // 4) * 256 < 1 << 32
+    assert L.muon_route(C.byref(c), A + 4, None, B, S, None) == L.MUON_ERR_ALIGNMENT
+    assert L.muon_route_backward(C.byref(c), A + 4, B, S, O, 8, None) == L.MUON_ERR_ALIGNMENT
