@@ -395,8 +395,12 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         const int share = p.n_groups <= 2 ? 3 : p.n_groups <= 4 ? 2 : p.n_groups <= 8 ? 1 : 0, step = 1 << share;
-        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // lane l: groups l + 16 i, their two largest added up
-        kept = 0;
+        // lane l: groups l + 16 i, their two largest added up, and what float32 may be off by
+        float worth[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, off[4] = {0.f, 0.f, 0.f, 0.f};
+        // Scores are off by less than 2^-21, a key and a sum by their rounding, 2^-24 of a size that is at most the larger of the two
+        // keys (which may cancel) or twice that: 2^-20 + 2^-22 of that size in all.  With a bias the softmax's sum counts,
+        // too (without one it is a factor of all groups): 2^-18 of the scores.
+        const float margin = softmax && p.bias ? 0x1p-18f + 0x1p-19f : 0x1p-19f;
 #pragma unroll 1
         for (int i = 0; 16 * i < p.n_groups; ++i) {
             const int g = (l >> share) + 16 * i, first = g * per, end = g < p.n_groups ? first + per : first;
@@ -412,48 +416,65 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
             if (share >= 1) merge2(m1, m2, dppf<XCHG_1>(m1), dppf<XCHG_1>(m2));
             if (share >= 2) merge2(m1, m2, dppf<XCHG_2>(m1), dppf<XCHG_2>(m2));
             if (share >= 3) merge2(m1, m2, dppf<XCHG_4>(m1), dppf<XCHG_4>(m2));
-            // (two of the lowest value stay above a group without an expert)
-            const float w = m1 == -INFINITY ? -INFINITY : fmaxf(m1 + (m2 == -INFINITY ? 0.f : m2), -F32_MAX);
-            const float mine = __shfl(w, (lane & 48) + ((l << share) & 15), 64);
+            m2 = m2 == -INFINITY ? 0.f : m2;
+            // an infinite key is exact; finite sums stay finite (and so above a group without an expert)
+            const bool sum = fabsf(m1) != INFINITY;
+            const float w = sum ? fminf(fmaxf(m1 + m2, -F32_MAX), F32_MAX) : m1;
+            const float d = sum ? margin * fmaxf(1.f, fmaxf(fabsf(m1), fabsf(m2))) : 0.f;
+            const int from = (lane & 48) + ((l << share) & 15);
+            const float my_w = __shfl(w, from, 64), my_d = __shfl(d, from, 64);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                if (q == i && l + 16 * i < p.n_groups) best[q] = mine;
+                if (q == i && l + 16 * i < p.n_groups) {
+                    worth[q] = my_w;
+                    off[q] = my_d;
+                }
         }
-        // the largest top_groups of them; how near the next one comes, and those on either side of the two
-        float prev = INFINITY;
-        bool near_in = false, near = false, near_out = false;
-        int last_in = 0, first_out = 0;
-        for (int r = 0; r < min(p.top_groups + 2, p.n_groups); ++r) {
+        float best[4] = {worth[0], worth[1], worth[2], worth[3]};
+        kept = 0;
+        for (int r = 0; r < p.top_groups; ++r) {           // the largest; of equal sums the lowest group
             const float w = token_maxf<LT>(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])));
-            const bool here = r > 0 && w > -INFINITY && !(prev - w > 0x1p-19f * fmaxf(1.f, fabsf(prev)));
-            if (r == p.top_groups - 1) near_in = here;
-            if (r == p.top_groups) near = here;
-            if (r == p.top_groups + 1) {
-                near_out = here;
-                break;
-            }
-            prev = w;
-            // which group it is; of equal sums the lowest
             uint32_t at = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (best[i] == w && l + 16 * i < p.n_groups && !((kept >> (l + 16 * i)) & 1)) at = max(at, (uint32_t)(64 - (l + 16 * i)));
             at = token_max<LT>(at);
-            const int g = 64 - (int)at;
-            if (r < p.top_groups) {
-                if (at != 0) kept |= 1ull << g;
-                last_in = g;
-            } else {
-                first_out = g;
-            }
+            if (at != 0) kept |= 1ull << (64 - (int)at);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (l + 16 * i == g) best[i] = -INFINITY;
+                if (l + 16 * i == 64 - (int)at) best[i] = -INFINITY;
         }
+        // what those that stay are worth at least, the others at most
+        float low = INFINITY, high = -INFINITY;
+        auto stays_in = [&](int i) { return (kept >> (l + 16 * i)) & 1; };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (l + 16 * i >= p.n_groups) continue;
+            if (stays_in(i)) low = fminf(low, worth[i] - off[i]);
+            else if (worth[i] > -INFINITY) high = fmaxf(high, worth[i] + off[i]);
+        }
+        low = -token_maxf<LT>(-low);
+        high = token_maxf<LT>(high);
+        const bool near = high > -INFINITY && !(low > high);
         if (__ballot(near)) {
-            // those two groups alone in float64, unless their scores need the whole row's sum
-            again |= near && (near_in || near_out || (softmax && p.bias));
-            double worth[2];
+            // which of either side could belong to the other
+            float both = 0.f;
+            uint32_t in = 0, out = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (l + 16 * i >= p.n_groups || worth[i] == -INFINITY) continue;
+                if (stays_in(i)) {
+                    if (!(worth[i] - off[i] > high)) { both += 1.f; in = (uint32_t)(l + 16 * i); }
+                } else if (!(worth[i] + off[i] < low)) {
+                    both += 64.f;
+                    out = (uint32_t)(l + 16 * i);
+                }
+            }
+            both = token_sum<LT>(both);
+            const int last_in = (int)token_max<LT>(in), first_out = (int)token_max<LT>(out);
+            // one of each: those two groups alone in float64, unless their scores need the whole row's sum
+            again |= near && (both != 65.f || (softmax && p.bias));
+            double sums[2];
 #pragma unroll 1
             for (int side = 0; side < 2; ++side) {
                 double k1 = -INFINITY, k2 = -INFINITY;
@@ -470,9 +491,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
                         merge2(k1, k2, k, -INFINITY);
                     }
                 row_best2(k1, k2);
-                worth[side] = worth_of(k1, k2);
+                sums[side] = worth_of(k1, k2);
             }
-            if (near && (worth[1] > worth[0] || (worth[1] == worth[0] && first_out < last_in)))
+            if (near && both == 65.f && (sums[1] > sums[0] || (sums[1] == sums[0] && first_out < last_in)))
                 kept ^= 1ull << last_in | 1ull << first_out;
         }
     }

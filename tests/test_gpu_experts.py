@@ -294,6 +294,67 @@ def test_route_bias_infinite_and_nan():
         assert (experts[:, 0] == 3).all() and not ((experts == 5) | (experts == 7)).any()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("power", [8, 16, 20, 30])
+def test_route_groups_whose_keys_cancel(score, power):
+    """Large biases of both signs in a group: its sum is small, the rounding of its float32 keys is not."""
+    for E, groups, top in ((4, 2, 1), (8, 4, 2), (64, 8, 3), (160, 40, 7)):
+        T, per = 600, E // groups
+        x = torch.randn(T, E, device="cuda", generator=_gen(61 + E))
+        bias = torch.full((E,), -2.0 ** power, device="cuda")
+        bias[::per] = 2.0 ** power                              # one forced, the others banned
+        bias[per * (groups - 1):] = 0.25                         # but for one group, whose sum is like theirs
+        for b in (bias, bias.where(torch.arange(E, device="cuda") >= E // 2, torch.zeros_like(bias))):
+            kw = dict(score=score, groups=groups, top_groups=top)
+            experts, weights = X().route(x, 2, bias=b, **kw)
+            e_ref, w_ref = orc.route(_np(x), 2, _np(b), **kw)
+            got = experts.cpu().numpy()
+            # at 2^power float64's own step is 2^(power - 52): sums nearer than 4 of them fall by their rounding
+            key = orc.scores(_np(x), score)[0] + _np(b)
+            worth = np.sort(key.reshape(T, groups, per), axis=2)[:, :, -2:].sum(axis=2)
+            border = np.sort(worth, axis=1)[:, ::-1]
+            sure = border[:, top - 1] - border[:, top] > 2.0 ** (power - 50)
+            assert sure.mean() > 0.9 or power == 30
+            assert np.array_equal(got[sure], e_ref[sure])
+            w, w_ref = _np(weights)[sure], w_ref[sure]
+            assert (np.abs(w - w_ref) <= 256 * U * np.abs(w_ref) + 1e-32).all()
+
+
+def test_route_groups_at_the_softmax_sums_rounding():
+    """A row whose float32 exponentials are lost one by one as they are added to the largest: the sum is 2.08e-6 short,
+    and a group whose keys are biases lies in between."""
+    E, ulp = 512, 2.0 ** -23
+    x = np.zeros(E)
+    for e in range(1, E):
+        lane = e % 64 // 4                                      # of 16; lane 0 has the largest
+        beside = 1 if lane < 2 else 2 if lane < 4 else 4 if lane < 8 else 8
+        x[e] = np.log((0.4999 if lane == 0 else 0.49 / (32 * beside)) * ulp)
+    x = torch.tensor(x, dtype=torch.float32, device="cuda").repeat(5, 1)
+    kept = set()
+    for j in range(50, 80):
+        bias = torch.zeros(E, device="cuda")
+        bias[64], bias[65] = 0.5, 0.5 - j * 2.0 ** -25
+        kw = dict(score="softmax", groups=8, top_groups=1)
+        experts, weights = X().route(x, 1, bias=bias, **kw)
+        want = orc.route(_np(x), 1, _np(bias), **kw)
+        _check_route(x, experts, weights, want, 1)
+        kept.add(int(want[0][0, 0]) // 64)
+    assert kept == {0, 1}                                       # both sides of the border
+
+
+def test_route_infinite_biases_in_groups():
+    """A forced expert makes its group's sum infinite; groups of equal infinite sums stay by lowest index."""
+    x = torch.randn(300, 64, device="cuda", generator=_gen(71))
+    bias = torch.zeros(64, device="cuda")
+    bias[[3, 40, 41, 50]] = float("inf")
+    bias[48], bias[56:60] = -float("inf"), torch.finfo(torch.float32).max
+    for score in ("softmax", "sigmoid"):
+        for top in (1, 2, 3, 4, 5):
+            kw = dict(score=score, groups=8, top_groups=top)
+            experts, weights = X().route(x, 6, bias=bias, **kw)
+            _check_route(x, experts, weights, orc.route(_np(x), 6, _np(bias), **kw), 6)
+
+
 def test_route_strided_and_large_rows():
     base = torch.randn(70, 200, device="cuda", generator=_gen(3))
     x = base[:, 3:100]                                        # neither aligned rows nor contiguous
