@@ -431,7 +431,7 @@ typedef struct muon_route_config {
 
 /* Routing.  Scores s of a token's logits x: softmax over its experts, or sigmoid.  An expert
  * whose logit is -inf or NaN is out for that token (score 0, never chosen, left out of the
- * softmax); +inf counts as the largest finite value.  The choice goes by the key s + bias (bias:
+ * softmax); +inf counts as the largest finite float32.  The choice goes by the key s + bias (bias:
  * n_experts floats; an expert with a NaN key is out), or by x itself where bias is NULL.
  * With n_groups > 1 only the experts of the top_groups groups stay whose two largest s + bias
  * add up to the most (a group without an expert comes last).  experts (tokens x top_k) gets

@@ -498,7 +498,8 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
         }
     }
     // Each lane's 4 largest keys, ordered, the place in the lane in the last 6 bits (larger: lower expert).  bfloat16
-    // logits are decided by 16 bits: there the expert itself fits behind them, and equal logits need no second look.
+    // logits are decided by 16 bits: there the expert itself fits behind them, and equal logits need no second look.  (One
+    // up: +inf, as float32's largest value, is above bfloat16's largest; the others' lower bits are all zeros or, negative, ones.)
     const bool whole = sizeof(T) == 2 && !p.bias;
     uint32_t bits[C][4];
     const uint32_t inv = GROUPS ? (1u << 20) / (uint32_t)per + 1 : 0;   // e / per is e * inv >> 20 for e * per < 2^20
@@ -511,7 +512,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
             const float k = !p.bias ? x[c][v] : GROUPS ? keys[66 * c + 4 * l + (l >> 3) + v] : key[c][v];
             const bool in = stays && x[c][v] > -INFINITY && k > -INFINITY;
             const uint32_t o = ordered(k);
-            const uint32_t kv = whole ? (o & 0xffff0000u) | (uint32_t)(1023 - expert(c, v)) : (o & ~63u) | (uint32_t)(63 - (4 * c + v));
+            const uint32_t kv = whole ? ((o + 1u) & 0xffff0000u) | (uint32_t)(1023 - expert(c, v)) : (o & ~63u) | (uint32_t)(63 - (4 * c + v));
             bits[c][v] = in ? kv : 0u;
         }
     }

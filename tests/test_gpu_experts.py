@@ -355,6 +355,25 @@ def test_route_infinite_biases_in_groups():
             _check_route(x, experts, weights, orc.route(_np(x), 6, _np(bias), **kw), 6)
 
 
+@pytest.mark.parametrize("T", [6, 4200])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_route_infinity_is_float32s_largest_value(T, dtype):
+    """+inf comes before bfloat16's largest value and is equal to float32's, whichever kernel takes the token."""
+    x = torch.randn(T, 64, device="cuda", generator=_gen(81))
+    x[:, [5, 9]] = torch.finfo(dtype).max
+    x[:, [8, 11, 60]] = float("inf")
+    x[::2, 1] = torch.finfo(dtype).min
+    x = x.to(dtype)
+    for k in (1, 4, 20):                                       # 20: the float64 kernel
+        for kw in (dict(score="softmax", renormalize=False), dict(score="softmax"), dict(score="sigmoid"),
+                   dict(score="softmax", groups=8, top_groups=3)):
+            experts, weights = X().route(x, k, **kw)
+            for rows in (slice(0, 6), slice(T - 6, T)):
+                _check_route(x[rows], experts[rows], weights[rows], orc.route(_np(x[rows]), k, **kw), k)
+        first = X().route(x, 1)[0]
+        assert (first == (8 if dtype == torch.bfloat16 else 5)).all()
+
+
 def test_route_strided_and_large_rows():
     base = torch.randn(70, 200, device="cuda", generator=_gen(3))
     x = base[:, 3:100]                                        # neither aligned rows nor contiguous
