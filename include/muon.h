@@ -438,7 +438,7 @@ typedef struct muon_route_config {
  * the experts of the top_k largest keys in falling order, equal keys (and equal groups) by
  * lowest index, and -1 where a token has no further expert; weights (tokens x top_k,
  * float32) gets scale * s without the bias, divided by the sum of the chosen s with
- * renormalize (0 where that sum underflows in float64), and 0 beside -1.  The choice is that of
+ * renormalize (the ratio itself, also where the scores underflow), and 0 beside -1.  The choice is that of
  * scores and keys in float64, so that near ties fall as the formulas say; the weights are
  * formed in float32.
  * Errors: INVALID_ARG (NULL, enum, n_groups not a divisor of n_experts or above 64,

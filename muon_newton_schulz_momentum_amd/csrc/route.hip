@@ -30,6 +30,10 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = dev::f3
 // -inf for an expert that is out (-inf, NaN), the largest finite value for +inf.
 __device__ __forceinline__ float clean_logit(float x) { return x > -INFINITY ? fminf(x, F32_MAX) : -INFINITY; }
 
+// Renormalised weights are ratios, which exist where the scores underflow: the softmax's are formed from the largest chosen
+// logit on, and so are the sigmoid's where all chosen logits are below this (there 1 / (1 + exp(-x)) is exp(x) in float64).
+constexpr float TINY_SIGMOID = -700.f;
+
 __device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -195,11 +199,15 @@ __device__ __forceinline__ void route_exact(const RouteArgs& p, int64_t t, float
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // other lanes' places of x
     __builtin_amdgcn_wave_barrier();
-    const double my_score = my_expert >= 0 ? raw(x[my_expert]) / z : 0.0;
-    double w = my_score;
+    const float my_x = my_expert >= 0 ? x[my_expert] : -INFINITY;
+    double w;
     if (p.renormalize) {
-        const double total = dev::wave_sum(my_score);
-        w = total > 0.0 ? my_score / total : 0.0;
+        const float high = wave_max(my_x);
+        const double s = my_expert < 0 ? 0.0 : softmax || high < TINY_SIGMOID ? exp((double)my_x - (double)high) : raw(my_x);
+        const double total = dev::wave_sum(s);
+        w = total > 0.0 ? s / total : 0.0;
+    } else {
+        w = my_expert >= 0 ? raw(my_x) / z : 0.0;
     }
     if (lane < p.top_k) {
         p.experts[t * p.top_k + lane] = my_expert;
@@ -679,8 +687,10 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
         for (int v = 0; v < 4; ++v) out[c][v] = 0.f;
     float dx;                                              // what slot l adds to its expert
     if (p.score == MUON_SCORE_SIGMOID) {
-        const double ex = exp(-fabs((double)xj));          // s and 1 - s without cancellation
-        const double big = 1.0 / (1.0 + ex), small = ex * big;
+        const float high = token_maxf<16>(xj);
+        const bool tiny = p.renormalize && high < TINY_SIGMOID;
+        const double ex = exp(tiny ? (double)xj - (double)high : -fabs((double)xj));   // s and 1 - s without cancellation
+        const double big = tiny ? 1.0 : 1.0 / (1.0 + ex), small = ex * big;
         const double s = e < 0 ? 0.0 : xj >= 0.f ? big : small, rest = xj >= 0.f ? small : big;
         if (p.renormalize) {
             const double total = token_sum16(s);
@@ -780,7 +790,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
     for (int i = 0; i < V; ++i) out[i] = 0.f;
     float dx = 0.f;                                        // lane j: what slot j adds to its expert
     if (p.score == MUON_SCORE_SIGMOID) {
-        const double s = e >= 0 ? sigmoid64((double)xj) : 0.0;
+        const float high = wave_max(xj);
+        const bool tiny = p.renormalize && high < TINY_SIGMOID;
+        const double s = e < 0 ? 0.0 : tiny ? exp((double)xj - (double)high) : sigmoid64((double)xj);
         const double rest = e >= 0 ? 1.0 / (1.0 + exp((double)xj)) : 0.0;   // 1 - s
         if (p.renormalize) {
             const double total = dev::wave_sum(s);

@@ -31,6 +31,14 @@ def scores(x, score):
     return s, there
 
 
+def ratios(x, score):
+    """Scores of the chosen logits x over their sum, from the scores' logarithms: also where the scores underflow."""
+    x = np.asarray(x, dtype=np.float64)
+    log_s = -np.logaddexp(0.0, -x) if score == "sigmoid" else x
+    e = np.exp(log_s - log_s.max())
+    return e / e.sum()
+
+
 def route(x, top_k, bias=None, score="softmax", groups=1, top_groups=1, renormalize=True, scale=1.0):
     s, there = scores(x, score)
     x = np.minimum(np.asarray(x, dtype=np.float64), F32_MAX)
@@ -52,8 +60,7 @@ def route(x, top_k, bias=None, score="softmax", groups=1, top_groups=1, renormal
         experts[t, :len(order)] = order
         w = s[t, order]
         if renormalize and len(order):
-            total = w.sum()
-            w = w / total if total > 0 else np.zeros_like(w)
+            w = ratios(x[t, order], score)
         weights[t, :len(order)] = w * scale
     return experts, weights
 
@@ -68,11 +75,13 @@ def route_backward(x, experts, grad, score="softmax", renormalize=True, scale=1.
         g = np.asarray([float(grad[t, j]) * scale for j in slots])
         if not chosen:
             continue
-        sel = s[t, chosen]
-        ds = g.copy()
         if renormalize:
-            total = sel.sum()
-            ds = (g - (g * sel).sum() / total) / total if total > 0 else np.zeros_like(g)
+            # with w = s / sum s: ds = (g - sum g w) / sum s, and the softmax's inner sum is zero
+            w = ratios([min(float(x[t, e]), F32_MAX) for e in chosen], score)
+            for e, d in zip(chosen, w * (g - (g * w).sum())):
+                dx[t, e] += d * (1.0 - s[t, e] if score == "sigmoid" else 1.0)
+            continue
+        ds = g
         full = np.zeros(E)
         for e, d in zip(chosen, ds):
             full[e] += d

@@ -374,6 +374,35 @@ def test_route_infinity_is_float32s_largest_value(T, dtype):
         assert (first == (8 if dtype == torch.bfloat16 else 5)).all()
 
 
+@pytest.mark.parametrize("k", [2, 5, 20])
+@pytest.mark.parametrize("T", [3, 4099])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_ratios_of_scores_that_underflow(k, T, score):
+    """A bias chooses experts far below the row's largest logit, or all logits are far below zero: renormalised weights are
+    the ratios that they are of larger scores, and the gradient is that of those weights."""
+    x = torch.randn(T, 40, device="cuda", generator=_gen(91))
+    x[:, 20:] += 800.0 if score == "softmax" else 0.0
+    x[1::3] -= 700.0                                            # about where exp(-x) overflows
+    x[2::3] -= 20000.0
+    bias = torch.zeros(40, device="cuda")
+    bias[:20] = 3.0
+    at = np.r_[0:3, T - 3:T]
+    for b in (bias, None):
+        kw = dict(score=score, scale=1.5)
+        experts, weights = X().route(x, k, bias=b, **kw)
+        e_ref, w_ref = orc.route(_np(x[at]), k, None if b is None else _np(b), **kw)
+        assert (np.abs(w_ref.sum(axis=1) - 1.5) < 1e-12).all()
+        _check_route(x[at], experts[at], weights[at], (e_ref, w_ref), k)
+        grad = torch.randn(T, k, device="cuda", generator=_gen(92))
+        dx = _np(X().route_backward(x, experts, grad, **kw)[at])
+        ref = orc.route_backward(_np(x[at]), e_ref, _np(grad[at]), **kw)
+        size = np.zeros_like(ref)                                # the weights (of scale 1) bound the terms
+        np.put_along_axis(size, e_ref, w_ref / 1.5, axis=1)
+        gmax = 1.5 * np.abs(_np(grad[at])).max(axis=1, keepdims=True)
+        assert (np.abs(dx - ref) <= 8 * U * size * gmax + U * (1 + 1e-3) * np.abs(ref) + 1e-40).all()
+        assert np.abs(ref).max(axis=1).min() > 1e-4
+
+
 def test_route_strided_and_large_rows():
     base = torch.randn(70, 200, device="cuda", generator=_gen(3))
     x = base[:, 3:100]                                        # neither aligned rows nor contiguous
