@@ -408,7 +408,8 @@ MUON_API muon_status muon_step_noalloc(const muon_plan* plan, const muon_step_co
  * their arguments, they never allocate or synchronise, and they can be captured.  Calls on
  * different streams may overlap unless they share a written buffer or a workspace.
  * Device pointers are 16-byte aligned; where a size is 0 nothing is launched and the
- * pointers are not looked at.  Outputs must not overlap inputs unless stated. */
+ * pointers are not looked at.  Outputs must not overlap inputs or each other unless stated
+ * (a buffer reaches from its first byte to its last, gaps between its rows included). */
 
 #define MUON_MAX_EXPERTS 1024
 #define MUON_MAX_TOP_K 64
@@ -520,7 +521,7 @@ typedef struct muon_fp8_quantize_config {
  * or 57344 * 2^e (e5m2), -127 for a block of zeros; a code is the value * 2^-e rounded to
  * nearest even.  An infinity or NaN becomes a NaN code and has no part in its block's scale.
  * Errors: INVALID_ARG (NULL, enum, no output, one of a codes / scales pair NULL, gather or
- * limit with batch > 1 or limit with square, per < 1, an output that overlaps src),
+ * limit with batch > 1 or limit with square, per < 1, an output that overlaps an input or another),
  * SHAPE (sizes, strides), ALIGNMENT, HIP. */
 MUON_API muon_status muon_fp8_quantize(const muon_fp8_quantize_config* config, void* stream);
 
@@ -566,7 +567,7 @@ typedef struct muon_fp8_product_config {
  * out the codes go through the bfloat16 instruction, at half its rate, and the sums
  * are full float32 sums (values below 2^-126 count as zero).
  * Errors: INVALID_ARG (NULL, enum, groups, accumulate into bfloat16, out overlapping an
- * operand), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
+ * operand or offsets), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
 MUON_API muon_status muon_fp8_product(const muon_fp8_product_config* config, void* stream);
 
 /* ---- per-kernel timing (HIP events on the launching stream) --------------------------- */

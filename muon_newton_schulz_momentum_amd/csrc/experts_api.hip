@@ -30,9 +30,21 @@ bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-bool overlap(const void* a, double na, const void* b, double nb) {
-    const double x = (double)(uintptr_t)a, y = (double)(uintptr_t)b;
-    return a && b && na > 0 && nb > 0 && x < y + nb && y < x + na;
+// The bytes of a buffer from the first that a call may touch to the last.  Rows and matrices lie a stride apart and the last
+// of them ends with its own columns: what follows belongs to someone else.
+struct Extent {
+    const void* p;
+    double bytes;                         // (sizes are products that may pass 64 bits)
+};
+Extent extent(const void* p, double bytes) { return {p, bytes}; }
+// `count` matrices of `rows` x `cols` elements
+Extent extent(const void* p, int64_t count, double stride, int64_t rows, int64_t ld, int64_t cols, int64_t size = 1) {
+    if (count < 1 || rows < 1) return {p, 0};
+    return {p, ((double)(count - 1) * stride + (double)(rows - 1) * (double)ld + (double)cols) * (double)size};
+}
+bool overlap(const Extent& a, const Extent& b) {
+    const double x = (double)(uintptr_t)a.p, y = (double)(uintptr_t)b.p;
+    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
 }
 
 bool is_dtype(int32_t d) { return d == MUON_DTYPE_F32 || d == MUON_DTYPE_BF16; }
@@ -98,8 +110,12 @@ muon_status check_operand(const muon_fp8_operand& o, int64_t rows, int64_t k, in
     return MUON_OK;
 }
 
-double operand_bytes(const muon_fp8_operand& o, int64_t rows, int64_t groups) {
-    return (double)rows * (double)o.ld + (double)(groups - 1) * (double)o.stride;
+Extent codes_of(const muon_fp8_operand& o, int64_t rows, int64_t k, int64_t groups) {
+    return extent(o.codes, groups, (double)o.stride, rows, o.ld, round_up(k, 128));
+}
+Extent scales_of(const muon_fp8_operand& o, int64_t rows, int64_t k, int64_t groups) {
+    return extent(o.scales, groups, (double)o.stride_scales, o.square ? ceil_div(rows, 128) : rows, o.ld_scales,
+                  round_up(ceil_div(k, 128), 4));
 }
 
 }  // namespace
@@ -274,12 +290,20 @@ muon_status muon_fp8_quantize(const muon_fp8_quantize_config* c, void* stream) t
     a.sp = round_up(a.tiles_c, 4);
     a.kp_t = round_up(c->rows, 128);
     a.sp_t = round_up(a.tiles_r, 4);
-    const double src_bytes = ((double)(c->batch - 1) * (double)c->batch_stride + (double)src_rows * (double)c->ld) *
-                             (c->src_dtype == MUON_DTYPE_F32 ? 4.0 : 2.0);
+    const Extent in[] = {extent(c->src, c->batch, (double)c->batch_stride, src_rows, c->ld, c->cols,
+                                c->src_dtype == MUON_DTYPE_F32 ? 4 : 2),
+                         extent(c->gather, 4.0 * (double)c->rows), extent(c->limit, 4.0)};
     const double n = (double)c->batch;
-    if (overlap(c->codes, n * (double)c->rows * (double)a.kp, c->src, src_bytes) ||
-        overlap(c->codes_t, n * (double)c->cols * (double)a.kp_t, c->src, src_bytes))
-        return fail(MUON_ERR_INVALID_ARG, who, "an output overlaps src");
+    const Extent out[] = {extent(c->codes, n * (double)c->rows * (double)a.kp),
+                          extent(c->scales, n * (double)(c->square ? a.tiles_r : c->rows) * (double)a.sp),
+                          extent(c->codes_t, n * (double)c->cols * (double)a.kp_t),
+                          extent(c->scales_t, n * (double)(c->square ? a.tiles_c : c->cols) * (double)a.sp_t)};
+    for (int i = 0; i < 4; ++i) {
+        for (const Extent& e : in)
+            if (overlap(out[i], e)) return fail(MUON_ERR_INVALID_ARG, who, "an output overlaps src, gather or limit");
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return fail(MUON_ERR_INVALID_ARG, who, "two outputs overlap");
+    }
     a.src = c->src;
     a.gather = c->gather;
     a.limit = c->limit;
@@ -331,11 +355,6 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
         if (st != MUON_OK) return st;
     }
     const int64_t size = c->out_dtype == MUON_DTYPE_F32 ? 4 : 2;
-    const double out_bytes =
-        ((double)(depth ? c->groups - 1 : 0) * (double)c->out_stride + (double)c->m * (double)c->ld_out) * (double)size;
-    if (c->k > 0 && (overlap(c->out, out_bytes, c->a.codes, operand_bytes(c->a, c->m, 1)) ||
-                     overlap(c->out, out_bytes, c->b.codes, operand_bytes(c->b, c->n, rows ? c->groups : 1))))
-        return fail(MUON_ERR_INVALID_ARG, who, "out overlaps an operand");
     ProductArgs a{};
     a.a = static_cast<const uint8_t*>(c->a.codes);
     a.as = static_cast<const uint8_t*>(c->a.scales);
@@ -360,9 +379,14 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
     a.mode = c->mode;
     a.accumulate = c->accumulate;
     a.vec = c->ld_out * size % 16 == 0 && a.out_stride * size % 16 == 0;
-    const hipError_t e = launch_product(a, c->a.format, c->out_dtype, static_cast<hipStream_t>(stream));
-    if (e == hipErrorInvalidConfiguration) return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
-    return launched(e, who);
+    if (!product_fits(a)) return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
+    const Extent out = extent(c->out, depth ? c->groups : 1, (double)c->out_stride, c->m, c->ld_out, c->n, size);
+    const int64_t b_groups = rows ? c->groups : 1;
+    if (overlap(out, extent(c->offsets, 4.0 * (double)(c->groups + 1))) ||
+        (c->k > 0 && (overlap(out, codes_of(c->a, c->m, c->k, 1)) || overlap(out, scales_of(c->a, c->m, c->k, 1)) ||
+                      overlap(out, codes_of(c->b, c->n, c->k, b_groups)) || overlap(out, scales_of(c->b, c->n, c->k, b_groups)))))
+        return fail(MUON_ERR_INVALID_ARG, who, "out overlaps an operand or offsets");
+    return launched(launch_product(a, c->a.format, c->out_dtype, static_cast<hipStream_t>(stream)), who);
 } catch (...) {
     return MUON_ERR_INVALID_ARG;
 }

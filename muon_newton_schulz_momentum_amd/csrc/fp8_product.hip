@@ -714,7 +714,6 @@ template <int AFMT, class OUT>
 hipError_t product_as(ProductArgs a, hipStream_t s) {
     ProductArgs few = a, thin = a;
     const int64_t n_big = count_tiles(a, TILE, TILE), n_few = count_tiles(few, FEW_ROWS, 64), n_thin = count_tiles(thin, FEW_ROWS, 16);
-    if (n_big < 0) return hipErrorInvalidConfiguration;
     if (n_big == 0) return hipSuccess;
     // What each would take, in us, from what they measured: big tiles by the round of 256 (256 x 4096 x 4096: 38 us in
     // bfloat16, 76 in float32), the others by the depth of a wave where there are few tiles and by the blocks of all
@@ -739,6 +738,8 @@ hipError_t product_as(ProductArgs a, hipStream_t s) {
 }
 
 }  // namespace
+
+bool product_fits(ProductArgs a) { return count_tiles(a, TILE, TILE) >= 0; }
 
 hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, hipStream_t s) {
     const bool f32 = out_dtype == MUON_DTYPE_F32;

@@ -292,3 +292,33 @@ def test_route_launches_stay_below_2_32_threads():
     assert -(-c.tokens // 4) * 256 < 1 << 32
     assert L.muon_route(C.byref(c), A + 4, None, B, S, None) == L.MUON_ERR_ALIGNMENT
     assert L.muon_route_backward(C.byref(c), A + 4, B, S, O, 8, None) == L.MUON_ERR_ALIGNMENT
+
+
+# ---- buffers that overlap -----------------------------------------------------------------------
+
+# 4 x 200 float32 in (3200 bytes), codes 4 x 256, scales 4 x 4, transposed codes 200 x 128, scales 200 x 4
+@pytest.mark.parametrize("kw", [
+    dict(codes=A + 3184), dict(codes=A - 1008), dict(scales=A + 3184), dict(scales=A), dict(codes_t=A + 3184), dict(scales_t=A - 784),
+    dict(scales=B + 1008), dict(codes_t=B + 1008), dict(codes_t=B - 25584), dict(scales_t=B - 784), dict(codes_t=S), dict(scales_t=S),
+    dict(scales_t=T + 25584), dict(codes_t=B, scales_t=S),
+    dict(gather=W, src_rows=4, codes=W), dict(gather=W, src_rows=4, scales=W), dict(gather=W, src_rows=4, scales_t=W - 784),
+    dict(limit=B + 1020), dict(limit=S + 12), dict(limit=O + 796),
+    dict(square=1, codes=None, scales=None, scales_t=A + 3184), dict(square=1, scales=T + 25584, scales_t=S),
+    dict(batch=3, batch_stride=1000, codes=A + 4 * 2784), dict(batch=3, batch_stride=1000, scales=A + 4 * 2784),
+])
+def test_quantize_refuses_every_overlap(kw):
+    c = _quant(**kw)
+    assert L.muon_fp8_quantize(C.byref(c), None) == L.MUON_ERR_INVALID_ARG
+    assert b"overlap" in L.muon_last_error()
+
+
+# a 8 x 256 codes and 8 x 4 scales, b (of 3 groups) 200 x 256 and 200 x 4, out 8 x 200 float32
+@pytest.mark.parametrize("mode,kw", [
+    (0, dict(out=A + 2032)), (0, dict(out=A - 6384)), (0, dict(out=S + 16)), (0, dict(out=S - 6384)), (0, dict(out=B + 51184)),
+    (0, dict(out=T + 784)), (1, dict(out=T + 2384)), (1, dict(out=B + 153584)), (1, dict(out=W)), (1, dict(out=W - 6384)),
+    (2, dict(out=W)), (2, dict(out=T + 784)), (2, dict(out=S - 3 * 6400 + 16)), (0, dict(out=T - 6384, b__square=1)),
+])
+def test_product_refuses_every_overlap(mode, kw):
+    c = _product(mode, **kw)
+    assert L.muon_fp8_product(C.byref(c), None) == L.MUON_ERR_INVALID_ARG
+    assert b"overlap" in L.muon_last_error()

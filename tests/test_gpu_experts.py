@@ -897,6 +897,49 @@ def test_product_nan_stays_in_its_row():
     assert bad.nonzero().flatten().tolist() == [3, 4] and torch.isfinite(out[~bad]).all()
 
 
+def _carve(*sizes):
+    """Tensors directly behind one another, in one allocation: of (shape, dtype)."""
+    bytes_of = [int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size() for shape, dtype in sizes]
+    assert all(b % 16 == 0 for b in bytes_of[:-1])             # every one begins on a 16-byte boundary
+    block, at, out = torch.empty(sum(bytes_of), dtype=torch.uint8, device="cuda"), 0, []
+    for (shape, dtype), b in zip(sizes, bytes_of):
+        out.append(block[at:at + b].view(dtype).view(shape))
+        at += b
+    return out
+
+
+def test_column_slices_beside_their_outputs():
+    """Columns away from the left end with their rows' last column: what follows is another buffer's, and may be written."""
+    R, K, n = 512, 2048, 256
+    e8 = torch.float8_e8m0fnu
+    base, codes, scales = _carve(((R, K), torch.bfloat16), ((R, K // 2), torch.float8_e4m3fn), ((R, 8), e8))
+    base.normal_(generator=_gen(1))
+    half = base[:, K // 2:]
+    q = X().Fp8(codes, scales, K // 2, False)
+    X().quantize(half, out=q)
+    _check_fp8(q, orc.quantize(_np(half), "e4m3", False), "e4m3")
+    stack, codes, scales = _carve(((3, 64, 512), torch.float32), ((3, 64, 256), torch.float8_e4m3fn), ((3, 1, 4), e8))
+    stack.normal_(generator=_gen(2))
+    q = X().Fp8(codes, scales, 256, True)
+    X().quantize(stack[:, :, 256:], block="square", out=q)
+    for i in range(3):
+        _check_fp8(X().Fp8(codes[i], scales[i], 256, True), orc.quantize(_np(stack[i, :, 256:]), "e4m3", True), "e4m3")
+    # both halves of a gate / up result, the operands right behind it
+    y, ac, asc, bc, bsc = _carve(((R, 2 * n), torch.bfloat16), ((R, 512), torch.float8_e4m3fn), ((R, 4), e8), ((n, 512), torch.float8_e4m3fn),
+                                 ((n // 128, 4), e8))
+    a, b = X().Fp8(ac, asc, 512, False), X().Fp8(bc, bsc, 512, True)
+    for q, src, block in ((a, _source(R, 512, torch.float32, 3), "row"), (b, _source(n, 512, torch.float32, 4), "square")):
+        X().quantize(src, block=block, out=q)
+    y.fill_(3.0)
+    X().product(a, b, out=y[:, n:])
+    assert (y[:, :n] == 3.0).all()
+    right = y[:, n:].clone()
+    X().product(a, b, out=y[:, :n])
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    _check_product(y[:, :n], va, vb, 512)
+    assert torch.equal(y[:, n:], right) and torch.equal(y[:, :n], right)
+
+
 def test_wrapper_refusals_on_the_gpu():
     a, b = _random_fp8(4, 128, "e4m3", False, 1), _random_fp8(8, 128, "e5m2", True, 2)
     with pytest.raises(ValueError, match="dtype"):
