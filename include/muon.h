@@ -409,7 +409,8 @@ MUON_API muon_status muon_step_noalloc(const muon_plan* plan, const muon_step_co
  * different streams may overlap unless they share a written buffer or a workspace.
  * Device pointers are 16-byte aligned; where a size is 0 nothing is launched and the
  * pointers are not looked at.  Outputs must not overlap inputs or each other unless stated
- * (a buffer reaches from its first byte to its last, gaps between its rows included). */
+ * (a buffer reaches from its first byte to its last; another one may lie in the gaps
+ * between its rows where the two have the same row stride). */
 
 #define MUON_MAX_EXPERTS 1024
 #define MUON_MAX_TOP_K 64
@@ -443,7 +444,7 @@ typedef struct muon_route_config {
  * scores and keys in float64, so that near ties fall as the formulas say; the weights are
  * formed in float32.
  * Errors: INVALID_ARG (NULL, enum, n_groups not a divisor of n_experts or above 64,
- * top_groups, non-finite scale), SHAPE (tokens < 0, n_experts, top_k, ld), ALIGNMENT, HIP. */
+ * top_groups, non-finite scale, overlap), SHAPE (tokens, n_experts, top_k, ld), ALIGNMENT, HIP. */
 MUON_API muon_status muon_route(const muon_route_config* config, const void* logits, const float* bias,
                                 int32_t* experts, float* weights, void* stream);
 
@@ -469,7 +470,7 @@ MUON_API muon_status muon_group_rows_capacity(int64_t n, int32_t n_experts, int3
  * (1, 2, 4, ..., 128; 128 is what MUON_PRODUCT_DEPTH needs).  rows[r] (muon_group_rows_capacity
  * entries, all written) is the index of the choice in row r, so rows[r] / top_k is its token,
  * or -1 in the padding and behind the last segment; position[i] (n) is the row of choice i, or
- * -1.  The same on every run.  Errors: INVALID_ARG, SHAPE (n, n_experts, or a capacity of
+ * -1.  The same on every run.  Errors: INVALID_ARG (NULL, align, overlap), SHAPE (n, n_experts, or a capacity of
  * 2^31 or more), ALIGNMENT, WORKSPACE_TOO_SMALL, HIP. */
 MUON_API muon_status muon_group_rows(const int32_t* experts, int64_t n, int32_t n_experts, int32_t align,
                                      int32_t* counts, int32_t* offsets, int32_t* rows, int32_t* position,
@@ -477,7 +478,7 @@ MUON_API muon_status muon_group_rows(const int32_t* experts, int64_t n, int32_t 
 
 /* The step of the selection bias, which no gradient reaches: bias_out[e] = bias[e] + rate *
  * sign(mean of counts - counts[e]) in float32, the sign exact.  bias_out may be bias.
- * Errors: INVALID_ARG (NULL, non-finite rate), SHAPE (n_experts), ALIGNMENT, HIP. */
+ * Errors: INVALID_ARG (NULL, non-finite rate, overlap), SHAPE (n_experts), ALIGNMENT, HIP. */
 MUON_API muon_status muon_balance_step(const float* bias, const int32_t* counts, int32_t n_experts, float rate,
                                        float* bias_out, void* stream);
 

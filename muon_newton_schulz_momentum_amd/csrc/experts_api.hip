@@ -35,16 +35,38 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 struct Extent {
     const void* p;
     double bytes;                         // (sizes are products that may pass 64 bits)
+    uint64_t step = 0, width = 0;         // rows of `width` bytes, `step` bytes apart; 0: no gaps
 };
 Extent extent(const void* p, double bytes) { return {p, bytes}; }
 // `count` matrices of `rows` x `cols` elements
-Extent extent(const void* p, int64_t count, double stride, int64_t rows, int64_t ld, int64_t cols, int64_t size = 1) {
+Extent extent(const void* p, int64_t count, int64_t stride, int64_t rows, int64_t ld, int64_t cols, int64_t size = 1) {
     if (count < 1 || rows < 1) return {p, 0};
-    return {p, ((double)(count - 1) * stride + (double)(rows - 1) * (double)ld + (double)cols) * (double)size};
+    Extent e{p, ((double)(count - 1) * (double)stride + (double)(rows - 1) * (double)ld + (double)cols) * (double)size};
+    if (ld > cols && (count == 1 || stride % ld == 0)) {
+        e.step = (uint64_t)(ld * size);
+        e.width = (uint64_t)(cols * size);
+    }
+    return e;
 }
 bool overlap(const Extent& a, const Extent& b) {
     const double x = (double)(uintptr_t)a.p, y = (double)(uintptr_t)b.p;
-    return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes;
+    if (!(a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + b.bytes && y < x + a.bytes)) return false;
+    if (a.step == 0 || a.step != b.step) return true;
+    // b's rows in the gaps between a's: two column ranges of one matrix
+    const uint64_t d = ((uintptr_t)b.p % a.step + a.step - (uintptr_t)a.p % a.step) % a.step;
+    return d < a.width || d + b.width > a.step;
+}
+
+// Whether an output overlaps an input or another output.
+template <int N, int M>
+bool collide(const Extent (&out)[N], const Extent (&in)[M]) {
+    for (int i = 0; i < N; ++i) {
+        for (const Extent& e : in)
+            if (overlap(out[i], e)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return true;
+    }
+    return false;
 }
 
 bool is_dtype(int32_t d) { return d == MUON_DTYPE_F32 || d == MUON_DTYPE_BF16; }
@@ -70,6 +92,11 @@ muon_status check_route(const muon_route_config* c, const char* who) {
     if (!std::isfinite(c->scale)) return fail(MUON_ERR_INVALID_ARG, who, "scale must be finite");
     return MUON_OK;
 }
+
+Extent logits_of(const muon_route_config& c, const void* p, int64_t ld) {
+    return extent(p, 1, 0, c.tokens, ld, c.n_experts, c.dtype == MUON_DTYPE_F32 ? 4 : 2);
+}
+Extent choices_of(const muon_route_config& c, const void* p) { return extent(p, 4.0 * (double)c.tokens * (double)c.top_k); }
 
 muon_status check_group(int64_t n, int32_t n_experts, int32_t align, const char* who) {
     if (n_experts < 1 || n_experts > MUON_MAX_EXPERTS)
@@ -111,10 +138,10 @@ muon_status check_operand(const muon_fp8_operand& o, int64_t rows, int64_t k, in
 }
 
 Extent codes_of(const muon_fp8_operand& o, int64_t rows, int64_t k, int64_t groups) {
-    return extent(o.codes, groups, (double)o.stride, rows, o.ld, round_up(k, 128));
+    return extent(o.codes, groups, o.stride, rows, o.ld, round_up(k, 128));
 }
 Extent scales_of(const muon_fp8_operand& o, int64_t rows, int64_t k, int64_t groups) {
-    return extent(o.scales, groups, (double)o.stride_scales, o.square ? ceil_div(rows, 128) : rows, o.ld_scales,
+    return extent(o.scales, groups, o.stride_scales, o.square ? ceil_div(rows, 128) : rows, o.ld_scales,
                   round_up(ceil_div(k, 128), 4));
 }
 
@@ -132,6 +159,9 @@ muon_status muon_route(const muon_route_config* c, const void* logits, const flo
     if (!logits || !experts || !weights) return fail(MUON_ERR_INVALID_ARG, who, "NULL buffer");
     if (misaligned(logits) || misaligned(bias) || misaligned(experts) || misaligned(weights))
         return fail(MUON_ERR_ALIGNMENT, who, "buffers must be 16-byte aligned");
+    const Extent out[] = {choices_of(*c, experts), choices_of(*c, weights)};
+    const Extent in[] = {logits_of(*c, logits, c->ld), extent(bias, 4.0 * (double)c->n_experts)};
+    if (collide(out, in)) return fail(MUON_ERR_INVALID_ARG, who, "an output overlaps an input or another output");
     RouteArgs a{};
     a.logits = logits;
     a.bias = bias;
@@ -163,6 +193,11 @@ muon_status muon_route_backward(const muon_route_config* c, const void* logits, 
     if (!logits || !experts || !grad_weights || !grad_logits) return fail(MUON_ERR_INVALID_ARG, who, "NULL buffer");
     if (misaligned(logits) || misaligned(experts) || misaligned(grad_weights) || misaligned(grad_logits))
         return fail(MUON_ERR_ALIGNMENT, who, "buffers must be 16-byte aligned");
+    const bool in_place = grad_logits == logits && ld_grad == c->ld;
+    const Extent out[] = {logits_of(*c, grad_logits, ld_grad)};
+    const Extent in[] = {choices_of(*c, experts), choices_of(*c, grad_weights), logits_of(*c, in_place ? nullptr : logits, c->ld)};
+    if (collide(out, in))
+        return fail(MUON_ERR_INVALID_ARG, who, "grad_logits overlaps an input (it may be logits, with the same ld)");
     RouteBackwardArgs a{};
     a.logits = logits;
     a.experts = experts;
@@ -226,6 +261,11 @@ muon_status muon_group_rows(const int32_t* experts, int64_t n, int32_t n_experts
     if (need > 0 && !workspace) return fail(MUON_ERR_INVALID_ARG, who, "workspace is NULL");
     if (workspace_bytes < need)
         return fail(MUON_ERR_WORKSPACE_TOO_SMALL, who, "workspace below muon_group_rows_workspace()");
+    const Extent out[] = {extent(counts, 4.0 * n_experts), extent(offsets, 4.0 * (n_experts + 1)),
+                          extent(rows, 4.0 * (double)a.capacity), extent(position, 4.0 * (double)n),
+                          extent(workspace, (double)need)};
+    const Extent in[] = {extent(experts, 4.0 * (double)n)};
+    if (collide(out, in)) return fail(MUON_ERR_INVALID_ARG, who, "an output overlaps an input or another output");
     a.experts = experts;
     a.counts = counts;
     a.offsets = offsets;
@@ -249,6 +289,9 @@ muon_status muon_balance_step(const float* bias, const int32_t* counts, int32_t 
     if (!std::isfinite(rate)) return fail(MUON_ERR_INVALID_ARG, who, "rate must be finite");
     if (misaligned(bias) || misaligned(counts) || misaligned(bias_out))
         return fail(MUON_ERR_ALIGNMENT, who, "buffers must be 16-byte aligned");
+    const Extent out[] = {extent(bias_out, 4.0 * n_experts)};
+    const Extent in[] = {extent(counts, 4.0 * n_experts), extent(bias_out == bias ? nullptr : bias, 4.0 * n_experts)};
+    if (collide(out, in)) return fail(MUON_ERR_INVALID_ARG, who, "bias_out overlaps an input (it may be bias)");
     return launched(launch_balance(bias, counts, n_experts, rate, bias_out, static_cast<hipStream_t>(stream)), who);
 } catch (...) {
     return MUON_ERR_INVALID_ARG;
@@ -290,7 +333,7 @@ muon_status muon_fp8_quantize(const muon_fp8_quantize_config* c, void* stream) t
     a.sp = round_up(a.tiles_c, 4);
     a.kp_t = round_up(c->rows, 128);
     a.sp_t = round_up(a.tiles_r, 4);
-    const Extent in[] = {extent(c->src, c->batch, (double)c->batch_stride, src_rows, c->ld, c->cols,
+    const Extent in[] = {extent(c->src, c->batch, c->batch_stride, src_rows, c->ld, c->cols,
                                 c->src_dtype == MUON_DTYPE_F32 ? 4 : 2),
                          extent(c->gather, 4.0 * (double)c->rows), extent(c->limit, 4.0)};
     const double n = (double)c->batch;
@@ -298,12 +341,7 @@ muon_status muon_fp8_quantize(const muon_fp8_quantize_config* c, void* stream) t
                           extent(c->scales, n * (double)(c->square ? a.tiles_r : c->rows) * (double)a.sp),
                           extent(c->codes_t, n * (double)c->cols * (double)a.kp_t),
                           extent(c->scales_t, n * (double)(c->square ? a.tiles_c : c->cols) * (double)a.sp_t)};
-    for (int i = 0; i < 4; ++i) {
-        for (const Extent& e : in)
-            if (overlap(out[i], e)) return fail(MUON_ERR_INVALID_ARG, who, "an output overlaps src, gather or limit");
-        for (int j = 0; j < i; ++j)
-            if (overlap(out[i], out[j])) return fail(MUON_ERR_INVALID_ARG, who, "two outputs overlap");
-    }
+    if (collide(out, in)) return fail(MUON_ERR_INVALID_ARG, who, "an output overlaps an input or another output");
     a.src = c->src;
     a.gather = c->gather;
     a.limit = c->limit;
@@ -380,7 +418,7 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
     a.accumulate = c->accumulate;
     a.vec = c->ld_out * size % 16 == 0 && a.out_stride * size % 16 == 0;
     if (!product_fits(a)) return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
-    const Extent out = extent(c->out, depth ? c->groups : 1, (double)c->out_stride, c->m, c->ld_out, c->n, size);
+    const Extent out = extent(c->out, depth ? c->groups : 1, c->out_stride, c->m, c->ld_out, c->n, size);
     const int64_t b_groups = rows ? c->groups : 1;
     if (overlap(out, extent(c->offsets, 4.0 * (double)(c->groups + 1))) ||
         (c->k > 0 && (overlap(out, codes_of(c->a, c->m, c->k, 1)) || overlap(out, scales_of(c->a, c->m, c->k, 1)) ||

@@ -322,3 +322,32 @@ def test_product_refuses_every_overlap(mode, kw):
     c = _product(mode, **kw)
     assert L.muon_fp8_product(C.byref(c), None) == L.MUON_ERR_INVALID_ARG
     assert b"overlap" in L.muon_last_error()
+
+
+# 4 tokens of 8 float32 logits (128 bytes), 2 choices each (32 bytes)
+def test_routing_refuses_every_overlap():
+    c = _route(ld=16)                                           # logits: 3 * 64 + 32 bytes
+    for bad in ((A, None, A + 208, S), (A, None, B, A - 16), (A, None, B, B + 16), (A, B, B + 16, S), (A, B, O, B - 16)):
+        assert L.muon_route(C.byref(c), *bad, None) == L.MUON_ERR_INVALID_ARG
+        assert b"overlap" in L.muon_last_error()
+    # logits, experts, grad_weights, grad_logits, ld_grad
+    for *bad, ld in ((A, B, S, A + 16, 16), (A, B, S, A, 8), (A, B, S, A - 208, 16), (A, B, S, B + 16, 8), (A, B, S, S - 112, 8),
+                     (A, B, S, A + 208, 8), (A, B, S, A + 48, 16), (A, B, S, A + 16, 16), (A, B, S, A - 48, 16)):
+        assert L.muon_route_backward(C.byref(c), *bad, ld, None) == L.MUON_ERR_INVALID_ARG
+        assert b"overlap" in L.muon_last_error()
+
+
+def test_grouping_refuses_every_overlap():
+    # 9000 choices of 5 experts: experts, counts, offsets, rows, position, workspace
+    rows, ws = C.c_int64(), C.c_uint64()
+    assert L.muon_group_rows_capacity(9000, 5, 16, C.byref(rows)) == L.MUON_OK
+    assert L.muon_group_rows_workspace(9000, 5, C.byref(ws)) == L.MUON_OK
+    last = lambda size: (size - 1) // 16 * 16                    # noqa: E731  the last 16-byte step inside
+    good = dict(experts=A, counts=B, offsets=S, rows=T, position=O, work=W)
+    for kw in (dict(position=A), dict(counts=A + last(36000)), dict(offsets=B + 16), dict(rows=A + last(36000)),
+               dict(position=T + last(4 * rows.value)), dict(work=A), dict(work=O + last(36000)), dict(offsets=W + last(ws.value))):
+        a = dict(good, **kw)
+        st = L.muon_group_rows(a["experts"], 9000, 5, 16, a["counts"], a["offsets"], a["rows"], a["position"], a["work"], ws.value, None)
+        assert st == L.MUON_ERR_INVALID_ARG and b"overlap" in L.muon_last_error()
+    for out in (B, A + 16, B - 16, B + 16):
+        assert L.muon_balance_step(A, B, 8, 0.1, out, None) == L.MUON_ERR_INVALID_ARG and b"overlap" in L.muon_last_error()

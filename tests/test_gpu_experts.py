@@ -940,6 +940,26 @@ def test_column_slices_beside_their_outputs():
     assert torch.equal(y[:, n:], right) and torch.equal(y[:, :n], right)
 
 
+def test_column_ranges_of_one_buffer():
+    """A result in the columns beside its input's: the rows of one lie in the gaps of the other's."""
+    both = torch.zeros(70, 128, device="cuda")
+    both[:, :64].normal_(generator=_gen(5))
+    x = both[:, :64].clone()
+    experts, _ = X().route(both[:, :64], 4)
+    grad = torch.randn(70, 4, device="cuda", generator=_gen(6))
+    X().route_backward(both[:, :64], experts, grad, out=both[:, 64:])
+    assert torch.equal(both[:, 64:], X().route_backward(x, experts, grad)) and torch.equal(both[:, :64], x)
+    codes = torch.zeros(40, 512, dtype=torch.uint8, device="cuda")
+    src = _source(40, 128, torch.float32, 7)
+    q = X().quantize(src)
+    codes[:, :128] = q.codes.view(torch.uint8)
+    a = X().Fp8(codes[:, :128].view(torch.float8_e4m3fn), q.scales, 128, False)
+    out = codes.view(torch.float32)[:, 64:104]                 # bytes 256 to 416 of rows of 512
+    X().product(a, q, out=out)
+    assert torch.equal(out, X().product(q, q, dtype=torch.float32))
+    assert torch.equal(codes[:, :128], q.codes.view(torch.uint8))
+
+
 def test_wrapper_refusals_on_the_gpu():
     a, b = _random_fp8(4, 128, "e4m3", False, 1), _random_fp8(8, 128, "e5m2", True, 2)
     with pytest.raises(ValueError, match="dtype"):
