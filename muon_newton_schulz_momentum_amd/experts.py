@@ -14,9 +14,14 @@ One layer's matrices in a training step, with the optimizer's `harness.Plan` at 
     product(dy_t, x_t, offsets=g.offsets, group="depth", out=G)      # the gradients that the plan reads
     bias = balance_step(bias, g.counts, rate)
 
-Every operator runs in libmuon's HIP kernels on the current stream of its tensors' device (or on
-`stream`); this module checks tensors, allocates outputs and marshals arguments.  Sizes that only the
-device knows (segments, the number of grouped rows) are never read back.
+Every operator runs in libmuon's HIP kernels on the current stream of its tensors' device; this module
+checks tensors, allocates outputs and marshals arguments.  Sizes that only the device knows (segments, the
+number of grouped rows) are never read back.
+
+With `stream` it runs there instead: that stream has to come after the work that makes the inputs (wait_stream), and
+whoever uses the outputs elsewhere waits for it.  Tensors passed in may be dropped after the call (their memory is
+kept until the stream is done with them); outputs made by the call belong to the stream, like all that is allocated
+under torch.cuda.stream.
 """
 from __future__ import annotations
 
@@ -44,14 +49,18 @@ _AS_IT_IS = contextlib.nullcontext()
 
 
 @contextlib.contextmanager
-def _switched(device: torch.device, stream: Optional[torch.cuda.Stream]):
+def _switched(device: torch.device, stream: Optional[torch.cuda.Stream], tensors):
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
+        if stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
 
 
-def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
-    """The device of t, and the stream if one is given, made current: outputs are then allocated for the
-    stream that the kernels run on."""
+def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream], *others: Optional[torch.Tensor]):
+    """The device of t, and the stream if one is given, made current: outputs are then allocated for the stream that the
+    kernels run on.  t and the others are kept from reuse until that stream is done with them."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
     if stream is None:
@@ -59,7 +68,7 @@ def _on(t: torch.Tensor, stream: Optional[torch.cuda.Stream]):
             return _AS_IT_IS
     elif stream.device != t.device:
         raise ValueError(f"stream is on {stream.device}, expected {t.device}")
-    return _switched(t.device, stream)
+    return _switched(t.device, stream, (t, *others))
 
 
 def _stream_ptr(t: torch.Tensor) -> int:
@@ -108,7 +117,7 @@ def route(logits: torch.Tensor, top_k: int, *, bias: Optional[torch.Tensor] = No
     token with fewer experts gets -1 and weight 0 in the remaining places.
     """
     k = _route_config(logits, top_k, score, groups, top_groups, renormalize, scale)
-    with _on(logits, stream):
+    with _on(logits, stream, bias):
         if bias is not None:
             _tensor("bias", bias, logits, torch.float32, (logits.shape[1],))
         size = (k.tokens, max(int(top_k), 0))
@@ -127,7 +136,7 @@ def route_backward(logits: torch.Tensor, experts: torch.Tensor, grad_weights: to
     if experts.dim() != 2:
         raise ValueError("experts must be route's (tokens, top_k)")
     k = _route_config(logits, experts.shape[1], score, 1, 1, renormalize, scale)
-    with _on(logits, stream):
+    with _on(logits, stream, experts, grad_weights, out):
         size = (k.tokens, k.top_k)
         _tensor("experts", experts, logits, torch.int32, size)
         _tensor("grad_weights", grad_weights, logits, torch.float32, size)
@@ -177,7 +186,7 @@ def balance_step(bias: torch.Tensor, counts: torch.Tensor, rate: float, *, out: 
                  stream=None) -> torch.Tensor:
     """The selection bias after one step: + rate where an expert had fewer choices than the mean, - rate where
     more.  `out` may be `bias`."""
-    with _on(bias, stream):
+    with _on(bias, stream, counts, out):
         if bias.dim() != 1:
             raise ValueError("bias must be (experts,)")
         _tensor("bias", bias, bias, torch.float32)
@@ -259,7 +268,8 @@ def quantize(src: torch.Tensor, *, block: str = "row", format: str = "e4m3", tra
     if rows is not None and stack is not None:
         raise ValueError("rows goes with one matrix")
     cols, n = src.shape[-1], src.shape[-2] if rows is None else rows.numel()
-    with _on(src, stream):
+    kept = [] if out is None else [t for q in (out if isinstance(out, (tuple, list)) else [out]) for t in (q.codes, q.scales)]
+    with _on(src, stream, rows, limit, *kept):
         if rows is not None:
             _tensor("rows", rows, src, torch.int32, (n,))
         if limit is not None:
@@ -331,7 +341,7 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     codes = a.codes
-    with _on(codes, stream):
+    with _on(codes, stream, a.scales, b.codes, b.scales, offsets, out):
         k = L.muon_fp8_product_config()
         k.mode, k.groups = _GROUPS[group], 1
         (m, _), (*stack, n, _) = _operand(k.a, "a", a, False), _operand(k.b, "b", b, group == "rows")

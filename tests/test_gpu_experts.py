@@ -1147,3 +1147,42 @@ def test_stream_argument():
     e2, w2 = X().route(x, 3)
     assert torch.equal(e, e2) and torch.equal(w, w2) and torch.equal(g.rows, X().group_rows(e2, 64).rows)
     assert torch.equal(y, X().product(q, q, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("name", ["route", "route_backward", "group_rows", "balance_step", "quantize", "product"])
+def test_tensors_dropped_behind_a_stream(name):
+    """A tensor that the caller drops after a call on another stream is not handed out again before that stream is done."""
+    x, s = X(), torch.cuda.Stream()
+    q = x.quantize(torch.randn(512, 4096, device="cuda", generator=_gen(1)))
+    logits = torch.randn(4096, 256, device="cuda", generator=_gen(2))
+    experts, weights = x.route(logits, 8)
+    off = torch.tensor([0, 128, 1024], dtype=torch.int32, device="cuda")
+    made = {
+        "route": (lambda a, b: x.route(a, 8, bias=b, stream=s), lambda: [logits.clone(), torch.randn(256, device="cuda", generator=_gen(3))]),
+        "route_backward": (lambda a, b, c: x.route_backward(a, b, c, stream=s), lambda: [logits.clone(), experts.clone(), weights.clone()]),
+        "group_rows": (lambda a: x.group_rows(a, 256, align=16, stream=s), lambda: [experts.clone()]),
+        "balance_step": (lambda a, b: x.balance_step(a, b, 0.5, stream=s),
+                         lambda: [torch.randn(1024, device="cuda", generator=_gen(4)), torch.arange(1024, dtype=torch.int32, device="cuda")]),
+        "quantize": (lambda a, b: x.quantize(a, rows=b, per=2, stream=s),
+                     lambda: [logits.clone(), torch.arange(8191, -1, -1, dtype=torch.int32, device="cuda")]),
+        "product": (lambda a, b, c, d, e: x.product(x.Fp8(a, b, 4096, False), x.Fp8(c, d, 4096, False), dtype=torch.float32, stream=s,
+                                                    offsets=e, group="depth"),
+                    lambda: [q.codes.clone(), q.scales.clone(), q.codes.clone(), q.scales.clone(), off.clone()]),
+    }
+    call, inputs = made[name]
+    flat = lambda r: [t for t in (vars(r).values() if isinstance(r, x.Groups) else r if isinstance(r, tuple) else    # noqa: E731
+                                  [r.codes, r.scales] if isinstance(r, x.Fp8) else [r])]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)                         # longer than the host takes for what follows
+    given = inputs()
+    sizes = [(t.shape, t.dtype) for t in given]
+    s.wait_stream(torch.cuda.current_stream())
+    got = call(*given)
+    del given
+    again = [torch.zeros(shape, dtype=torch.uint8 if dtype.itemsize == 1 else dtype, device="cuda") for shape, dtype in sizes]
+    torch.cuda.synchronize()
+    del again
+    for a, b in zip(flat(got), flat(call(*inputs()))):
+        torch.cuda.synchronize()
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
