@@ -618,7 +618,8 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
     float s = 0.f;
     if (mine >= 0) {
         const float xj = clean_logit(load_logit(row + mine));
-        s = softmax ? expf(xj - top) : 1.f / (1.f + expf(-xj));
+        const float ex = expf(softmax ? xj - top : -fabsf(xj));   // (exp(-x) overflows before the score is lost)
+        s = softmax ? ex : (xj >= 0.f ? 1.f : ex) / (1.f + ex);
     }
     float weight = s;
     if (p.renormalize) {

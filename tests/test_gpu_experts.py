@@ -403,6 +403,18 @@ def test_route_ratios_of_scores_that_underflow(k, T, score):
         assert np.abs(ref).max(axis=1).min() > 1e-4
 
 
+@pytest.mark.parametrize("T", [40, 4200])
+def test_route_small_sigmoids_keep_their_digits(T):
+    """Down to float32's least number: e^-103 is 2^-149, and exp(-x) overflows at x = -88.8."""
+    x = -86.0 - 18.0 * torch.rand(T, 64, device="cuda", generator=_gen(95))
+    experts, weights = X().route(x, 6, score="sigmoid", renormalize=False)
+    e_ref, w_ref = orc.route(_np(x), 6, score="sigmoid", renormalize=False)
+    assert np.array_equal(experts.cpu().numpy(), e_ref)
+    # a number below 2^-126 is rounded to a multiple of 2^-149: once by exp, which may be a step off, and once by the quotient
+    assert (np.abs(_np(weights) - w_ref) <= 256 * U * w_ref + 2.5 * 2.0 ** -149).all()
+    assert (w_ref < 2.0 ** -126).any() and (w_ref > 2.0 ** -126).any()
+
+
 def test_route_strided_and_large_rows():
     base = torch.randn(70, 200, device="cuda", generator=_gen(3))
     x = base[:, 3:100]                                        # neither aligned rows nor contiguous
