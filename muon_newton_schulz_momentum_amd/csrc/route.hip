@@ -41,11 +41,6 @@ __device__ __forceinline__ float wave_max(float v) {
     for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
     return v;
 }
-__device__ __forceinline__ float wave_sum32(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
-}
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
@@ -660,6 +655,35 @@ __device__ __forceinline__ double token_sum16(double v) {
     return v;
 }
 
+// The plain softmax's gradient from its row's exponentials: dx_e = s_e (sum of e's g - sum_i g_i s_i) of a chosen expert, and
+// what the others' exponentials are multiplied by, -(sum_i g_i s_i) / z.
+// Near s = 1 that difference is g (1 - s), all of whose digits come from the sum z without the largest term.  So z is
+// summed in float64, with the chosen experts' terms (float32 in z as it comes) in float64 as in the numerators; what is left of
+// float32 is the exponentials of the others, good to some 2^-18 of themselves.
+struct ChosenSoftmax {
+    float dx;
+    float other;
+};
+template <int LT, class SUM>
+__device__ __forceinline__ ChosenSoftmax chosen_softmax(int e, float xj, float top, float gw, double scale, double z, int top_k, SUM sum) {
+    const int lane = threadIdx.x & 63, l = lane & (LT - 1);
+    double all = 0.0;                                      // of the slots that have this lane's expert
+    bool first = true;
+    for (int j = 0; j < top_k; ++j) {
+        const int ej = __shfl(e, (lane & ~(LT - 1)) + j, 64);
+        const float gj = __shfl(gw, (lane & ~(LT - 1)) + j, 64);
+        if (ej == e) {
+            all += (double)gj * scale;
+            first &= j >= l;
+        }
+    }
+    const double ex = e >= 0 ? exp((double)xj - (double)top) : 0.0;
+    z += sum(e >= 0 && first ? ex - (double)__expf(xj - top) : 0.0);
+    const double inv = z > 0.0 ? 1.0 / z : 0.0, s = ex * inv;
+    const double mean = sum((double)gw * scale * s);       // (scaled here: float32's rounding would be a part of the difference)
+    return {e >= 0 ? (float)(s * (all - mean)) : 0.f, (float)(-mean * inv)};
+}
+
 // Backward for up to 16 slots: 16 lanes a token as in route_kernel, lane j also slot j.  Renormalised weights and sigmoids
 // need the chosen logits only; the plain softmax reads the row.  Bound by memory: 65537 x 512 float32 by plain softmax
 // 45 us (6.0 TB/s), renormalised 27 us (5.0 TB/s written).
@@ -673,14 +697,15 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
     const T* row = static_cast<const T*>(p.logits) + t * p.ld;
     T* grad = static_cast<T*>(p.grad_logits) + t * p.ld_grad;
     int e = -1;
-    float xj = -INFINITY, g = 0.f;
+    float xj = -INFINITY, gw = 0.f;
     if (l < p.top_k) {
         e = p.experts[t * p.top_k + l];
         if (e < 0 || e >= p.n_experts) e = -1;
         if (e >= 0) xj = clean_logit(load_logit(row + e));
         if (!(xj > -INFINITY)) e = -1;
-        if (e >= 0) g = p.grad_weights[t * p.top_k + l] * p.scale;
+        if (e >= 0) gw = p.grad_weights[t * p.top_k + l];
     }
+    const double g = (double)gw * (double)p.scale;         // (exact: where gradients are nearly alike, their differences count)
     float out[C][4];
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -696,18 +721,18 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
         if (p.renormalize) {
             const double total = token_sum16(s);
             const double w = total > 0.0 ? s / total : 0.0;
-            const double mean = token_sum16((double)g * w);
-            dx = e >= 0 ? (float)(w * rest * ((double)g - mean)) : 0.f;
+            const double mean = token_sum16(g * w);
+            dx = e >= 0 ? (float)(w * rest * (g - mean)) : 0.f;
         } else {
-            dx = e >= 0 ? (float)((double)g * s * rest) : 0.f;
+            dx = e >= 0 ? (float)(g * s * rest) : 0.f;
         }
     } else if (p.renormalize) {
         const float top = token_maxf<16>(xj);
         const double ex = e >= 0 ? exp((double)xj - (double)top) : 0.0;
         const double total = token_sum16(ex);
         const double w = total > 0.0 ? ex / total : 0.0;
-        const double mean = token_sum16((double)g * w);
-        dx = e >= 0 ? (float)(w * ((double)g - mean)) : 0.f;
+        const double mean = token_sum16(g * w);
+        dx = e >= 0 ? (float)(w * (g - mean)) : 0.f;
     } else {
         float top = -INFINITY;
 #pragma unroll
@@ -727,24 +752,23 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
             }
         }
         top = token_maxf<16>(top);
-        float z = 0.f;
+        double z = 0.0;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 out[c][v] = out[c][v] > -INFINITY ? __expf(out[c][v] - top) : 0.f;
-                z += out[c][v];
+                z += (double)out[c][v];
             }
-        z = token_sum<16>(z);
-        const float inv = z > 0.f ? 1.f / z : 0.f;
-        const float pj = e >= 0 ? __expf(xj - top) * inv : 0.f;
-        dx = e >= 0 ? g * pj : 0.f;
-        const float mean = token_sum<16>(dx) * -inv;
+        z = token_sum16(z);
+        const ChosenSoftmax r = chosen_softmax<16>(e, xj, top, gw, (double)p.scale, z, p.top_k, [](double v) { return token_sum16(v); });
+        dx = r.dx;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) out[c][v] *= mean;
+            for (int v = 0; v < 4; ++v) out[c][v] *= r.other;
     }
+    const float stays = p.score == MUON_SCORE_SOFTMAX && !p.renormalize ? 0.f : 1.f;   // there dx is all of it
     for (int j = 0; j < p.top_k; ++j) {
         const int ej = __shfl(e, (lane & 48) + j, 64);
         const float dj = __shfl(dx, (lane & 48) + j, 64);
@@ -752,7 +776,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                if (ej == 64 * c + 4 * l + v) out[c][v] += dj;
+                if (ej == 64 * c + 4 * l + v) out[c][v] = fmaf(out[c][v], stays, dj);
     }
     if (!live) return;
 #pragma unroll
@@ -778,14 +802,15 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
     T* grad = static_cast<T*>(p.grad_logits) + t * p.ld_grad;
     // lane j: slot j's expert, logit and gradient
     int e = -1;
-    float xj = -INFINITY, g = 0.f;
+    float xj = -INFINITY, gw = 0.f;
     if (lane < p.top_k) {
         e = p.experts[t * p.top_k + lane];
         if (e < 0 || e >= p.n_experts) e = -1;
         if (e >= 0) xj = clean_logit(load_logit(row + e));
         if (!(xj > -INFINITY)) e = -1;
-        if (e >= 0) g = p.grad_weights[t * p.top_k + lane] * p.scale;
+        if (e >= 0) gw = p.grad_weights[t * p.top_k + lane];
     }
+    const double g = (double)gw * (double)p.scale;         // (exact: where gradients are nearly alike, their differences count)
     float out[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = 0.f;
@@ -798,18 +823,18 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
         if (p.renormalize) {
             const double total = dev::wave_sum(s);
             const double w = total > 0.0 ? s / total : 0.0;
-            const double mean = dev::wave_sum((double)g * w);
-            dx = e >= 0 ? (float)(w * rest * ((double)g - mean)) : 0.f;
+            const double mean = dev::wave_sum(g * w);
+            dx = e >= 0 ? (float)(w * rest * (g - mean)) : 0.f;
         } else {
-            dx = (float)((double)g * s * rest);
+            dx = (float)(g * s * rest);
         }
     } else if (p.renormalize) {
         const float top = wave_max(xj);
         const double ex = e >= 0 ? exp((double)xj - (double)top) : 0.0;
         const double total = dev::wave_sum(ex);
         const double w = total > 0.0 ? ex / total : 0.0;
-        const double mean = dev::wave_sum((double)g * w);
-        dx = e >= 0 ? (float)(w * ((double)g - mean)) : 0.f;
+        const double mean = dev::wave_sum(g * w);
+        dx = e >= 0 ? (float)(w * (g - mean)) : 0.f;
     } else {
         float x[V], top = -INFINITY;
 #pragma unroll
@@ -819,26 +844,25 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
             top = fmaxf(top, x[i]);
         }
         top = wave_max(top);
-        float z = 0.f;
+        double z = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
-            z += x[i];
+            x[i] = x[i] > -INFINITY ? __expf(x[i] - top) : 0.f;
+            z += (double)x[i];
         }
-        z = wave_sum32(z);
-        const float inv = z > 0.f ? 1.f / z : 0.f;
-        const float pj = e >= 0 ? expf(xj - top) * inv : 0.f;
-        const float mean = wave_sum32(g * pj);
-        dx = g * pj;
+        z = dev::wave_sum(z);
+        const ChosenSoftmax r = chosen_softmax<64>(e, xj, top, gw, (double)p.scale, z, p.top_k, [](double v) { return dev::wave_sum(v); });
+        dx = r.dx;
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = -x[i] * inv * mean;
+        for (int i = 0; i < V; ++i) out[i] = x[i] * r.other;
     }
+    const float stays = p.score == MUON_SCORE_SOFTMAX && !p.renormalize ? 0.f : 1.f;   // there dx is all of it
     for (int j = 0; j < p.top_k; ++j) {
         const int ej = __shfl(e, j, 64);
         const float dj = __shfl(dx, j, 64);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (ej == lane + 64 * i) out[i] += dj;
+            if (ej == lane + 64 * i) out[i] = fmaf(out[i], stays, dj);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {

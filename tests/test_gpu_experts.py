@@ -415,6 +415,43 @@ def test_route_small_sigmoids_keep_their_digits(T):
     assert (w_ref < 2.0 ** -126).any() and (w_ref > 2.0 ** -126).any()
 
 
+@pytest.mark.parametrize("E,k", [(40, 4), (300, 7), (512, 16), (512, 20), (1024, 33)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_softmax_gradient_near_one(E, k, dtype):
+    """The plain softmax's gradient where one score is nearly 1, or the chosen ones are nearly all: its terms cancel, and the
+    result is compared by what is left of them.
+
+    dx_e = s_e (g_e (1 - s_e) - sum over i != e of g_i s_i) for a chosen e, -s_e sum_i g_i s_i for another.  The exponentials of
+    experts that are not chosen are float32's: (|x - max| <= 45 here) the argument off by 45 u, its product with log2 e by as
+    much again, exp2 by 2 u, and other factors by 4 u: 100 u of them, and 1 - s_e = (sum of the others) / z with them.  g_e (1 - s_e)
+    less the chosen others' part is the others' part and a difference of exact terms; so 128 u of the terms."""
+    x = torch.randn(64, E, device="cuda", generator=_gen(E + k))
+    x[::2, 3] += 15.0
+    x[1::4, :k] += 16.0
+    x = x.to(dtype)
+    experts, _ = X().route(x, k, renormalize=False)
+    grad = torch.randn(64, k, device="cuda", generator=_gen(6))
+    grad[3::4] = 1.0                                            # all alike: what is left is the part of those not chosen
+    dx = _np(X().route_backward(x, experts, grad, renormalize=False, scale=1.5))
+    s, _ = orc.scores(_np(x), "softmax")
+    e, g = experts.cpu().numpy().astype(np.int64), 1.5 * _np(grad)
+    sel = np.take_along_axis(s, e, axis=1)
+    rest = np.ones_like(s)
+    np.put_along_axis(rest, e, 0.0, axis=1)
+    rest = (s * rest).sum(axis=1, keepdims=True)                # of the experts not chosen, without a difference
+    ref, size = -s * (g * sel).sum(axis=1, keepdims=True), s * (np.abs(g) * sel).sum(axis=1, keepdims=True)
+    for j in range(k):
+        # g_j - sum g_i s_i = g_j rest + sum (g_j - g_i) s_i, as rest + sum s_i = 1
+        left = g[:, j:j + 1] * rest + ((g[:, j:j + 1] - g) * sel).sum(axis=1, keepdims=True)
+        terms = np.abs(g[:, j:j + 1]) * rest + (np.abs(g[:, j:j + 1] - g) * sel).sum(axis=1, keepdims=True)
+        np.put_along_axis(ref, e[:, j:j + 1], sel[:, j:j + 1] * left, axis=1)
+        np.put_along_axis(size, e[:, j:j + 1], sel[:, j:j + 1] * terms, axis=1)
+    err = np.abs(dx - ref)
+    tol = 128 * U * size + HALF[dtype] * (1 + 1e-3) * np.abs(ref) + 1e-40
+    assert (err <= tol).all(), float((err / tol).max())
+    assert (rest < 1e-4).any()
+
+
 def test_route_strided_and_large_rows():
     base = torch.randn(70, 200, device="cuda", generator=_gen(3))
     x = base[:, 3:100]                                        # neither aligned rows nor contiguous
