@@ -77,6 +77,6 @@ hipError_t launch_balance(const float* bias, const int32_t* counts, int32_t n, f
 hipError_t launch_quantize(const QuantizeArgs& a, int32_t src_dtype, int32_t format, int32_t square, hipStream_t s);
 // Whether the output tiles can be counted; launch_product takes no others.
 bool product_fits(ProductArgs a);
-hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, hipStream_t s);
+hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, bool full_sums, hipStream_t s);
 
 }  // namespace muon

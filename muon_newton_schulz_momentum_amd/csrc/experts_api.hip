@@ -378,6 +378,7 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
     if (!is_dtype(c->out_dtype)) return fail(MUON_ERR_INVALID_ARG, who, "out_dtype must be F32 or BF16");
     if (c->accumulate != 0 && (c->accumulate != 1 || c->out_dtype != MUON_DTYPE_F32))
         return fail(MUON_ERR_INVALID_ARG, who, "accumulate must be 0 or, for a float32 out, 1");
+    if (c->full_sums != 0 && c->full_sums != 1) return fail(MUON_ERR_INVALID_ARG, who, "full_sums must be 0 or 1");
     if (c->ld_out < c->n) return fail(MUON_ERR_SHAPE, who, "ld_out must be at least n");
     if (c->ld_out > MAX_I32) return fail(MUON_ERR_SHAPE, who, "ld_out must be below 2^31");
     if (depth && c->groups > 1 && (double)c->out_stride < (double)(c->m - 1) * (double)c->ld_out + (double)c->n)
@@ -424,7 +425,7 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
         (c->k > 0 && (overlap(out, codes_of(c->a, c->m, c->k, 1)) || overlap(out, scales_of(c->a, c->m, c->k, 1)) ||
                       overlap(out, codes_of(c->b, c->n, c->k, b_groups)) || overlap(out, scales_of(c->b, c->n, c->k, b_groups)))))
         return fail(MUON_ERR_INVALID_ARG, who, "out overlaps an operand or offsets");
-    return launched(launch_product(a, c->a.format, c->out_dtype, static_cast<hipStream_t>(stream)), who);
+    return launched(launch_product(a, c->a.format, c->out_dtype, c->full_sums != 0, static_cast<hipStream_t>(stream)), who);
 } catch (...) {
     return MUON_ERR_INVALID_ARG;
 }

@@ -11,9 +11,12 @@
 //
 // That instruction adds 8 products at a time after shifting them to the largest one's exponent, and drops
 // what falls below 2^-13 of it (measured: 256 * 256 - 256 * 256 + 1 is 0 within such a group and 1 across
-// groups): 1.4e-5 of a sum of normal values.  A bfloat16 out (half step 3.9e-3) does not see it.  A float32
-// out is asked for where sums go on being added up, so there the codes become bfloat16
-// values (exact, the scale included) and v_mfma_f32_32x32x16_bf16 keeps full float32 sums, at half the rate.
+// groups).  It is the choice for a bfloat16 out: codes of 4 bits leave a product uncertain by 2^-4 of itself, 70 times
+// the 7 * 2^-13 that its 7 neighbours may lose, and of sums of normal values 1.4e-5 is lost, where bfloat16's half step
+// is 3.9e-3.  But where a group's largest products cancel, its small ones are gone.  So full float32 sums can be asked for
+// (full_sums), and a float32 out, which is there to go on being added up, always has them: the codes become
+// bfloat16 values (exact, the scale included) and v_mfma_f32_32x32x16_bf16 adds them up, at half the rate (16381 x 5632 x 2048
+// to bfloat16: 178 us and 351; 57344 rows of 128 experts: 296 and 589; 112 rows of 512, bound by memory: 96 and 92).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -261,9 +264,10 @@ using ic = std::integral_constant<int, N>;
 // 16381 x 5632 x 2048 in bfloat16: 170 us, 2.2 PFLOP/s; 8192 x 8192 x 8320: 2.5.  57344 rows of 128 experts, 1024 x 4096:
 // 274-282 us.  Weight gradients of 64 experts, 1024 x 4096 in float32 over 28672 rows: 398 us, about 140 of products and
 // 200 of stores (1.07 GB), one after the other: a wave's loads and stores retire in order.
-template <int AFMT, class OUT>
+// PRECISE: full float32 sums, by the bfloat16 instruction.
+template <int AFMT, class OUT, bool PRECISE>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_kernel(ProductArgs p) {
-    constexpr bool PRECISE = sizeof(OUT) == 4;
+    constexpr bool F32 = sizeof(OUT) == 4;
     constexpr int LA = TILE / 64, NLOAD = 2 * LA;          // load instructions of a step: 64 rows each
     constexpr int ROW = 144, PANEL = TILE * ROW, STAGE = 2 * PANEL;
     constexpr int EPL = 16 / sizeof(OUT);                  // values of out in 16 bytes
@@ -486,7 +490,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
             for (int q = 0; q < 4; ++q) {
                 uint8_t* o = mine + (ln & 31) * OROW + (32 * j + 8 * q + 4 * (ln >> 5)) * sizeof(OUT);
                 const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                if constexpr (PRECISE) *reinterpret_cast<f32x4*>(o) = v;
+                if constexpr (F32) *reinterpret_cast<f32x4*>(o) = v;
                 else *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -500,7 +504,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
             const uint4 w = *reinterpret_cast<const uint4*>(mine + (q * RPS + row) * OROW + col * sizeof(OUT));
             if (r0 + q * RPS + row >= done.rows_a) continue;
             if (EPL <= left) {
-                if constexpr (PRECISE) {
+                if constexpr (F32) {
                     f32x4 v = __builtin_bit_cast(f32x4, w);
                     if (p.accumulate) v += *reinterpret_cast<const f32x4_any*>(o);
                     if (p.vec) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(o));
@@ -514,7 +518,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 #pragma unroll
                 for (int e = 0; e < EPL; ++e) {
                     if (e >= left) continue;
-                    if constexpr (PRECISE) o[e] = p.accumulate ? o[e] + __uint_as_float(u[e]) : __uint_as_float(u[e]);
+                    if constexpr (F32) o[e] = p.accumulate ? o[e] + __uint_as_float(u[e]) : __uint_as_float(u[e]);
                     else o[e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
                 }
             }
@@ -569,9 +573,9 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // of kernel; 256 rows: 30 us).
 constexpr int FEW_ROWS = 32;
 
-template <int AFMT, class OUT, int NB, int AHEAD>
+template <int AFMT, class OUT, bool PRECISE, int NB, int AHEAD>
 __global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
-    constexpr bool PRECISE = sizeof(OUT) == 4;
+    constexpr bool F32 = sizeof(OUT) == 4;
     constexpr int COLS = 16 * NB, SUMS = COLS + 4;         // columns of a tile; a row of sums in LDS
     __shared__ __attribute__((aligned(16))) float sums[WAVES][FEW_ROWS * SUMS];
     __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
@@ -675,7 +679,7 @@ __global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
                          (x.m0 + row) * p.ld_out + x.n0 + col;
                 const int64_t left = p.n - x.n0 - col;
                 if (left >= 4) {
-                    if constexpr (PRECISE) {
+                    if constexpr (F32) {
                         f32x4_any* o4 = reinterpret_cast<f32x4_any*>(o);
                         if (p.accumulate) v += *o4;
                         *o4 = v;
@@ -686,7 +690,7 @@ __global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if (e >= left) continue;
-                        if constexpr (PRECISE) o[e] = p.accumulate ? o[e] + v[e] : v[e];
+                        if constexpr (F32) o[e] = p.accumulate ? o[e] + v[e] : v[e];
                         else o[e] = dev::f32_to_bf16(v[e]);
                     }
                 }
@@ -710,20 +714,20 @@ int64_t count_tiles(ProductArgs& a, int tile_rows, int tile_cols) {
     return total;
 }
 
-template <int AFMT, class OUT>
+template <int AFMT, class OUT, bool PRECISE>
 hipError_t product_as(ProductArgs a, hipStream_t s) {
     ProductArgs few = a, thin = a;
     const int64_t n_big = count_tiles(a, TILE, TILE), n_few = count_tiles(few, FEW_ROWS, 64), n_thin = count_tiles(thin, FEW_ROWS, 16);
     if (n_big == 0) return hipSuccess;
     // What each would take, in us, from what they measured: big tiles by the round of 256 (256 x 4096 x 4096: 38 us in
-    // bfloat16, 76 in float32), the others by the depth of a wave where there are few tiles and by the blocks of all
+    // bfloat16, 76 with full sums), the others by the depth of a wave where there are few tiles and by the blocks of all
     // tiles where there are many.  1 row by 4096 x 4096: 26 us in big tiles, 12 in 32 x 64, 6 in 32 x 16; 256 rows: 38,
     // 30, 61; 512 rows: 40, 55, 118; 256 x 256 x 16384: 128, 52, 31; 112 rows of 512 experts, 1024 x 4096: 94, 104, 115.
     const double kb = (double)((a.k + KB - 1) / KB) / (a.mode == MUON_PRODUCT_DEPTH ? a.groups : 1);
     // (a big tile runs as many of its 4 row blocks as it has rows for: of its 64 rows each)
     const int64_t rows = a.mode == MUON_PRODUCT_ROWS ? a.m / std::min<int64_t>(a.m, a.groups) : a.m;
     const double more = (double)std::min<int64_t>((std::min<int64_t>(rows, TILE) + 63) / 64 - 1, 3) / 3.0;
-    const double step = sizeof(OUT) == 4 ? 1.0 + 1.2 * more : 0.66 + 0.39 * more;
+    const double step = PRECISE ? 1.0 + 1.2 * more : 0.66 + 0.39 * more;
     const double t_big = std::ceil((double)n_big / CUS) * (5.0 + kb * step);
     const double t_few = n_few < 0 ? 1e30 : 5.0 + std::max(kb / WAVES * 2.5, (double)n_few * (kb + 2.0) / 590.0);
     const double t_thin = n_thin < 0 ? 1e30 : 4.0 + std::max(kb / WAVES * 1.6, (double)n_thin * (kb + 1.5) / 1150.0);
@@ -731,9 +735,9 @@ hipError_t product_as(ProductArgs a, hipStream_t s) {
     const int64_t total = pick == 0 ? n_big : pick == 1 ? n_few : n_thin;
     const int64_t most = pick == 0 ? CUS : 2 * CUS;        // workgroups that run at once
     const dim3 grid((unsigned)std::min<int64_t>((total + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)), block(THREADS);
-    if (pick == 0) hipLaunchKernelGGL((product_kernel<AFMT, OUT>), grid, block, 0, s, a);
-    else if (pick == 1) hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, 4, 2>), grid, block, 0, s, few);
-    else hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, 1, 4>), grid, block, 0, s, thin);
+    if (pick == 0) hipLaunchKernelGGL((product_kernel<AFMT, OUT, PRECISE>), grid, block, 0, s, a);
+    else if (pick == 1) hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, PRECISE, 4, 2>), grid, block, 0, s, few);
+    else hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, PRECISE, 1, 4>), grid, block, 0, s, thin);
     return hipGetLastError();
 }
 
@@ -741,10 +745,11 @@ hipError_t product_as(ProductArgs a, hipStream_t s) {
 
 bool product_fits(ProductArgs a) { return count_tiles(a, TILE, TILE) >= 0; }
 
-hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, hipStream_t s) {
-    const bool f32 = out_dtype == MUON_DTYPE_F32;
-    if (a_format == MUON_FP8_E4M3) return f32 ? product_as<0, float>(a, s) : product_as<0, uint16_t>(a, s);
-    return f32 ? product_as<1, float>(a, s) : product_as<1, uint16_t>(a, s);
+hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, bool full_sums, hipStream_t s) {
+    const bool e4m3 = a_format == MUON_FP8_E4M3;
+    if (out_dtype == MUON_DTYPE_F32) return e4m3 ? product_as<0, float, true>(a, s) : product_as<1, float, true>(a, s);
+    if (full_sums) return e4m3 ? product_as<0, uint16_t, true>(a, s) : product_as<1, uint16_t, true>(a, s);
+    return e4m3 ? product_as<0, uint16_t, false>(a, s) : product_as<1, uint16_t, false>(a, s);
 }
 
 }  // namespace muon

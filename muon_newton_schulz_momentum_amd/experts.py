@@ -326,13 +326,17 @@ def _operand(o: L.muon_fp8_operand, name: str, q: Fp8, stacked: bool) -> torch.S
 
 def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Optional[str] = None,
             out: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16, accumulate: bool = False,
-            stream=None) -> torch.Tensor:
-    """a times the transpose of b in 8 bits with float32 sums (muon_fp8_product).
+            full_sums: bool = False, stream=None) -> torch.Tensor:
+    """a times the transpose of b in 8 bits (muon_fp8_product).
 
     group None: (m, n) of a (m, k) and b (n, k).  "rows": b is a stack (groups, n, k), and the rows offsets[g] to
     offsets[g + 1] of a go by b[g]; rows outside every segment are not written.
     "depth": out (groups, m, n), group g's over columns offsets[g] to offsets[g + 1] (multiples of 128) of both;
     with `accumulate` added to a float32 `out`.  a is e4m3 or e5m2, b e4m3.
+
+    A float32 result has full float32 sums.  A bfloat16 one is summed by the 8-bit matrix instruction, which of 8
+    neighbouring products drops what is below 2^-13 of the largest; with `full_sums` it has full float32 sums, too, at
+    half the rate.
     """
     if group not in _GROUPS:
         raise ValueError("group must be None, 'rows' or 'depth'")
@@ -366,5 +370,6 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
             k.ld_out = _rows("out", out)
             k.out_stride = out.stride(0) if group == "depth" and k.groups > 1 else m * k.ld_out
         k.out, k.out_dtype, k.accumulate = out.data_ptr(), _DTYPES[out.dtype], 1 if accumulate else 0
+        k.full_sums = 1 if full_sums else 0
         L.check(L.muon_fp8_product(C.byref(k), _stream_ptr(codes)), "muon_fp8_product")
     return out

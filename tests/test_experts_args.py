@@ -351,3 +351,10 @@ def test_grouping_refuses_every_overlap():
         assert st == L.MUON_ERR_INVALID_ARG and b"overlap" in L.muon_last_error()
     for out in (B, A + 16, B - 16, B + 16):
         assert L.muon_balance_step(A, B, 8, 0.1, out, None) == L.MUON_ERR_INVALID_ARG and b"overlap" in L.muon_last_error()
+
+
+@pytest.mark.parametrize("value", [2, -1])
+def test_product_refuses_an_unknown_kind_of_sums(value):
+    c = _product(0, full_sums=value)
+    assert L.muon_fp8_product(C.byref(c), None) == L.MUON_ERR_INVALID_ARG
+    assert b"full_sums" in L.muon_last_error()

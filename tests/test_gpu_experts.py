@@ -802,6 +802,57 @@ def test_product_depth(sizes, m, n, fmt, dtype):
             _check_product(acc[g], va[:, s], vb[:, s], ends[g + 1] - ends[g], before=_np(before[g]))
 
 
+def _check_full_sums(out, a, b, k):
+    """As _check_product, without what the 8-bit instruction drops."""
+    ref, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+    tol = 2 * U * (-(-k // 128) + 16) * mag + HALF[out.dtype] * (1 + 1e-3) * np.abs(ref) + 1e-37
+    err = np.abs(_np(out) - ref)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+def test_product_full_sums_where_products_cancel():
+    """256 * 256 - 256 * 256 + 1 in one group of 8: the 1 is there with full sums."""
+    for rows, cols, k in ((1, 1, 128), (40, 70, 384), (2100, 2300, 256)):
+        x, y = torch.zeros(rows, k, device="cuda"), torch.zeros(cols, k, device="cuda")
+        x[:, 0], x[:, 1], x[:, 2] = 256.0, 256.0, 1.0
+        y[:, 0], y[:, 1], y[:, 2] = 256.0, -256.0, 1.0
+        a, b = X().quantize(x), X().quantize(y)
+        assert (X().product(a, b, full_sums=True) == 1.0).all()
+        assert (X().product(a, b, dtype=torch.float32) == 1.0).all()
+        assert ((X().product(a, b) - 1.0).abs() <= 7 * 2.0 ** -13 * 65536).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (17, 100, 300), (129, 255, 1000), (300, 513, 640), (2053, 1100, 640), (4500, 4300, 400)])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_product_full_sums_dense(m, n, k, fmt):
+    a, b = _random_fp8(m, k, fmt, False, m + k), _random_fp8(n, k, "e4m3", True, n + k)
+    got = X().product(a, b, full_sums=True)
+    _check_full_sums(got, _np(a.dequantize()), _np(b.dequantize()), k)
+    assert torch.equal(got, X().product(a, b, dtype=torch.float32).bfloat16())      # the same sums, rounded once
+
+
+def test_product_full_sums_in_groups():
+    sizes, n, k = [300, 0, 513, 64, 65, 1000, 1, 129, 192, 193, 255, 256], 2100, 900
+    ends = np.concatenate([[0], np.cumsum(sizes)])
+    a, b = _random_fp8(int(ends[-1]) + 3, k, "e4m3", False, 1), _random_fp8(n, k, "e4m3", True, 2, stack=len(sizes))
+    offsets = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    out = torch.full((int(ends[-1]) + 3, n + 1), 7.5, dtype=torch.bfloat16, device="cuda")
+    X().product(a, b, offsets=offsets, group="rows", out=out[:, :n], full_sums=True)
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    for g, s in enumerate(sizes):
+        if s:
+            _check_full_sums(out[ends[g]:ends[g + 1], :n], va[ends[g]:ends[g + 1]], vb[g], k)
+    assert (out[ends[-1]:] == 7.5).all() and (out[:, n] == 7.5).all()
+    cols = [300, 0, 128, 5, 640]
+    ends = np.concatenate([[0], np.cumsum([-(-s // 128) * 128 for s in cols])])
+    a, b = _random_fp8(130, int(ends[-1]), "e5m2", False, 3), _random_fp8(515, int(ends[-1]), "e4m3", False, 4)
+    out = X().product(a, b, offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"), group="depth", full_sums=True)
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    for g in range(len(cols)):
+        s = slice(ends[g], ends[g + 1])
+        _check_full_sums(out[g], va[:, s], vb[:, s], max(1, int(ends[g + 1] - ends[g])))
+
+
 def test_product_offsets_are_clamped():
     """Offsets outside the operand reach neither past it nor past out."""
     a, b = _random_fp8(40, 128, "e4m3", False, 1), _random_fp8(32, 128, "e4m3", True, 2, stack=3)
