@@ -569,8 +569,8 @@ typedef struct muon_fp8_product_config {
  * largest products (about 1.4e-5 of a sum of normal values; but where large products
  * cancel, small ones beside them are lost), before full float32 sums over the groups of 8.
  * With full_sums, and always for a float32 out, all sums are full float32 sums: the codes go
- * through the bfloat16 instruction, at half the rate, where a value below 2^-126 counts as
- * zero and one that its code rounded up to 2^128 as an infinity.
+ * through the bfloat16 instruction, at half the rate, where a value below 2^-126 is rounded
+ * to a multiple of 2^-133 and one whose code was rounded up to 2^128 is an infinity.
  * Errors: INVALID_ARG (NULL, enum, groups, accumulate into bfloat16, out overlapping an
  * operand or offsets), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
 MUON_API muon_status muon_fp8_product(const muon_fp8_product_config* config, void* stream);

@@ -452,6 +452,22 @@ def test_route_softmax_gradient_near_one(E, k, dtype):
     assert (rest < 1e-4).any()
 
 
+@pytest.mark.parametrize("T", [50, 4150])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_saturated_scores(T, score):
+    """All keys equal or within 2^-16: nothing that float32 could decide, so every token goes the float64 way."""
+    at = np.r_[0:20, T - 20:T]
+    x = torch.randn(T, 128, device="cuda", generator=_gen(97)) + 45.0       # sigmoids of 1 in float64
+    flat = 1e-6 * torch.randn(T, 128, device="cuda", generator=_gen(98))
+    bias = 1e-7 * torch.randn(128, device="cuda", generator=_gen(99))
+    for y in (x, flat):
+        for b in (torch.zeros_like(bias), bias):
+            for kw in (dict(score=score), dict(score=score, groups=8, top_groups=3)):
+                experts, weights = X().route(y, 7, bias=b, **kw)
+                want = orc.route(_np(y[at]), 7, _np(b), **kw)
+                _check_route(y[at], experts[at], weights[at], want, 7)
+
+
 def test_route_strided_and_large_rows():
     base = torch.randn(70, 200, device="cuda", generator=_gen(3))
     x = base[:, 3:100]                                        # neither aligned rows nor contiguous
@@ -802,10 +818,10 @@ def test_product_depth(sizes, m, n, fmt, dtype):
             _check_product(acc[g], va[:, s], vb[:, s], ends[g + 1] - ends[g], before=_np(before[g]))
 
 
-def _check_full_sums(out, a, b, k):
+def _check_full_sums(out, a, b, k, more=0.0):
     """As _check_product, without what the 8-bit instruction drops."""
     ref, mag = a @ b.T, np.abs(a) @ np.abs(b).T
-    tol = 2 * U * (-(-k // 128) + 16) * mag + HALF[out.dtype] * (1 + 1e-3) * np.abs(ref) + 1e-37
+    tol = 2 * U * (-(-k // 128) + 16) * mag + HALF[out.dtype] * (1 + 1e-3) * np.abs(ref) + 1e-37 + more
     err = np.abs(_np(out) - ref)
     assert (err <= tol).all(), float((err / tol).max())
 
@@ -1058,6 +1074,102 @@ def test_column_ranges_of_one_buffer():
     X().product(a, q, out=out)
     assert torch.equal(out, X().product(q, q, dtype=torch.float32))
     assert torch.equal(codes[:, :128], q.codes.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_gather_into_squares(dtype):
+    """Rows gathered into 128 x 128 squares, both orientations; -1 and rows past the source are zeros."""
+    tokens, cols, per = 70, 333, 2
+    x = _source(tokens, cols, dtype, 21)
+    rows = torch.randint(0, tokens * per, (301,), device="cuda", generator=_gen(22), dtype=torch.int32)
+    rows[::9], rows[4] = -1, tokens * per
+    rows[128:256] = -1                                         # a square of zeros
+    r = rows.cpu().numpy().astype(np.int64)
+    full = np.where(((r >= 0) & (r < tokens * per))[:, None], _np(x)[np.clip(r // per, 0, tokens - 1)], 0.0)
+    for fmt in ("e4m3", "e5m2"):
+        q, qt = X().quantize(x, rows=rows, per=per, block="square", format=fmt, transpose=True)
+        _check_fp8(q, orc.quantize(full, fmt, True), fmt)
+        _check_fp8(qt, orc.quantize(full.T, fmt, True), fmt)
+
+
+@pytest.mark.parametrize("sizes,n,k", [([5, 0, 130, 7], 70, 300), ([300, 1, 513, 0, 640, 90] * 3, 1030, 400)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_rows_of_squares(sizes, n, k, dtype):
+    """a in squares, whose 128 rows straddle the segments, and b in rows."""
+    m, E = sum(sizes), len(sizes)
+    a, b = _random_fp8(m, k, "e5m2", True, m), _random_fp8(n, k, "e4m3", False, n, stack=E)
+    ends = np.concatenate([[0], np.cumsum(sizes)])
+    out = X().product(a, b, offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"), group="rows", dtype=dtype)
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    for g in range(E):
+        if sizes[g]:
+            _check_product(out[ends[g]:ends[g + 1]], va[ends[g]:ends[g + 1]], vb[g], k)
+
+
+@pytest.mark.parametrize("blocks,m,n", [([1, 0, 2, 3], 100, 260), ([3, 1, 0, 5, 2, 1], 1030, 2060)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_product_depth_of_squares(blocks, m, n, dtype):
+    """Both operands as square copies' transposes."""
+    ends = 128 * np.concatenate([[0], np.cumsum(blocks)])
+    xa, xb = (_source(int(ends[-1]), c, torch.float32, c) for c in (m, n))
+    a, b = X().quantize(xa, block="square", transpose=True)[1], X().quantize(xb, block="square", transpose=True)[1]
+    out = X().product(a, b, offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"), group="depth", dtype=dtype)
+    va, vb = _np(a.dequantize()), _np(b.dequantize())
+    for g in range(len(blocks)):
+        s = slice(ends[g], ends[g + 1])
+        _check_product(out[g], va[:, s], vb[:, s], max(1, int(ends[g + 1] - ends[g])))
+
+
+@pytest.mark.parametrize("magnitude", [3e38, 1e30, 2e-36, 1e-37])
+def test_product_of_extreme_scales(magnitude):
+    """Scale bytes at both ends of their range.
+
+    Full float32 sums take the values as bfloat16: one below 2^-126 is rounded to a multiple of 2^-133, by at most half of that, and its
+    products are off by as much of the other factor."""
+    def step(v):
+        return np.where((np.abs(v) < 2.0 ** -126) & (v != 0), 2.0 ** -134, 0.0)
+
+    x = _source(40, 256, torch.float32, 31).sign() * magnitude * (0.5 + 0.4 * torch.rand(40, 256, device="cuda", generator=_gen(32)))
+    y = torch.randn(70, 256, device="cuda", generator=_gen(33)) / magnitude
+    for fmt in ("e4m3", "e5m2"):
+        a, b = X().quantize(x, format=fmt), X().quantize(y)
+        _check_fp8(a, orc.quantize(_np(x), fmt, False), fmt)
+        va, vb = _np(a.dequantize()), _np(b.dequantize())
+        assert np.isfinite(va).all()
+        _check_product(X().product(a, b), va, vb, 256)
+        more = step(va) @ np.abs(vb).T + np.abs(va) @ step(vb).T + step(va) @ step(vb).T
+        _check_full_sums(X().product(a, b, dtype=torch.float32), va, vb, 256, more)
+        _check_full_sums(X().product(a, b, full_sums=True), va, vb, 256, more * (1 + HALF[torch.bfloat16]))
+        assert ((step(va) > 0).any() or (step(vb) > 0).any()) == (magnitude == 3e38)
+
+
+def test_stream_argument_captured():
+    """Calls that name their stream, captured on it and replayed."""
+    s = torch.cuda.Stream()
+    x = torch.randn(300, 64, device="cuda", generator=_gen(1))
+    w = X().quantize(torch.randn(48, 64, device="cuda", generator=_gen(2)), block="square")
+
+    def run():
+        e, weights = X().route(x, 3, stream=s)
+        g = X().group_rows(e, 64, stream=s)
+        q = X().quantize(x, rows=g.rows, per=3, limit=g.limit, stream=s)
+        return e, weights, g.rows, X().product(q, w, dtype=torch.float32, stream=s)
+
+    torch.cuda.synchronize()
+    run()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = run()
+    for replay in range(3):
+        x.copy_(torch.randn(300, 64, device="cuda", generator=_gen(10 + replay)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
 
 
 def test_wrapper_refusals_on_the_gpu():
