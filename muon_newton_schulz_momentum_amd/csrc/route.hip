@@ -400,10 +400,11 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
         const int share = p.n_groups <= 2 ? 3 : p.n_groups <= 4 ? 2 : p.n_groups <= 8 ? 1 : 0, step = 1 << share;
         // lane l: groups l + 16 i, their two largest added up, and what float32 may be off by
         float worth[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, off[4] = {0.f, 0.f, 0.f, 0.f};
-        // Scores are off by less than 2^-21, a key and a sum by their rounding, 2^-24 of a size that is at most the larger of the two
-        // keys (which may cancel) or twice that: 2^-20 + 2^-22 of that size in all.  With a bias the softmax's sum counts,
-        // too (without one it is a factor of all groups): 2^-18 of the scores.
-        const float margin = softmax && p.bias ? 0x1p-18f + 0x1p-19f : 0x1p-19f;
+        // A sigmoid is off by less than 2^-21, a softmax (but for its row's sum) by less than that part of the largest one, 1 / z; a
+        // key and the sum by their rounding, 2^-24 of a size that is at most the larger of the two keys (which may cancel) or
+        // twice that.  With a bias the error of z counts, too (without one it is a factor of all groups): 2^-18 of the scores.
+        const float largest = !softmax ? 1.f : any ? 1.f / z : 0.f;
+        const float of_scores = 0x1p-20f * largest + (softmax && p.bias ? 0x1p-18f * fminf(2.f * largest, 1.f) : 0.f);
 #pragma unroll 1
         for (int i = 0; 16 * i < p.n_groups; ++i) {
             const int g = (l >> share) + 16 * i, first = g * per, end = g < p.n_groups ? first + per : first;
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) __attribute__((amdgpu_waves_per_e
             // an infinite key is exact; finite sums stay finite (and so above a group without an expert)
             const bool sum = fabsf(m1) != INFINITY;
             const float w = sum ? fminf(fmaxf(m1 + m2, -F32_MAX), F32_MAX) : m1;
-            const float d = sum ? margin * fmaxf(1.f, fmaxf(fabsf(m1), fabsf(m2))) : 0.f;
+            const float d = sum ? of_scores + 0x1p-21f * fmaxf(fabsf(m1), fabsf(m2)) : 0.f;
             const int from = (lane & 48) + ((l << share) & 15);
             const float my_w = __shfl(w, from, 64), my_d = __shfl(d, from, 64);
 #pragma unroll
