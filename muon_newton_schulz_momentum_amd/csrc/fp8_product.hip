@@ -264,6 +264,10 @@ using ic = std::integral_constant<int, N>;
 // 16381 x 5632 x 2048 in bfloat16: 170 us, 2.2 PFLOP/s; 8192 x 8192 x 8320: 2.5.  57344 rows of 128 experts, 1024 x 4096:
 // 274-282 us.  Weight gradients of 64 experts, 1024 x 4096 in float32 over 28672 rows: 398 us, about 140 of products and
 // 200 of stores (1.07 GB), one after the other: a wave's loads and stores retire in order.
+// All 256 registers of a lane are taken: accumulators 128, staged operands 32, fragments 48 or 64, scales 6, addresses.  14 values
+// (20 for PRECISE) that a tile's beginning and end use spill to scratch, before and behind the main loops: inside there is
+// no scratch access, which would wait for the staged loads.
+//
 // PRECISE: full float32 sums, by the bfloat16 instruction.
 template <int AFMT, class OUT, bool PRECISE>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void product_kernel(ProductArgs p) {
@@ -733,7 +737,8 @@ hipError_t product_as(ProductArgs a, hipStream_t s) {
     const double t_thin = n_thin < 0 ? 1e30 : 4.0 + std::max(kb / WAVES * 1.6, (double)n_thin * (kb + 1.5) / 1150.0);
     const int pick = t_big <= std::min(t_few, t_thin) ? 0 : t_few <= t_thin ? 1 : 2;
     const int64_t total = pick == 0 ? n_big : pick == 1 ? n_few : n_thin;
-    const int64_t most = pick == 0 ? CUS : 2 * CUS;        // workgroups that run at once
+    // workgroups: as many as run at once, and of 32 x 64 tiles (153 registers and more: one a CU) as many again
+    const int64_t most = pick == 0 ? CUS : 2 * CUS;
     const dim3 grid((unsigned)std::min<int64_t>((total + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)), block(THREADS);
     if (pick == 0) hipLaunchKernelGGL((product_kernel<AFMT, OUT, PRECISE>), grid, block, 0, s, a);
     else if (pick == 1) hipLaunchKernelGGL((product_few_kernel<AFMT, OUT, PRECISE, 4, 2>), grid, block, 0, s, few);
