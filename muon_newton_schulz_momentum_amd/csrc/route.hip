@@ -230,8 +230,9 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_exact_kernel(RouteArgs
 // They (with a bias, in one token of forty at 512 experts) are settled by
 // taking on to 16 experts and ranking those by their float64 keys, and two groups at the border by their float64 sums;
 // whatever is left is done again by the whole wave in float64.  So the choice is always the float64 one.
-// 65537 tokens of 512 float32 logits, 7 by softmax: 40 us, 3.4 TB/s, the sorting's vector instructions; 8192 in 8 groups by
-// sigmoid and bias, bfloat16: 20 us, two waves a SIMD, each a chain of reductions.
+// 65537 tokens of 512 float32 logits, 7 by softmax: 40 us, 3.4 TB/s, bound by the sorting's vector instructions (1140 a wave:
+// issued in all of its busy cycles); 8192 in 8 groups by sigmoid and bias, bfloat16: 21 us, two waves a SIMD, each a
+// chain of reductions (vector instructions in half of the busy cycles).
 constexpr int FAST_MAX_K = 15;
 constexpr int64_t WIDE_MAX_TOKENS = 4096;
 
@@ -651,9 +652,27 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
 }
 
 __device__ __forceinline__ double token_sum16(double v) {
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
+    v += dppd<XCHG_1>(v);
+    v += dppd<XCHG_2>(v);
+    v += dppd<XCHG_4>(v);
+    return v + dppd<XCHG_8>(v);
+}
+
+// The sum of v over the slots that have this lane's expert, in their order, and whether this is the first of them.
+template <int LT, class S>
+__device__ __forceinline__ S of_expert(int e, float v, int top_k, bool& first) {
+    const int lane = threadIdx.x & 63, l = lane & (LT - 1);
+    S all = 0;
+    first = true;
+    for (int j = 0; j < top_k; ++j) {
+        const int ej = __shfl(e, (lane & ~(LT - 1)) + j, 64);
+        const float vj = __shfl(v, (lane & ~(LT - 1)) + j, 64);
+        if (ej == e) {
+            all += (S)vj;
+            first &= j >= l;
+        }
+    }
+    return all;
 }
 
 // The plain softmax's gradient from its row's exponentials: dx_e = s_e (sum of e's g - sum_i g_i s_i) of a chosen expert, and
@@ -667,17 +686,8 @@ struct ChosenSoftmax {
 };
 template <int LT, class SUM>
 __device__ __forceinline__ ChosenSoftmax chosen_softmax(int e, float xj, float top, float gw, double scale, double z, int top_k, SUM sum) {
-    const int lane = threadIdx.x & 63, l = lane & (LT - 1);
-    double all = 0.0;                                      // of the slots that have this lane's expert
-    bool first = true;
-    for (int j = 0; j < top_k; ++j) {
-        const int ej = __shfl(e, (lane & ~(LT - 1)) + j, 64);
-        const float gj = __shfl(gw, (lane & ~(LT - 1)) + j, 64);
-        if (ej == e) {
-            all += (double)gj * scale;
-            first &= j >= l;
-        }
-    }
+    bool first;
+    const double all = of_expert<LT, double>(e, gw, top_k, first) * scale;
     const double ex = e >= 0 ? exp((double)xj - (double)top) : 0.0;
     z += sum(e >= 0 && first ? ex - (double)__expf(xj - top) : 0.0);
     const double inv = z > 0.0 ? 1.0 / z : 0.0, s = ex * inv;
@@ -686,8 +696,8 @@ __device__ __forceinline__ ChosenSoftmax chosen_softmax(int e, float xj, float t
 }
 
 // Backward for up to 16 slots: 16 lanes a token as in route_kernel, lane j also slot j.  Renormalised weights and sigmoids
-// need the chosen logits only; the plain softmax reads the row.  Bound by memory: 65537 x 512 float32 by plain softmax
-// 45 us (6.0 TB/s), renormalised 27 us (5.0 TB/s written).
+// need the chosen logits only; the plain softmax reads the row.  65537 x 512 float32: renormalised 27 us (5.0 TB/s written,
+// bound by memory), by plain softmax 47 us (5.7 TB/s; the vector instructions are as near their limit).
 template <class T, int C>
 __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteBackwardArgs p, int vec) {
     const int lane = threadIdx.x & 63, l = lane & 15;
@@ -712,7 +722,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int v = 0; v < 4; ++v) out[c][v] = 0.f;
-    float dx;                                              // what slot l adds to its expert
+    float dx;                                              // what slot l's expert gets from it
     if (p.score == MUON_SCORE_SIGMOID) {
         const float high = token_maxf<16>(xj);
         const bool tiny = p.renormalize && high < TINY_SIGMOID;
@@ -769,15 +779,17 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
 #pragma unroll
             for (int v = 0; v < 4; ++v) out[c][v] *= r.other;
     }
-    const float stays = p.score == MUON_SCORE_SOFTMAX && !p.renormalize ? 0.f : 1.f;   // there dx is all of it
+    // from here on dx is all that the slot's expert gets
+    bool first;
+    if (p.score == MUON_SCORE_SIGMOID || p.renormalize) dx = of_expert<16, float>(e, dx, p.top_k, first);
     for (int j = 0; j < p.top_k; ++j) {
-        const int ej = __shfl(e, (lane & 48) + j, 64);
+        const int place = __shfl(e, (lane & 48) + j, 64) - 4 * l;
         const float dj = __shfl(dx, (lane & 48) + j, 64);
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                if (ej == 64 * c + 4 * l + v) out[c][v] = fmaf(out[c][v], stays, dj);
+                out[c][v] = place == 64 * c + v ? dj : out[c][v];
     }
     if (!live) return;
 #pragma unroll
@@ -815,7 +827,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
     float out[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = 0.f;
-    float dx = 0.f;                                        // lane j: what slot j adds to its expert
+    float dx = 0.f;                                        // lane j: what slot j's expert gets from it
     if (p.score == MUON_SCORE_SIGMOID) {
         const float high = wave_max(xj);
         const bool tiny = p.renormalize && high < TINY_SIGMOID;
@@ -857,13 +869,14 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = x[i] * r.other;
     }
-    const float stays = p.score == MUON_SCORE_SOFTMAX && !p.renormalize ? 0.f : 1.f;   // there dx is all of it
+    bool first;
+    if (p.score == MUON_SCORE_SIGMOID || p.renormalize) dx = of_expert<64, float>(e, dx, p.top_k, first);   // all that the slot's expert gets
     for (int j = 0; j < p.top_k; ++j) {
         const int ej = __shfl(e, j, 64);
         const float dj = __shfl(dx, j, 64);
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (ej == lane + 64 * i) out[i] = fmaf(out[i], stays, dj);
+            if (ej == lane + 64 * i) out[i] = dj;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
