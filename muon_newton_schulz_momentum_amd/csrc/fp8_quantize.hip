@@ -10,8 +10,9 @@
 // 8 values down a column are 8 consecutive bytes of the transposed copy.
 //
 // Bound by memory: 64 float32 matrices of 1024 x 4096 in squares, both orientations, 1.61 GB in 283 us (5.7 TB/s);
-// 57344 rows of 4096 bfloat16 gathered from 8192, both orientations, 0.54 GB in 119 us (4.5 TB/s).  A value costs
-// about 8 vector instructions; twice the tiles a workgroup held more registers and was slower.
+// 57344 rows of 4096 bfloat16 gathered from 8192, both orientations, 0.54 GB in 119 us (4.5 TB/s), where the
+// vector instructions are as near their limit (about 8 a value, issued in 93 % of the busy cycles; 26 % in the first).
+// Twice the tiles a workgroup held more registers and was slower.
 #include "device_common.h"
 #include "experts.h"
 

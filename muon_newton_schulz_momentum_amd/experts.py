@@ -9,7 +9,7 @@ One layer's matrices in a training step, with the optimizer's `harness.Plan` at 
     x, x_t = quantize(tokens, rows=g.rows, per=top_k, limit=g.limit, transpose=True)
     y = product(x, w, offsets=g.offsets, group="rows")               # rows of g, each by its expert
     ...
-    dy, dy_t = quantize(grad_y, limit=g.limit, transpose=True)
+    dy, dy_t = quantize(grad_y, limit=g.limit, transpose=True)       # grad_y: zeros in the rows that pad a segment
     dx = product(dy, w_t, offsets=g.offsets, group="rows")
     product(dy_t, x_t, offsets=g.offsets, group="depth", out=G)      # the gradients that the plan reads
     bias = balance_step(bias, g.counts, rate)
