@@ -547,9 +547,11 @@ typedef struct muon_fp8_operand {
  * empty (weight gradients).  offsets are multiples of 128 (muon_group_rows with align 128):
  * a segment's blocks of 128 must be its own.  Others are rounded down. */
 #define MUON_PRODUCT_DEPTH 2
+/* Added to one of the three: full float32 sums for a bfloat16 out, too (see muon_fp8_product). */
+#define MUON_PRODUCT_FULL_SUMS 16
 
 typedef struct muon_fp8_product_config {
-    int32_t mode;             /* MUON_PRODUCT_*                                             */
+    int32_t mode;             /* MUON_PRODUCT_*, and MUON_PRODUCT_FULL_SUMS if wanted       */
     int32_t groups;           /* 1 for MUON_PRODUCT_DENSE; at most MUON_MAX_EXPERTS         */
     int64_t m, n, k;
     muon_fp8_operand a, b;
@@ -560,7 +562,6 @@ typedef struct muon_fp8_product_config {
     int64_t out_stride;       /* MUON_PRODUCT_DEPTH: elements between groups                */
     int32_t out_dtype;        /* MUON_DTYPE_*                                               */
     int32_t accumulate;       /* 1: added to out (float32 only)                             */
-    int32_t full_sums;        /* 1: full float32 sums for a bfloat16 out, too               */
 } muon_fp8_product_config;
 
 /* 8-bit product on the matrix cores, one rounding to out's type.  A bfloat16 out is by default
@@ -568,7 +569,7 @@ typedef struct muon_fp8_product_config {
  * below 2^-13 of the largest, so a sum is off by up to 7 * 2^-13 of the sum of those
  * largest products (about 1.4e-5 of a sum of normal values; but where large products
  * cancel, small ones beside them are lost), before full float32 sums over the groups of 8.
- * With full_sums, and always for a float32 out, all sums are full float32 sums: the codes go
+ * With MUON_PRODUCT_FULL_SUMS, and always for a float32 out, all sums are full float32 sums: the codes go
  * through the bfloat16 instruction, at half the rate, where a value below 2^-126 is rounded
  * to a multiple of 2^-133 and one whose code was rounded up to 2^128 is an infinity.
  * Errors: INVALID_ARG (NULL, enum, groups, accumulate into bfloat16, out overlapping an

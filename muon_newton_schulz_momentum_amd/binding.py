@@ -77,6 +77,7 @@ MUON_FP8_E5M2 = 1
 MUON_PRODUCT_DENSE = 0
 MUON_PRODUCT_ROWS = 1
 MUON_PRODUCT_DEPTH = 2
+MUON_PRODUCT_FULL_SUMS = 16
 
 
 class muon_param_desc(C.Structure):
@@ -140,8 +141,7 @@ class muon_fp8_operand(C.Structure):
 class muon_fp8_product_config(C.Structure):
     _fields_ = [("mode", C.c_int32), ("groups", C.c_int32), ("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64),
                 ("a", muon_fp8_operand), ("b", muon_fp8_operand), ("offsets", C.c_void_p), ("out", C.c_void_p),
-                ("ld_out", C.c_int64), ("out_stride", C.c_int64), ("out_dtype", C.c_int32), ("accumulate", C.c_int32),
-                ("full_sums", C.c_int32)]
+                ("ld_out", C.c_int64), ("out_stride", C.c_int64), ("out_dtype", C.c_int32), ("accumulate", C.c_int32)]
 
 
 _P = C.c_void_p  # muon_plan*

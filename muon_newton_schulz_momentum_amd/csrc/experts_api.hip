@@ -365,10 +365,12 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
     clear_error();
     const char* who = "muon_fp8_product";
     if (!c) return fail(MUON_ERR_INVALID_ARG, who, "config is NULL");
-    if (c->mode != MUON_PRODUCT_DENSE && c->mode != MUON_PRODUCT_ROWS && c->mode != MUON_PRODUCT_DEPTH)
+    const bool full_sums = (c->mode & MUON_PRODUCT_FULL_SUMS) != 0;
+    const int32_t mode = c->mode & ~MUON_PRODUCT_FULL_SUMS;
+    if (mode != MUON_PRODUCT_DENSE && mode != MUON_PRODUCT_ROWS && mode != MUON_PRODUCT_DEPTH)
         return fail(MUON_ERR_INVALID_ARG, who, "unknown mode");
-    const bool rows = c->mode == MUON_PRODUCT_ROWS, depth = c->mode == MUON_PRODUCT_DEPTH;
-    if (c->groups < 1 || c->groups > MUON_MAX_EXPERTS || (c->mode == MUON_PRODUCT_DENSE && c->groups != 1))
+    const bool rows = mode == MUON_PRODUCT_ROWS, depth = mode == MUON_PRODUCT_DEPTH;
+    if (c->groups < 1 || c->groups > MUON_MAX_EXPERTS || (mode == MUON_PRODUCT_DENSE && c->groups != 1))
         return fail(MUON_ERR_INVALID_ARG, who, "groups must be in [1, 1024], and 1 without groups");
     if (c->m < 0 || c->n < 0 || c->k < 0 || c->m > MAX_I32 || c->n > MAX_I32 || c->k > MAX_I32 - 127)
         return fail(MUON_ERR_SHAPE, who, "m, n and k must be at least 0 and below 2^31 - 127");
@@ -378,13 +380,12 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
     if (!is_dtype(c->out_dtype)) return fail(MUON_ERR_INVALID_ARG, who, "out_dtype must be F32 or BF16");
     if (c->accumulate != 0 && (c->accumulate != 1 || c->out_dtype != MUON_DTYPE_F32))
         return fail(MUON_ERR_INVALID_ARG, who, "accumulate must be 0 or, for a float32 out, 1");
-    if (c->full_sums != 0 && c->full_sums != 1) return fail(MUON_ERR_INVALID_ARG, who, "full_sums must be 0 or 1");
     if (c->ld_out < c->n) return fail(MUON_ERR_SHAPE, who, "ld_out must be at least n");
     if (c->ld_out > MAX_I32) return fail(MUON_ERR_SHAPE, who, "ld_out must be below 2^31");
     if (depth && c->groups > 1 && (double)c->out_stride < (double)(c->m - 1) * (double)c->ld_out + (double)c->n)
         return fail(MUON_ERR_SHAPE, who, "out_stride must hold one group");
     if (c->m == 0 || c->n == 0) return MUON_OK;
-    if (!c->out || (c->mode != MUON_PRODUCT_DENSE && !c->offsets))
+    if (!c->out || (mode != MUON_PRODUCT_DENSE && !c->offsets))
         return fail(MUON_ERR_INVALID_ARG, who, "out and, with groups, offsets must be non-NULL");
     if (misaligned(c->out) || ((uintptr_t)c->offsets & 3u) != 0)
         return fail(MUON_ERR_ALIGNMENT, who, "out must be 16-byte aligned (offsets 4-byte)");
@@ -415,7 +416,7 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
     a.n = c->n;
     a.k = c->k;
     a.groups = c->groups;
-    a.mode = c->mode;
+    a.mode = mode;
     a.accumulate = c->accumulate;
     a.vec = c->ld_out * size % 16 == 0 && a.out_stride * size % 16 == 0;
     if (!product_fits(a)) return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
@@ -425,7 +426,7 @@ muon_status muon_fp8_product(const muon_fp8_product_config* c, void* stream) try
         (c->k > 0 && (overlap(out, codes_of(c->a, c->m, c->k, 1)) || overlap(out, scales_of(c->a, c->m, c->k, 1)) ||
                       overlap(out, codes_of(c->b, c->n, c->k, b_groups)) || overlap(out, scales_of(c->b, c->n, c->k, b_groups)))))
         return fail(MUON_ERR_INVALID_ARG, who, "out overlaps an operand or offsets");
-    return launched(launch_product(a, c->a.format, c->out_dtype, c->full_sums != 0, static_cast<hipStream_t>(stream)), who);
+    return launched(launch_product(a, c->a.format, c->out_dtype, full_sums, static_cast<hipStream_t>(stream)), who);
 } catch (...) {
     return MUON_ERR_INVALID_ARG;
 }

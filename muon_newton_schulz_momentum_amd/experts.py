@@ -347,7 +347,7 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
     codes = a.codes
     with _on(codes, stream, a.scales, b.codes, b.scales, offsets, out):
         k = L.muon_fp8_product_config()
-        k.mode, k.groups = _GROUPS[group], 1
+        k.mode, k.groups = _GROUPS[group] | (L.MUON_PRODUCT_FULL_SUMS if full_sums else 0), 1
         (m, _), (*stack, n, _) = _operand(k.a, "a", a, False), _operand(k.b, "b", b, group == "rows")
         if b.codes.device != codes.device or b.codes.dtype != torch.float8_e4m3fn:
             raise ValueError(f"b must have dtype float8_e4m3fn on {codes.device}")
@@ -370,6 +370,5 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
             k.ld_out = _rows("out", out)
             k.out_stride = out.stride(0) if group == "depth" and k.groups > 1 else m * k.ld_out
         k.out, k.out_dtype, k.accumulate = out.data_ptr(), _DTYPES[out.dtype], 1 if accumulate else 0
-        k.full_sums = 1 if full_sums else 0
         L.check(L.muon_fp8_product(C.byref(k), _stream_ptr(codes)), "muon_fp8_product")
     return out

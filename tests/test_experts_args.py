@@ -353,8 +353,23 @@ def test_grouping_refuses_every_overlap():
         assert L.muon_balance_step(A, B, 8, 0.1, out, None) == L.MUON_ERR_INVALID_ARG and b"overlap" in L.muon_last_error()
 
 
-@pytest.mark.parametrize("value", [2, -1])
-def test_product_refuses_an_unknown_kind_of_sums(value):
-    c = _product(0, full_sums=value)
-    assert L.muon_fp8_product(C.byref(c), None) == L.MUON_ERR_INVALID_ARG
-    assert b"full_sums" in L.muon_last_error()
+@pytest.mark.parametrize("mode", [8, 32, 16 + 3, 16 + 4, -1])
+def test_product_refuses_modes_that_it_does_not_know(mode):
+    c = _product(mode, groups=1)
+    assert L.muon_fp8_product(C.byref(c), None) == L.MUON_ERR_INVALID_ARG and b"unknown mode" in L.muon_last_error()
+
+
+@pytest.mark.parametrize("mode,kw,status", [
+    (0, dict(groups=2), L.MUON_ERR_INVALID_ARG), (1, dict(offsets=None), L.MUON_ERR_INVALID_ARG),
+    (1, dict(b__stride=200 * 256 - 16), L.MUON_ERR_SHAPE), (2, dict(out_stride=1599), L.MUON_ERR_SHAPE),
+    (0, dict(out=A), L.MUON_ERR_INVALID_ARG),
+])
+def test_full_sums_are_checked_like_the_mode_they_go_with(mode, kw, status):
+    c = _product(mode, **kw)
+    c.mode |= L.MUON_PRODUCT_FULL_SUMS
+    assert L.muon_fp8_product(C.byref(c), None) == status
+
+
+def test_product_config_has_its_size():
+    """Programs built against the header pass it by its layout."""
+    assert C.sizeof(L.muon_fp8_product_config) == 184
