@@ -658,6 +658,10 @@ __device__ __forceinline__ double token_sum16(double v) {
     return v + dppd<XCHG_8>(v);
 }
 
+// The exponentials of a row: by the instruction where 16 lanes have all of it (what is below 2^-126 is lost).
+template <int LT>
+__device__ __forceinline__ float row_exp(float v) { return LT == 16 ? __expf(v) : expf(v); }
+
 // The sum of v over the slots that have this lane's expert, in their order, and whether this is the first of them.
 template <int LT, class S>
 __device__ __forceinline__ S of_expert(int e, float v, int top_k, bool& first) {
@@ -689,7 +693,7 @@ __device__ __forceinline__ ChosenSoftmax chosen_softmax(int e, float xj, float t
     bool first;
     const double all = of_expert<LT, double>(e, gw, top_k, first) * scale;
     const double ex = e >= 0 ? exp((double)xj - (double)top) : 0.0;
-    z += sum(e >= 0 && first ? ex - (double)__expf(xj - top) : 0.0);
+    z += sum(e >= 0 && first ? ex - (double)row_exp<LT>(xj - top) : 0.0);
     const double inv = z > 0.0 ? 1.0 / z : 0.0, s = ex * inv;
     const double mean = sum((double)gw * scale * s);       // (scaled here: float32's rounding would be a part of the difference)
     return {e >= 0 ? (float)(s * (all - mean)) : 0.f, (float)(-mean * inv)};
@@ -768,7 +772,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_kernel(RouteB
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                out[c][v] = out[c][v] > -INFINITY ? __expf(out[c][v] - top) : 0.f;
+                out[c][v] = out[c][v] > -INFINITY ? row_exp<16>(out[c][v] - top) : 0.f;
                 z += (double)out[c][v];
             }
         z = token_sum16(z);
@@ -860,7 +864,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void route_backward_wave_kernel(R
         double z = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            x[i] = x[i] > -INFINITY ? __expf(x[i] - top) : 0.f;
+            x[i] = x[i] > -INFINITY ? row_exp<64>(x[i] - top) : 0.f;
             z += (double)x[i];
         }
         z = dev::wave_sum(z);
