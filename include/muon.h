@@ -566,12 +566,12 @@ typedef struct muon_fp8_product_config {
 
 /* 8-bit product on the matrix cores, one rounding to out's type.  A bfloat16 out is by default
  * summed by the 8-bit matrix instruction: of each 8 neighbouring products it drops what is
- * below 2^-13 of the largest, so a sum is off by up to 7 * 2^-13 of the sum of those
- * largest products (about 1.4e-5 of a sum of normal values; but where large products
- * cancel, small ones beside them are lost), before full float32 sums over the groups of 8.
- * With MUON_PRODUCT_FULL_SUMS, and always for a float32 out, all sums are full float32 sums: the codes go
- * through the bfloat16 instruction, at half the rate, where a value below 2^-126 is rounded
- * to a multiple of 2^-133 and one whose code was rounded up to 2^128 is an infinity.
+ * below 2^-13 of the largest, and adds up the groups of 8 in float32.  So a sum is off by up
+ * to 7 * 2^-13 of the sum of those largest products: about 1.4e-5 of a sum of normal values,
+ * but where large products cancel, small ones beside them are lost.
+ * With MUON_PRODUCT_FULL_SUMS, and always for a float32 out, all sums are full float32 sums:
+ * the codes go through the bfloat16 instruction, at half the rate, where a value below 2^-126
+ * is rounded to a multiple of 2^-133 and one whose code was rounded up to 2^128 is an infinity.
  * Errors: INVALID_ARG (NULL, enum, groups, accumulate into bfloat16, out overlapping an
  * operand or offsets), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
 MUON_API muon_status muon_fp8_product(const muon_fp8_product_config* config, void* stream);
