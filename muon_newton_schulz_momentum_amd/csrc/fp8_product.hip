@@ -24,6 +24,7 @@
 #include "device_common.h"
 #include "experts.h"
 #include "fp8_panel.h"
+#include "tile_walk.h"
 
 namespace muon {
 namespace {
@@ -38,25 +39,10 @@ typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef i32x4 i32x4_any __attribute__((aligned(2)));
 typedef uint2 uint2_any __attribute__((aligned(2)));
 
-constexpr int NUM_XCD = 8, CUS = 256;
+using namespace tiles;
+
 constexpr int KB = 128;                   // values that share a scale
-
-// Bands of BAND tile rows, each walked column by column: the tiles an XCD runs at once share panels.
-constexpr int BAND = 8;
-__device__ __forceinline__ void band_decode(int t, int tm, int tn, int& ti, int& tj) {
-    const int band = t / (BAND * tn);
-    const int r0 = band * BAND;
-    const int rows = min(BAND, tm - r0);
-    const int w = t - band * BAND * tn;
-    tj = w / rows;
-    ti = r0 + (w - tj * rows);
-}
-
-__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
-    const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-    return (const uint8_t*)(((uint64_t)hi << 32) | lo);
-}
+constexpr int WAVES = 8, THREADS = 64 * WAVES;
 
 // 4 bytes a lane from the buffer at offset + soffset to lds_base + 4 * lane; past the buffer's end zeros arrive.
 // The compiler does not track the load; loads end in order, so waiting for a later one covers it.
@@ -93,150 +79,6 @@ __device__ __forceinline__ void pin(f32x16 (&acc)[FM][FN]) {
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
-}
-
-constexpr int WAVES = 8, THREADS = 64 * WAVES;
-
-struct Tile {
-    int64_t m0, n0;            // first row of a, of b
-    int rows_a, rows_b;        // rows of either inside the tile
-    int group, kb0, kb1;       // blocks of k [kb0, kb1)
-};
-
-// Whether a depth-grouped launch deals every group's tiles to all XCDs (see Walk): where that leaves an XCD 8 of them,
-// which share operand panels, and workgroups have several tiles.
-__device__ __forceinline__ bool in_parts(const ProductArgs& p) {
-    return p.mode == MUON_PRODUCT_DEPTH && p.tiles_m * p.tiles_n >= 8 * NUM_XCD && p.tiles > (int)gridDim.x;
-}
-
-// The segments' bounds, clamped to the operand, and in ends how many tile rows lie before each segment (rows-grouped),
-// or the groups in the order of falling depth (depth-grouped), into LDS, by the whole workgroup.
-constexpr int SORT_MAX_GROUPS = 256;      // each thread compares with every group; many groups even out by themselves
-__device__ __forceinline__ void read_segments(const ProductArgs& p, int tile_rows, int* bounds, int* ends, int64_t* wave_tot) {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int64_t limit = p.mode == MUON_PRODUCT_ROWS ? p.m : (p.k + KB - 1) / KB * KB;
-    for (int g = tid; g <= p.groups; g += THREADS) bounds[g] = (int)min(max((int64_t)p.offsets[g], (int64_t)0), limit);
-    if (tid == 0 && p.mode == MUON_PRODUCT_ROWS) ends[0] = 0;
-    __syncthreads();
-    if (p.mode != MUON_PRODUCT_ROWS) {
-        auto depth = [&](int g) { return bounds[g + 1] / KB - bounds[g] / KB; };
-        for (int g = tid; g < p.groups; g += THREADS) {
-            int before = g;
-            if (in_parts(p) && p.groups <= SORT_MAX_GROUPS) {
-                before = 0;
-                const int mine = depth(g);
-                for (int h = 0; h < p.groups; ++h) {
-                    const int other = depth(h);
-                    before += other > mine || (other == mine && h < g);
-                }
-            }
-            ends[before] = g;
-        }
-        __syncthreads();
-        return;
-    }
-    // sums in 64 bits and capped: falling offsets, which are not allowed, must not lead outside the operand either
-    int64_t before = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += THREADS) {
-        const int g = g0 + tid;
-        int64_t inc = g < p.groups ? ((int64_t)max(bounds[g + 1] - bounds[g], 0) + tile_rows - 1) / tile_rows : 0;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int64_t o = __shfl_up(inc, off, 64);
-            if (lane >= off) inc += o;
-        }
-        if (lane == 63) wave_tot[wave] = inc;
-        __syncthreads();
-        int64_t total = 0;
-        for (int w = 0; w < WAVES; ++w) {
-            if (w < wave) inc += wave_tot[w];
-            total += wave_tot[w];
-        }
-        if (g < p.groups) ends[g + 1] = (int)min(before + inc, (int64_t)1 << 30);
-        before += total;
-        __syncthreads();
-    }
-}
-
-// Tile t of the launch, of up to tile_rows x tile_cols.
-__device__ __forceinline__ Tile decode(const ProductArgs& p, int t, int tile_rows, int tile_cols, const int* bounds,
-                                       const int* ends) {
-    auto at = [](const int* v) { return __builtin_amdgcn_readfirstlane(*v); };
-    Tile r;
-    r.group = 0;
-    r.kb0 = 0;
-    r.kb1 = (int)((p.k + KB - 1) / KB);
-    int64_t m1 = p.m;
-    int tm, tn;
-    if (p.mode == MUON_PRODUCT_ROWS) {
-        tm = t / p.tiles_n;
-        tn = t - tm * p.tiles_n;
-        int lo = 0, hi = p.groups;                         // the last g with ends[g] <= tm
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (at(ends + mid) <= tm) lo = mid;
-            else hi = mid;
-        }
-        r.group = lo;
-        r.m0 = at(bounds + lo) + (int64_t)(tm - at(ends + lo)) * tile_rows;
-        m1 = at(bounds + lo + 1);
-    } else {
-        if (p.mode == MUON_PRODUCT_DEPTH) {
-            const int per = p.tiles_m * p.tiles_n, nth = t / per;
-            t -= nth * per;
-            r.group = at(ends + nth);
-            r.kb0 = at(bounds + r.group) / KB;
-            r.kb1 = max(at(bounds + r.group + 1) / KB, r.kb0);
-        }
-        band_decode(t, p.tiles_m, p.tiles_n, tm, tn);
-        r.m0 = (int64_t)tm * tile_rows;
-    }
-    r.n0 = (int64_t)tn * tile_cols;
-    r.rows_a = (int)min(m1 - r.m0, (int64_t)tile_rows);
-    r.rows_b = (int)min(p.n - r.n0, (int64_t)tile_cols);
-    return r;
-}
-
-// A workgroup's tiles.  Workgroups are dealt to the XCDs in turn.  Each XCD takes a contiguous share of the tiles and its
-// workgroups walk it together, so that the tiles that run at once share operand panels in its L2.
-//
-// Depth-grouped, tiles of different groups take different times.  In parts, each XCD takes an eighth of every group's
-// tiles, the deepest group first, and its workgroups walk them to and fro: 8 groups of 1024 x 4096 over 9000 in
-// float32 82 us against 104, 64 groups 390 against 406; with one tile in a part the shared panels are lost (128 groups of
-// 512 x 1024: 57 us against 42).
-struct Walk {
-    int pos, last, step, turn; // tile or place in the XCD's share, its end, step; to and fro: a step's other length
-    int chunk, chunks;         // tiles of a group in a part, parts of a group; 0 without parts
-};
-__device__ __forceinline__ Walk walk(const ProductArgs& p, const int* ends) {
-    const int xcd = blockIdx.x % NUM_XCD, nth = blockIdx.x / NUM_XCD, all = gridDim.x / NUM_XCD;
-    if (in_parts(p)) {
-        const int per = p.tiles_m * p.tiles_n;
-        const int chunk = (per + NUM_XCD - 1) / NUM_XCD, chunks = (per + chunk - 1) / chunk;
-        const int mine = (p.groups * chunks - xcd + NUM_XCD - 1) / NUM_XCD;
-        return {nth, mine * chunk, 2 * (all - nth) - 1, 2 * nth + 1, chunk, chunks};
-    }
-    int total = p.tiles;
-    if (p.mode == MUON_PRODUCT_ROWS)
-        total = (int)min((int64_t)__builtin_amdgcn_readfirstlane(ends[p.groups]) * p.tiles_n, (int64_t)p.tiles);
-    const int share = total / NUM_XCD, rest = total % NUM_XCD;
-    const int first = xcd * share + min(xcd, rest);
-    return {first + nth, first + share + (xcd < rest ? 1 : 0), all, all, 0, 0};
-}
-// The tile at the walk's place or the next one that has one, which the walk is put past; -1 at the end.
-__device__ __forceinline__ int next_tile(const ProductArgs& p, Walk& w) {
-    while (w.pos < w.last) {
-        const int at = w.pos, step = w.step;
-        w.pos += step;
-        w.step = w.turn;
-        w.turn = step;
-        if (w.chunk == 0) return at;
-        // part q of all groups' parts is the XCD's q / 8-th; the last part of a group may be short
-        const int q = at / w.chunk * NUM_XCD + blockIdx.x % NUM_XCD, group = q / w.chunks;
-        const int t = (q - group * w.chunks) * w.chunk + at % w.chunk, per = p.tiles_m * p.tiles_n;
-        if (t < per) return group * per + t;
-    }
-    return -1;
 }
 
 // ---- 256 x 256 tiles ----------------------------------------------------------------------
@@ -286,8 +128,8 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const int fr = lane & 31, fk = lane >> 5;
     const int kp = (int)((p.k + KB - 1) / KB) * KB, sp = (kp / KB + 3) / 4 * 4;
 
-    if (p.mode != MUON_PRODUCT_DENSE) read_segments(p, TILE, bounds, ends, wave_tot);
-    Walk my = walk(p, ends);
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments<KB, THREADS>(p, TILE, bounds, ends, wave_tot);
+    Walk my = walk<1>(p, ends);
     int t = next_tile(p, my);
     if (t < 0) return;
 
@@ -531,7 +373,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         __builtin_amdgcn_wave_barrier();
     };
 
-    Tile x = decode(p, t, TILE, TILE, bounds, ends);
+    Tile x = decode<KB, 1>(p, t, TILE, TILE, bounds, ends);
     begin(x);
     fill();
     for (;;) {
@@ -555,7 +397,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         const bool more = t >= 0;
         // the next tile's first loads run beside this one's stores
         if (more) {
-            x = decode(p, t, TILE, TILE, bounds, ends);
+            x = decode<KB, 1>(p, t, TILE, TILE, bounds, ends);
             begin(x);
         }
         write(0);
@@ -586,10 +428,10 @@ __global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
     __shared__ int64_t wave_tot[WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fr = lane & 15, fk = lane >> 4;
-    if (p.mode != MUON_PRODUCT_DENSE) read_segments(p, FEW_ROWS, bounds, ends, wave_tot);
-    Walk my = walk(p, ends);
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments<KB, THREADS>(p, FEW_ROWS, bounds, ends, wave_tot);
+    Walk my = walk<1>(p, ends);
     for (int t = next_tile(p, my); t >= 0; t = next_tile(p, my)) {
-        const Tile x = decode(p, t, FEW_ROWS, COLS, bounds, ends);
+        const Tile x = decode<KB, 1>(p, t, FEW_ROWS, COLS, bounds, ends);
         const bool per_group = p.mode == MUON_PRODUCT_ROWS;
         // offsets of the lane's rows from the tile's first; rows past the end repeat the last: their sums are not stored
         const uint8_t* abase = p.a + x.m0 * p.lda;
@@ -704,24 +546,10 @@ __global__ __launch_bounds__(THREADS) void product_few_kernel(ProductArgs p) {
     }
 }
 
-// Tiles of a launch, at most; -1 for too many.
-int64_t count_tiles(ProductArgs& a, int tile_rows, int tile_cols) {
-    a.tiles_n = (int32_t)((a.n + tile_cols - 1) / tile_cols);
-    a.tiles_m = (int32_t)((a.m + tile_rows - 1) / tile_rows);
-    // every segment may end inside a tile, but not more of them than there are rows
-    int64_t rows = a.tiles_m;
-    if (a.mode == MUON_PRODUCT_ROWS) rows = a.m / tile_rows + (a.m < a.groups ? a.m : (int64_t)a.groups);
-    if (a.mode == MUON_PRODUCT_DEPTH) rows *= a.groups;
-    const int64_t total = rows * a.tiles_n;
-    if (total >= ((int64_t)1 << 31) - 2 * CUS) return -1;   // a workgroup's step past its last tile stays an int
-    a.tiles = (int32_t)total;
-    return total;
-}
-
 template <int AFMT, class OUT, bool PRECISE>
 hipError_t product_as(ProductArgs a, hipStream_t s) {
     ProductArgs few = a, thin = a;
-    const int64_t n_big = count_tiles(a, TILE, TILE), n_few = count_tiles(few, FEW_ROWS, 64), n_thin = count_tiles(thin, FEW_ROWS, 16);
+    const int64_t n_big = count_tiles<1>(a, TILE, TILE), n_few = count_tiles<1>(few, FEW_ROWS, 64), n_thin = count_tiles<1>(thin, FEW_ROWS, 16);
     if (n_big == 0) return hipSuccess;
     // What each would take, in us, from what they measured: big tiles by the round of 256 (256 x 4096 x 4096: 38 us in
     // bfloat16, 76 with full sums), the others by the depth of a wave where there are few tiles and by the blocks of all
@@ -748,7 +576,7 @@ hipError_t product_as(ProductArgs a, hipStream_t s) {
 
 }  // namespace
 
-bool product_fits(ProductArgs a) { return count_tiles(a, TILE, TILE) >= 0; }
+bool product_fits(ProductArgs a) { return count_tiles<1>(a, TILE, TILE) >= 0; }
 
 hipError_t launch_product(ProductArgs a, int32_t a_format, int32_t out_dtype, bool full_sums, hipStream_t s) {
     const bool e4m3 = a_format == MUON_FP8_E4M3;
