@@ -576,6 +576,182 @@ typedef struct muon_fp8_product_config {
  * operand or offsets), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
 MUON_API muon_status muon_fp8_product(const muon_fp8_product_config* config, void* stream);
 
+/* ---- expert layers: gated blocks, 8-bit integer products, rows gathered and combined ------ */
+
+/* What stands between the calls above in an expert's layer: its rows gathered, the gated block of its first two
+ * projections with the gradients that a plan's step reads, products with 8-bit integer weights for serving, and
+ * the rows combined to their tokens by muon_route's weights.  All of the above holds here too: no plan, no
+ * allocation, no synchronisation, capture, 16-byte aligned pointers, sizes of 0, overlaps.
+ * bfloat16 and float32 rows may begin anywhere (any row stride >= the columns) unless stated. */
+
+#define MUON_ACT_SILU 0  /* v / (1 + exp(-v))                                                 */
+#define MUON_ACT_GELU 1  /* v * P(N < v), N standard normal (no approximation by tanh)         */
+#define MUON_ACT_RELU 2  /* max(v, 0), slope 0 at 0                                            */
+
+#define MUON_OPERANDS_BF16 0
+#define MUON_OPERANDS_INT8 1
+
+/* A matrix, or one per group, of bfloat16 values, or of 8-bit integer codes with a float32 scale for each row. */
+typedef struct muon_operand {
+    const void* data;
+    const float* scales;   /* 8-bit integers: one per row (4-byte aligned); else NULL            */
+    int64_t ld;            /* row stride in elements; of codes a multiple of 16, at least round_up(k, 128);
+                              below 2^22 (codes: 2^23)                                          */
+    int64_t stride;        /* elements between the groups' matrices (of codes a multiple of 16) */
+    int64_t stride_scales; /* and their scales                                                  */
+} muon_operand;
+
+typedef struct muon_int8_quantize_config {
+    const void* src;       /* batch matrices of float32 or bfloat16                             */
+    int32_t src_dtype;     /* MUON_DTYPE_*                                                      */
+    int32_t per;           /* with gather: choices per source row (top_k), >= 1                 */
+    int64_t batch;         /* batch * rows below 2^31                                           */
+    int64_t rows, cols;    /* of each quantised matrix                                          */
+    int64_t ld;            /* row stride of src in elements, >= cols                            */
+    int64_t batch_stride;  /* between src's matrices, in elements                               */
+    /* Device, nullable (batch 1): quantised row r is source row gather[r] / per, or zero where
+     * that is outside [0, src_rows). */
+    const int32_t* gather;
+    int64_t src_rows;
+    /* Device, nullable (batch 1): one int32; rows from *limit on are left as they were. */
+    const int32_t* limit;
+    int8_t* codes;         /* batch x rows x round_up(cols, 128), zeros outside cols            */
+    float* scales;         /* batch x rows                                                      */
+} muon_int8_quantize_config;
+
+/* Quantises rows (tokens, or a weight's output channels) to 8-bit integers.  A row's scale is its largest magnitude
+ * / 127 rounded to float32, a code is value / scale (the exact quotient) rounded to the nearest whole number,
+ * ties to even, and kept in [-127, 127]; where the scale is 0 codes are 0.  A row with an infinity or a NaN gets
+ * the scale NaN and codes 0, so that its products are NaN and no others.
+ * Errors: INVALID_ARG (NULL, enum, gather or limit with batch > 1, per < 1, overlap), SHAPE (sizes, strides),
+ * ALIGNMENT, HIP. */
+MUON_API muon_status muon_int8_quantize(const muon_int8_quantize_config* config, void* stream);
+
+typedef struct muon_int8_product_config {
+    int32_t mode;             /* MUON_PRODUCT_DENSE or MUON_PRODUCT_ROWS                        */
+    int32_t groups;           /* 1 for MUON_PRODUCT_DENSE; at most MUON_MAX_EXPERTS             */
+    int64_t m, n, k;          /* k at most 131071, so that no sum leaves 32 bits                */
+    muon_operand a, b;        /* a: m x k; b: n x k, with MUON_PRODUCT_ROWS one per group       */
+    const int32_t* offsets;   /* device, groups + 1, not falling (NULL for DENSE); values outside a's rows are
+                                 clamped to them                                                */
+    void* out;                /* m rows of n                                                    */
+    int64_t ld_out;           /* in elements, >= n                                              */
+    int32_t out_dtype;        /* MUON_DTYPE_*                                                   */
+    int32_t reserved;
+} muon_int8_product_config;
+
+/* out[i][j] = (sum over k of a's codes times b's) * a.scales[i] * b.scales[j]: the sum exact, in 32-bit integers, then
+ * float32 products from left to right and one rounding to out's type.  MUON_PRODUCT_ROWS as in muon_fp8_product: rows
+ * outside every segment are left as they were.
+ * Errors: INVALID_ARG (NULL, enum, groups, overlap), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
+MUON_API muon_status muon_int8_product(const muon_int8_product_config* config, void* stream);
+
+typedef struct muon_gated_config {
+    int32_t mode;             /* MUON_PRODUCT_DENSE or MUON_PRODUCT_ROWS                        */
+    int32_t groups;           /* 1 for MUON_PRODUCT_DENSE; at most MUON_MAX_EXPERTS             */
+    int32_t operands;         /* MUON_OPERANDS_*, of x, gate and up alike (INT8: k at most 131071) */
+    int32_t activation;       /* MUON_ACT_*                                                     */
+    int64_t m, n, k;          /* rows, features of the block, values of a row                   */
+    muon_operand x;           /* m x k                                                          */
+    muon_operand gate, up;    /* n x k, with MUON_PRODUCT_ROWS one per group                    */
+    const int32_t* offsets;   /* as in muon_int8_product                                        */
+    uint16_t* out;            /* bfloat16, m rows of n                                          */
+    int64_t ld_out;           /* in elements, >= n                                              */
+    /* bfloat16, m rows of n each, both or neither: x gate^T and x up^T, for muon_gated_backward. */
+    uint16_t* pre_gate;
+    uint16_t* pre_up;
+    int64_t ld_pre;           /* in elements, >= n                                              */
+} muon_gated_config;
+
+/* The gated block of a feed-forward layer in one pass: out = act(x gate^T) * (x up^T), each row by its group's
+ * matrices.  Sums in float32 (8-bit integers: exact, then scaled as in muon_int8_product); the activation and
+ * the product are formed from the unrounded sums and rounded once.  Rows outside every segment are left as they were.
+ * Errors: as muon_int8_product; one of pre_gate / pre_up NULL. */
+MUON_API muon_status muon_gated(const muon_gated_config* config, void* stream);
+
+typedef struct muon_gated_backward_config {
+    int32_t mode, groups, activation;   /* muon_gated's                                         */
+    int32_t grad_dtype;       /* of grad_gate and grad_up: MUON_DTYPE_*                         */
+    int32_t accumulate;       /* 1: added to grad_gate and grad_up (float32 only)               */
+    int32_t reserved;
+    int64_t m, n, k;
+    muon_operand x, gate, up; /* muon_gated's, bfloat16                                         */
+    const int32_t* offsets;
+    const uint16_t* grad;     /* gradient of out: bfloat16, m rows of n                         */
+    int64_t ld_grad;
+    const uint16_t* pre_gate; /* as muon_gated left them                                        */
+    const uint16_t* pre_up;
+    int64_t ld_pre;
+    /* Written: the gradients of x gate^T and x up^T, bfloat16, m rows of n each (the operands of the products below,
+     * rounded to bfloat16 as those take them).  They may be pre_gate and pre_up, with the same stride. */
+    uint16_t* grad_pre_gate;
+    uint16_t* grad_pre_up;
+    int64_t ld_grad_pre;
+    uint16_t* grad_x;         /* nullable: bfloat16, m rows of k                                */
+    int64_t ld_grad_x;
+    void* grad_gate;          /* nullable, both or neither: per group n rows of k               */
+    void* grad_up;
+    int64_t ld_grad_w;
+    int64_t stride_grad_w;    /* elements between groups                                        */
+} muon_gated_backward_config;
+
+/* The gradients of muon_gated.  With d = grad, g = pre_gate, u = pre_up:
+ *     dg = d u act'(g),  du = d act(g)   (float32, rounded once),
+ *     grad_x = dg gate + du up,  grad_gate = dg^T x,  grad_up = du^T x over each group's rows (zeros without rows),
+ * sums in float32.  Rows of the row outputs outside every segment are left as they were and have no part in the
+ * weight gradients.  x is not read without weight gradients, gate and up not without grad_x.
+ * Errors: as muon_gated; accumulate into bfloat16. */
+MUON_API muon_status muon_gated_backward(const muon_gated_backward_config* config, void* stream);
+
+typedef struct muon_gather_rows_config {
+    const void* src;          /* src_rows x cols                                                */
+    int64_t src_rows, cols, ld;
+    int32_t dtype;            /* MUON_DTYPE_*, of src, out and y                                */
+    int32_t per;              /* choices per source row (top_k), >= 1                           */
+    const int32_t* rows;      /* device, n_rows: muon_group_rows' rows                          */
+    int64_t n_rows;           /* at most 2^30                                                   */
+    const int32_t* limit;     /* device, nullable: one int32; rows of out from *limit on are left as they were */
+    void* out;                /* nullable: n_rows x cols                                        */
+    int64_t ld_out;
+    /* Nullable: src_rows * per factors (muon_route's weights). */
+    const float* weights;
+    /* Nullable, together: n_rows x cols, muon_group_rows' position (src_rows * per), and the gradient of the weights. */
+    const void* y;
+    int64_t ld_y;
+    const int32_t* position;
+    float* grad_weights;      /* src_rows * per                                                 */
+} muon_gather_rows_config;
+
+/* Rows in expert order: out[r] = src[c / per] for the choice c = rows[r] (times weights[c], in float32, rounded once), zeros
+ * where c is outside [0, src_rows * per).  Without weights that is how tokens reach their experts.  With them and
+ * src the gradient of muon_combine_rows' out it is the gradient of its rows, and with y those rows grad_weights[c] =
+ * sum over columns of src[c / per] * y[r] for r = position[c] (float32; 0 where that is outside [0, n_rows)).
+ * Errors: INVALID_ARG (NULL, enum, per, no output, overlap), SHAPE (sizes, strides, src_rows * per of 2^31 or more),
+ * ALIGNMENT, HIP. */
+MUON_API muon_status muon_gather_rows(const muon_gather_rows_config* config, void* stream);
+
+typedef struct muon_combine_rows_config {
+    const void* src;          /* n_rows x cols                                                  */
+    int64_t n_rows, cols, ld;
+    int32_t dtype;            /* of src: MUON_DTYPE_*                                           */
+    int32_t out_dtype;        /* MUON_DTYPE_*                                                   */
+    int64_t tokens;           /* tokens * top_k below 2^31                                      */
+    int32_t top_k;            /* 1..MUON_MAX_TOP_K                                              */
+    int32_t reserved;
+    const int32_t* position;  /* device, tokens x top_k: muon_group_rows' position              */
+    const float* weights;     /* nullable (all 1): tokens x top_k                               */
+    const void* residual;     /* nullable: tokens x cols of out_dtype, added; may be out        */
+    int64_t ld_residual;
+    void* out;                /* tokens x cols                                                  */
+    int64_t ld_out;
+} muon_combine_rows_config;
+
+/* Rows back to their tokens: out[t] = residual[t] + sum over j of weights[t][j] * src[position[t][j]], j in rising order,
+ * in float32 and rounded once; positions outside [0, n_rows) add nothing, whatever their weight.  Without weights
+ * it is the gradient of muon_gather_rows' src.
+ * Errors: INVALID_ARG (NULL, enum, overlap), SHAPE (sizes, strides), ALIGNMENT, HIP. */
+MUON_API muon_status muon_combine_rows(const muon_combine_rows_config* config, void* stream);
+
 /* ---- per-kernel timing (HIP events on the launching stream) --------------------------- */
 
 #define MUON_KERNEL_MOMENTUM 0

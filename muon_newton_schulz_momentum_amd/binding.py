@@ -78,6 +78,11 @@ MUON_PRODUCT_DENSE = 0
 MUON_PRODUCT_ROWS = 1
 MUON_PRODUCT_DEPTH = 2
 MUON_PRODUCT_FULL_SUMS = 16
+MUON_ACT_SILU = 0
+MUON_ACT_GELU = 1
+MUON_ACT_RELU = 2
+MUON_OPERANDS_BF16 = 0
+MUON_OPERANDS_INT8 = 1
 
 
 class muon_param_desc(C.Structure):
@@ -144,6 +149,56 @@ class muon_fp8_product_config(C.Structure):
                 ("ld_out", C.c_int64), ("out_stride", C.c_int64), ("out_dtype", C.c_int32), ("accumulate", C.c_int32)]
 
 
+class muon_operand(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("scales", C.c_void_p), ("ld", C.c_int64), ("stride", C.c_int64),
+                ("stride_scales", C.c_int64)]
+
+
+class muon_int8_quantize_config(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("src_dtype", C.c_int32), ("per", C.c_int32), ("batch", C.c_int64),
+                ("rows", C.c_int64), ("cols", C.c_int64), ("ld", C.c_int64), ("batch_stride", C.c_int64),
+                ("gather", C.c_void_p), ("src_rows", C.c_int64), ("limit", C.c_void_p), ("codes", C.c_void_p),
+                ("scales", C.c_void_p)]
+
+
+class muon_int8_product_config(C.Structure):
+    _fields_ = [("mode", C.c_int32), ("groups", C.c_int32), ("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64),
+                ("a", muon_operand), ("b", muon_operand), ("offsets", C.c_void_p), ("out", C.c_void_p),
+                ("ld_out", C.c_int64), ("out_dtype", C.c_int32), ("reserved", C.c_int32)]
+
+
+class muon_gated_config(C.Structure):
+    _fields_ = [("mode", C.c_int32), ("groups", C.c_int32), ("operands", C.c_int32), ("activation", C.c_int32),
+                ("m", C.c_int64), ("n", C.c_int64), ("k", C.c_int64), ("x", muon_operand), ("gate", muon_operand),
+                ("up", muon_operand), ("offsets", C.c_void_p), ("out", C.c_void_p), ("ld_out", C.c_int64),
+                ("pre_gate", C.c_void_p), ("pre_up", C.c_void_p), ("ld_pre", C.c_int64)]
+
+
+class muon_gated_backward_config(C.Structure):
+    _fields_ = [("mode", C.c_int32), ("groups", C.c_int32), ("activation", C.c_int32), ("grad_dtype", C.c_int32),
+                ("accumulate", C.c_int32), ("reserved", C.c_int32), ("m", C.c_int64), ("n", C.c_int64),
+                ("k", C.c_int64), ("x", muon_operand), ("gate", muon_operand), ("up", muon_operand),
+                ("offsets", C.c_void_p), ("grad", C.c_void_p), ("ld_grad", C.c_int64), ("pre_gate", C.c_void_p),
+                ("pre_up", C.c_void_p), ("ld_pre", C.c_int64), ("grad_pre_gate", C.c_void_p),
+                ("grad_pre_up", C.c_void_p), ("ld_grad_pre", C.c_int64), ("grad_x", C.c_void_p),
+                ("ld_grad_x", C.c_int64), ("grad_gate", C.c_void_p), ("grad_up", C.c_void_p),
+                ("ld_grad_w", C.c_int64), ("stride_grad_w", C.c_int64)]
+
+
+class muon_gather_rows_config(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("src_rows", C.c_int64), ("cols", C.c_int64), ("ld", C.c_int64),
+                ("dtype", C.c_int32), ("per", C.c_int32), ("rows", C.c_void_p), ("n_rows", C.c_int64),
+                ("limit", C.c_void_p), ("out", C.c_void_p), ("ld_out", C.c_int64), ("weights", C.c_void_p),
+                ("y", C.c_void_p), ("ld_y", C.c_int64), ("position", C.c_void_p), ("grad_weights", C.c_void_p)]
+
+
+class muon_combine_rows_config(C.Structure):
+    _fields_ = [("src", C.c_void_p), ("n_rows", C.c_int64), ("cols", C.c_int64), ("ld", C.c_int64),
+                ("dtype", C.c_int32), ("out_dtype", C.c_int32), ("tokens", C.c_int64), ("top_k", C.c_int32),
+                ("reserved", C.c_int32), ("position", C.c_void_p), ("weights", C.c_void_p), ("residual", C.c_void_p),
+                ("ld_residual", C.c_int64), ("out", C.c_void_p), ("ld_out", C.c_int64)]
+
+
 _P = C.c_void_p  # muon_plan*
 
 
@@ -201,6 +256,12 @@ muon_balance_step = _fn("muon_balance_step", C.c_int32,
                         [C.c_void_p, C.c_void_p, C.c_int32, C.c_float, C.c_void_p, C.c_void_p])
 muon_fp8_quantize = _fn("muon_fp8_quantize", C.c_int32, [C.POINTER(muon_fp8_quantize_config), C.c_void_p])
 muon_fp8_product = _fn("muon_fp8_product", C.c_int32, [C.POINTER(muon_fp8_product_config), C.c_void_p])
+muon_int8_quantize = _fn("muon_int8_quantize", C.c_int32, [C.POINTER(muon_int8_quantize_config), C.c_void_p])
+muon_int8_product = _fn("muon_int8_product", C.c_int32, [C.POINTER(muon_int8_product_config), C.c_void_p])
+muon_gated = _fn("muon_gated", C.c_int32, [C.POINTER(muon_gated_config), C.c_void_p])
+muon_gated_backward = _fn("muon_gated_backward", C.c_int32, [C.POINTER(muon_gated_backward_config), C.c_void_p])
+muon_gather_rows = _fn("muon_gather_rows", C.c_int32, [C.POINTER(muon_gather_rows_config), C.c_void_p])
+muon_combine_rows = _fn("muon_combine_rows", C.c_int32, [C.POINTER(muon_combine_rows_config), C.c_void_p])
 muon_timing_enable = _fn("muon_timing_enable", C.c_int32, [_P, C.c_int32])
 muon_timing_read = _fn("muon_timing_read", C.c_int32,
                        [_P, C.c_int32, C.POINTER(C.c_double), C.POINTER(C.c_int64), C.POINTER(C.c_double)])
@@ -218,7 +279,8 @@ EXPORTED = [
     "muon_graph_capture", "muon_graph_capture_ex", "muon_graph_launch",
     "muon_graph_node_count", "muon_graph_destroy", "muon_route", "muon_route_backward",
     "muon_group_rows_workspace", "muon_group_rows_capacity", "muon_group_rows", "muon_balance_step",
-    "muon_fp8_quantize", "muon_fp8_product", "muon_timing_enable", "muon_timing_read",
+    "muon_fp8_quantize", "muon_fp8_product", "muon_int8_quantize", "muon_int8_product", "muon_gated",
+    "muon_gated_backward", "muon_gather_rows", "muon_combine_rows", "muon_timing_enable", "muon_timing_read",
     "muon_timing_reset", "muon_kernel_name", "muon_plan_destroy", "muon_status_string",
     "muon_last_error",
 ]

@@ -22,7 +22,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 
 HIP_SOURCES = ["api.hip", "elementwise.hip", "ns_gemm.hip", "ns_small.hip",
-               "experts_api.hip", "route.hip", "fp8_quantize.hip", "fp8_product.hip"]
+               "experts_api.hip", "route.hip", "fp8_quantize.hip", "fp8_product.hip",
+               "layers_api.hip", "layer_rows.hip", "layer_product.hip"]
 CXX_SOURCES = ["plan.cpp"]
 ARCH = "gfx950"
 

@@ -1,5 +1,6 @@
 """Torch-side wrapper of the routed-expert operators of libmuon: routing, grouping rows by expert, 8-bit
-block quantisation and 8-bit products.
+block quantisation and 8-bit products; the gated block and its gradients, 8-bit integer products, and rows gathered to
+the experts and combined back.
 
 One layer's matrices in a training step, with the optimizer's `harness.Plan` at its end:
 
@@ -13,6 +14,26 @@ One layer's matrices in a training step, with the optimizer's `harness.Plan` at 
     dx = product(dy, w_t, offsets=g.offsets, group="rows")
     product(dy_t, x_t, offsets=g.offsets, group="depth", out=G)      # the gradients that the plan reads
     bias = balance_step(bias, g.counts, rate)
+
+The same layer in bfloat16 between its ends, and back:
+
+    x = gather_rows(tokens, g.rows, per=top_k, limit=g.limit)
+    h, pre_gate, pre_up = gated(x, W_gate, W_up, offsets=g.offsets, save=True)
+    ...                                                              # y: h through the experts' third matrices
+    out = combine_rows(y, g.position, weights, residual=tokens)
+    ...
+    dy, dweights = combine_rows_backward(dout, y, g.rows, g.position, weights, limit=g.limit)
+    ...                                                              # dh: dy through the third matrices
+    dx, *_ = gated_backward(dh, x, W_gate, W_up, pre_gate, pre_up, offsets=g.offsets, grad_gate=G_gate, grad_up=G_up)
+    dtokens = combine_rows(dx, g.position)
+    dlogits = route_backward(logits, chosen, dweights, score="sigmoid")
+
+and in 8-bit integers for serving (weights quantised once, a scale for each output channel):
+
+    q = quantize_int8(tokens, rows=g.rows, per=top_k, limit=g.limit)
+    h = gated(q, Q_gate, Q_up, offsets=g.offsets)
+    y = product_int8(quantize_int8(h, limit=g.limit), Q_down, offsets=g.offsets)
+    out = combine_rows(y, g.position, weights, residual=tokens)
 
 Every operator runs in libmuon's HIP kernels on the current stream of its tensors' device; this module
 checks tensors, allocates outputs and marshals arguments.  Sizes that only the device knows (segments, the
@@ -38,6 +59,7 @@ BLOCK = 128
 _SCORES = {"softmax": L.MUON_SCORE_SOFTMAX, "sigmoid": L.MUON_SCORE_SIGMOID}
 _FORMATS = {"e4m3": (L.MUON_FP8_E4M3, torch.float8_e4m3fn), "e5m2": (L.MUON_FP8_E5M2, torch.float8_e5m2)}
 _GROUPS = {None: L.MUON_PRODUCT_DENSE, "rows": L.MUON_PRODUCT_ROWS, "depth": L.MUON_PRODUCT_DEPTH}
+_ACTIVATIONS = {"silu": L.MUON_ACT_SILU, "gelu": L.MUON_ACT_GELU, "relu": L.MUON_ACT_RELU}
 _DTYPES = {torch.float32: L.MUON_DTYPE_F32, torch.bfloat16: L.MUON_DTYPE_BF16}
 
 
@@ -372,3 +394,313 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
         k.out, k.out_dtype, k.accumulate = out.data_ptr(), _DTYPES[out.dtype], 1 if accumulate else 0
         L.check(L.muon_fp8_product(C.byref(k), _stream_ptr(codes)), "muon_fp8_product")
     return out
+
+
+@dataclass
+class Int8:
+    """A matrix of 8-bit integers, or a stack of them: codes (.., rows, cols rounded up to 128) and a float32 scale for
+    each row (.., rows)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    cols: int
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[-2]
+
+    @staticmethod
+    def empty(rows: int, cols: int, *, stack: Optional[int] = None, device="cuda") -> "Int8":
+        lead = () if stack is None else (stack,)
+        return Int8(torch.empty(*lead, rows, _up(cols, BLOCK), dtype=torch.int8, device=device),
+                    torch.empty(*lead, rows, dtype=torch.float32, device=device), cols)
+
+    def dequantize(self) -> torch.Tensor:
+        """The float32 values (with torch operations; for looking at them)."""
+        return self.codes[..., :self.cols].float() * self.scales.unsqueeze(-1)
+
+
+def _check_int8(name: str, q: Int8, like: torch.Tensor) -> torch.Size:
+    shape = q.codes.shape
+    if q.cols < 1 or len(shape) < 2 or shape[-1] != _up(q.cols, BLOCK) or q.scales.shape != shape[:-1]:
+        raise ValueError(f"{name}: codes {tuple(shape)} and scales {tuple(q.scales.shape)} are not those of {q.cols} columns")
+    if q.codes.dtype != torch.int8 or q.scales.dtype != torch.float32:
+        raise ValueError(f"{name} must have int8 codes and float32 scales")
+    if q.codes.device != like.device or q.scales.device != like.device:
+        raise ValueError(f"{name} is on {q.codes.device}, expected {like.device}")
+    return shape
+
+
+def quantize_int8(src: torch.Tensor, *, rows: Optional[torch.Tensor] = None, per: int = 1,
+                  limit: Optional[torch.Tensor] = None, out: Optional[Int8] = None, stream=None) -> Int8:
+    """8-bit integer copy of a float32 or bfloat16 matrix (or stack of them), with a scale for each row: tokens of
+    activations, output channels of weights (muon_int8_quantize).
+
+    With `rows` (int32), quantised row r is src row rows[r] // per, or zeros for -1.  `limit` (one int32 on the
+    device): rows from there on are left as they were.  `out`: an Int8 to write into.
+    """
+    if src.dim() not in (2, 3) or src.dtype not in _DTYPES:
+        raise ValueError("src must be a float32 or bfloat16 matrix or stack of matrices")
+    stack = src.shape[0] if src.dim() == 3 else None
+    if stack is not None and (rows is not None or limit is not None):
+        raise ValueError("rows and limit go with one matrix")
+    cols, n = src.shape[-1], src.shape[-2] if rows is None else rows.numel()
+    with _on(src, stream, rows, limit, *(() if out is None else (out.codes, out.scales))):
+        if rows is not None:
+            _tensor("rows", rows, src, torch.int32, (n,))
+        if limit is not None:
+            _tensor("limit", limit, src, torch.int32, (1,))
+        if out is None:
+            out = Int8.empty(n, cols, stack=stack, device=src.device)
+        else:
+            shape = _check_int8("out", out, src)
+            if tuple(shape[:-1]) != ((n,) if stack is None else (stack, n)) or out.cols != cols:
+                raise ValueError(f"out must hold {(n, cols)}")
+            if not out.codes.is_contiguous() or not out.scales.is_contiguous():
+                raise ValueError("out must be contiguous")
+        k = L.muon_int8_quantize_config()
+        k.src, k.src_dtype = src.data_ptr(), _DTYPES[src.dtype]
+        k.batch, k.rows, k.cols, k.ld = 1 if stack is None else stack, n, cols, _rows("src", src)
+        k.batch_stride = src.stride(0) if stack is not None and stack > 1 else 0
+        if rows is not None:
+            k.gather, k.per, k.src_rows = rows.data_ptr(), per, src.shape[0]
+        if limit is not None:
+            k.limit = limit.data_ptr()
+        k.codes, k.scales = out.codes.data_ptr(), out.scales.data_ptr()
+        L.check(L.muon_int8_quantize(C.byref(k), _stream_ptr(src)), "muon_int8_quantize")
+    return out
+
+
+def _layer_operand(o: L.muon_operand, name: str, t, like: torch.Tensor, stacked: bool):
+    """Fills o with a bfloat16 tensor or an Int8, checked; (groups or None, rows, columns)."""
+    if isinstance(t, Int8):
+        shape, cols, data = _check_int8(name, t, like), t.cols, t.codes
+        if t.scales.dim() and t.scales.shape[-1] > 1 and t.scales.stride(-1) != 1:
+            raise ValueError(f"{name}.scales must be contiguous")
+        o.scales = t.scales.data_ptr()
+        if stacked and shape[0] > 1:
+            o.stride_scales = t.scales.stride(0)
+    else:
+        data = _tensor(name, t, like, torch.bfloat16, contiguous=False)
+        shape, cols = t.shape, t.shape[-1] if t.dim() else 0
+    if len(shape) != (3 if stacked else 2):
+        raise ValueError(f"{name} must be {'a stack of matrices' if stacked else 'one matrix'}")
+    o.data, o.ld = data.data_ptr(), _rows(name, data)
+    if stacked and shape[0] > 1:
+        o.stride = data.stride(0)
+    return (shape[0] if stacked else None), shape[-2], cols
+
+
+def _tensors(*operands):
+    return [t for o in operands for t in ((o.codes, o.scales) if isinstance(o, Int8) else (o,))]
+
+
+def _by_group(k, offsets: Optional[torch.Tensor], like: torch.Tensor, *groups) -> None:
+    """Mode, groups and offsets of k, checked against the stacks'."""
+    k.mode, k.groups = L.MUON_PRODUCT_DENSE, 1
+    if offsets is not None:
+        _tensor("offsets", offsets, like, torch.int32)
+        k.mode, k.groups, k.offsets = L.MUON_PRODUCT_ROWS, offsets.numel() - 1, offsets.data_ptr()
+        if offsets.dim() != 1 or any(g != k.groups for g in groups):
+            raise ValueError("offsets must be (groups + 1,)")
+
+
+def _result(name: str, out: Optional[torch.Tensor], like: torch.Tensor, shape, dtype) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _tensor(name, out, like, dtype, shape, contiguous=False)
+
+
+def product_int8(a: Int8, b: Int8, *, offsets: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """a times the transpose of b in 8-bit integers (muon_int8_product): exact sums, times both rows' scales.
+
+    (m, n) of a (m, k) and b (n, k), or with `offsets` of a stack b (groups, n, k), the rows offsets[g] to
+    offsets[g + 1] of a by b[g]; rows outside every segment are not written.
+    """
+    codes = a.codes
+    with _on(codes, stream, *_tensors(a, b), offsets, out):
+        k = L.muon_int8_product_config()
+        _, m, ka = _layer_operand(k.a, "a", a, codes, False)
+        groups, n, kb = _layer_operand(k.b, "b", b, codes, offsets is not None)
+        if ka != kb:
+            raise ValueError(f"a has {ka} columns, b {kb}")
+        k.m, k.n, k.k = m, n, ka
+        _by_group(k, offsets, codes, groups)
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        out = _result("out", out, codes, (m, n), dtype if out is None else _DTYPES)
+        k.out, k.ld_out, k.out_dtype = out.data_ptr(), _rows("out", out), _DTYPES[out.dtype]
+        L.check(L.muon_int8_product(C.byref(k), _stream_ptr(codes)), "muon_int8_product")
+    return out
+
+
+def gated(x, gate, up, *, activation: str = "silu", offsets: Optional[torch.Tensor] = None, save: bool = False,
+          out: Optional[torch.Tensor] = None, stream=None):
+    """The gated block act(x gate^T) * (x up^T) in one pass (muon_gated), in bfloat16.
+
+    x (rows, k) and gate, up (n, k), or with `offsets` stacks (groups, n, k), the rows offsets[g] to offsets[g + 1] by
+    gate[g] and up[g]; rows outside every segment are not written.  All three are bfloat16 or all three Int8.
+    activation: "silu", "gelu" or "relu".  With `save` the triple of the result, x gate^T and x up^T, which
+    gated_backward takes.
+    """
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    i8 = isinstance(x, Int8)
+    if isinstance(gate, Int8) != i8 or isinstance(up, Int8) != i8:
+        raise ValueError("x, gate and up must be of one kind")
+    like = x.codes if i8 else x
+    with _on(like, stream, *_tensors(x, gate, up), offsets, out):
+        k = L.muon_gated_config()
+        k.operands, k.activation = L.MUON_OPERANDS_INT8 if i8 else L.MUON_OPERANDS_BF16, _ACTIVATIONS[activation]
+        _, k.m, k.k = _layer_operand(k.x, "x", x, like, False)
+        groups, k.n, kg = _layer_operand(k.gate, "gate", gate, like, offsets is not None)
+        shape_up = _layer_operand(k.up, "up", up, like, offsets is not None)
+        if kg != k.k or shape_up != (groups, k.n, kg):
+            raise ValueError("x, gate and up must agree in their columns, gate and up in their shape")
+        _by_group(k, offsets, like, groups)
+        size = (k.m, k.n)
+        out = _result("out", out, like, size, torch.bfloat16)
+        k.out, k.ld_out = out.data_ptr(), _rows("out", out)
+        if save:
+            pre = torch.empty(2, *size, dtype=torch.bfloat16, device=like.device)
+            if pre[1].data_ptr() % 16:                         # odd sizes: each begins on a boundary of its own
+                pre = [torch.empty(size, dtype=torch.bfloat16, device=like.device) for _ in range(2)]
+            k.pre_gate, k.pre_up, k.ld_pre = pre[0].data_ptr(), pre[1].data_ptr(), k.n
+        L.check(L.muon_gated(C.byref(k), _stream_ptr(like)), "muon_gated")
+    return (out, pre[0], pre[1]) if save else out
+
+
+def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, pre_gate: torch.Tensor,
+                   pre_up: torch.Tensor, *, activation: str = "silu", offsets: Optional[torch.Tensor] = None,
+                   grad_x: Optional[torch.Tensor] = None, grad_gate: Optional[torch.Tensor] = None,
+                   grad_up: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.bfloat16, accumulate: bool = False,
+                   reuse: bool = False, stream=None):
+    """The gradients of `gated` with respect to x, gate and up (muon_gated_backward), from the gradient of its result and
+    what it saved.
+
+    grad_x is bfloat16; grad_gate and grad_up are of `dtype` or go into the given tensors (float32 ones are added to
+    with `accumulate`).  Rows outside every segment of offsets are not written in grad_x and have no part in the others.
+    With `reuse` the saved tensors serve as the workspace and do not keep their values.
+    """
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
+    if accumulate and (grad_gate is None or grad_up is None):
+        raise ValueError("accumulate needs grad_gate and grad_up")
+    with _on(x, stream, grad, gate, up, pre_gate, pre_up, offsets, grad_x, grad_gate, grad_up):
+        k = L.muon_gated_backward_config()
+        k.activation, k.accumulate = _ACTIVATIONS[activation], 1 if accumulate else 0
+        _, k.m, k.k = _layer_operand(k.x, "x", x, x, False)
+        groups, k.n, kg = _layer_operand(k.gate, "gate", gate, x, offsets is not None)
+        shape_up = _layer_operand(k.up, "up", up, x, offsets is not None)
+        if kg != k.k or shape_up != (groups, k.n, kg):
+            raise ValueError("x, gate and up must agree in their columns, gate and up in their shape")
+        _by_group(k, offsets, x, groups)
+        size = (k.m, k.n)
+        _tensor("grad", grad, x, torch.bfloat16, size, contiguous=False)
+        k.grad, k.ld_grad = grad.data_ptr(), _rows("grad", grad)
+        for name, t in (("pre_gate", pre_gate), ("pre_up", pre_up)):
+            _tensor(name, t, x, torch.bfloat16, size, contiguous=False)
+        k.pre_gate, k.pre_up, k.ld_pre = pre_gate.data_ptr(), pre_up.data_ptr(), _rows("pre_gate", pre_gate)
+        if _rows("pre_up", pre_up) != k.ld_pre:
+            raise ValueError("pre_gate and pre_up must have the same row stride")
+        if reuse:
+            work = (pre_gate, pre_up)
+            k.ld_grad_pre = k.ld_pre
+        else:
+            work = [torch.empty(k.m, _up(k.n, 8), dtype=torch.bfloat16, device=x.device) for _ in range(2)]
+            k.ld_grad_pre = _up(k.n, 8)
+        k.grad_pre_gate, k.grad_pre_up = work[0].data_ptr(), work[1].data_ptr()
+        grad_x = _result("grad_x", grad_x, x, (k.m, k.k), torch.bfloat16)
+        k.grad_x, k.ld_grad_x = grad_x.data_ptr(), _rows("grad_x", grad_x)
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        if (grad_gate is None) != (grad_up is None):
+            raise ValueError("grad_gate and grad_up go together")
+        shape = tuple(gate.shape)
+        dtype = dtype if grad_gate is None else grad_gate.dtype
+        if dtype not in _DTYPES:
+            raise ValueError("grad_gate must be float32 or bfloat16")
+        grad_gate, grad_up = _result("grad_gate", grad_gate, x, shape, dtype), _result("grad_up", grad_up, x, shape, dtype)
+        k.grad_gate, k.grad_up, k.grad_dtype = grad_gate.data_ptr(), grad_up.data_ptr(), _DTYPES[dtype]
+        k.ld_grad_w = _rows("grad_gate", grad_gate)
+        if groups is not None and groups > 1:
+            k.stride_grad_w = grad_gate.stride(0)
+        if _rows("grad_up", grad_up) != k.ld_grad_w or (k.groups > 1 and grad_up.stride(0) != k.stride_grad_w):
+            raise ValueError("grad_gate and grad_up must have the same strides")
+        L.check(L.muon_gated_backward(C.byref(k), _stream_ptr(x)), "muon_gated_backward")
+    return grad_x, grad_gate, grad_up
+
+
+def _gather(src, rows, per, limit, out, stream, weights=None, y=None, position=None):
+    if src.dim() != 2 or src.dtype not in _DTYPES:
+        raise ValueError("the source must be a float32 or bfloat16 matrix")
+    with _on(src, stream, rows, limit, out, weights, y, position):
+        _tensor("rows", rows, src, torch.int32)
+        if rows.dim() != 1:
+            raise ValueError("rows must be (rows,)")
+        if limit is not None:
+            _tensor("limit", limit, src, torch.int32, (1,))
+        n, cols = rows.numel(), src.shape[1]
+        out = _result("out", out, src, (n, cols), src.dtype)
+        k = L.muon_gather_rows_config()
+        k.src, k.src_rows, k.cols, k.ld = src.data_ptr(), src.shape[0], cols, _rows("source", src)
+        k.dtype, k.per, k.rows, k.n_rows = _DTYPES[src.dtype], per, rows.data_ptr(), n
+        k.limit = None if limit is None else limit.data_ptr()
+        k.out, k.ld_out = out.data_ptr(), _rows("out", out)
+        grad = None
+        if weights is not None:
+            _tensor("weights", weights, src, torch.float32, (src.shape[0], per))
+            _tensor("position", position, src, torch.int32, weights.shape)
+            _tensor("y", y, src, src.dtype, (n, cols), contiguous=False)
+            grad = torch.empty_like(weights)
+            k.weights, k.y, k.ld_y, k.position, k.grad_weights = (weights.data_ptr(), y.data_ptr(), _rows("y", y),
+                                                                  position.data_ptr(), grad.data_ptr())
+        if n > 0 or (grad is not None and grad.numel() > 0):
+            L.check(L.muon_gather_rows(C.byref(k), _stream_ptr(src)), "muon_gather_rows")
+    return out, grad
+
+
+def gather_rows(src: torch.Tensor, rows: torch.Tensor, *, per: int = 1, limit: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Tokens in expert order: row r is src row rows[r] // per, or zeros for -1 (muon_gather_rows).  `limit` (one int32
+    on the device): rows from there on are left as they were.  Its gradient is `combine_rows` without weights."""
+    return _gather(src, rows, per, limit, out, stream)[0]
+
+
+def combine_rows(src: torch.Tensor, position: torch.Tensor, weights: Optional[torch.Tensor] = None, *,
+                 residual: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Experts' rows back to their tokens: out[t] = residual[t] + the sum over j of weights[t, j] * src[position[t, j]]
+    (muon_combine_rows); positions of -1 add nothing.  The result is of `dtype` (src's if not given).  `residual`
+    may be `out`."""
+    if src.dim() != 2 or src.dtype not in _DTYPES or position.dim() != 2:
+        raise ValueError("src must be a float32 or bfloat16 matrix, position (tokens, top_k)")
+    with _on(src, stream, position, weights, residual, out):
+        _tensor("position", position, src, torch.int32)
+        size = (position.shape[0], src.shape[1])
+        if weights is not None:
+            _tensor("weights", weights, src, torch.float32, position.shape)
+        dtype = out.dtype if out is not None else src.dtype if dtype is None else dtype
+        if dtype not in _DTYPES:
+            raise ValueError("dtype must be float32 or bfloat16")
+        out = _result("out", out, src, size, dtype)
+        k = L.muon_combine_rows_config()
+        k.src, k.n_rows, k.cols, k.ld, k.dtype = src.data_ptr(), src.shape[0], src.shape[1], _rows("src", src), _DTYPES[src.dtype]
+        k.tokens, k.top_k, k.position = position.shape[0], position.shape[1], position.data_ptr()
+        k.weights = None if weights is None else weights.data_ptr()
+        if residual is not None:
+            _tensor("residual", residual, src, dtype, size, contiguous=False)
+            k.residual, k.ld_residual = residual.data_ptr(), _rows("residual", residual)
+        k.out, k.ld_out, k.out_dtype = out.data_ptr(), _rows("out", out), _DTYPES[dtype]
+        L.check(L.muon_combine_rows(C.byref(k), _stream_ptr(src)), "muon_combine_rows")
+    return out
+
+
+def combine_rows_backward(grad: torch.Tensor, src: torch.Tensor, rows: torch.Tensor, position: torch.Tensor,
+                          weights: torch.Tensor, *, limit: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None, stream=None):
+    """The gradients of `combine_rows` with respect to src and weights, from the gradient of its result (of src's dtype):
+    zeros in the rows that pad a segment; rows from `limit` on are left as they were; 0 for a weight without a row."""
+    if position.dim() != 2:
+        raise ValueError("position must be (tokens, top_k)")
+    return _gather(grad, rows, position.shape[1], limit, out, stream, weights, src, position)

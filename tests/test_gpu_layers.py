@@ -1,0 +1,627 @@
+"""The expert layers' operators on the GPU against their float64 definitions (oracle/layers_oracle.py).
+
+Tolerances.  u = 2^-24 is float32's half step, h = 2^-8 bfloat16's.
+  * a sum of k bfloat16 products: the products are exact in float32; instructions add 16 of them at a time into a float32
+    sum, and a tile may add up to 8 partial sums: (ceil(k / 16) + 16 + 8) roundings of at most 2 u (a sum that cuts
+    off rather than rounds) of the sum of magnitudes S: sum_tol(k) S;
+  * the activations' slopes are at most 1.13 (gelu; silu 1.1), so a pre-activation's error e moves the value by
+    1.13 e and what lies beyond it in second order; 1.2 covers both here, where e is far below 1;
+    expf and erfcf are within 4 steps of 2 u and their argument's rounding moves them by x^2 u (|x| < 12
+    here: 144 u), the rest is at most 8 roundings: 160 u of the value;
+  * 8-bit integer sums are exact: conversion to float32 and two products, 3 u;
+  * every result: its own rounding, u or h, and 2^-126 where it is below the normal numbers;
+  * codes and scales are compared for equality.
+Gradients of x and of the weights are compared with the definition's of the pre-activations' gradients that the call
+formed and rounded (with reuse they are left where the saved values were), and these with theirs.
+"""
+import itertools
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+from oracle import layers_oracle as orc  # noqa: E402
+
+U, H, TINY = 2.0 ** -24, 2.0 ** -8, 2.0 ** -126
+HALF = {torch.float32: U, torch.bfloat16: H}
+ACTS = ("silu", "gelu", "relu")
+
+
+def X():
+    from muon_newton_schulz_momentum_amd import experts
+    return experts
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def sum_tol(k):
+    return (-(-k // 16) + 24) * 2 * U
+
+
+def _close(got, want, tol, what=""):
+    got, off = _np(got), np.abs(_np(got) - want)
+    worst = np.unravel_index(np.argmax(off - tol), off.shape) if off.size else ()
+    assert (off <= tol).all(), f"{what} at {worst}: {got[worst]} is not {want[worst]} within {np.broadcast_to(tol, off.shape)[worst]}"
+
+
+def _matrix(seed, *shape, std=1.0, dtype=torch.bfloat16, gap=0):
+    """Normal values; with a gap between the rows, which holds NaN."""
+    *lead, rows, cols = shape
+    t = torch.full((*lead, rows, cols + gap), float("nan"), dtype=dtype, device="cuda")
+    t[..., :cols] = (torch.randn(*shape, device="cuda", generator=_gen(seed)) * std).to(dtype)
+    return t[..., :cols]
+
+
+def _offsets(ends):
+    return None if ends is None else torch.tensor(ends, dtype=torch.int32, device="cuda")
+
+
+# rows, n, k, offsets, gap
+SHAPES = [
+    (1, 1, 1, None, 0),
+    (1, 64, 64, None, 0),
+    (2, 40, 96, None, 8),
+    (3, 7, 31, None, 0),
+    (5, 130, 8, None, 1),
+    (17, 65, 257, None, 3),
+    (33, 256, 128, None, 0),
+    (64, 129, 200, None, 0),
+    (129, 128, 64, None, 8),
+    (255, 300, 192, None, 0),
+    (257, 384, 320, None, 0),
+    (300, 127, 999, None, 0),
+    (513, 520, 130, None, 2),
+    (1, 24, 40, [0, 1], 0),
+    (1, 24, 40, [0, 0, 1, 1], 0),
+    (7, 33, 72, [0, 0, 3, 3, 7], 0),
+    (60, 64, 128, [5, 20, 20, 41], 0),                     # rows before the first and behind the last segment
+    (60, 70, 65, [-3, 10, 30, 900], 5),                    # bounds outside the rows
+    (300, 136, 264, [0, 1, 2, 130, 130, 299, 300], 0),
+    (700, 257, 136, [0, 256, 300, 300, 699, 700], 8),
+    (900, 128, 192, [0, 10, 520, 890], 0),
+    (40, 96, 80, [20] * 9, 0),                             # no segment has a row
+    (2000, 40, 24, list(range(0, 2001, 10)), 0),           # many short segments
+    (1500, 512, 640, [0, 700, 1500], 0),
+    (1100, 1024, 512, None, 0),
+    (48, 2048, 1024, None, 0),
+    (9, 1000, 2056, [0, 2, 2, 9], 0),
+]
+
+
+def _rows_kept(t, hit, sentinel):
+    return bool((t[~torch.from_numpy(hit).cuda()] == sentinel).all())
+
+
+@pytest.mark.parametrize("m,n,k,ends,gap", SHAPES)
+@pytest.mark.parametrize("act", ACTS)
+def test_gated(m, n, k, ends, gap, act):
+    lead = () if ends is None else (len(ends) - 1,)
+    x, w = _matrix(1, m, k, gap=gap), [_matrix(2 + i, *lead, n, k, std=1.5 / math.sqrt(k), gap=gap) for i in range(2)]
+    out = torch.full((m, n + gap), 7.0, dtype=torch.bfloat16, device="cuda")
+    h, g, u = X().gated(x, *w, activation=act, offsets=_offsets(ends), save=True, out=out[:, :n])
+    again = X().gated(x, *w, activation=act, offsets=_offsets(ends))
+    assert h.data_ptr() == out.data_ptr()
+    hit = orc.rows_product(_np(x), _np(w[0]), ends)[2]
+    assert _rows_kept(out, hit, 7.0) and (gap == 0 or bool((out[:, n:] == 7.0).all()))
+    assert torch.equal(h[torch.from_numpy(hit).cuda()], again[torch.from_numpy(hit).cuda()])
+    (gr, gs, _), (ur, us, _) = (orc.rows_product(_np(x), _np(v), ends) for v in w)
+    eg, eu = sum_tol(k) * gs, sum_tol(k) * us
+    _close(g[torch.from_numpy(hit).cuda()], gr[hit], (eg + H * np.abs(gr) + TINY)[hit], "gate")
+    _close(u[torch.from_numpy(hit).cuda()], ur[hit], (eu + H * np.abs(ur) + TINY)[hit], "up")
+    a, _ = orc.activation(gr, act)
+    tol = 1.2 * eg * (np.abs(ur) + eu) + np.abs(a) * eu + (H + 160 * U) * np.abs(a * ur) + TINY
+    _close(h[torch.from_numpy(hit).cuda()], (a * ur)[hit], tol[hit], "h")
+
+
+def _int8(seed, *shape, stack_gap=0):
+    """Random codes over the whole range, the padding zero, and scales."""
+    *lead, rows, cols = shape
+    codes = torch.zeros(*lead, rows + stack_gap, -(-cols // 128) * 128, dtype=torch.int8, device="cuda")[..., :rows, :]
+    codes[..., :cols] = torch.randint(-128, 128, shape, device="cuda", generator=_gen(seed)).to(torch.int8)
+    scales = torch.rand(*lead, rows, device="cuda", generator=_gen(seed + 50)) * 0.02 / math.sqrt(cols) + 1e-4
+    return X().Int8(codes, scales, cols)
+
+
+def _scaled(a, b, ends):
+    """(product, rows covered): the sums of whole numbers, exact in float64, times the scales."""
+    y, _, hit = orc.rows_product(_np(a.codes[..., :a.cols]), _np(b.codes[..., :b.cols]), ends)
+    y *= _np(a.scales)[:, None]
+    for g, lo, hi in orc.segments(ends, len(y)):
+        y[lo:hi] *= _np(b.scales if g is None else b.scales[g])
+    return y, hit
+
+
+@pytest.mark.parametrize("m,n,k,ends,gap", SHAPES)
+def test_product_int8(m, n, k, ends, gap):
+    lead = () if ends is None else (len(ends) - 1,)
+    a, b = _int8(3, m, k), _int8(4, *lead, n, k, stack_gap=gap)
+    want, hit = _scaled(a, b, ends)
+    pick = torch.from_numpy(hit).cuda()
+    for dtype in (torch.float32, torch.bfloat16):
+        out = torch.full((m, n + gap), 7.0, dtype=dtype, device="cuda")
+        X().product_int8(a, b, offsets=_offsets(ends), out=out[:, :n])
+        assert _rows_kept(out, hit, 7.0) and (gap == 0 or bool((out[:, n:] == 7.0).all()))
+        _close(out[:, :n][pick], want[hit], ((HALF[dtype] + 3 * U) * np.abs(want) + TINY)[hit], str(dtype))
+        assert torch.equal(out[:, :n][pick], X().product_int8(a, b, offsets=_offsets(ends), dtype=dtype)[pick])
+
+
+@pytest.mark.parametrize("m,n,k,ends,gap", SHAPES[::2] + SHAPES[-3:])
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_int8(m, n, k, ends, gap, act):
+    lead = () if ends is None else (len(ends) - 1,)
+    x, g, u = _int8(5, m, k), _int8(6, *lead, n, k, stack_gap=gap), _int8(7, *lead, n, k, stack_gap=gap)
+    x.scales.mul_(100)
+    out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    h, pg, pu = X().gated(x, g, u, activation=act, offsets=_offsets(ends), save=True, out=out)
+    (gr, hit), (ur, _) = _scaled(x, g, ends), _scaled(x, u, ends)
+    pick = torch.from_numpy(hit).cuda()
+    assert _rows_kept(out, hit, 7.0)
+    eg, eu = 3 * U * np.abs(gr), 3 * U * np.abs(ur)
+    _close(pg[pick], gr[hit], (eg + H * np.abs(gr) + TINY)[hit], "gate")
+    _close(pu[pick], ur[hit], (eu + H * np.abs(ur) + TINY)[hit], "up")
+    a, _ = orc.activation(gr, act)
+    _close(h[pick], (a * ur)[hit], (1.2 * eg * (np.abs(ur) + eu) + np.abs(a) * eu + (H + 160 * U) * np.abs(a * ur) + TINY)[hit], "h")
+
+
+@pytest.mark.parametrize("m,n,k,ends,gap", SHAPES)
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_backward(m, n, k, ends, gap, act):
+    lead = () if ends is None else (len(ends) - 1,)
+    x, w = _matrix(1, m, k, gap=gap), [_matrix(2 + i, *lead, n, k, std=1.5 / math.sqrt(k), gap=gap) for i in range(2)]
+    d, g, u = (_matrix(8 + i, m, n, std=s, gap=gap) for i, s in enumerate((0.1, 1.5, 1.0)))
+    kept = [t.clone() for t in (g, u)]
+    grad_x = torch.full((m, k + gap), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, w16g, w16u = X().gated_backward(d, x, *w, g, u, activation=act, offsets=_offsets(ends), grad_x=grad_x[:, :k])
+    assert torch.equal(g, kept[0]) and torch.equal(u, kept[1])
+    hit = orc.rows_product(_np(x), _np(w[0]), ends)[2]
+    pick = torch.from_numpy(hit).cuda()
+    assert _rows_kept(grad_x, hit, 7.0) and (gap == 0 or bool((grad_x[:, k:] == 7.0).all()))
+    before = [torch.randn(w[0].shape, device="cuda", generator=_gen(20 + i)) for i in range(2)]
+    acc = [t.clone() for t in before]
+    again, *acc = X().gated_backward(d, x, *w, g, u, activation=act, offsets=_offsets(ends), grad_gate=acc[0], grad_up=acc[1],
+                                     accumulate=True, reuse=True)
+    assert torch.equal(again[pick], grad_x[:, :k][pick])
+    # the pre-activations' gradients, as the call left them
+    want = orc.gated_pre_grads(_np(d), _np(kept[0]), _np(kept[1]), act)
+    value, slope = orc.activation(_np(kept[0]), act)
+    # the slope is a sum whose terms are at most 1.2 + |g| / 4 in magnitude
+    slack = 160 * U * np.abs(_np(d) * _np(kept[1])) * (1.2 + np.abs(_np(kept[0])) / 4), 160 * U * np.abs(_np(d) * value)
+    for got, ref, extra, name in zip((g, u), want, slack, ("dg", "du")):
+        _close(got[pick], ref[hit], (H * np.abs(ref) + extra + TINY)[hit], name)
+    dg, du = _np(g), _np(u)
+    ref, size = orc.gated_grad_x(dg, du, _np(w[0]), _np(w[1]), ends)
+    _close(grad_x[:, :k][pick], ref[hit], (sum_tol(2 * n + 32) * size + H * np.abs(ref) + TINY)[hit], "grad_x")
+    for got16, got32, start, dd, name in ((w16g, acc[0], before[0], dg, "gate"), (w16u, acc[1], before[1], du, "up")):
+        ref, size = orc.gated_grad_w(dd, _np(x), ends)
+        longest = max([hi - lo for _, lo, hi in orc.segments(ends, m)], default=1)
+        tol = sum_tol(longest) * size
+        _close(got16, ref, tol + H * np.abs(ref) + TINY, name)
+        _close(got32, ref + _np(start), tol + U * (np.abs(ref) + np.abs(ref + _np(start))) + TINY, name + " added")
+
+
+@pytest.mark.parametrize("ends", [None, [0, 0, 0]])
+def test_gated_backward_without_rows(ends):
+    lead = () if ends is None else (2,)
+    x, w = _matrix(1, 0, 24), [_matrix(2 + i, *lead, 40, 24) for i in range(2)]
+    d = _matrix(3, 0, 40)
+    gx, gg, gu = X().gated_backward(d, x, *w, d, d, offsets=_offsets(ends), dtype=torch.float32)
+    assert gx.shape == (0, 24) and not gg.any() and not gu.any() and gg.shape == w[0].shape
+    assert X().gated(x, *w, offsets=_offsets(ends)).shape == (0, 40)
+
+
+def test_gradients_against_differences():
+    """Of the whole block in the oracle's float64: the formula's gradients are those of the formula, and the call's are the
+    formula's (above)."""
+    rng = np.random.Generator(np.random.PCG64(4))
+    x, G, U_, d = rng.normal(size=(9, 12)), rng.normal(size=(2, 10, 12)), rng.normal(size=(2, 10, 12)), rng.normal(size=(9, 10))
+    ends = [0, 4, 9]
+    for act in ("silu", "gelu"):
+        g, u = orc.rows_product(x, G, ends)[0], orc.rows_product(x, U_, ends)[0]
+        dg, du = orc.gated_pre_grads(d, g, u, act)
+        grads = (orc.gated_grad_x(dg, du, G, U_, ends)[0], orc.gated_grad_w(dg, x, ends)[0], orc.gated_grad_w(du, x, ends)[0])
+        for which, grad in enumerate(grads):
+            args = [x, G, U_]
+            step = rng.normal(size=args[which].shape)
+            loss = [(d * orc.gated(*[a + s * step if i == which else a for i, a in enumerate(args)], act, ends)).sum() for s in (1e-5, -1e-5)]
+            assert abs((loss[0] - loss[1]) / 2e-5 - (grad * step).sum()) < 1e-5 * (1 + abs((grad * step).sum()))
+
+
+def test_values_that_are_not_numbers_stay_in_their_rows():
+    m, n, k = 140, 150, 96
+    x, w = _matrix(1, m, k), [_matrix(2 + i, n, k, std=0.1) for i in range(2)]
+    clean = X().gated(x, *w)
+    x[3, 5], x[77, 0] = float("nan"), float("inf")
+    h = X().gated(x, *w)
+    other = torch.ones(m, dtype=torch.bool, device="cuda")
+    other[[3, 77]] = False
+    assert torch.equal(h[other], clean[other]) and bool(h[3].isnan().all()) and not bool(h[77].isfinite().any())
+    # a weight's NaN stays in its column, a group's in its rows
+    wn = [t.clone() for t in w]
+    wn[1][10, 3] = float("nan")
+    h = X().gated(_matrix(1, m, k), *wn)
+    cols = torch.ones(n, dtype=torch.bool, device="cuda")
+    cols[10] = False
+    assert torch.equal(h[:, cols], clean[:, cols]) and bool(h[:, 10].isnan().all())
+    # gradients: a NaN behind the last segment or in another group's rows reaches no weight
+    x, ends = _matrix(1, m, k), [0, 50, 90, 120]
+    W = [_matrix(2 + i, 3, n, k, std=0.1) for i in range(2)]
+    d, g, u = (_matrix(8 + i, m, n) for i in range(3))
+    want = X().gated_backward(d, x, *W, g, u, offsets=_offsets(ends))
+    for t in (x, d, g, u):
+        t[120:] = float("nan")
+        t[60] = float("nan")
+    got = X().gated_backward(d, x, *W, g, u, offsets=_offsets(ends))
+    for grp in (0, 2):
+        assert torch.equal(got[1][grp], want[1][grp]) and torch.equal(got[2][grp], want[2][grp])
+    keep = [r for r in range(120) if r != 60]
+    assert torch.equal(got[0][keep], want[0][keep]) and bool(got[0][60].isnan().all())
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_pre_gradients_at_the_ends(act):
+    """Large, small and zero pre-activations: no overflow on the way to a finite result."""
+    v = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3.0, -3.0, 9.0, -9.0, -12.0, 60.0, -60.0, -80.0, 100.0, -100.0, 1e4, -1e4, 3e38, -3e38],
+                     device="cuda").to(torch.bfloat16)
+    n = v.numel()
+    g, u, d = v.repeat(2, 1), _matrix(1, 2, n), _matrix(2, 2, n, std=0.1)
+    x, w = _matrix(3, 2, 8), [_matrix(4 + i, n, 8) for i in range(2)]
+    v, kept = _np(g), _np(u)
+    X().gated_backward(d, x, *w, g, u, activation=act, reuse=True)
+    value, slope = orc.activation(v, act)
+    want = orc.gated_pre_grads(_np(d), v, kept, act)
+    # v is exact here, so only erfc's argument is rounded (2 * 72 u where its value is not below 2^-120 at -12)
+    terms = {"silu": np.abs(slope) + 2 * np.exp(-np.abs(v)) * np.minimum(np.abs(v), 800), "gelu": np.abs(slope) + np.minimum(np.abs(v), 40) * np.exp(-0.5 * v * v),
+             "relu": np.abs(slope)}[act]
+    for got, ref, size in zip((g, u), want, (_np(d) * kept * terms, _np(d) * value)):
+        _close(got, ref, H * np.abs(ref) + 180 * U * np.abs(size) + 2.0 ** -120, act)
+
+
+# ---- 8-bit integer quantisation ---------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,gap", [(1, 1, 0), (3, 7, 0), (5, 128, 0), (2, 129, 3), (17, 1000, 0), (300, 511, 1), (4, 4096, 0),
+                                           (70, 2048, 8), (3, 8704, 0), (2, 16385, 0), (1, 40001, 0), (1025, 33, 0)])
+def test_quantize_int8(dtype, rows, cols, gap):
+    x = _matrix(1, rows, cols, dtype=dtype, gap=gap)
+    x[0] = 0
+    if rows > 2:
+        x[1] = (torch.arange(cols, device="cuda") % 255 - 127).to(dtype) / 2      # ties
+        x[2, 0] = 1e-44 if dtype == torch.float32 else 1e-40
+    if rows > 4:
+        x[3] *= 1e37
+        x[4] *= 1e-38
+    q = X().quantize_int8(x)
+    codes, scales = orc.quantize_int8(_np(x))
+    assert np.array_equal(q.scales.cpu().numpy(), scales)
+    assert np.array_equal(q.codes[:, :cols].cpu().numpy(), codes) and not q.codes[:, cols:].any()
+
+
+def test_quantize_int8_next_to_borders():
+    """Values that are a code and a half of their scale, or one step of float32 beside that."""
+    s = torch.tensor([1.0, 3.0, 0.7, 1e-20, 1e20, 1.1754944e-38, 1e-42], device="cuda")
+    half = (torch.arange(-127, 127, device="cuda").double() + 0.5)
+    x = torch.zeros(s.numel(), 3 * 254 + 1, device="cuda")
+    x[:, 0] = s * 127
+    scale = (x[:, 0].double() / 127).float()
+    v = (half[None] * scale[:, None].double()).float()
+    x[:, 1:255], x[:, 255:509], x[:, 509:763] = v, torch.nextafter(v, torch.full_like(v, 1e38)), torch.nextafter(v, torch.full_like(v, -1e38))
+    q = X().quantize_int8(x)
+    codes, scales = orc.quantize_int8(_np(x))
+    assert np.array_equal(q.scales.cpu().numpy(), scales) and np.array_equal(q.codes[:, :763].cpu().numpy(), codes)
+
+
+def test_quantize_int8_gathers_and_keeps():
+    x = _matrix(1, 20, 200)
+    rows = torch.tensor([3, -1, 39, 40, 0, 7, 2 ** 31 - 1, 5], dtype=torch.int32, device="cuda")
+    out = X().Int8(torch.full((8, 256), 9, dtype=torch.int8, device="cuda"), torch.full((8,), 9.0, device="cuda"), 200)
+    for limit in (7, 0, 100, -5):
+        out.codes.fill_(9)
+        out.scales.fill_(9)
+        X().quantize_int8(x, rows=rows, per=2, limit=torch.tensor([limit], dtype=torch.int32, device="cuda"), out=out)
+        codes, scales = orc.quantize_int8(orc.gather(_np(x), rows.cpu().numpy().astype(np.int64), 2))
+        end = min(max(limit, 0), 8)
+        assert np.array_equal(out.codes[:end, :200].cpu().numpy(), codes[:end]) and np.array_equal(out.scales[:end].cpu().numpy(), scales[:end])
+        assert bool((out.codes[end:] == 9).all()) and bool((out.scales[end:] == 9).all()) and not out.codes[:end, 200:].any()
+
+
+def test_quantize_int8_stacks_and_bad_rows():
+    x = torch.randn(3, 50, 300, device="cuda", generator=_gen(1))[:, :40, 4:204]
+    x[1, 2, 3], x[2, 0, 0] = float("nan"), float("inf")
+    q = X().quantize_int8(x)
+    codes, scales = orc.quantize_int8(_np(x))
+    assert np.array_equal(q.codes[..., :200].cpu().numpy(), codes) and np.array_equal(q.scales.cpu().numpy(), scales, equal_nan=True)
+    y = X().product_int8(X().Int8(q.codes[1], q.scales[1], 200), X().Int8(q.codes[0], q.scales[0], 200))
+    assert bool(y[2].isnan().all()) and bool(y[torch.arange(40, device="cuda") != 2].isfinite().all())
+
+
+# ---- rows to experts and back -----------------------------------------------------------------
+
+def _grouped(tokens, top_k, experts, align, seed, drop=0):
+    chosen = torch.rand(tokens, experts, device="cuda", generator=_gen(seed)).topk(top_k, dim=-1).indices.to(torch.int32)
+    if drop:
+        chosen[:drop] = -1
+        chosen[-1, 0] = -1
+    return X().group_rows(chosen, experts, align=align)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,top_k,experts,align,cols,gap,drop", [
+    (1, 1, 1, 1, 1, 0, 0), (1, 4, 9, 16, 64, 0, 0), (5, 2, 7, 1, 33, 1, 1), (64, 7, 32, 16, 200, 0, 3), (300, 3, 16, 128, 513, 8, 0),
+    (16, 7, 512, 1, 4096, 0, 2), (1000, 2, 4, 32, 1000, 0, 10), (3, 64, 64, 4, 40, 0, 0)])
+def test_gather_combine_and_back(dtype, tokens, top_k, experts, align, cols, gap, drop):
+    g = _grouped(tokens, top_k, experts, align, 5, drop)
+    rows, position = g.rows.cpu().numpy(), g.position.cpu().numpy()
+    used = int(g.offsets[-1])
+    src = _matrix(1, tokens, cols, dtype=dtype, gap=gap)
+    out = torch.full((rows.size, cols + gap), 7.0, dtype=dtype, device="cuda")
+    X().gather_rows(src, g.rows, per=top_k, limit=g.limit, out=out[:, :cols])
+    assert np.array_equal(_np(out[:used, :cols]), orc.gather(_np(src), rows, top_k)[:used])
+    assert bool((out[used:] == 7.0).all()) and (gap == 0 or bool((out[:, cols:] == 7.0).all()))
+    assert np.array_equal(_np(X().gather_rows(src, g.rows, per=top_k)), orc.gather(_np(src), rows, top_k))
+    w = torch.rand(tokens, top_k, device="cuda", generator=_gen(3))
+    y = _matrix(4, rows.size, cols, dtype=dtype, gap=gap)
+    y[used:] = float("nan")
+    for weights, residual, kind in itertools.product((w, None), (None, "in", "out"), (torch.float32, torch.bfloat16)):
+        res = None if residual is None else _matrix(6, tokens, cols, dtype=kind, gap=gap)
+        into = res if residual == "out" else None
+        ref, size = orc.combine(_np(y), position, None if weights is None else _np(weights), None if res is None else _np(res))
+        got = X().combine_rows(y, g.position, weights, residual=res, dtype=None if into is not None else kind, out=into)
+        _close(got, ref, (top_k + 1) * 2 * U * size + HALF[kind] * np.abs(ref) + TINY, "combined")
+    d = _matrix(7, tokens, cols, dtype=dtype, gap=gap)
+    out.fill_(7.0)
+    dy, dw = X().combine_rows_backward(d, y, g.rows, g.position, w, limit=g.limit, out=out[:, :cols])
+    ref_y, ref_w, size = orc.combine_backward(_np(d), _np(y), rows, position, _np(w))
+    assert bool((out[used:] == 7.0).all())
+    _close(dy[:used], ref_y[:used], (HALF[dtype] * np.abs(ref_y) + TINY)[:used], "grad of rows")
+    # 64 lanes' sums of cols / 64 products each, and 6 steps over the lanes
+    _close(dw, ref_w, (-(-cols // 512) * 8 + 7) * 2 * U * size + TINY, "grad of weights")
+
+
+def test_indices_of_another_grouping():
+    """rows and position that are not each other's: every gradient as its formula says; indices outside go nowhere."""
+    T, k, n, cols = 6, 3, 10, 70
+    d, y, w = _matrix(1, T, cols), _matrix(2, n, cols), torch.rand(T, k, device="cuda", generator=_gen(3))
+    rows = torch.tensor([0, 0, 17, 18, -1, 5, 5, -2 ** 31, 2 ** 31 - 1, 2], dtype=torch.int32, device="cuda")
+    position = torch.randint(-2, n + 2, (T, k), device="cuda", generator=_gen(4)).to(torch.int32)
+    dy, dw = X().combine_rows_backward(d, y, rows, position, w)
+    ref_y, ref_w, size = orc.combine_backward(_np(d), _np(y), rows.cpu().numpy().astype(np.int64), position.cpu().numpy(), _np(w))
+    _close(dy, ref_y, H * np.abs(ref_y) + TINY)
+    _close(dw, ref_w, 40 * U * size + TINY)
+    limit = torch.tensor([3], dtype=torch.int32, device="cuda")
+    out = torch.full_like(dy, 7.0)
+    dy, dw = X().combine_rows_backward(d, y, rows, position, w, limit=limit, out=out)
+    _close(dw, ref_w, 40 * U * size + TINY)
+    assert bool((out[3:] == 7.0).all())
+    ref, size = orc.combine(_np(y), position.cpu().numpy(), _np(w))
+    _close(X().combine_rows(y, position, w), ref, 8 * U * size + H * np.abs(ref) + TINY)
+
+
+def test_rows_beyond_32_bits():
+    """Rows whose byte and element offsets pass 2^32."""
+    n, cols = 530000, 8200
+    y = torch.empty(n, cols, dtype=torch.bfloat16, device="cuda")
+    far = [0, n - 1, n - 2, 262000]
+    y[far] = _matrix(1, 4, cols)
+    position = torch.tensor([[n - 1, 0], [n - 2, -1], [262000, n]], dtype=torch.int32, device="cuda")
+    got = X().combine_rows(y, position)
+    want = torch.stack([y[n - 1].float() + y[0].float(), y[n - 2].float(), y[262000].float()]).bfloat16()
+    assert torch.equal(got, want)
+    rows = torch.tensor([n - 1, 262000], dtype=torch.int32, device="cuda")
+    assert torch.equal(X().gather_rows(y, rows), y[[n - 1, 262000]])
+    q = X().quantize_int8(y, rows=rows)
+    codes, scales = orc.quantize_int8(_np(y[[n - 1, 262000]]))
+    assert np.array_equal(q.codes[:, :cols].cpu().numpy(), codes) and np.array_equal(q.scales.cpu().numpy(), scales)
+
+
+def test_products_beyond_32_bits():
+    """Weights, rows and results whose offsets pass 2^32 bytes."""
+    k, n, groups, m = 512, 1024, 4100, 60
+    w = torch.empty(groups, n, k, dtype=torch.bfloat16, device="cuda")
+    used = [0, 4096, groups - 1]
+    for i, g in enumerate(used):
+        w[g] = _matrix(10 + i, n, k, std=0.05)
+    ends = np.zeros(1025, dtype=np.int64)
+    x = _matrix(1, m, k)
+    # at most 1024 groups: the last ones of the stack
+    part = w[groups - 1024:]
+    first = {4096 - (groups - 1024): 25, 1023: 35}
+    ends[4096 - (groups - 1024) + 1:] = 25
+    ends[1024] = 60
+    got = X().gated(x, part, part, offsets=_offsets(ends.tolist()))
+    for g, (lo, hi) in zip((4096 - (groups - 1024), 1023), ((0, 25), (25, 60))):
+        assert torch.equal(got[lo:hi], X().gated(x[lo:hi].contiguous(), part[g], part[g])), (g, first)
+    big = torch.empty(1100000, 2048, dtype=torch.bfloat16, device="cuda")
+    y = X().gated(x, w[0][:512], w[0][512:], out=big[-m:, :512])
+    assert torch.equal(y, X().gated(x, w[0][:512], w[0][512:]))
+
+
+# ---- whole layers, streams, graphs ---------------------------------------------------------------
+
+def _layer(T, E, k, d, n, seed):
+    ex = X()
+    tokens, logits = _matrix(seed, T, d), torch.randn(T, E, device="cuda", generator=_gen(seed + 1))
+    W = [_matrix(seed + 2 + i, E, n, d, std=1 / math.sqrt(d)) for i in range(2)]
+    down = _matrix(seed + 4, E, d, n, std=1 / math.sqrt(n))
+    return ex, tokens, logits, W, down
+
+
+@pytest.mark.parametrize("T,E,k,d,n,align", [(1, 4, 2, 64, 48, 1), (50, 8, 2, 136, 72, 1), (300, 16, 3, 256, 192, 16)])
+def test_training_layer(T, E, k, d, n, align):
+    """Route, group, gather, gated block, a product with the down projection, combine, and all the way back."""
+    ex, tokens, logits, W, down = _layer(T, E, k, d, n, 40)
+    chosen, weights = ex.route(logits, k, score="sigmoid")
+    g = ex.group_rows(chosen, E, align=align)
+    x = ex.gather_rows(tokens, g.rows, per=k, limit=g.limit, out=torch.zeros(g.rows.numel(), d, dtype=torch.bfloat16, device="cuda"))
+    h, pg, pu = ex.gated(x, *W, offsets=g.offsets, save=True, out=torch.zeros(g.rows.numel(), n, dtype=torch.bfloat16, device="cuda"))
+    ends = g.offsets.tolist()
+    y = torch.zeros(g.rows.numel(), d, device="cuda")
+    for e in range(E):
+        y[ends[e]:ends[e + 1]] = h[ends[e]:ends[e + 1]].float() @ down[e].float().T
+    y = y.bfloat16()
+    out = ex.combine_rows(y, g.position, weights, residual=tokens)
+    # forwards, token by token: bfloat16 roundings of h and y are in the sums, h of each of their terms
+    xt, c, wt = _np(tokens), chosen.cpu().numpy(), _np(weights)
+    want, size = xt.copy(), np.abs(xt)
+    for t, j in itertools.product(range(T), range(k)):
+        e = c[t, j]
+        hh = orc.gated(xt[t:t + 1], _np(W[0][e]), _np(W[1][e]), "silu")[0]
+        D = _np(down[e])
+        want[t] += wt[t, j] * (D @ hh)
+        size[t] += wt[t, j] * (np.abs(D) @ np.abs(hh) + np.abs(D @ hh))
+    _close(out, want, (2 * H + 1e-4) * size, "layer")
+    # back
+    dout = _matrix(60, T, d)
+    dy, dw = ex.combine_rows_backward(dout, y, g.rows, g.position, weights, limit=g.limit, out=torch.zeros_like(y))
+    dh = torch.zeros(g.rows.numel(), n, device="cuda")
+    for e in range(E):
+        dh[ends[e]:ends[e + 1]] = dy[ends[e]:ends[e + 1]].float() @ down[e].float()
+    dh = dh.bfloat16()
+    dx, dG, dU = ex.gated_backward(dh, x, *W, pg, pu, offsets=g.offsets, dtype=torch.float32)
+    dtokens = ex.combine_rows(dx, g.position, residual=dout)
+    rows, position = g.rows.cpu().numpy(), g.position.cpu().numpy()
+    used = ends[-1]
+    pre = orc.gated_pre_grads(_np(dh), _np(pg), _np(pu), "silu")
+    pre = [np.where(rows[:, None] >= 0, np.where(np.arange(len(rows))[:, None] < used, v, 0.0), 0.0) for v in pre]
+    for got, dd in ((dG, pre[0]), (dU, pre[1])):
+        ref, size = orc.gated_grad_w(dd[:used], _np(x)[:used], ends)
+        _close(got, ref, (H + sum_tol(T * k)) * size + TINY, "weights")
+    gx, size = orc.gated_grad_x(pre[0], pre[1], _np(W[0]), _np(W[1]), ends)
+    ref, rsize = orc.combine(gx, position, None, _np(dout))
+    tol = orc.combine(size, position)[0] * (H + sum_tol(2 * n + 32)) + (2 * H) * rsize
+    _close(dtokens, ref, tol + TINY, "tokens")
+    ref_w = orc.combine_backward(_np(dout), _np(y), rows, position, wt)
+    _close(dw, ref_w[1], (-(-d // 512) * 8 + 7) * 2 * U * ref_w[2] + TINY, "routing weights")
+    assert ex.route_backward(logits, chosen, dw, score="sigmoid").isfinite().all()
+
+
+@pytest.mark.parametrize("T,E,k,d,n", [(1, 8, 2, 256, 128), (16, 64, 7, 512, 256), (200, 8, 2, 300, 140)])
+def test_serving_layer(T, E, k, d, n):
+    ex, tokens, logits, W, down = _layer(T, E, k, d, n, 70)
+    Q = [ex.quantize_int8(w) for w in (*W, down)]
+    chosen, weights = ex.route(logits, k)
+    g = ex.group_rows(chosen, E)
+    q = ex.quantize_int8(tokens, rows=g.rows, per=k, limit=g.limit)
+    h = ex.gated(q, Q[0], Q[1], offsets=g.offsets)
+    qh = ex.quantize_int8(h, limit=g.limit)
+    y = ex.product_int8(qh, Q[2], offsets=g.offsets)
+    out = ex.combine_rows(y, g.position, weights, residual=tokens)
+    # with the layer's own codes as operands, each step as its formula says
+    ends, used = g.offsets.tolist(), int(g.offsets[-1])
+    q = ex.Int8(q.codes[:used], q.scales[:used], d)
+    gr, ur = _scaled(q, Q[0], ends)[0], _scaled(q, Q[1], ends)[0]
+    want = orc.activation(gr, "silu")[0] * ur
+    _close(h[:used], want, (H + 166 * U) * np.abs(want) + 3.6 * U * np.abs(gr * ur) + TINY, "h")
+    codes, scales = orc.quantize_int8(_np(h[:used]))
+    assert np.array_equal(qh.codes[:used, :n].cpu().numpy(), codes) and np.array_equal(qh.scales[:used].cpu().numpy(), scales)
+    ref = _scaled(ex.Int8(qh.codes[:used], qh.scales[:used], n), Q[2], ends)[0]
+    _close(y[:used], ref, (H + 3 * U) * np.abs(ref) + TINY, "y")
+    ref, size = orc.combine(_np(y), g.position.cpu().numpy(), _np(weights), _np(tokens))
+    _close(out, ref, (k + 1) * 2 * U * size + H * np.abs(ref) + TINY, "out")
+
+
+def test_two_graphs_and_streams():
+    """A serving step and a training step captured, replayed in turn with eager work between, on streams of their own."""
+    ex, tokens, logits, W, down = _layer(40, 8, 2, 256, 128, 90)
+    Q = [ex.quantize_int8(w) for w in (*W, down)]
+    zeros = lambda r, c: torch.zeros(r, c, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+
+    def serve():
+        chosen, weights = ex.route(logits, 2)
+        g = ex.group_rows(chosen, 8)
+        q = ex.quantize_int8(tokens, rows=g.rows, per=2, limit=g.limit)
+        y = ex.product_int8(ex.quantize_int8(ex.gated(q, Q[0], Q[1], offsets=g.offsets)), Q[2], offsets=g.offsets)
+        return ex.combine_rows(y, g.position, weights)
+
+    def train():
+        chosen, weights = ex.route(logits, 2)
+        g = ex.group_rows(chosen, 8, align=16)
+        x = ex.gather_rows(tokens, g.rows, per=2)
+        h, pg, pu = ex.gated(x, *W, offsets=g.offsets, save=True, out=zeros(g.rows.numel(), 128))
+        return ex.gated_backward(h, x, *W, pg, pu, offsets=g.offsets, grad_x=zeros(g.rows.numel(), 256), dtype=torch.float32)
+
+    graphs = []
+    for f in (serve, train):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            f()
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = f()
+        graphs.append((graph, got))
+    for turn in range(4):
+        tokens.copy_(_matrix(100 + turn, 40, 256))
+        logits.copy_(torch.randn(40, 8, device="cuda", generator=_gen(200 + turn)))
+        for graph, _ in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[0][1], serve())
+        for a, b in zip(graphs[1][1], train()):
+            assert torch.equal(a, b)
+    # a named stream: inputs may be dropped, the result belongs to it
+    want = ex.gated(tokens, W[0][0], W[1][0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    copies = [t.clone() for t in (tokens, W[0][0], W[1][0])]
+    side.wait_stream(torch.cuda.current_stream())
+    got = ex.gated(*copies, stream=side)
+    del copies
+    torch.empty(1 << 20, device="cuda").fill_(float("nan"))
+    side.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_wrapper_refuses():
+    ex = X()
+    x, w = _matrix(1, 4, 64), _matrix(2, 8, 64)
+    st = _matrix(3, 2, 8, 64)
+    off = _offsets([0, 2, 4])
+    q, qw = ex.quantize_int8(x), ex.quantize_int8(w)
+    bad = [
+        lambda: ex.gated(x, w, w, activation="tanh"),
+        lambda: ex.gated(x.float(), w, w),
+        lambda: ex.gated(x, w, _matrix(2, 9, 64)),
+        lambda: ex.gated(x, w, _matrix(2, 8, 65)),
+        lambda: ex.gated(x, w, w, offsets=off),
+        lambda: ex.gated(x, st, st),
+        lambda: ex.gated(x, st, st, offsets=_offsets([0, 4])),
+        lambda: ex.gated(x, st, st, offsets=off.long()),
+        lambda: ex.gated(q, w, w),
+        lambda: ex.gated(x, w.T.contiguous().T, w),
+        lambda: ex.gated(x, w, w.cpu()),
+        lambda: ex.gated(x.cpu(), w.cpu(), w.cpu()),
+        lambda: ex.gated(x, w, w, out=torch.empty(4, 9, dtype=torch.bfloat16, device="cuda")),
+        lambda: ex.gated(x, w, w, out=torch.empty(4, 8, device="cuda")),
+        lambda: ex.product_int8(q, ex.quantize_int8(_matrix(1, 4, 65))),
+        lambda: ex.product_int8(q, qw, dtype=torch.float16),
+        lambda: ex.product_int8(q, ex.Int8(qw.codes, qw.scales[:4], 64)),
+        lambda: ex.product_int8(q, ex.Int8(qw.codes, qw.scales, 200)),
+        lambda: ex.gated_backward(x[:, :8], x, w, w, x[:, :8], x[:, 1:9], accumulate=True),
+        lambda: ex.gated_backward(x[:3, :8], x, w, w, x[:, :8], x[:, :8]),
+        lambda: ex.gated_backward(x[:, :8], x, w, w, x[:, :8], x[:, :8].contiguous()),
+        lambda: ex.quantize_int8(x.half()),
+        lambda: ex.quantize_int8(st, rows=off),
+        lambda: ex.quantize_int8(x, out=ex.quantize_int8(w)),
+        lambda: ex.gather_rows(x, off.view(1, 3)),
+        lambda: ex.gather_rows(x.expand(2, 4, 64), off),
+        lambda: ex.combine_rows(x, off),
+        lambda: ex.combine_rows(x, off.view(1, 3), torch.ones(1, 2, device="cuda")),
+        lambda: ex.combine_rows(x, off.view(1, 3), dtype=torch.float16),
+        lambda: ex.combine_rows_backward(x, x, off, off.view(3, 1), torch.ones(3, 1, device="cuda")),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} is accepted")
