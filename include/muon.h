@@ -653,7 +653,7 @@ typedef struct muon_gated_config {
     int32_t activation;       /* MUON_ACT_*                                                     */
     int64_t m, n, k;          /* rows, features of the block, values of a row                   */
     muon_operand x;           /* m x k                                                          */
-    muon_operand gate, up;    /* n x k, with MUON_PRODUCT_ROWS one per group                    */
+    muon_operand gate, up;    /* n x k, with MUON_PRODUCT_ROWS one per group; the same strides  */
     const int32_t* offsets;   /* as in muon_int8_product                                        */
     uint16_t* out;            /* bfloat16, m rows of n                                          */
     int64_t ld_out;           /* in elements, >= n                                              */
@@ -683,10 +683,11 @@ typedef struct muon_gated_backward_config {
     const uint16_t* pre_up;
     int64_t ld_pre;
     /* Written: the gradients of x gate^T and x up^T, bfloat16, m rows of n each (the operands of the products below,
-     * rounded to bfloat16 as those take them).  They may be pre_gate and pre_up, with the same stride. */
+     * rounded to bfloat16 as those take them), and zeros from column n on to a multiple of 64.  They may be pre_gate
+     * and pre_up, with the same stride. */
     uint16_t* grad_pre_gate;
     uint16_t* grad_pre_up;
-    int64_t ld_grad_pre;
+    int64_t ld_grad_pre;      /* in elements, a multiple of 64, at least n and below 2^22       */
     uint16_t* grad_x;         /* nullable: bfloat16, m rows of k                                */
     int64_t ld_grad_x;
     void* grad_gate;          /* nullable, both or neither: per group n rows of k               */

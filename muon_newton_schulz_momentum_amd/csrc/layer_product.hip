@@ -4,6 +4,7 @@
 // An operand is a panel of rows with the depth along them (x and weights forwards, the pre-activations' gradients in
 // FORM_GRAD_X) or, "across", of depth rows (weights in FORM_GRAD_X, both operands of FORM_GRAD_W, whose depth is the tokens).
 // b's rows are the matrix instruction's first operand: a lane then holds runs of 4 consecutive columns of one row of out.
+#include <algorithm>
 #include <type_traits>
 
 #include "activation.h"
@@ -21,7 +22,9 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef i32x4 i32x4_any __attribute__((aligned(1)));       // 16 bytes that may begin anywhere
+// 16 bytes that may begin anywhere
+typedef i32x4 i32x4_any __attribute__((aligned(1)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 // bfloat16 or 8-bit integer values: 16 bytes of a row are a lane's part of one instruction of either kind.
 template <class E>
@@ -99,7 +102,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
                             if (r < x.rows_a) row = p.a[part] + (x.m0 + r) * p.lda;
                         } else {
                             const int w = GATED ? r / COLS : part, c = GATED ? r % COLS : r;
-                            if (c < x.rows_b) row = p.b[w] + group_b * p.stride_b[w] + (x.n0 + c) * p.ldb[w];
+                            if (c < x.rows_b) row = p.b[w] + group_b * p.stride_b + (x.n0 + c) * p.ldb;
                         }
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -111,7 +114,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
                     } else {
                         const int kk = tid >> 3, c0 = 16 * (tid & 7);
                         const int w = op == 0 ? x.which : part;
-                        const uint8_t* row = op == 0 ? p.a[w] + (k0 + kk) * p.lda : p.b[w] + group_b * p.stride_b[w] + (k0 + kk) * p.ldb[w];
+                        const uint8_t* row = op == 0 ? p.a[w] + (k0 + kk) * p.lda : p.b[w] + group_b * p.stride_b + (k0 + kk) * p.ldb;
                         const int64_t first = (op == 0 ? x.m0 : x.n0) + c0, end = op == 0 ? p.m : p.n;
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -147,7 +150,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
             const int r = 64 * wm + 32 * i + fr;
             if (r >= x.rows_a) continue;
             const float sa = I8 ? p.sa[x.m0 + r] : 1.f;
-            auto column = [&](int w, int64_t c, float v) { return I8 ? v * sa * p.sb[w][group_b * p.stride_sb[w] + c] : v; };
+            auto column = [&](int w, int64_t c, float v) { return I8 ? v * sa * p.sb[w][group_b * p.stride_sb + c] : v; };
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
                 const int c = 8 * (v >> 2) + 4 * fk + (v & 3);
@@ -158,7 +161,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
                     static_cast<uint16_t*>(p.out[0])[(x.m0 + r) * p.ld_out[0] + col] = dev::f32_to_bf16(gated_value(p.activation, g, u));
                     if (p.out[1]) {
                         static_cast<uint16_t*>(p.out[1])[(x.m0 + r) * p.ld_out[1] + col] = dev::f32_to_bf16(g);
-                        static_cast<uint16_t*>(p.out[2])[(x.m0 + r) * p.ld_out[2] + col] = dev::f32_to_bf16(u);
+                        static_cast<uint16_t*>(p.out[2])[(x.m0 + r) * p.ld_out[1] + col] = dev::f32_to_bf16(u);
                     }
                 } else {
 #pragma unroll
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
                         const int64_t col = x.n0 + 64 * wn + 32 * j + c;
                         const float s = column(0, col, (float)acc[i][j][v]);
                         OUT* o = static_cast<OUT*>(p.out[x.which]) + (p.mode == MUON_PRODUCT_DEPTH ? x.group * p.out_stride : 0) +
-                                 (x.m0 + r) * p.ld_out[x.which] + col;
+                                 (x.m0 + r) * p.ld_out[0] + col;
                         if constexpr (sizeof(OUT) == 4) *o = p.accumulate ? *o + s : s;
                         else *o = dev::f32_to_bf16(s);
                     }
@@ -177,12 +180,415 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
     }
 }
 
+// ---- 256 x 256 tiles ------------------------------------------------------------------------
+//
+// One workgroup of 8 waves per CU that goes through its share of the tiles.  Wave (h, c) of 2 x 4 takes the 32-row blocks
+// 2 i + h of a and 64 rows of b, so that a tile with fewer rows (a segment's end) leaves both wave rows half of what there is:
+// a wave runs its first NB of 4 row blocks.  Of a gated block a tile is 256 x 128: b's panel holds 128 rows of gate and the
+// same 128 of up, a wave 32 of each, so a lane has both sums of a value of out.
+constexpr int TILE = 256, WAVES = 8, THREADS = 64 * WAVES;
+constexpr int FM = 4, FN = 2;                              // 32 x 32 blocks of a wave
+constexpr int STEP = 128;                                  // bytes of a row in a step: 64 bfloat16 values, 128 codes
+
+template <int N>
+using ic = std::integral_constant<int, N>;
+
+// Keeps the matrix instructions that have written acc so far in front of what follows.
+template <class S>
+__device__ __forceinline__ void pin(S (&acc)[FM][FN]) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+}
+
+// A fragment of a panel that lies across: 4 x 4 blocks of 16-bit values are transposed among 16 lanes.
+__device__ __forceinline__ uint64_t read_transposed(const uint8_t* at) {
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                            (__attribute__((address_space(3))) i16x4*)(const __attribute__((address_space(3))) uint8_t*)at));
+}
+
+// Operands go global -> VGPR -> LDS, a step (128 bytes of depth) ahead of the stage that is multiplied, of which there are
+// two; the step's one barrier comes in the middle of its last sub-step, whose fragments are then in registers.
+//
+// A panel along its rows lies in LDS in rows of 144 bytes: the 16 rows that a fragment read touches fall on 16 different
+// 16-byte slots of the 256 bytes that LDS serves at once.  A panel across lies in 64 depth rows of 512 bytes whose 64-byte granules
+// are permuted by the row, so that the 8 rows of a transposing read fall on 8 different ones.
+//
+// Nothing in the main loop deals with ends:
+//   * a depth that is no multiple of the step is taken with its remainder first, whose loads are masked where they are stored
+//     before the loop; of GRAD_X the rows of a are padded to whole steps with zeros;
+//   * rows of a panel along, and depth rows of one across, that are behind the end lie behind the end of the buffer that the
+//     loads go through (the row is in the vector part of the offset: see fp8_panel.h) and arrive as zeros;
+//   * of a panel across the last 8 columns are loaded again where fewer than 8 are left: in those 8 places of the tile
+//     the last columns come last, and out is stored accordingly.
+// So a 16-byte load never crosses the end of a row, and rows may begin anywhere.
+template <class E, int FORM, class OUT>
+__global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void layer_kernel(LayerArgs p) {
+    constexpr bool GATED = FORM == FORM_GATED, I8 = sizeof(E) == 1, F32 = sizeof(OUT) == 4;
+    constexpr bool ACROSS_A = a_across<FORM>, ACROSS_B = b_across<FORM>, TWO = parts<FORM> == 2;
+    constexpr int ES = (int)sizeof(E), UNIT = STEP / ES;   // values of a step
+    constexpr int COLS = GATED ? TILE / 2 : TILE;
+    constexpr int LA = 4, NLOAD = 2 * LA;                  // load instructions of a step
+    constexpr int ROW = STEP + 16, KROW = 2 * TILE;        // LDS rows of a panel along, across
+    constexpr int PANEL_A = ACROSS_A ? UNIT * KROW : TILE * ROW, PANEL_B = ACROSS_B ? UNIT * KROW : TILE * ROW, STAGE = PANEL_A + PANEL_B;
+    constexpr int EPL = 16 / (int)sizeof(OUT);             // values of out in 16 bytes
+    constexpr int OCOLS = GATED ? 96 : 64;                 // columns that a wave stages: out, gate and up; or out
+    constexpr int OROW = OCOLS * (int)sizeof(OUT) + 16;
+    constexpr int OUT_STAGE = WAVES * 32 * OROW;           // out goes through the second stage
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGE + (STAGE > OUT_STAGE ? STAGE : OUT_STAGE)];
+    __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
+    __shared__ int64_t wave_tot[WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wh = wave >> 2, wc = wave & 3;               // wave row and column
+    const int fr = lane & 31, fk = lane >> 5;
+
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, THREADS>(p, TILE, bounds, ends, wave_tot);
+    Walk my = walk<pair<FORM>>(p, ends);
+    int t = next_tile(p, my);
+    if (t < 0) return;
+
+    // staging: along, load i brings rows 64 i + lrow, chunk lchunk; across, depth rows 16 i + krow, chunk kchunk
+    const int lrow = 8 * wave + (lane >> 3), lchunk = lane & 7, krow = tid >> 5, kchunk = tid & 31;
+    auto swizzle = [](int k) { return (k & 3) | ((k >> 1) & 4); };
+    const int along = lrow * ROW + 16 * lchunk, across = krow * KROW + (((kchunk >> 2) ^ swizzle(krow)) << 6) + ((kchunk & 3) << 4);
+
+    // of the tile: operands' first rows (along) or depth row 0 (across), the lane's offset from there in load 0, sizes of
+    // the buffers along; the depth's begin, its values before the whole steps, those of each part, and all steps
+    const uint8_t *base_a, *base_b;
+    int va, vb, bytes_a, bytes_b, first, rest, whole, steps;
+    const int lda = (int)p.lda, ldb = (int)p.ldb;
+    i32x4 staged[NLOAD];
+    // Where a step's loads go: operands' buffers, and their scalar offset along (pieces of this are the same for all of a step).
+    struct Aim {
+        const uint8_t *a, *b;
+        int bytes_a, bytes_b, along;
+    };
+    // Step `step` of the run, or nowhere where keep is 0 and not -1 (from an empty buffer, which fetches nothing).  No branch, which
+    // in the main loop would let the compiler move the matrix instructions behind it.
+    auto aim = [&](int step, int keep, bool begins) {
+        const int lead = rest > 0, w = step - lead;
+        const int part = TWO ? (whole - 1 - w) >> 31 : 0;  // 0, or -1 for the second
+        int at = UNIT * (w - (whole & part)), valid = UNIT;
+        if (TWO) valid = min(valid, (int)p.k - at);
+        else at += first + rest;
+        if (begins && lead) {
+            at = first;
+            valid = rest;
+        }
+        at &= keep;
+        Aim r;
+        r.a = base_a + (TWO ? (p.a[1] - p.a[0]) & (int64_t)part : 0) + (ACROSS_A ? (int64_t)at * lda : 0);
+        r.b = base_b + (TWO ? (p.b[1] - p.b[0]) & (int64_t)part : 0) + (ACROSS_B ? (int64_t)at * ldb : 0);
+        r.bytes_a = (ACROSS_A ? (valid - 1) * lda + 2 * (int)p.m : bytes_a) & keep;
+        r.bytes_b = (ACROSS_B ? (valid - 1) * ldb + 2 * (int)p.n : bytes_b) & keep;
+        r.along = at * ES;
+        return r;
+    };
+    // Chunk d of a step into its register.
+    auto load = [&](int d, const Aim& r) {
+        const bool is_a = d < LA;
+        const int i = is_a ? d : d - LA;
+        const bool across = is_a ? ACROSS_A : ACROSS_B;
+        // (opaque, or the sums of all d stay in registers)
+        int32_t rows_on = (across ? 16 * i : 64 * (GATED && !is_a ? i & 1 : i)) * (is_a ? lda : ldb);
+        asm volatile("" : "+s"(rows_on));
+        // (of a gated block b's loads 0 and 1 bring gate, 2 and 3 up)
+        const uint8_t* base = (is_a ? r.a : r.b) + (GATED && !is_a && i >= 2 ? p.b[1] - p.b[0] : 0);
+        const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, is_a ? r.bytes_a : r.bytes_b, 0x00020000);
+        staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, (is_a ? va : vb) + rows_on, across ? 0 : r.along, 0);
+    };
+    auto mask = [](bool valid) {
+        int keep = __builtin_amdgcn_readfirstlane(valid ? -1 : 0);
+        asm volatile("" : "+s"(keep));
+        return keep;
+    };
+    auto store = [&](int d, int st) {
+        const bool is_a = d < LA;
+        const int i = is_a ? d : d - LA;
+        const int at = (is_a ? ACROSS_A : ACROSS_B) ? across + 16 * KROW * i : along + 64 * ROW * i;
+        *reinterpret_cast<i32x4*>(smem + st * STAGE + (is_a ? 0 : PANEL_A) + at) = staged[d];
+    };
+    // The tile's operands, and the first loads of them.
+    auto begin = [&](const Tile& x) {
+        int ln = lane, kr = krow, kc = kchunk;
+        asm volatile("" : "+v"(ln), "+v"(kr), "+v"(kc));   // worked out per tile instead of being kept
+        const int64_t to_group = p.mode == MUON_PRODUCT_ROWS ? x.group * p.stride_b : 0;
+        base_a = p.a[ACROSS_A ? x.which : 0] + (ACROSS_A ? 0 : x.m0 * p.lda);
+        base_b = p.b[0] + to_group + (ACROSS_B ? 0 : x.n0 * p.ldb);
+        const int depth = x.kb1 - x.kb0;
+        first = __builtin_amdgcn_readfirstlane(x.kb0);
+        rest = __builtin_amdgcn_readfirstlane(I8 || TWO ? 0 : depth % UNIT);
+        whole = __builtin_amdgcn_readfirstlane(I8 || TWO ? (depth + UNIT - 1) / UNIT : depth / UNIT);
+        steps = __builtin_amdgcn_readfirstlane((rest > 0) + parts<FORM> * whole);
+        const int row_bytes = I8 || TWO ? whole * STEP : x.kb1 * ES;
+        bytes_a = (x.rows_a - 1) * lda + row_bytes;
+        bytes_b = (x.rows_b - 1) * ldb + row_bytes;
+        auto column = [&](int64_t c, int64_t n) { return 2 * (int)min(c + 8 * kc, n - 8); };
+        va = ACROSS_A ? kr * lda + column(x.m0, p.m) : (8 * wave + (ln >> 3)) * lda + 16 * (ln & 7);
+        vb = ACROSS_B ? kr * ldb + column(x.n0, p.n) : (8 * wave + (ln >> 3)) * ldb + 16 * (ln & 7);
+        const Aim r = aim(0, mask(steps > 0), true);
+#pragma unroll
+        for (int d = 0; d < NLOAD; ++d) load(d, r);
+    };
+    // The first step into LDS, the second into the registers.
+    auto fill = [&]() {
+        if (steps == 0) return;
+        // values of a lane's chunk that are in the partial step; the others follow in the next one
+        const int have = rest > 0 ? min(max(rest * ES - 16 * lchunk, 0), 16) : 16;
+        i32x4 inside;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) inside[e] = have >= 4 * e + 4 ? -1 : have == 4 * e + 2 ? 0xffff : 0;
+        const Aim r = aim(1, mask(1 < steps), false);
+#pragma unroll
+        for (int d = 0; d < NLOAD; ++d) {
+            if (!I8 && !TWO && !(d < LA ? ACROSS_A : ACROSS_B)) staged[d] &= inside;
+            store(d, 0);
+            load(d, r);
+        }
+    };
+
+    // a fragment, 16 bytes of a row's depth, in sub-step kk: along in one read; across in two, whose lanes take depth
+    // rows tk and columns tc
+    const int tk = 8 * (lane >> 5) + ((lane & 15) >> 2), tc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    int ra[ACROSS_A ? FM : 1], rb[ACROSS_B ? FN : 1];
+    if (ACROSS_A) {
+#pragma unroll
+        for (int i = 0; i < (ACROSS_A ? FM : 1); ++i) ra[i] = tk * KROW + (((2 * i + wh) ^ swizzle(tk)) << 6) + 2 * tc;
+    } else {
+        ra[0] = (32 * wh + fr) * ROW + 16 * fk;
+    }
+    if (ACROSS_B) {
+#pragma unroll
+        for (int j = 0; j < (ACROSS_B ? FN : 1); ++j) rb[j] = PANEL_A + tk * KROW + (((2 * wc + j) ^ swizzle(tk)) << 6) + 2 * tc;
+    } else {
+        rb[0] = PANEL_A + ((GATED ? 32 : 64) * wc + fr) * ROW + 16 * fk;
+    }
+    auto read_across = [&](const uint8_t* at) {
+        typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(i32x4, u64x2{read_transposed(at), read_transposed(at + 4 * KROW)});
+    };
+    auto read_a = [&](int i, int st, int kk) {
+        if constexpr (ACROSS_A) return read_across(smem + st * STAGE + ra[ACROSS_A ? i : 0] + 16 * KROW * kk);
+        else return *reinterpret_cast<const i32x4*>(smem + st * STAGE + ra[0] + 64 * i * ROW + 32 * kk);
+    };
+    auto read_b = [&](int j, int st, int kk) {
+        if constexpr (ACROSS_B) return read_across(smem + st * STAGE + rb[ACROSS_B ? j : 0] + 16 * KROW * kk);
+        else return *reinterpret_cast<const i32x4*>(smem + st * STAGE + rb[0] + (GATED ? TILE / 2 : 32) * j * ROW + 32 * kk);
+    };
+
+    typename Cores<E>::sums acc[FM][FN];
+    // The steps of a tile for a wave with NB row blocks.
+    auto multiply = [&](auto nb_) {
+        constexpr int NB = decltype(nb_)::value;
+        // A sub-step's slots are its matrix instructions, behind which staging and the next sub-step's reads go; in the last
+        // one the barrier comes before slot BAR, reads behind it.
+        constexpr int SUBS = 4, SLOTS = NB * FN, BAR = SLOTS / 2, ALL = (SUBS - 1) * SLOTS + BAR, READS = NB + FN;
+        i32x4 fa[2][NB], fb[2][FN];
+        auto read = [&](int r, int to, int st, int kk) {   // b's first and a's first come first
+            if (r == 0) fb[to][0] = read_b(0, st, kk);
+            else if (r == 1) fa[to][0] = read_a(0, st, kk);
+            else if (r == 2) fb[to][1] = read_b(1, st, kk);
+            else fa[to][r - 2] = read_a(r - 2, st, kk);
+        };
+#pragma unroll
+        for (int r = 0; r < READS; ++r) read(r, 0, 0, 0);
+        for (int step = 0; step < steps; ++step) {
+            const Aim ahead = aim(step + 2, mask(step + 2 < steps), false);
+            const int st = step & 1, st_next = st ^ 1;
+#pragma unroll
+            for (int kk = 0; kk < SUBS; ++kk) {
+                const int cur = kk & 1, nxt = cur ^ 1;
+                const bool last = kk == SUBS - 1;
+#pragma unroll
+                for (int f = 0; f < SLOTS; ++f) {
+                    const int i = f / FN, j = f % FN;
+                    if (last && f == BAR) {
+                        pin(acc);
+                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                        __builtin_amdgcn_s_barrier();
+                        asm volatile("" ::: "memory");
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    acc[i][j] = Cores<E>::mul(fb[cur][j], fa[cur][i], acc[i][j]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    const int g = kk * SLOTS + f;
+                    if (g < ALL)
+#pragma unroll
+                        for (int d = g * NLOAD / ALL; d < (g + 1) * NLOAD / ALL; ++d) {
+                            store(d, st_next);
+                            load(d, ahead);
+                        }
+                    const int lo = last ? BAR : 0, n = SLOTS - lo;
+                    if (f >= lo)
+#pragma unroll
+                        for (int r = (f - lo) * READS / n; r < (f - lo + 1) * READS / n; ++r) read(r, nxt, last ? st_next : st, last ? 0 : kk + 1);
+                }
+            }
+        }
+    };
+
+    // Scales of the lane's rows and columns (8-bit integers), asked for before the next tile's loads.
+    float sa[I8 ? FM : 1];
+    f32x4 sb[I8 ? FN : 1][4];
+    Tile done;
+    auto read_scales = [&](const Tile& x) {
+        if constexpr (I8) {
+            const int64_t group = p.mode == MUON_PRODUCT_ROWS ? x.group * p.stride_sb : 0;
+#pragma unroll
+            for (int i = 0; i < FM; ++i) sa[i] = p.sa[x.m0 + min(64 * i + 32 * wh + fr, x.rows_a - 1)];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sb[j][q][e] = p.sb[GATED ? j : 0][group + x.n0 + min((GATED ? 32 : 64) * wc + (GATED ? 0 : 32) * j + 8 * q + 4 * fk + e, x.rows_b - 1)];
+        }
+    };
+    // Row block i of out: 32 rows of the wave through its part of the second stage (which nobody reads between a tile's
+    // last barrier and the next one's first step), then in 16-byte stores along the rows, which leave the caches to the operands.
+    auto write = [&](int i) {
+        // opaque, so that the addresses are worked out per tile instead of being kept through the main loop
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        uint8_t* mine = smem + STAGE + wave * 32 * OROW;
+        const int r0 = 64 * i + 32 * wh;
+        if (r0 >= done.rows_a) return;
+        auto scaled = [&](int j, int v) {
+            if constexpr (I8) return (float)acc[i][j][v] * sa[i] * sb[j][v >> 2][v & 3];
+            else return acc[i][j][v];
+        };
+        auto put = [&](int col, const f32x4& v) {
+            uint8_t* o = mine + (ln & 31) * OROW + col * (int)sizeof(OUT);
+            if constexpr (F32) *reinterpret_cast<f32x4*>(o) = v;
+            else *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int c = 8 * q + 4 * (ln >> 5);
+            f32x4 v[2];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[j][e] = scaled(j, 4 * q + e);
+            if constexpr (GATED) {
+                f32x4 h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = gated_value(p.activation, v[0][e], v[1][e]);
+                put(c, h);
+                put(32 + c, v[0]);
+                put(64 + c, v[1]);
+            } else {
+                put(c, v[0]);
+                put(32 + c, v[1]);
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int WIDTH = GATED ? 32 : 64;             // columns of out of the wave
+        constexpr int LPR = WIDTH / EPL, RPS = 64 / LPR;   // lanes per row, rows per store
+        const int col = ln % LPR * EPL, row = ln / LPR;
+        const int64_t c0 = done.n0 + WIDTH * wc + col;     // the lane's first column
+        const int64_t left = p.n - c0;
+        // places of 8 columns (across: of rows too) with fewer left hold the last 8
+        const int64_t back = ACROSS_B && (c0 & ~7) + 8 > p.n ? (c0 & ~7) + 8 - p.n : 0;
+#pragma unroll
+        for (int w = 0; w < (GATED ? 3 : 1); ++w) {
+            OUT* out = static_cast<OUT*>(p.out[GATED ? w : done.which]);
+            if (GATED && !out) continue;
+            const int64_t ld = p.ld_out[GATED && w ? 1 : 0];
+            if (p.mode == MUON_PRODUCT_DEPTH) out += done.group * p.out_stride;
+#pragma unroll
+            for (int q = 0; q < 32 / RPS; ++q) {
+                const uint4 u = *reinterpret_cast<const uint4*>(mine + (q * RPS + row) * OROW + (32 * w + col) * (int)sizeof(OUT));
+                int64_t r = done.m0 + r0 + q * RPS + row;
+                if (ACROSS_A && (r & ~7) + 8 > p.m) {
+                    const int64_t place = r & ~7;
+                    r += p.m - 8 - place;
+                    if (r < place) continue;
+                } else if (r0 + q * RPS + row >= done.rows_a) {
+                    continue;
+                }
+                OUT* o = out + r * ld + c0;
+                if (EPL <= left && back == 0) {
+                    if constexpr (F32) {
+                        f32x4 v = __builtin_bit_cast(f32x4, u);
+                        if (p.accumulate) v += *reinterpret_cast<const f32x4_any*>(o);
+                        if (p.vec) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(o));
+                        else *reinterpret_cast<f32x4_any*>(o) = v;
+                    } else {
+                        if (p.vec) __builtin_nontemporal_store(__builtin_bit_cast(i32x4, u), reinterpret_cast<i32x4*>(o));
+                        else *reinterpret_cast<i32x4_any*>(o) = __builtin_bit_cast(i32x4, u);
+                    }
+                } else {
+                    const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < EPL; ++e) {
+                        const int64_t c = e - back;        // from c0; the place begins (c0 & 7) before it
+                        if (c >= left || c < -(c0 & 7)) continue;
+                        if constexpr (F32) o[c] = p.accumulate ? o[c] + __uint_as_float(word[e]) : __uint_as_float(word[e]);
+                        else o[c] = (uint16_t)(word[e / 2] >> (16 * (e & 1)));
+                    }
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+
+    Tile x = decode<1, pair<FORM>>(p, t, TILE, COLS, bounds, ends);
+    begin(x);
+    fill();
+    for (;;) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = typename Cores<E>::sums{};
+        if (steps > 0) {
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            const int blocks = (x.rows_a - 32 * wh + 63) / 64;
+            if (blocks >= 4) multiply(ic<4>{});
+            else if (blocks == 3) multiply(ic<3>{});
+            else if (blocks == 2) multiply(ic<2>{});
+            else multiply(ic<1>{});
+        }
+        done = x;
+        read_scales(done);
+        t = next_tile(p, my);
+        const bool more = t >= 0;
+        // the next tile's first loads run beside this one's stores
+        if (more) {
+            x = decode<1, pair<FORM>>(p, t, TILE, COLS, bounds, ends);
+            begin(x);
+        }
+        write(0);
+        write(1);
+        if (more) fill();
+        write(2);
+        write(3);
+        if (!more) break;
+    }
+}
+
+// Whether the 256 x 256 tiles' loads fit: at least one of 16 bytes in a row (and a whole step where the depth's remainder
+// comes first and its loads reach beyond it).
+template <class E, int FORM>
+bool tile_loads_fit(const LayerArgs& a) {
+    if (a_across<FORM>) return a.m >= 8 && a.n >= 8;
+    return b_across<FORM> ? a.n >= 8 : sizeof(E) == 1 || a.k >= STEP / 2;
+}
+
 template <class E, int FORM, class OUT>
 hipError_t layer_as(LayerArgs a, hipStream_t s) {
-    const int64_t total = count_tiles<pair<FORM>>(a, ANY, FORM == FORM_GATED ? ANY / 2 : ANY);
-    if (total == 0) return hipSuccess;
-    const dim3 grid((unsigned)std::min<int64_t>((total + NUM_XCD - 1) / NUM_XCD * NUM_XCD, 2 * CUS)), block(ANY_THREADS);
-    hipLaunchKernelGGL((layer_any_kernel<E, FORM, OUT>), grid, block, 0, s, a);
+    LayerArgs any = a;
+    const int64_t n_big = count_tiles<pair<FORM>>(a, TILE, FORM == FORM_GATED ? TILE / 2 : TILE);
+    const int64_t n_any = count_tiles<pair<FORM>>(any, ANY, FORM == FORM_GATED ? ANY / 2 : ANY);
+    if (n_big == 0) return hipSuccess;
+    auto grid = [](int64_t tiles, int64_t most) { return dim3((unsigned)std::min<int64_t>((tiles + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)); };
+    if (tile_loads_fit<E, FORM>(a)) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT>), grid(n_big, CUS), dim3(THREADS), 0, s, a);
+    else hipLaunchKernelGGL((layer_any_kernel<E, FORM, OUT>), grid(n_any, 2 * CUS), dim3(ANY_THREADS), 0, s, any);
     return hipGetLastError();
 }
 

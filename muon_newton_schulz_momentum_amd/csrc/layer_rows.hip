@@ -212,6 +212,7 @@ __global__ __launch_bounds__(THREADS) void gated_grad_kernel(GatedGradArgs p, in
         first = min(max((int64_t)p.offsets[0], first), p.m);
         end = min(max((int64_t)p.offsets[p.groups], first), p.m);
     }
+    const int64_t padded = (int64_t)parts * V;             // zeros from n on
     for (int64_t id = first * parts + (int64_t)blockIdx.x * THREADS + threadIdx.x; id < end * parts; id += (int64_t)gridDim.x * THREADS) {
         const int64_t r = id / parts, i = id % parts * V;
         float d[V], g[V], u[V], dg[V], du[V];
@@ -225,8 +226,8 @@ __global__ __launch_bounds__(THREADS) void gated_grad_kernel(GatedGradArgs p, in
             dg[e] = d[e] * u[e] * slope;
             du[e] = d[e] * value;
         }
-        store8(p.grad_pre_gate + r * p.ld_out, i, p.n, dg);
-        store8(p.grad_pre_up + r * p.ld_out, i, p.n, du);
+        store8(p.grad_pre_gate + r * p.ld_out, i, padded, dg);
+        store8(p.grad_pre_up + r * p.ld_out, i, padded, du);
     }
 }
 
@@ -237,7 +238,7 @@ unsigned blocks_of(int64_t items, int64_t per) { return (unsigned)std::min<int64
 
 hipError_t launch_gated_grad(const GatedGradArgs& a, hipStream_t s) {
     if (a.m == 0 || a.n == 0) return hipSuccess;
-    const int32_t parts = (int32_t)((a.n + V - 1) / V);
+    const int32_t parts = (int32_t)((a.n + 63) / 64 * (64 / V));
     const dim3 grid(blocks_of(a.m * parts, THREADS)), block(THREADS);
     if (a.activation == MUON_ACT_SILU) hipLaunchKernelGGL((gated_grad_kernel<MUON_ACT_SILU>), grid, block, 0, s, a, parts);
     else if (a.activation == MUON_ACT_GELU) hipLaunchKernelGGL((gated_grad_kernel<MUON_ACT_GELU>), grid, block, 0, s, a, parts);

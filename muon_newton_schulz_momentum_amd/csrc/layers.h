@@ -12,24 +12,25 @@ namespace muon {
 // One launch of products.  What it computes goes by its form:
 //   FORM_GATED   out[0] = act(a[0] b[0]^T) * (a[0] b[1]^T), the two sums into out[1] and out[2] where those are there
 //   FORM_SCALED  out[0] = a[0] b[0]^T by their rows' scales (8-bit integers)
-//   FORM_GRAD_X  out[0] = a[0] b[0] + a[1] b[1]
+//   FORM_GRAD_X  out[0] = a[0] b[0] + a[1] b[1]; a's rows are padded to multiples of 64 with zeros
 //   FORM_GRAD_W  out[w] = a[w]^T b[0] for w = 0, 1, over each group's rows
 enum LayerForm { FORM_GATED, FORM_SCALED, FORM_GRAD_X, FORM_GRAD_W };
 
 struct LayerArgs {
     const uint8_t *a[2], *b[2];
     const float *sa, *sb[2];           // scales of 8-bit integers' rows
-    int64_t lda, ldb[2], stride_b[2];  // in bytes
-    int64_t stride_sb[2];              // in scales
+    int64_t lda, ldb, stride_b;        // in bytes
+    int64_t stride_sb;                 // in scales
     const int32_t* offsets;            // nullable: no groups
     void* out[3];
-    int64_t ld_out[3], out_stride;     // in elements
+    int64_t ld_out[2], out_stride;     // in elements; ld_out[1]: of out[1] and out[2] (FORM_GATED)
     int64_t m, n, k;                   // rows and columns of out, depth (of each product that is added up)
     int32_t groups, mode, accumulate, activation;
     int32_t tiles_m, tiles_n, tiles;
+    int32_t vec;                       // rows of out are 16-byte aligned
 };
 
-// dg = d u act'(g), du = d act(g) for rows [offsets[0], offsets[groups]) of m, or all
+// dg = d u act'(g), du = d act(g) for rows [offsets[0], offsets[groups]) of m, or all; zeros from column n on to a multiple of 64
 struct GatedGradArgs {
     const uint16_t *grad, *pre_gate, *pre_up;
     uint16_t *grad_pre_gate, *grad_pre_up;

@@ -42,6 +42,11 @@ muon_status check_operand(const muon_operand& o, int32_t operands, int64_t rows,
     }
     return MUON_OK;
 }
+muon_status check_alike(const muon_operand& gate, const muon_operand& up, int32_t operands, int64_t groups, const char* who) {
+    if (gate.ld != up.ld || (groups > 1 && (gate.stride != up.stride || (operands == MUON_OPERANDS_INT8 && gate.stride_scales != up.stride_scales))))
+        return fail(MUON_ERR_SHAPE, who, "gate and up must have the same strides");
+    return MUON_OK;
+}
 Extent values_of(const muon_operand& o, int32_t operands, int64_t rows, int64_t k, int64_t groups) {
     const bool i8 = operands == MUON_OPERANDS_INT8;
     return extent(o.data, groups, o.stride, rows, o.ld, i8 ? round_up(k, 128) : k, i8 ? 1 : 2);
@@ -80,9 +85,9 @@ void set_a(LayerArgs& a, int i, const void* p, const float* scales, int64_t ld, 
 void set_b(LayerArgs& a, int i, const muon_operand& o, int64_t size) {
     a.b[i] = static_cast<const uint8_t*>(o.data);
     a.sb[i] = o.scales;
-    a.ldb[i] = o.ld * size;
-    a.stride_b[i] = a.groups > 1 ? o.stride * size : 0;
-    a.stride_sb[i] = a.groups > 1 ? o.stride_scales : 0;
+    a.ldb = o.ld * size;
+    a.stride_b = a.groups > 1 ? o.stride * size : 0;
+    a.stride_sb = a.groups > 1 ? o.stride_scales : 0;
 }
 
 #define MUON_RETURN_IF(e)                \
@@ -154,6 +159,7 @@ muon_status muon_int8_product(const muon_int8_product_config* c, void* stream) t
     set_b(a, 0, c->b, 1);
     a.out[0] = c->out;
     a.ld_out[0] = c->ld_out;
+    a.vec = c->ld_out * size_of(c->out_dtype) % 16 == 0;
     if (!layer_fits(a, FORM_SCALED)) return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
     const Extent out[] = {extent(c->out, 1, 0, c->m, c->ld_out, c->n, size_of(c->out_dtype))};
     const Extent in[] = {values_of(c->a, MUON_OPERANDS_INT8, c->m, c->k, 1), scales_of(c->a, c->m, 1),
@@ -183,6 +189,7 @@ muon_status muon_gated(const muon_gated_config* c, void* stream) try {
     MUON_RETURN_IF(check_operand(c->x, c->operands, c->m, c->k, 1, who, "x"));
     MUON_RETURN_IF(check_operand(c->gate, c->operands, c->n, c->k, c->groups, who, "gate"));
     MUON_RETURN_IF(check_operand(c->up, c->operands, c->n, c->k, c->groups, who, "up"));
+    MUON_RETURN_IF(check_alike(c->gate, c->up, c->operands, c->groups, who));
     const int64_t size = i8 ? 1 : 2;
     LayerArgs a = layer_args(c->mode, c->groups, c->offsets, c->m, c->n, c->k);
     set_a(a, 0, c->x.data, c->x.scales, c->x.ld, size);
@@ -192,7 +199,8 @@ muon_status muon_gated(const muon_gated_config* c, void* stream) try {
     a.out[1] = c->pre_gate;
     a.out[2] = c->pre_up;
     a.ld_out[0] = c->ld_out;
-    a.ld_out[1] = a.ld_out[2] = c->ld_pre;
+    a.ld_out[1] = c->ld_pre;
+    a.vec = c->ld_out % 8 == 0 && (!c->pre_gate || c->ld_pre % 8 == 0);
     a.activation = c->activation;
     if (!layer_fits(a, FORM_GATED)) return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
     const Extent out[] = {extent(c->out, 1, 0, c->m, c->ld_out, c->n, 2), extent(c->pre_gate, 1, 0, c->m, c->ld_pre, c->n, 2),
@@ -234,13 +242,15 @@ muon_status muon_gated_backward(const muon_gated_backward_config* c, void* strea
         MUON_RETURN_IF(check_rows(c->pre_up, c->ld_pre, c->n, who, "pre_up"));
         MUON_RETURN_IF(check_rows(c->grad_pre_gate, c->ld_grad_pre, c->n, who, "grad_pre_gate"));
         MUON_RETURN_IF(check_rows(c->grad_pre_up, c->ld_grad_pre, c->n, who, "grad_pre_up"));
-        if (c->ld_grad_pre >= MAX_LD_BYTES / 2) return fail(MUON_ERR_SHAPE, who, "ld_grad_pre must be below 2^22");
+        if (c->ld_grad_pre % 64 != 0 || c->ld_grad_pre >= MAX_LD_BYTES / 2)
+            return fail(MUON_ERR_SHAPE, who, "ld_grad_pre must be a multiple of 64 and below 2^22");
         if (weights) MUON_RETURN_IF(check_operand(c->x, bf16, c->m, c->k, 1, who, "x"));
     }
     if (to_x) {
         MUON_RETURN_IF(check_rows(c->grad_x, c->ld_grad_x, c->k, who, "grad_x"));
         MUON_RETURN_IF(check_operand(c->gate, bf16, c->n, c->k, c->groups, who, "gate"));
         MUON_RETURN_IF(check_operand(c->up, bf16, c->n, c->k, c->groups, who, "up"));
+        MUON_RETURN_IF(check_alike(c->gate, c->up, bf16, c->groups, who));
     }
     LayerArgs x = layer_args(c->mode, c->groups, c->offsets, c->m, c->k, c->n);
     set_a(x, 0, c->grad_pre_gate, nullptr, c->ld_grad_pre, 2);
@@ -249,22 +259,24 @@ muon_status muon_gated_backward(const muon_gated_backward_config* c, void* strea
     set_b(x, 1, c->up, 2);
     x.out[0] = c->grad_x;
     x.ld_out[0] = c->ld_grad_x;
+    x.vec = c->ld_grad_x % 8 == 0;
     LayerArgs w = layer_args(rows ? MUON_PRODUCT_DEPTH : MUON_PRODUCT_DENSE, c->groups, c->offsets, c->n, c->k, c->m);
     set_a(w, 0, c->grad_pre_gate, nullptr, c->ld_grad_pre, 2);
     set_a(w, 1, c->grad_pre_up, nullptr, c->ld_grad_pre, 2);
     set_b(w, 0, c->x, 2);
-    w.stride_b[0] = 0;
+    w.stride_b = 0;
     w.out[0] = c->grad_gate;
     w.out[1] = c->grad_up;
-    w.ld_out[0] = w.ld_out[1] = c->ld_grad_w;
+    w.ld_out[0] = c->ld_grad_w;
     w.out_stride = c->groups > 1 ? c->stride_grad_w : 0;
+    w.vec = c->ld_grad_w * size_of(c->grad_dtype) % 16 == 0 && w.out_stride * size_of(c->grad_dtype) % 16 == 0;
     w.accumulate = c->accumulate;
     if ((to_x && !layer_fits(x, FORM_GRAD_X)) || (weights && !layer_fits(w, FORM_GRAD_W)))
         return fail(MUON_ERR_SHAPE, who, "2^31 or more output tiles");
     const bool in_place = c->grad_pre_gate == c->pre_gate && c->grad_pre_up == c->pre_up && c->ld_grad_pre == c->ld_pre;
     const int64_t size = size_of(c->grad_dtype);
-    const Extent out[] = {extent(c->m > 0 ? c->grad_pre_gate : nullptr, 1, 0, c->m, c->ld_grad_pre, c->n, 2),
-                          extent(c->m > 0 ? c->grad_pre_up : nullptr, 1, 0, c->m, c->ld_grad_pre, c->n, 2),
+    const Extent out[] = {extent(c->m > 0 ? c->grad_pre_gate : nullptr, 1, 0, c->m, c->ld_grad_pre, round_up(c->n, 64), 2),
+                          extent(c->m > 0 ? c->grad_pre_up : nullptr, 1, 0, c->m, c->ld_grad_pre, round_up(c->n, 64), 2),
                           extent(to_x ? c->grad_x : nullptr, 1, 0, c->m, c->ld_grad_x, c->k, 2),
                           extent(weights ? c->grad_gate : nullptr, c->groups, c->stride_grad_w, c->n, c->ld_grad_w, c->k, size),
                           extent(weights ? c->grad_up : nullptr, c->groups, c->stride_grad_w, c->n, c->ld_grad_w, c->k, size)};

@@ -541,7 +541,7 @@ def gated(x, gate, up, *, activation: str = "silu", offsets: Optional[torch.Tens
     x (rows, k) and gate, up (n, k), or with `offsets` stacks (groups, n, k), the rows offsets[g] to offsets[g + 1] by
     gate[g] and up[g]; rows outside every segment are not written.  All three are bfloat16 or all three Int8.
     activation: "silu", "gelu" or "relu".  With `save` the triple of the result, x gate^T and x up^T, which
-    gated_backward takes.
+    gated_backward takes (their rows are padded to multiples of 64).
     """
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
@@ -562,10 +562,9 @@ def gated(x, gate, up, *, activation: str = "silu", offsets: Optional[torch.Tens
         out = _result("out", out, like, size, torch.bfloat16)
         k.out, k.ld_out = out.data_ptr(), _rows("out", out)
         if save:
-            pre = torch.empty(2, *size, dtype=torch.bfloat16, device=like.device)
-            if pre[1].data_ptr() % 16:                         # odd sizes: each begins on a boundary of its own
-                pre = [torch.empty(size, dtype=torch.bfloat16, device=like.device) for _ in range(2)]
-            k.pre_gate, k.pre_up, k.ld_pre = pre[0].data_ptr(), pre[1].data_ptr(), k.n
+            pre = torch.empty(2, k.m, _up(k.n, 64), dtype=torch.bfloat16, device=like.device)
+            k.pre_gate, k.pre_up, k.ld_pre = pre[0].data_ptr(), pre[1].data_ptr(), pre.shape[2]
+            pre = pre[:, :, :k.n]
         L.check(L.muon_gated(C.byref(k), _stream_ptr(like)), "muon_gated")
     return (out, pre[0], pre[1]) if save else out
 
@@ -580,7 +579,7 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
 
     grad_x is bfloat16; grad_gate and grad_up are of `dtype` or go into the given tensors (float32 ones are added to
     with `accumulate`).  Rows outside every segment of offsets are not written in grad_x and have no part in the others.
-    With `reuse` the saved tensors serve as the workspace and do not keep their values.
+    With `reuse` the saved tensors (as `gated` made them) serve as the workspace and do not keep their values.
     """
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
@@ -604,11 +603,14 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
         if _rows("pre_up", pre_up) != k.ld_pre:
             raise ValueError("pre_gate and pre_up must have the same row stride")
         if reuse:
+            # rows of `gated`'s are padded, which the stride of one row alone tells as well
+            k.ld_pre = k.ld_grad_pre = pre_gate.stride(0)
+            if k.ld_pre % 64 or pre_up.stride(0) != k.ld_pre:
+                raise ValueError("reuse needs saved tensors whose rows are padded to multiples of 64")
             work = (pre_gate, pre_up)
-            k.ld_grad_pre = k.ld_pre
         else:
-            work = [torch.empty(k.m, _up(k.n, 8), dtype=torch.bfloat16, device=x.device) for _ in range(2)]
-            k.ld_grad_pre = _up(k.n, 8)
+            work = torch.empty(2, k.m, _up(k.n, 64), dtype=torch.bfloat16, device=x.device)
+            k.ld_grad_pre = work.shape[2]
         k.grad_pre_gate, k.grad_pre_up = work[0].data_ptr(), work[1].data_ptr()
         grad_x = _result("grad_x", grad_x, x, (k.m, k.k), torch.bfloat16)
         k.grad_x, k.ld_grad_x = grad_x.data_ptr(), _rows("grad_x", grad_x)

@@ -179,7 +179,7 @@ def test_gated_int8(m, n, k, ends, gap, act):
 def test_gated_backward(m, n, k, ends, gap, act):
     lead = () if ends is None else (len(ends) - 1,)
     x, w = _matrix(1, m, k, gap=gap), [_matrix(2 + i, *lead, n, k, std=1.5 / math.sqrt(k), gap=gap) for i in range(2)]
-    d, g, u = (_matrix(8 + i, m, n, std=s, gap=gap) for i, s in enumerate((0.1, 1.5, 1.0)))
+    d, g, u = (_matrix(8 + i, m, n, std=s, gap=-n % 64 if i else gap) for i, s in enumerate((0.1, 1.5, 1.0)))
     kept = [t.clone() for t in (g, u)]
     grad_x = torch.full((m, k + gap), 7.0, dtype=torch.bfloat16, device="cuda")
     _, w16g, w16u = X().gated_backward(d, x, *w, g, u, activation=act, offsets=_offsets(ends), grad_x=grad_x[:, :k])
@@ -274,7 +274,8 @@ def test_pre_gradients_at_the_ends(act):
     v = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 3.0, -3.0, 9.0, -9.0, -12.0, 60.0, -60.0, -80.0, 100.0, -100.0, 1e4, -1e4, 3e38, -3e38],
                      device="cuda").to(torch.bfloat16)
     n = v.numel()
-    g, u, d = v.repeat(2, 1), _matrix(1, 2, n), _matrix(2, 2, n, std=0.1)
+    g, u, d = _matrix(0, 2, n, gap=-n % 64), _matrix(1, 2, n, gap=-n % 64), _matrix(2, 2, n, std=0.1)
+    g.copy_(v)
     x, w = _matrix(3, 2, 8), [_matrix(4 + i, n, 8) for i in range(2)]
     v, kept = _np(g), _np(u)
     X().gated_backward(d, x, *w, g, u, activation=act, reuse=True)

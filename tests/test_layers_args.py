@@ -47,7 +47,7 @@ def _gated(i8=False, **kw):
 
 def _backward(**kw):
     c = L.muon_gated_backward_config(L.MUON_PRODUCT_ROWS, 4, L.MUON_ACT_SILU, L.MUON_DTYPE_F32, 0, 0, 10, 20, 200, _operand(P[0]),
-                                     _operand(P[1]), _operand(P[2]), P[3], P[4], 20, P[5], P[6], 20, P[7], P[8], 20, P[9], 200,
+                                     _operand(P[1]), _operand(P[2]), P[3], P[4], 20, P[5], P[6], 64, P[7], P[8], 64, P[9], 200,
                                      P[10], P[11], 200, 4000)
     return _set(c, kw)
 
@@ -96,12 +96,12 @@ REFUSED = [
     *[("gated_backward", kw, st) for kw, st in [
         (dict(activation=3), INVALID), (dict(grad_dtype=2), INVALID), (dict(accumulate=2), INVALID),
         (dict(accumulate=1, grad_dtype=L.MUON_DTYPE_BF16), INVALID), (dict(grad_up=None), INVALID), (dict(ld_grad=19), SHAPE), (dict(ld_pre=19), SHAPE),
-        (dict(ld_grad_pre=19), SHAPE), (dict(ld_grad_pre=1 << 22), SHAPE), (dict(ld_grad_x=199), SHAPE), (dict(ld_grad_w=199), SHAPE),
+        (dict(ld_grad_pre=0), SHAPE), (dict(ld_grad_pre=96), SHAPE), (dict(ld_grad_pre=1 << 22), SHAPE), (dict(ld_grad_x=199), SHAPE), (dict(ld_grad_w=199), SHAPE),
         (dict(stride_grad_w=3999), SHAPE), (dict(x__ld=199), SHAPE), (dict(gate__ld=199), SHAPE), (dict(x__data=None), INVALID),
         (dict(up__data=None), INVALID), (dict(grad=None), INVALID), (dict(grad_pre_up=None), INVALID), (dict(pre_gate=P[5] + 2), ALIGN),
         (dict(offsets=None), INVALID), (dict(grad_x=P[0]), INVALID), (dict(grad_pre_gate=P[4]), INVALID),
         (dict(grad_pre_gate=P[5]), INVALID), (dict(grad_pre_gate=P[6], grad_pre_up=P[5]), INVALID),
-        (dict(grad_pre_gate=P[5], grad_pre_up=P[6], ld_grad_pre=24), INVALID), (dict(grad_up=P[10] + 64), INVALID), (dict(grad_x=P[7]), INVALID),
+        (dict(grad_pre_gate=P[5], grad_pre_up=P[6], ld_grad_pre=128), INVALID), (dict(grad_up=P[10] + 64), INVALID), (dict(grad_x=P[7]), INVALID),
         (dict(grad_gate=P[1]), INVALID)]],
     *[("gather_rows", kw, st) for kw, st in [
         (dict(dtype=2), INVALID), (dict(per=0), INVALID), (dict(src_rows=-1), SHAPE), (dict(src_rows=1 << 30, per=3), SHAPE), (dict(n_rows=(1 << 30) + 1), SHAPE),
