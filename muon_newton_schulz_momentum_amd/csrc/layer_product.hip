@@ -5,6 +5,7 @@
 // FORM_GRAD_X) or, "across", of depth rows (weights in FORM_GRAD_X, both operands of FORM_GRAD_W, whose depth is the tokens).
 // b's rows are the matrix instruction's first operand: a lane then holds runs of 4 consecutive columns of one row of out.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "activation.h"
@@ -25,6 +26,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 // 16 bytes that may begin anywhere
 typedef i32x4 i32x4_any __attribute__((aligned(1)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
 // bfloat16 or 8-bit integer values: 16 bytes of a row are a lane's part of one instruction of either kind.
 template <class E>
@@ -32,14 +34,20 @@ struct Cores;
 template <>
 struct Cores<uint16_t> {
     typedef f32x16 sums;
+    typedef f32x4 few_sums;
     static __device__ __forceinline__ sums mul(i32x4 b, i32x4 a, sums c) {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ few_sums mul(i32x4 b, i32x4 a, few_sums c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
     }
 };
 template <>
 struct Cores<int8_t> {
     typedef i32x16 sums;
+    typedef i32x4 few_sums;
     static __device__ __forceinline__ sums mul(i32x4 b, i32x4 a, sums c) { return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0); }
+    static __device__ __forceinline__ few_sums mul(i32x4 b, i32x4 a, few_sums c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0); }
 };
 
 template <int FORM>
@@ -57,11 +65,6 @@ __device__ __forceinline__ float gated_value(int activation, float g, float u) {
                                           : dev::activate<MUON_ACT_RELU>(g)) * u;
 }
 
-// ---- 128 x 128 tiles for any alignment ------------------------------------------------------
-//
-// 4 waves of 64 x 64; every 16 bytes of an operand are checked against its end, so rows may begin anywhere.
-constexpr int ANY = 128, ANY_THREADS = 256;
-
 // 16 bytes at byte `at` of a row of `end` bytes; zeros behind its end.
 template <class E>
 __device__ __forceinline__ i32x4 load_checked(const uint8_t* row, int64_t at, int64_t end) {
@@ -75,11 +78,14 @@ __device__ __forceinline__ i32x4 load_checked(const uint8_t* row, int64_t at, in
     return v;
 }
 
-template <class E, int FORM, class OUT>
+// ---- gradients with fewer than 8 features or columns ----------------------------------------------
+//
+// 128 x 128 tiles, 4 waves of 64 x 64, one step at a time; every 16 bytes of an operand are checked against its end.
+constexpr int ANY = 128, ANY_THREADS = 256;
+
+template <int FORM, class OUT>
 __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
-    constexpr bool GATED = FORM == FORM_GATED, I8 = sizeof(E) == 1;
     constexpr int STEP = 64, ROW = STEP + 16;              // bytes of a row in a step, and apart in LDS
-    constexpr int COLS = GATED ? ANY / 2 : ANY;            // columns of out in a tile
     __shared__ __attribute__((aligned(16))) uint8_t smem[2][ANY * ROW];
     __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
     __shared__ int64_t wave_tot[ANY_THREADS / 64];
@@ -88,46 +94,36 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
     if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, ANY_THREADS>(p, ANY, bounds, ends, wave_tot);
     Walk my = walk<pair<FORM>>(p, ends);
     for (int t = next_tile(p, my); t >= 0; t = next_tile(p, my)) {
-        const Tile x = decode<1, pair<FORM>>(p, t, ANY, COLS, bounds, ends);
-        const int64_t group_b = p.mode == MUON_PRODUCT_ROWS ? x.group : 0;
-        typename Cores<E>::sums acc[2][2] = {};
+        const Tile x = decode<1, pair<FORM>>(p, t, ANY, ANY, bounds, ends);
+        const int64_t to_group = p.mode == MUON_PRODUCT_ROWS ? x.group * p.stride_b : 0;
+        f32x16 acc[2][2] = {};
         for (int part = 0; part < parts<FORM>; ++part)
-            for (int64_t k0 = x.kb0; k0 < x.kb1; k0 += STEP / (int)sizeof(E)) {
-                // operand `op`: 128 rows of its panel
-                auto stage = [&](int op, bool across) {
-                    if (!across) {
-                        const int r = tid >> 1;
-                        const uint8_t* row = nullptr;
-                        if (op == 0) {
-                            if (r < x.rows_a) row = p.a[part] + (x.m0 + r) * p.lda;
-                        } else {
-                            const int w = GATED ? r / COLS : part, c = GATED ? r % COLS : r;
-                            if (c < x.rows_b) row = p.b[w] + group_b * p.stride_b + (x.n0 + c) * p.ldb;
-                        }
+            for (int64_t k0 = x.kb0; k0 < x.kb1; k0 += STEP / 2) {
+                // 128 rows of a panel along: two chunks of one a thread
+                auto along = [&](uint8_t* to, const uint8_t* row) {
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int at = 32 * (tid & 1) + 16 * c;
-                            i32x4 v = {0, 0, 0, 0};
-                            if (row) v = load_checked<E>(row, k0 * (int)sizeof(E) + at, (int64_t)x.kb1 * (int)sizeof(E));
-                            *reinterpret_cast<i32x4*>(smem[op] + r * ROW + at) = v;
-                        }
-                    } else {
-                        const int kk = tid >> 3, c0 = 16 * (tid & 7);
-                        const int w = op == 0 ? x.which : part;
-                        const uint8_t* row = op == 0 ? p.a[w] + (k0 + kk) * p.lda : p.b[w] + group_b * p.stride_b + (k0 + kk) * p.ldb;
-                        const int64_t first = (op == 0 ? x.m0 : x.n0) + c0, end = op == 0 ? p.m : p.n;
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            i32x4 v = {0, 0, 0, 0};
-                            if (k0 + kk < x.kb1) v = load_checked<E>(row, 2 * (first + 8 * c), 2 * end);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                *reinterpret_cast<uint16_t*>(smem[op] + (c0 + 8 * c + e) * ROW + 2 * kk) = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        const int at = 32 * (tid & 1) + 16 * c;
+                        i32x4 v = {0, 0, 0, 0};
+                        if (row) v = load_checked<uint16_t>(row, 2 * k0 + at, 2 * (int64_t)x.kb1);
+                        *reinterpret_cast<i32x4*>(to + (tid >> 1) * ROW + at) = v;
                     }
                 };
-                stage(0, a_across<FORM>);
-                stage(1, b_across<FORM>);
+                // or 32 depth rows across, transposed: 16 columns from `first` a thread
+                auto across = [&](uint8_t* to, const uint8_t* base, int64_t ld, int64_t first, int64_t end) {
+                    const int kk = tid >> 3, c0 = 16 * (tid & 7);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        i32x4 v = {0, 0, 0, 0};
+                        if (k0 + kk < x.kb1) v = load_checked<uint16_t>(base + (k0 + kk) * ld, 2 * (first + c0 + 8 * c), 2 * end);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint16_t*>(to + (c0 + 8 * c + e) * ROW + 2 * kk) = (uint16_t)((uint32_t)v[e / 2] >> (16 * (e & 1)));
+                    }
+                };
+                if constexpr (a_across<FORM>) across(smem[0], p.a[x.which], p.lda, x.m0, p.m);
+                else along(smem[0], (tid >> 1) < x.rows_a ? p.a[part] + (x.m0 + (tid >> 1)) * p.lda : nullptr);
+                across(smem[1], p.b[part] + to_group, p.ldb, x.n0, p.n);
                 __syncthreads();
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
@@ -135,12 +131,12 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         fa[i] = *reinterpret_cast<const i32x4*>(smem[0] + (64 * wm + 32 * i + fr) * ROW + 32 * kk + 16 * fk);
-                        fb[i] = *reinterpret_cast<const i32x4*>(smem[1] + ((GATED ? 64 * i + 32 * wn : 64 * wn + 32 * i) + fr) * ROW + 32 * kk + 16 * fk);
+                        fb[i] = *reinterpret_cast<const i32x4*>(smem[1] + (64 * wn + 32 * i + fr) * ROW + 32 * kk + 16 * fk);
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[i][j] = Cores<E>::mul(fb[j], fa[i], acc[i][j]);
+                        for (int j = 0; j < 2; ++j) acc[i][j] = Cores<uint16_t>::mul(fb[j], fa[i], acc[i][j]);
                 }
                 __syncthreads();
             }
@@ -149,33 +145,17 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
         for (int i = 0; i < 2; ++i) {
             const int r = 64 * wm + 32 * i + fr;
             if (r >= x.rows_a) continue;
-            const float sa = I8 ? p.sa[x.m0 + r] : 1.f;
-            auto column = [&](int w, int64_t c, float v) { return I8 ? v * sa * p.sb[w][group_b * p.stride_sb + c] : v; };
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int c = 8 * (v >> 2) + 4 * fk + (v & 3);
-                if constexpr (GATED) {
-                    if (32 * wn + c >= x.rows_b) continue;
-                    const int64_t col = x.n0 + 32 * wn + c;
-                    const float g = column(0, col, (float)acc[i][0][v]), u = column(1, col, (float)acc[i][1][v]);
-                    static_cast<uint16_t*>(p.out[0])[(x.m0 + r) * p.ld_out[0] + col] = dev::f32_to_bf16(gated_value(p.activation, g, u));
-                    if (p.out[1]) {
-                        static_cast<uint16_t*>(p.out[1])[(x.m0 + r) * p.ld_out[1] + col] = dev::f32_to_bf16(g);
-                        static_cast<uint16_t*>(p.out[2])[(x.m0 + r) * p.ld_out[1] + col] = dev::f32_to_bf16(u);
-                    }
-                } else {
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (64 * wn + 32 * j + c >= x.rows_b) continue;
-                        const int64_t col = x.n0 + 64 * wn + 32 * j + c;
-                        const float s = column(0, col, (float)acc[i][j][v]);
-                        OUT* o = static_cast<OUT*>(p.out[x.which]) + (p.mode == MUON_PRODUCT_DEPTH ? x.group * p.out_stride : 0) +
-                                 (x.m0 + r) * p.ld_out[0] + col;
-                        if constexpr (sizeof(OUT) == 4) *o = p.accumulate ? *o + s : s;
-                        else *o = dev::f32_to_bf16(s);
-                    }
+                for (int v = 0; v < 16; ++v) {
+                    const int c = 64 * wn + 32 * j + 8 * (v >> 2) + 4 * fk + (v & 3);
+                    if (c >= x.rows_b) continue;
+                    OUT* o = static_cast<OUT*>(p.out[x.which]) + (p.mode == MUON_PRODUCT_DEPTH ? x.group * p.out_stride : 0) +
+                             (x.m0 + r) * p.ld_out[0] + x.n0 + c;
+                    if constexpr (sizeof(OUT) == 4) *o = p.accumulate ? *o + acc[i][j][v] : acc[i][j][v];
+                    else *o = dev::f32_to_bf16(acc[i][j][v]);
                 }
-            }
         }
     }
 }
@@ -244,7 +224,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const int wh = wave >> 2, wc = wave & 3;               // wave row and column
     const int fr = lane & 31, fk = lane >> 5;
 
-    if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, THREADS>(p, TILE, bounds, ends, wave_tot);
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, THREADS>(p, p.tile_rows, bounds, ends, wave_tot);
     Walk my = walk<pair<FORM>>(p, ends);
     int t = next_tile(p, my);
     if (t < 0) return;
@@ -327,6 +307,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         bytes_b = (x.rows_b - 1) * ldb + row_bytes;
         auto column = [&](int64_t c, int64_t n) { return 2 * (int)min(c + 8 * kc, n - 8); };
         va = ACROSS_A ? kr * lda + column(x.m0, p.m) : (8 * wave + (ln >> 3)) * lda + 16 * (ln & 7);
+        if (ACROSS_A && 8 * kc >= p.tile_rows) va = 0x60000000;   // nothing there: behind any buffer of 64 rows below 2^23 bytes
         vb = ACROSS_B ? kr * ldb + column(x.n0, p.n) : (8 * wave + (ln >> 3)) * ldb + 16 * (ln & 7);
         const Aim r = aim(0, mask(steps > 0), true);
 #pragma unroll
@@ -478,8 +459,10 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[e] = gated_value(p.activation, v[0][e], v[1][e]);
                 put(c, h);
-                put(32 + c, v[0]);
-                put(64 + c, v[1]);
+                if (p.out[1]) {
+                    put(32 + c, v[0]);
+                    put(64 + c, v[1]);
+                }
             } else {
                 put(c, v[0]);
                 put(32 + c, v[1]);
@@ -538,7 +521,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         __builtin_amdgcn_wave_barrier();
     };
 
-    Tile x = decode<1, pair<FORM>>(p, t, TILE, COLS, bounds, ends);
+    Tile x = decode<1, pair<FORM>>(p, t, p.tile_rows, COLS, bounds, ends);
     begin(x);
     fill();
     for (;;) {
@@ -560,7 +543,7 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         const bool more = t >= 0;
         // the next tile's first loads run beside this one's stores
         if (more) {
-            x = decode<1, pair<FORM>>(p, t, TILE, COLS, bounds, ends);
+            x = decode<1, pair<FORM>>(p, t, p.tile_rows, COLS, bounds, ends);
             begin(x);
         }
         write(0);
@@ -572,6 +555,127 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     }
 }
 
+// ---- few rows or few tiles: 16 or 32 rows by 16 or more columns, depth split over the waves -----------------
+//
+// For serving, where 256 x 256 tiles would leave most of the chip idle.  Each of 8 waves takes every eighth step (128 bytes) of the
+// depth of a tile of 16 RB rows of a by 16 NB rows of b (of a gated block NB / 2 blocks of gate and as many of up), its fragments
+// straight from memory into registers, AHEAD steps at a time, so that a tile's loads are under way together; the
+// waves' sums are added up through LDS in the order of the waves.  Bound by memory, and for a single call by its latency.
+template <class E, int FORM, class OUT, int RB, int NB, int AHEAD>
+__global__ __launch_bounds__(THREADS) void layer_few_kernel(LayerArgs p) {
+    constexpr bool GATED = FORM == FORM_GATED, I8 = sizeof(E) == 1, F32 = sizeof(OUT) == 4;
+    constexpr int ES = (int)sizeof(E), UNIT = STEP / ES;
+    constexpr int ROWS = 16 * RB, COLS = 16 * NB, SUMS = COLS + 4;  // of sums; a row of them in LDS
+    constexpr int OUT_COLS = GATED ? COLS / 2 : COLS;
+    typedef typename Cores<E>::few_sums sums_t;
+    __shared__ __attribute__((aligned(16))) int sums[WAVES][ROWS * SUMS];
+    __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
+    __shared__ int64_t wave_tot[WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int fr = lane & 15, fk = lane >> 4;
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, THREADS>(p, ROWS, bounds, ends, wave_tot);
+    Walk my = walk<1>(p, ends);
+    for (int t = next_tile(p, my); t >= 0; t = next_tile(p, my)) {
+        const Tile x = decode<1, 1>(p, t, ROWS, OUT_COLS, bounds, ends);
+        const int64_t group = p.mode == MUON_PRODUCT_ROWS ? x.group : 0;
+        // the lane's rows; those past the end repeat the last: their sums are not stored
+        const uint8_t *ra[RB], *rb[NB];
+#pragma unroll
+        for (int i = 0; i < RB; ++i) ra[i] = p.a[0] + (x.m0 + min(16 * i + fr, x.rows_a - 1)) * p.lda;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const int w = GATED ? j / (NB / 2) : 0, c = 16 * (GATED ? j % (NB / 2) : j) + fr;
+            rb[j] = p.b[w] + group * p.stride_b + (x.n0 + min(c, x.rows_b - 1)) * p.ldb;
+        }
+        sums_t acc[RB][NB] = {};
+        // U steps from `step` on, every eighth; a lane's 32 bytes of each are two instructions' parts
+        auto steps = [&](auto u_, auto load, int step) {
+            constexpr int U = decltype(u_)::value;
+            i32x4 fa[U][RB][2], fb[U][NB][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = (int64_t)(step + u * WAVES) * STEP + 32 * fk;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) fb[u][j][h] = load(rb[j], at + 16 * h);
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) fa[u][i][h] = load(ra[i], at + 16 * h);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < RB; ++i)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) acc[i][j] = Cores<E>::mul(fb[u][j][h], fa[u][i][h], acc[i][j]);
+        };
+        auto whole = [](const uint8_t* row, int64_t at) -> i32x4 { return *reinterpret_cast<const i32x4_any*>(row + at); };
+        const int depth = x.kb1;
+        const int n_steps = I8 ? (depth + UNIT - 1) / UNIT : depth / UNIT;   // rows of codes are whole steps
+        int step = wave;
+        for (; step + (AHEAD - 1) * WAVES < n_steps; step += AHEAD * WAVES) steps(ic<AHEAD>{}, whole, step);
+        for (; step < n_steps; step += WAVES) steps(ic<1>{}, whole, step);
+        if (!I8 && step == n_steps && depth % UNIT != 0)   // the remainder is the next wave's
+            steps(ic<1>{}, [&](const uint8_t* row, int64_t at) { return load_checked<E>(row, at, (int64_t)depth * ES); }, step);
+        // a lane's sums are rows 16 i + fr, columns 16 j + 4 fk + (0 .. 3)
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) *reinterpret_cast<sums_t*>(&sums[wave][(16 * i + fr) * SUMS + 16 * j + 4 * fk]) = acc[i][j];
+        __syncthreads();
+        for (int id = tid; id < ROWS * OUT_COLS / 4; id += THREADS) {
+            const int row = id / (OUT_COLS / 4), col = 4 * (id % (OUT_COLS / 4));
+            if (row >= x.rows_a) continue;
+            const int64_t left = p.n - x.n0 - col;
+            f32x4 v[GATED ? 2 : 1];
+#pragma unroll
+            for (int w = 0; w < (GATED ? 2 : 1); ++w) {
+                const int at = row * SUMS + w * OUT_COLS + col;
+                sums_t s = *reinterpret_cast<const sums_t*>(&sums[0][at]);
+#pragma unroll
+                for (int u = 1; u < WAVES; ++u) s += *reinterpret_cast<const sums_t*>(&sums[u][at]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[w][e] = (float)s[e];
+                    if constexpr (I8)
+                        if (e < left) v[w][e] = v[w][e] * p.sa[x.m0 + row] * p.sb[w][group * p.stride_sb + x.n0 + col + e];
+                }
+            }
+            auto put = [&](OUT* o, const f32x4& u) {
+                if (left >= 4) {
+                    if constexpr (F32) *reinterpret_cast<f32x4_any*>(o) = u;
+                    else *reinterpret_cast<u32x2_any*>(o) = u32x2_any{dev::f32x2_to_bf16x2(u[0], u[1]), dev::f32x2_to_bf16x2(u[2], u[3])};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (e >= left) continue;
+                        if constexpr (F32) o[e] = u[e];
+                        else o[e] = dev::f32_to_bf16(u[e]);
+                    }
+                }
+            };
+            const int64_t r = x.m0 + row, c = x.n0 + col;
+            OUT* o = static_cast<OUT*>(p.out[0]) + r * p.ld_out[0] + c;
+            if constexpr (GATED) {
+                f32x4 h;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = gated_value(p.activation, v[0][e], v[1][e]);
+                put(o, h);
+                if (p.out[1]) {
+                    put(static_cast<OUT*>(p.out[1]) + r * p.ld_out[1] + c, v[0]);
+                    put(static_cast<OUT*>(p.out[2]) + r * p.ld_out[1] + c, v[1]);
+                }
+            } else {
+                put(o, v[0]);
+            }
+        }
+        __syncthreads();                                   // the sums are read
+    }
+}
+
 // Whether the 256 x 256 tiles' loads fit: at least one of 16 bytes in a row (and a whole step where the depth's remainder
 // comes first and its loads reach beyond it).
 template <class E, int FORM>
@@ -580,22 +684,88 @@ bool tile_loads_fit(const LayerArgs& a) {
     return b_across<FORM> ? a.n >= 8 : sizeof(E) == 1 || a.k >= STEP / 2;
 }
 
+// What a launch would take, in us, from what these kernels measured with operands from L2 and the chip partly or fully busy: its
+// rounds of tiles, each a constant and so much a step.  A step of a 256 x 256 tile takes 1.0 us alone on the chip and
+// 1.55 with all CUs busy (clock and caches), with 128 rows 0.73 and 1.0, with 64 0.61 and 0.7 (4096 x 4096 by 1024 gate and up in
+// bfloat16: 79 us in 128 tiles of 256 rows, 71 in 256 of 128, 102 in 512 of 64; 1024 x 4096: 78, 55, 46).
+struct Cost {
+    int64_t tiles;
+    double us;
+};
+template <int FORM>
+Cost big_cost(LayerArgs a, int rows, double steps) {
+    a.tile_rows = rows;
+    const int64_t most = count_tiles<pair<FORM>>(a, rows, FORM == FORM_GATED ? TILE / 2 : TILE);
+    double n = (double)most, used = (double)rows;
+    if (a.mode == MUON_PRODUCT_ROWS) {
+        // segments end inside tiles, on average in the middle
+        const double segments = (double)std::min<int64_t>(a.m, a.groups);
+        n = std::max((double)a.m / rows + 0.5 * segments, segments) * a.tiles_n;
+        used = std::min(used, (double)a.m / segments);
+    } else {
+        used = std::min(used, (double)a.m);
+    }
+    static const double alone[] = {0.61, 0.73, 0.87, 1.0}, busy[] = {0.7, 1.0, 1.3, 1.55}, begin[] = {5.5, 7.0, 8.0, 9.0};
+    const int nb = std::min(std::max((int)std::ceil(used / 64.0), 1), 4) - 1;
+    const double share = std::min(n / CUS, 1.0);
+    return {most, std::ceil(n / CUS) * (begin[nb] + (FORM == FORM_GATED ? 2.0 : 0.0) + steps * (alone[nb] + (busy[nb] - alone[nb]) * share))};
+}
+
 template <class E, int FORM, class OUT>
 hipError_t layer_as(LayerArgs a, hipStream_t s) {
-    LayerArgs any = a;
-    const int64_t n_big = count_tiles<pair<FORM>>(a, TILE, FORM == FORM_GATED ? TILE / 2 : TILE);
-    const int64_t n_any = count_tiles<pair<FORM>>(any, ANY, FORM == FORM_GATED ? ANY / 2 : ANY);
-    if (n_big == 0) return hipSuccess;
+    constexpr bool GATED = FORM == FORM_GATED;
     auto grid = [](int64_t tiles, int64_t most) { return dim3((unsigned)std::min<int64_t>((tiles + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)); };
-    if (tile_loads_fit<E, FORM>(a)) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT>), grid(n_big, CUS), dim3(THREADS), 0, s, a);
-    else hipLaunchKernelGGL((layer_any_kernel<E, FORM, OUT>), grid(n_any, 2 * CUS), dim3(ANY_THREADS), 0, s, any);
+    if (a.m == 0 || a.n == 0) return hipSuccess;
+    const double depth = (double)a.k * (double)sizeof(E) / STEP / (a.mode == MUON_PRODUCT_DEPTH ? a.groups : 1);
+    const double steps = std::ceil(depth) * parts<FORM>;
+    int pick = -1;
+    Cost best{0, 1e30};
+    if (tile_loads_fit<E, FORM>(a))
+        for (int rows : {256, 128, 64}) {
+            const Cost c = big_cost<FORM>(a, rows, steps);
+            if (c.tiles >= 0 && c.us < best.us) {
+                best = c;
+                pick = rows;
+            }
+        }
+    if constexpr (GATED || FORM == FORM_SCALED) {
+        // 16 rows, 32 rows, 32 rows by 64 columns: bound by a wave's share of the depth where there are few tiles, by the steps of
+        // all tiles where there are many (1 row by 5632 x 2048 gate and up in bfloat16: 16, 18, 18 us and 32 in big tiles; 64 rows: 40, 31,
+        // 30, 33; 256 rows: 131, 95, 72, 53; 1 row by 2048 x 5632 in 8-bit integers: 7, 8, 15, 32)
+        constexpr int THIN = GATED ? 2 : 1;
+        static const double wait[2][3] = {{0.65, 0.75, 2.4}, {1.2, 1.55, 2.4}}, rate[2][3] = {{1900, 1290, 625}, {1500, 1024, 740}};
+        LayerArgs few[3] = {a, a, a};
+        for (int i = 0; i < 3; ++i) {
+            few[i].tile_rows = i == 0 ? 16 : 32;
+            const int64_t n = count_tiles<1>(few[i], few[i].tile_rows, i == 2 ? (GATED ? 32 : 64) : 16);
+            const double us = 3.0 + std::max(steps / WAVES * wait[GATED][i], (double)n * (steps + 2.0) / rate[GATED][i]);
+            if (n >= 0 && us < best.us) {
+                best = {n, us};
+                pick = i;
+            }
+        }
+        if (pick == 0) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 1, THIN, 4>), grid(best.tiles, 4 * CUS), dim3(THREADS), 0, s, few[0]);
+        else if (pick == 1) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 2, THIN, 4>), grid(best.tiles, 2 * CUS), dim3(THREADS), 0, s, few[1]);
+        else if (pick == 2) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 2, 4, 2>), grid(best.tiles, 2 * CUS), dim3(THREADS), 0, s, few[2]);
+        if (pick >= 0 && pick <= 2) return hipGetLastError();
+    }
+    if constexpr (b_across<FORM>)
+        if (pick < 0) {
+            const int64_t n = count_tiles<pair<FORM>>(a, ANY, ANY);
+            hipLaunchKernelGGL((layer_any_kernel<FORM, OUT>), grid(n, 2 * CUS), dim3(ANY_THREADS), 0, s, a);
+            return hipGetLastError();
+        }
+    a.tile_rows = pick;
+    count_tiles<pair<FORM>>(a, pick, GATED ? TILE / 2 : TILE);
+    hipLaunchKernelGGL((layer_kernel<E, FORM, OUT>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// (the kernel that takes any size of a form)
 bool layer_fits(LayerArgs a, LayerForm form) {
-    return (form == FORM_GRAD_W ? count_tiles<2>(a, ANY, ANY) : count_tiles<1>(a, ANY, ANY / 2)) >= 0;
+    return (form == FORM_GRAD_W ? count_tiles<2>(a, ANY, ANY) : form == FORM_GRAD_X ? count_tiles<1>(a, ANY, ANY) : count_tiles<1>(a, 32, 32)) >= 0;
 }
 
 hipError_t launch_layer(LayerArgs a, LayerForm form, int32_t operands, int32_t out_dtype, hipStream_t s) {

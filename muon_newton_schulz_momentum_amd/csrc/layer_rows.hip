@@ -64,10 +64,10 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t cols, c
 
 // ---- 8-bit integer quantisation ---------------------------------------------------------------
 
-// The whole number nearest x / s, ties to even, for |x| <= 127.5 s or so: rint of the approximate quotient is off by one at
-// most; what is left, x - c s, is exact in one fused multiply-add (its magnitude is near s / 2 or less and
-// it is a multiple of the smaller of x's and s's last places), and its double against s decides.
-__device__ __forceinline__ int nearest_code(float x, float s, float inverse) {
+// The whole number nearest x / s, ties to even, kept in [-127, 127], whatever x / s: rint of the approximate quotient is off by one
+// at most; what is left, x - c s, is exact in one fused multiply-add (its magnitude is near s / 2 or less and it is a
+// multiple of the smaller of x's and s's last places), and its double against s decides.
+__device__ __forceinline__ int exact_code(float x, float s, float inverse) {
     float c = fminf(fmaxf(rintf(x * inverse), -127.f), 127.f);
     const float left = fmaf(-c, s, x), twice = 2.f * fabsf(left);
     const bool odd = ((int)c & 1) != 0;
@@ -75,44 +75,150 @@ __device__ __forceinline__ int nearest_code(float x, float s, float inverse) {
     return (int)fminf(fmaxf(c, -127.f), 127.f);
 }
 
-// One wave per row, in two passes over it.
+// 8 values' codes.  x times the rounded inverse is within 127.5 * 2^-23 < 2^-16 of the quotient (s above 2^-64, where |x| <= 127 s
+// (1 + 2^-24)), so its nearest whole number is the code unless it lies within 2^-15 of a border: then the wave takes the exact
+// way.  Adding 1.5 * 2^23 rounds to a whole number, ties to even, and leaves its two's complement in the low bits.
+__device__ __forceinline__ uint2 codes8(const float (&v)[V], float s, float inverse) {
+    uint32_t q[V];
+    float worst = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        const float x = v[e] * inverse, f = x + 12582912.f;
+        q[e] = __float_as_uint(f);
+        worst = fmaxf(worst, fabsf(x - (f - 12582912.f)));
+    }
+    if (__builtin_amdgcn_ballot_w64(worst > 0.5f - 0x1p-15f) == 0) {
+        const uint32_t a = __builtin_amdgcn_perm(q[1], q[0], 0x0c0c0400), b = __builtin_amdgcn_perm(q[3], q[2], 0x04000c0c);
+        const uint32_t c = __builtin_amdgcn_perm(q[5], q[4], 0x0c0c0400), d = __builtin_amdgcn_perm(q[7], q[6], 0x04000c0c);
+        return make_uint2(a | b, c | d);
+    }
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e / 4] |= ((uint32_t)exact_code(v[e], s, inverse) & 255u) << (8 * (e & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+// 8 values as they are in memory.
 template <class T>
+struct Raw;
+template <>
+struct Raw<float> {
+    float v[V];
+    __device__ __forceinline__ void load(const float* at) {
+        const f32x4_any a = *reinterpret_cast<const f32x4_any*>(at), b = *reinterpret_cast<const f32x4_any*>(at + 4);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    __device__ __forceinline__ void load_checked(const float* row, int64_t c, int64_t cols) { load8(row, c, cols, v); }
+    __device__ __forceinline__ void get(float (&to)[V]) const {
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[e] = v[e];
+    }
+};
+template <>
+struct Raw<uint16_t> {
+    uint32_t w[V / 2];
+    __device__ __forceinline__ void load(const uint16_t* at) {
+        const u32x4_any a = *reinterpret_cast<const u32x4_any*>(at);
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    }
+    __device__ __forceinline__ void load_checked(const uint16_t* row, int64_t c, int64_t cols) {
+        float v[V];
+        load8(row, c, cols, v);
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) w[e] = dev::f32x2_to_bf16x2(v[2 * e], v[2 * e + 1]);
+    }
+    // (unpacked anew wherever they are used)
+    __device__ __forceinline__ void get(float (&to)[V]) {
+        asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+#pragma unroll
+        for (int e = 0; e < V; ++e) to[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+    }
+};
+
+// LANES (16, a wave or the workgroup) take a row, whose values stay in registers between its largest magnitude and its codes, CHUNKS of 8 a
+// lane; CHUNKS 0: longer rows, read twice, or shorter ones than 8.  A chunk that would pass the end of its row is the row's last 8 values,
+// whose codes are shifted to their place.  Bound by memory (16381 rows of 8704 bfloat16: 87 us, 4.9 TB/s; read twice
+// and checked at every load 127).
+template <class T, int LANES, int CHUNKS>
 __global__ __launch_bounds__(THREADS) void int8_quantize_kernel(Int8QuantizeArgs p) {
-    const int lane = threadIdx.x & 63;
+    __shared__ uint32_t tops[THREADS / WAVE];
+    const int tid = threadIdx.x, lane = tid % LANES;
     const int64_t end = p.limit ? min((int64_t)*p.limit, p.total) : p.total;
-    for (int64_t r = first_wave(); r < end; r += all_waves()) {
+    for (int64_t r = (int64_t)blockIdx.x * (THREADS / LANES) + tid / LANES; r < end; r += (int64_t)gridDim.x * (THREADS / LANES)) {
         const T* row = nullptr;
         if (p.gather) {
             const int c = p.gather[r];
             if (c >= 0 && c / p.per < p.src_rows) row = static_cast<const T*>(p.src) + (int64_t)(c / p.per) * p.ld;
+        } else if (p.batch_stride == 0) {
+            row = static_cast<const T*>(p.src) + r * p.ld;
         } else {
             row = static_cast<const T*>(p.src) + r / p.rows * p.batch_stride + r % p.rows * p.ld;
         }
-        uint32_t top = 0;                                      // bits of magnitudes are ordered as the magnitudes are
-        if (row)
-            for (int64_t c = lane * V; c < p.cols; c += WAVE * V) {
-                float v[V];
-                load8(row, c, p.cols, v);
+        Raw<T> raw[CHUNKS > 0 ? CHUNKS : 1];
+        uint32_t top = 0;                                  // bits of magnitudes are ordered as the magnitudes are
+        auto largest = [&](Raw<T>& x) {
+            float v[V];
+            x.get(v);
 #pragma unroll
-                for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+            for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        };
+        const int cols = (int)p.cols;
+        if (row) {
+            if constexpr (CHUNKS > 0) {
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) raw[i].load(row + min((i * LANES + lane) * V, cols - V));
+#pragma unroll
+                for (int i = 0; i < CHUNKS; ++i) largest(raw[i]);
+            } else {
+                for (int64_t c = lane * V; c < cols; c += LANES * V) {
+                    raw[0].load_checked(row, c, cols);
+                    largest(raw[0]);
+                }
             }
+        }
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+        for (int off = (LANES < WAVE ? LANES : WAVE) / 2; off > 0; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, 64));
+        if (LANES > WAVE) {
+            if (tid % WAVE == 0) tops[tid / WAVE] = top;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < THREADS / WAVE; ++w) top = max(top, tops[w]);
+            __syncthreads();                               // before the next row's
+        }
         const bool finite = top < 0x7f800000u;
         const float s = finite ? __uint_as_float(top) / 127.f : __uint_as_float(0x7fc00000u);
         if (lane == 0) p.scales[r] = s;
-        // small scales are brought to where their inverse and all steps are exact as above
-        const float lift = s < 0x1p-64f ? 0x1p64f : 1.f, lifted = s * lift, inverse = 1.f / lifted;
-        const bool any = row && finite && s > 0.f;
-        for (int64_t c = lane * V; c < p.kp; c += WAVE * V) {
-            uint32_t w[2] = {0, 0};
-            if (any && c < p.cols) {
-                float v[V];
-                load8(row, c, p.cols, v);
+        // small scales are brought to where their inverse and all steps are exact; there s may have been rounded far
+        const bool tiny = s < 0x1p-64f, any = row && finite && s > 0.f;
+        const float lift = tiny ? 0x1p64f : 1.f, lifted = s * lift, inverse = 1.f / lifted;
+        auto codes = [&](Raw<T>& x) {
+            float v[V];
+            x.get(v);
+            if (!tiny) return codes8(v, s, inverse);
 #pragma unroll
-                for (int e = 0; e < V; ++e) w[e / 4] |= ((uint32_t)nearest_code(v[e] * lift, lifted, inverse) & 255u) << (8 * (e & 3));
+            for (int e = 0; e < V; ++e) v[e] = (float)exact_code(v[e] * lift, lifted, inverse);
+            return codes8(v, 1.f, 1.f);
+        };
+        auto put = [&](int64_t c, uint64_t w) { __builtin_nontemporal_store(w, reinterpret_cast<uint64_t*>(p.codes + r * p.kp + c)); };
+        if constexpr (CHUNKS > 0) {
+#pragma unroll
+            for (int i = 0; i < CHUNKS; ++i) {
+                const int c = (i * LANES + lane) * V, before = c - max(cols - V, 0);
+                uint64_t w = 0;
+                if (any) w = __builtin_bit_cast(uint64_t, codes(raw[i]));
+                if (before > 0) w = before < V ? w >> (8 * before) : 0;
+                if (c < p.kp) put(c, w);
             }
-            *reinterpret_cast<uint2*>(p.codes + r * p.kp + c) = make_uint2(w[0], w[1]);
+        } else {
+            for (int64_t c = lane * V; c < p.kp; c += LANES * V) {
+                uint64_t w = 0;
+                if (any && c < cols) {
+                    raw[0].load_checked(row, c, cols);
+                    w = __builtin_bit_cast(uint64_t, codes(raw[0]));
+                }
+                put(c, w);
+            }
         }
     }
 }
@@ -246,12 +352,35 @@ hipError_t launch_gated_grad(const GatedGradArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+namespace {
+
+template <class T>
+hipError_t quantize_as(const Int8QuantizeArgs& a, hipStream_t s) {
+    // Where there are rows for all CUs: 16 lanes a row of up to 256 values (200000 rows of 128 bfloat16: NARROW_US us, with a wave 77), a
+    // wave up to 4096; else, and for longer ones, the workgroup.
+    const int64_t chunks = (a.kp + V - 1) / V;
+    const int lanes = a.cols < V || a.total < 4096 || chunks > 8 * WAVE ? THREADS : chunks > 32 ? WAVE : 16;
+    const int64_t each = a.cols < V ? 9 : (chunks + lanes - 1) / lanes;
+    const dim3 grid(blocks_of(a.total, THREADS / lanes)), block(THREADS);
+#define MUON_QUANTIZE(L, C) hipLaunchKernelGGL((int8_quantize_kernel<T, L, C>), grid, block, 0, s, a)
+    if (lanes == 16) MUON_QUANTIZE(16, 2);
+    else if (lanes == WAVE && each <= 2) MUON_QUANTIZE(WAVE, 2);
+    else if (lanes == WAVE && each <= 4) MUON_QUANTIZE(WAVE, 4);
+    else if (lanes == WAVE) MUON_QUANTIZE(WAVE, 8);
+    else if (each <= 1) MUON_QUANTIZE(THREADS, 1);
+    else if (each <= 2) MUON_QUANTIZE(THREADS, 2);
+    else if (each <= 5) MUON_QUANTIZE(THREADS, 5);
+    else if (each <= 8) MUON_QUANTIZE(THREADS, 8);
+    else MUON_QUANTIZE(THREADS, 0);
+#undef MUON_QUANTIZE
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_int8_quantize(const Int8QuantizeArgs& a, int32_t src_dtype, hipStream_t s) {
     if (a.total == 0) return hipSuccess;
-    const dim3 grid(blocks_of(a.total, THREADS / WAVE)), block(THREADS);
-    if (src_dtype == MUON_DTYPE_F32) hipLaunchKernelGGL((int8_quantize_kernel<float>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((int8_quantize_kernel<uint16_t>), grid, block, 0, s, a);
-    return hipGetLastError();
+    return src_dtype == MUON_DTYPE_F32 ? quantize_as<float>(a, s) : quantize_as<uint16_t>(a, s);
 }
 
 hipError_t launch_gather_rows(const GatherRowsArgs& a, int32_t dtype, hipStream_t s) {
