@@ -19,7 +19,6 @@ namespace {
 using namespace tiles;
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -28,26 +27,22 @@ typedef i32x4 i32x4_any __attribute__((aligned(1)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 
-// bfloat16 or 8-bit integer values: 16 bytes of a row are a lane's part of one instruction of either kind.
+// bfloat16 or 8-bit integer values: 16 bytes of a row are a lane's part of one instruction of either kind, which multiplies 16
+// rows by 16 over 64 bytes of depth.  The 32 x 32 forms are the slower ones here: with all CUs busy the card's power sets the clock,
+// and on normal values those alone reach 1.72 PFLOP/s in bfloat16 and 3.32 in 8-bit integers, these 1.95 and 3.94.
 template <class E>
 struct Cores;
 template <>
 struct Cores<uint16_t> {
-    typedef f32x16 sums;
-    typedef f32x4 few_sums;
+    typedef f32x4 sums;
     static __device__ __forceinline__ sums mul(i32x4 b, i32x4 a, sums c) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
-    }
-    static __device__ __forceinline__ few_sums mul(i32x4 b, i32x4 a, few_sums c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
     }
 };
 template <>
 struct Cores<int8_t> {
-    typedef i32x16 sums;
-    typedef i32x4 few_sums;
-    static __device__ __forceinline__ sums mul(i32x4 b, i32x4 a, sums c) { return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0); }
-    static __device__ __forceinline__ few_sums mul(i32x4 b, i32x4 a, few_sums c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0); }
+    typedef i32x4 sums;
+    static __device__ __forceinline__ sums mul(i32x4 b, i32x4 a, sums c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, c, 0, 0, 0); }
 };
 
 template <int FORM>
@@ -136,7 +131,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) acc[i][j] = Cores<uint16_t>::mul(fb[j], fa[i], acc[i][j]);
+                        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, fb[j]), __builtin_bit_cast(bf16x8, fa[i]), acc[i][j], 0, 0, 0);
                 }
                 __syncthreads();
             }
@@ -162,19 +157,19 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
 
 // ---- 256 x 256 tiles ------------------------------------------------------------------------
 //
-// One workgroup of 8 waves per CU that goes through its share of the tiles.  Wave (h, c) of 2 x 4 takes the 32-row blocks
+// One workgroup of 8 waves per CU that goes through its share of the tiles.  Wave (h, c) of 2 x 4 takes the 16-row blocks
 // 2 i + h of a and 64 rows of b, so that a tile with fewer rows (a segment's end) leaves both wave rows half of what there is:
-// a wave runs its first NB of 4 row blocks.  Of a gated block a tile is 256 x 128: b's panel holds 128 rows of gate and the
+// a wave runs its first NB of 8 row blocks.  Of a gated block a tile is 256 x 128: b's panel holds 128 rows of gate and the
 // same 128 of up, a wave 32 of each, so a lane has both sums of a value of out.
 constexpr int TILE = 256, WAVES = 8, THREADS = 64 * WAVES;
-constexpr int FM = 4, FN = 2;                              // 32 x 32 blocks of a wave
+constexpr int FN = 4;                                      // 16 x 16 blocks of a wave along b; along a: FM
 constexpr int STEP = 128;                                  // bytes of a row in a step: 64 bfloat16 values, 128 codes
 
 template <int N>
 using ic = std::integral_constant<int, N>;
 
 // Keeps the matrix instructions that have written acc so far in front of what follows.
-template <class S>
+template <class S, int FM>
 __device__ __forceinline__ void pin(S (&acc)[FM][FN]) {
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -192,9 +187,11 @@ __device__ __forceinline__ uint64_t read_transposed(const uint8_t* at) {
 // Operands go global -> VGPR -> LDS, a step (128 bytes of depth) ahead of the stage that is multiplied, of which there are
 // two; the step's one barrier comes in the middle of its last sub-step, whose fragments are then in registers.
 //
-// A panel along its rows lies in LDS in rows of 144 bytes: the 16 rows that a fragment read touches fall on 16 different
-// 16-byte slots of the 256 bytes that LDS serves at once.  A panel across lies in 64 depth rows of 512 bytes whose 64-byte granules
-// are permuted by the row, so that the 8 rows of a transposing read fall on 8 different ones.
+// LDS serves a 16-byte read 16 lanes at a time, which have all 16 rows of a block but not one depth (lanes 0 to 3, 12 to 15, 20 to 23
+// and 24 to 27 for one), and a 16-byte write 8 lanes at a time, here a row's 8 chunks.  So of a panel along its rows, chunk c of
+// row r lies in the r ^ c-th of the 16 slots of its block's c-th 256 bytes: reads fall on different rows' slots, writes on
+// different chunks'.  (Rows of 144 bytes had conflicts in 38 % of LDS's cycles.)  A panel across lies in 64 depth rows of 512 bytes whose 32-byte
+// pieces (16 columns) are permuted by the row, so that the 8 rows that half a wave's transposing read touches fall on 8 different ones.
 //
 // Nothing in the main loop deals with ends:
 //   * a depth that is no multiple of the step is taken with its remainder first, whose loads are masked where they are stored
@@ -204,67 +201,118 @@ __device__ __forceinline__ uint64_t read_transposed(const uint8_t* at) {
 //   * of a panel across the last 8 columns are loaded again where fewer than 8 are left: in those 8 places of the tile
 //     the last columns come last, and out is stored accordingly.
 // So a 16-byte load never crosses the end of a row, and rows may begin anywhere.
-template <class E, int FORM, class OUT>
+template <class E, int FORM, class OUT, int ROWS>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2))) void layer_kernel(LayerArgs p) {
     constexpr bool GATED = FORM == FORM_GATED, I8 = sizeof(E) == 1, F32 = sizeof(OUT) == 4;
     constexpr bool ACROSS_A = a_across<FORM>, ACROSS_B = b_across<FORM>, TWO = parts<FORM> == 2;
     constexpr int ES = (int)sizeof(E), UNIT = STEP / ES;   // values of a step
     constexpr int COLS = GATED ? TILE / 2 : TILE;
-    constexpr int LA = 4, NLOAD = 2 * LA;                  // load instructions of a step
-    constexpr int ROW = STEP + 16, KROW = 2 * TILE;        // LDS rows of a panel along, across
-    constexpr int PANEL_A = ACROSS_A ? UNIT * KROW : TILE * ROW, PANEL_B = ACROSS_B ? UNIT * KROW : TILE * ROW, STAGE = PANEL_A + PANEL_B;
+    constexpr int FM = ROWS / 32;                          // row blocks of a wave
+    constexpr int LA = ROWS / 64, NLOAD = LA + 4;          // load instructions of a step
+    constexpr int BLOCK = 16 * STEP, KROW_A = 2 * ROWS, KROW_B = 2 * TILE;  // LDS bytes of 16 rows of a panel along, of a depth row across
+    constexpr int PANEL_A = ROWS * STEP, STAGE = PANEL_A + TILE * STEP;
+    constexpr int CPA = ROWS / 8, CPB = TILE / 8, KA = THREADS / CPA, KB = THREADS / CPB;  // 16-byte chunks of a depth row, depth rows of a load
+    static_assert(ROWS >= 64 && KA * LA == UNIT * ES / 2, "loads make up a step");
     constexpr int EPL = 16 / (int)sizeof(OUT);             // values of out in 16 bytes
     constexpr int OCOLS = GATED ? 96 : 64;                 // columns that a wave stages: out, gate and up; or out
-    constexpr int OROW = OCOLS * (int)sizeof(OUT) + 16;
-    constexpr int OUT_STAGE = WAVES * 32 * OROW;           // out goes through the second stage
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGE + (STAGE > OUT_STAGE ? STAGE : OUT_STAGE)];
+    constexpr int OROW = OCOLS * (int)sizeof(OUT) + (F32 ? 0 : 16);  // (a float32 row's 16 pieces are permuted by the row instead)
+    constexpr int WB = WAVES * 32 * OROW <= STAGE ? 2 : 1; // row blocks of out that go through a stage at a time
+    static_assert(WAVES * 16 * WB * OROW <= STAGE && FM % WB == 0, "out goes through one stage");
+    // The next tile's first two steps are loaded in this one's last two.  That takes one loop for all tiles: with several, the loads in
+    // flight have other registers in each of them, and have to end where the loops' code meets.  Of the rows of an expert, 256 at
+    // a time, the last ones are too often few to be multiplied as if they were all there: those tiles have a loop of their own.
+    constexpr bool AHEAD = ACROSS_A || ROWS < 256;
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * STAGE];
     __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
     __shared__ int64_t wave_tot[WAVES];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wh = wave >> 2, wc = wave & 3;               // wave row and column
-    const int fr = lane & 31, fk = lane >> 5;
+    // opaque, so that what is worked out of it per tile is not kept through the main loop, which has registers for a few values only
+    auto thread = []() {
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));
+        return t;
+    };
 
-    if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, THREADS>(p, p.tile_rows, bounds, ends, wave_tot);
+    if (p.mode != MUON_PRODUCT_DENSE) read_segments<1, THREADS>(p, ROWS, bounds, ends, wave_tot);
     Walk my = walk<pair<FORM>>(p, ends);
     int t = next_tile(p, my);
     if (t < 0) return;
 
-    // staging: along, load i brings rows 64 i + lrow, chunk lchunk; across, depth rows 16 i + krow, chunk kchunk
-    const int lrow = 8 * wave + (lane >> 3), lchunk = lane & 7, krow = tid >> 5, kchunk = tid & 31;
-    auto swizzle = [](int k) { return (k & 3) | ((k >> 1) & 4); };
-    const int along = lrow * ROW + 16 * lchunk, across = krow * KROW + (((kchunk >> 2) ^ swizzle(krow)) << 6) + ((kchunk & 3) << 4);
+    // Staging: along, load i brings rows 64 i + t / 8, chunk t % 8; across, depth rows KA i + t / CPA, chunk t % CPA (KB, CPB).
+    // The permutation of 32-byte pieces does not change from load to load; rows of 128 bytes are two to 256.
+    auto swizzle = [](int k, int row_bytes) { return row_bytes == 128 ? ((k >> 1) & 1) | ((k >> 2) & 2) : ((k & 3) << 1) | ((k >> 3) & 1); };
+    int along = 0, across_a = 0, across_b = 0;
+    {
+        const int t = thread();
+        auto place = [&](int row, int chunk, int row_bytes) { return row * row_bytes + (((chunk >> 1) ^ swizzle(row, row_bytes)) << 5) + ((chunk & 1) << 4); };
+        if (!ACROSS_A || !ACROSS_B) along = (t >> 7) * BLOCK + (t & 7) * 256 + ((((t >> 3) & 15) ^ (t & 7)) << 4);
+        if (ACROSS_A) across_a = place(t / CPA, t % CPA, KROW_A);
+        if (ACROSS_B) across_b = place(t / CPB, t % CPB, KROW_B);
+    }
 
-    // of the tile: operands' first rows (along) or depth row 0 (across), the lane's offset from there in load 0, sizes of
-    // the buffers along; the depth's begin, its values before the whole steps, those of each part, and all steps
-    const uint8_t *base_a, *base_b;
-    int va, vb, bytes_a, bytes_b, first, rest, whole, steps;
+    // A tile's operands: their first rows (along) or depth row 0 (across), sizes of the buffers along; the depth's begin, its
+    // values before the whole steps, those of each part, and all steps.
+    struct Span {
+        const uint8_t *a, *b;
+        int bytes_a, bytes_b, first, rest, whole, steps;
+    };
+    Span cur{}, nxt{};                                     // of the tile that is multiplied, and (AHEAD) of the next one
+    int va = 0, vb = 0, va_next = 0, vb_next = 0;          // the lane's offset from there in load 0
+    int ahead_ok = 0;                                      // -1 where the next tile's first two steps are loaded in this one's last two
     const int lda = (int)p.lda, ldb = (int)p.ldb;
     i32x4 staged[NLOAD];
     // Where a step's loads go: operands' buffers, and their scalar offset along (pieces of this are the same for all of a step).
     struct Aim {
         const uint8_t *a, *b;
-        int bytes_a, bytes_b, along;
+        int bytes_a, bytes_b, along, va, vb;
     };
-    // Step `step` of the run, or nowhere where keep is 0 and not -1 (from an empty buffer, which fetches nothing).  No branch, which
+    auto mask = [](bool valid) {
+        int keep = __builtin_amdgcn_readfirstlane(valid ? -1 : 0);
+        asm volatile("" : "+s"(keep));
+        return keep;
+    };
+    // Step `step` of a tile, or nowhere where keep is 0 and not -1 (from an empty buffer, which fetches nothing).  No branch, which
     // in the main loop would let the compiler move the matrix instructions behind it.
-    auto aim = [&](int step, int keep, bool begins) {
-        const int lead = rest > 0, w = step - lead;
-        const int part = TWO ? (whole - 1 - w) >> 31 : 0;  // 0, or -1 for the second
-        int at = UNIT * (w - (whole & part)), valid = UNIT;
-        if (TWO) valid = min(valid, (int)p.k - at);
-        else at += first + rest;
-        if (begins && lead) {
-            at = first;
-            valid = rest;
+    auto aim = [&](const Span& x, int step, int keep) {
+        const int lead = min(x.rest, 1), w = step - lead;
+        const int partial = w >> 31;                       // -1 for the remainder
+        const int part = TWO ? (x.whole - 1 - w) >> 31 : 0;  // 0, or -1 for the second
+        int at = UNIT * (w - (x.whole & part)), valid;
+        if (TWO) {
+            valid = min(UNIT, (int)p.k - at);
+        } else {
+            at = x.first + ((x.rest + at) & ~partial);
+            valid = UNIT + ((x.rest - UNIT) & partial);
         }
         at &= keep;
         Aim r;
-        r.a = base_a + (TWO ? (p.a[1] - p.a[0]) & (int64_t)part : 0) + (ACROSS_A ? (int64_t)at * lda : 0);
-        r.b = base_b + (TWO ? (p.b[1] - p.b[0]) & (int64_t)part : 0) + (ACROSS_B ? (int64_t)at * ldb : 0);
-        r.bytes_a = (ACROSS_A ? (valid - 1) * lda + 2 * (int)p.m : bytes_a) & keep;
-        r.bytes_b = (ACROSS_B ? (valid - 1) * ldb + 2 * (int)p.n : bytes_b) & keep;
+        r.a = x.a + (TWO ? (p.a[1] - p.a[0]) & (int64_t)part : 0) + (ACROSS_A ? (int64_t)at * lda : 0);
+        r.b = x.b + (TWO ? (p.b[1] - p.b[0]) & (int64_t)part : 0) + (ACROSS_B ? (int64_t)at * ldb : 0);
+        r.bytes_a = (ACROSS_A ? (valid - 1) * lda + 2 * (int)p.m : x.bytes_a) & keep;
+        r.bytes_b = (ACROSS_B ? (valid - 1) * ldb + 2 * (int)p.n : x.bytes_b) & keep;
         r.along = at * ES;
+        r.va = va;
+        r.vb = vb;
         return r;
+    };
+    // Step `step` of the tile that is multiplied, or behind its last the next tile's first two, or nowhere.
+    auto aim_on = [&](int step) {
+        const int over = mask(step >= cur.steps);          // -1 or 0
+        if constexpr (!AHEAD) {
+            return aim(cur, step, ~over);
+        } else {
+            auto pick = [&](int x, int y) { return x ^ ((x ^ y) & over); };
+            auto pick_ptr = [&](const uint8_t* x, const uint8_t* y) {
+                return (const uint8_t*)((uint64_t)x ^ (((uint64_t)x ^ (uint64_t)y) & (uint64_t)(int64_t)over));
+            };
+            const Span x = {pick_ptr(cur.a, nxt.a), pick_ptr(cur.b, nxt.b), pick(cur.bytes_a, nxt.bytes_a), pick(cur.bytes_b, nxt.bytes_b),
+                            pick(cur.first, nxt.first), pick(cur.rest, nxt.rest), pick(cur.whole, nxt.whole), 0};
+            Aim r = aim(x, step - (cur.steps & over), ~over | ahead_ok);
+            if (ACROSS_A) r.va = pick(va, va_next);
+            if (ACROSS_B) r.vb = pick(vb, vb_next);
+            return r;
+        }
     };
     // Chunk d of a step into its register.
     auto load = [&](int d, const Aim& r) {
@@ -272,200 +320,242 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         const int i = is_a ? d : d - LA;
         const bool across = is_a ? ACROSS_A : ACROSS_B;
         // (opaque, or the sums of all d stay in registers)
-        int32_t rows_on = (across ? 16 * i : 64 * (GATED && !is_a ? i & 1 : i)) * (is_a ? lda : ldb);
+        int32_t rows_on = (across ? (is_a ? KA : KB) * i : 64 * (GATED && !is_a ? i & 1 : i)) * (is_a ? lda : ldb);
         asm volatile("" : "+s"(rows_on));
         // (of a gated block b's loads 0 and 1 bring gate, 2 and 3 up)
         const uint8_t* base = (is_a ? r.a : r.b) + (GATED && !is_a && i >= 2 ? p.b[1] - p.b[0] : 0);
         const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, is_a ? r.bytes_a : r.bytes_b, 0x00020000);
-        staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, (is_a ? va : vb) + rows_on, across ? 0 : r.along, 0);
-    };
-    auto mask = [](bool valid) {
-        int keep = __builtin_amdgcn_readfirstlane(valid ? -1 : 0);
-        asm volatile("" : "+s"(keep));
-        return keep;
+        staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, (is_a ? r.va : r.vb) + rows_on, across ? 0 : r.along, 0);
     };
     auto store = [&](int d, int st) {
         const bool is_a = d < LA;
         const int i = is_a ? d : d - LA;
-        const int at = (is_a ? ACROSS_A : ACROSS_B) ? across + 16 * KROW * i : along + 64 * ROW * i;
+        const int at = !(is_a ? ACROSS_A : ACROSS_B) ? along + 4 * BLOCK * i : is_a ? across_a + KA * KROW_A * i : across_b + KB * KROW_B * i;
         *reinterpret_cast<i32x4*>(smem + st * STAGE + (is_a ? 0 : PANEL_A) + at) = staged[d];
     };
-    // The tile's operands, and the first loads of them.
-    auto begin = [&](const Tile& x) {
-        int ln = lane, kr = krow, kc = kchunk;
-        asm volatile("" : "+v"(ln), "+v"(kr), "+v"(kc));   // worked out per tile instead of being kept
-        const int64_t to_group = p.mode == MUON_PRODUCT_ROWS ? x.group * p.stride_b : 0;
-        base_a = p.a[ACROSS_A ? x.which : 0] + (ACROSS_A ? 0 : x.m0 * p.lda);
-        base_b = p.b[0] + to_group + (ACROSS_B ? 0 : x.n0 * p.ldb);
+    auto span = [&](const Tile& x, bool there, int& va, int& vb) {
+        const int t = thread(), lrow = t >> 3, lchunk = t & 7;
+        auto all = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        Span r;
+        r.a = uniform(p.a[ACROSS_A ? x.which : 0] + (ACROSS_A ? 0 : x.m0 * p.lda));
+        r.b = uniform(p.b[0] + (p.mode == MUON_PRODUCT_ROWS ? x.group * p.stride_b : 0) + (ACROSS_B ? 0 : x.n0 * p.ldb));
         const int depth = x.kb1 - x.kb0;
-        first = __builtin_amdgcn_readfirstlane(x.kb0);
-        rest = __builtin_amdgcn_readfirstlane(I8 || TWO ? 0 : depth % UNIT);
-        whole = __builtin_amdgcn_readfirstlane(I8 || TWO ? (depth + UNIT - 1) / UNIT : depth / UNIT);
-        steps = __builtin_amdgcn_readfirstlane((rest > 0) + parts<FORM> * whole);
-        const int row_bytes = I8 || TWO ? whole * STEP : x.kb1 * ES;
-        bytes_a = (x.rows_a - 1) * lda + row_bytes;
-        bytes_b = (x.rows_b - 1) * ldb + row_bytes;
-        auto column = [&](int64_t c, int64_t n) { return 2 * (int)min(c + 8 * kc, n - 8); };
-        va = ACROSS_A ? kr * lda + column(x.m0, p.m) : (8 * wave + (ln >> 3)) * lda + 16 * (ln & 7);
-        if (ACROSS_A && 8 * kc >= p.tile_rows) va = 0x60000000;   // nothing there: behind any buffer of 64 rows below 2^23 bytes
-        vb = ACROSS_B ? kr * ldb + column(x.n0, p.n) : (8 * wave + (ln >> 3)) * ldb + 16 * (ln & 7);
-        const Aim r = aim(0, mask(steps > 0), true);
+        r.first = all(x.kb0);
+        r.rest = all(I8 || TWO ? 0 : depth % UNIT);
+        r.whole = all(I8 || TWO ? (depth + UNIT - 1) / UNIT : depth / UNIT);
+        r.steps = all(there ? (r.rest > 0) + parts<FORM> * r.whole : 0);
+        const int row_bytes = I8 || TWO ? r.whole * STEP : x.kb1 * ES;
+        r.bytes_a = all((x.rows_a - 1) * lda + row_bytes);
+        r.bytes_b = all((x.rows_b - 1) * ldb + row_bytes);
+        auto column = [](int64_t c, int64_t n) { return 2 * (int)min(c, n - 8); };
+        va = ACROSS_A ? t / CPA * lda + column(x.m0 + 8 * (t % CPA), p.m) : lrow * lda + 16 * lchunk;
+        vb = ACROSS_B ? t / CPB * ldb + column(x.n0 + 8 * (t % CPB), p.n) : lrow * ldb + 16 * lchunk;
+        return r;
+    };
+    // The first loads of a tile, or, where they were loaded ahead, none.
+    auto begin = [&](int keep) {
+        const Aim r = aim(cur, 0, mask(cur.steps > 0) & keep);
 #pragma unroll
         for (int d = 0; d < NLOAD; ++d) load(d, r);
     };
-    // The first step into LDS, the second into the registers.
-    auto fill = [&]() {
-        if (steps == 0) return;
+    // Its first step into LDS, the second into the registers.
+    auto fill = [&](int st) {
         // values of a lane's chunk that are in the partial step; the others follow in the next one
-        const int have = rest > 0 ? min(max(rest * ES - 16 * lchunk, 0), 16) : 16;
+        const int have = cur.rest > 0 ? min(max(cur.rest * ES - 16 * (thread() & 7), 0), 16) : 16;
         i32x4 inside;
 #pragma unroll
         for (int e = 0; e < 4; ++e) inside[e] = have >= 4 * e + 4 ? -1 : have == 4 * e + 2 ? 0xffff : 0;
-        const Aim r = aim(1, mask(1 < steps), false);
+        const Aim r = aim_on(1);
 #pragma unroll
         for (int d = 0; d < NLOAD; ++d) {
             if (!I8 && !TWO && !(d < LA ? ACROSS_A : ACROSS_B)) staged[d] &= inside;
-            store(d, 0);
+            store(d, st);
             load(d, r);
         }
     };
 
-    // a fragment, 16 bytes of a row's depth, in sub-step kk: along in one read; across in two, whose lanes take depth
-    // rows tk and columns tc
-    const int tk = 8 * (lane >> 5) + ((lane & 15) >> 2), tc = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-    int ra[ACROSS_A ? FM : 1], rb[ACROSS_B ? FN : 1];
-    if (ACROSS_A) {
-#pragma unroll
-        for (int i = 0; i < (ACROSS_A ? FM : 1); ++i) ra[i] = tk * KROW + (((2 * i + wh) ^ swizzle(tk)) << 6) + 2 * tc;
-    } else {
-        ra[0] = (32 * wh + fr) * ROW + 16 * fk;
+    // A fragment, 16 bytes of a row's depth, in sub-step kk: along in one read; across in two, whose lanes take depth rows tk and
+    // columns tc.  (Blocks i of a and j of b lie apart by bits of the address that nothing else of it has: 2 i + wh is
+    // i << 1 | wh, 4 wc + j is wc << 2 | j.)
+    int ra, rb;
+    {
+        const int t = thread(), fr = t & 15, fk = (t >> 4) & 3;
+        const int tk = 8 * fk + (fr >> 2), tc = 4 * (t & 3);
+        ra = ACROSS_A ? tk * KROW_A + ((wh ^ swizzle(tk, KROW_A)) << 5) + 2 * tc : wh * BLOCK + fk * 256 + ((fr ^ fk) << 4);
+        rb = PANEL_A + (ACROSS_B ? tk * KROW_B + (((4 * wc) ^ swizzle(tk, KROW_B)) << 5) + 2 * tc : (GATED ? 2 : 4) * wc * BLOCK + fk * 256 + ((fr ^ fk) << 4));
     }
-    if (ACROSS_B) {
-#pragma unroll
-        for (int j = 0; j < (ACROSS_B ? FN : 1); ++j) rb[j] = PANEL_A + tk * KROW + (((2 * wc + j) ^ swizzle(tk)) << 6) + 2 * tc;
-    } else {
-        rb[0] = PANEL_A + ((GATED ? 32 : 64) * wc + fr) * ROW + 16 * fk;
-    }
-    auto read_across = [&](const uint8_t* at) {
+    static_assert(PANEL_A % 512 == 0 && STAGE % 512 == 0, "stages and panels begin on multiples of all rows");
+    auto read_across = [&](int at, int row_bytes) {
         typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(i32x4, u64x2{read_transposed(at), read_transposed(at + 4 * KROW)});
+        return __builtin_bit_cast(i32x4, u64x2{read_transposed(smem + at), read_transposed(smem + at + 4 * row_bytes)});
     };
     auto read_a = [&](int i, int st, int kk) {
-        if constexpr (ACROSS_A) return read_across(smem + st * STAGE + ra[ACROSS_A ? i : 0] + 16 * KROW * kk);
-        else return *reinterpret_cast<const i32x4*>(smem + st * STAGE + ra[0] + 64 * i * ROW + 32 * kk);
+        if constexpr (ACROSS_A) return read_across(((ra + st * STAGE) ^ (i << 6)) + 32 * KROW_A * kk, KROW_A);
+        else return *reinterpret_cast<const i32x4*>(smem + ((ra + st * STAGE) ^ (kk << 6)) + 2 * BLOCK * i + 1024 * kk);
     };
     auto read_b = [&](int j, int st, int kk) {
-        if constexpr (ACROSS_B) return read_across(smem + st * STAGE + rb[ACROSS_B ? j : 0] + 16 * KROW * kk);
-        else return *reinterpret_cast<const i32x4*>(smem + st * STAGE + rb[0] + (GATED ? TILE / 2 : 32) * j * ROW + 32 * kk);
+        if constexpr (ACROSS_B) return read_across(((rb + st * STAGE) ^ (j << 5)) + 32 * KROW_B * kk, KROW_B);
+        else return *reinterpret_cast<const i32x4*>(smem + ((rb + st * STAGE) ^ (kk << 6)) + (GATED ? (j >> 1) * (TILE / 32) + (j & 1) : j) * BLOCK + 1024 * kk);
+    };
+
+    // Waits for the loads in flight, where they are the last steps' empty ones: what comes may have other uses for their registers, and
+    // would wait in the main loop.
+    auto settle = [&]() {
+#pragma unroll
+        for (int d = 0; d < NLOAD; ++d) asm volatile("" : : "v"(staged[d]));
     };
 
     typename Cores<E>::sums acc[FM][FN];
-    // The steps of a tile for a wave with NB row blocks.
-    auto multiply = [&](auto nb_) {
-        constexpr int NB = decltype(nb_)::value;
-        // A sub-step's slots are its matrix instructions, behind which staging and the next sub-step's reads go; in the last
-        // one the barrier comes before slot BAR, reads behind it.
-        constexpr int SUBS = 4, SLOTS = NB * FN, BAR = SLOTS / 2, ALL = (SUBS - 1) * SLOTS + BAR, READS = NB + FN;
-        i32x4 fa[2][NB], fb[2][FN];
-        auto read = [&](int r, int to, int st, int kk) {   // b's first and a's first come first
-            if (r == 0) fb[to][0] = read_b(0, st, kk);
-            else if (r == 1) fa[to][0] = read_a(0, st, kk);
-            else if (r == 2) fb[to][1] = read_b(1, st, kk);
-            else fa[to][r - 2] = read_a(r - 2, st, kk);
-        };
+    // The steps of a tile for a wave whose first `pairs` of 4 pairs of row blocks have rows (FULL: all of them).
+    //
+    // A step is two sub-steps; in each a pair's 8 matrix instructions stand together.  Behind them go staging, over the slots before the
+    // step's barrier (half way through the second sub-step), and the next sub-step's reads: a's in place, b's to the other
+    // registers.
+    int begins = 0;                                        // stage of the tile's first step
+    auto multiply = [&](auto full_, int pairs) {
+        constexpr bool FULL = decltype(full_)::value;
+        constexpr int PAIRS = FM / 2, TURN = PAIRS / 2;    // pairs of a sub-step; of the second one before the barrier
+        static_assert(FULL || NLOAD == PAIRS + 2 + TURN, "staging between the pairs");
+        i32x4 fa[FM], fb[2][FN];
+        // (in the order of the loop's reads, as a wait there covers both)
 #pragma unroll
-        for (int r = 0; r < READS; ++r) read(r, 0, 0, 0);
-        for (int step = 0; step < steps; ++step) {
-            const Aim ahead = aim(step + 2, mask(step + 2 < steps), false);
-            const int st = step & 1, st_next = st ^ 1;
+        for (int j = 0; j < FN; ++j) {
+            fb[0][j] = read_b(j, begins, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-            for (int kk = 0; kk < SUBS; ++kk) {
-                const int cur = kk & 1, nxt = cur ^ 1;
-                const bool last = kk == SUBS - 1;
+        for (int i = 0; i < FM; ++i) {
+            fa[i] = read_a(i, begins, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int step = 0; step < cur.steps; ++step) {
+            const Aim ahead = aim_on(step + 2);
+            const int st = (begins + step) & 1, st_next = st ^ 1;
+            auto stage = [&](int d) {
+                store(d, st_next);
+                load(d, ahead);
+            };
+            // Pair q in sub-step kk, read(f) behind its instruction f.
+            auto pair_of = [&](int q, int kk, auto read) {
+                constexpr int ALL = (PAIRS + TURN) * 2 * FN;   // slots of staging
 #pragma unroll
-                for (int f = 0; f < SLOTS; ++f) {
-                    const int i = f / FN, j = f % FN;
-                    if (last && f == BAR) {
-                        pin(acc);
-                        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                        __builtin_amdgcn_s_barrier();
-                        asm volatile("" ::: "memory");
-                    }
+                for (int f = 0; f < 2 * FN; ++f) {
+                    const int i = 2 * q + f / FN, j = f % FN, g = (PAIRS * kk + q) * 2 * FN + f;
                     __builtin_amdgcn_sched_barrier(0);
-                    acc[i][j] = Cores<E>::mul(fb[cur][j], fa[cur][i], acc[i][j]);
+                    acc[i][j] = Cores<E>::mul(fb[kk][j], fa[i], acc[i][j]);
                     __builtin_amdgcn_sched_barrier(0);
-                    const int g = kk * SLOTS + f;
-                    if (g < ALL)
+                    if (FULL && g < ALL && (g + 1) * NLOAD / ALL > g * NLOAD / ALL) stage(g * NLOAD / ALL);
+                    read(f);
+                }
+            };
+            // a's of pair q are read for the next sub-step behind their last use
+            auto renew = [&](int q, int f, int rst, int kk) {
+                if (f == FN - 1) fa[2 * q] = read_a(2 * q, rst, kk);
+                if (f == 2 * FN - 1) fa[2 * q + 1] = read_a(2 * q + 1, rst, kk);
+            };
+            // the next step's first fragments: b's, and the a's that were used before the barrier
+            auto first = [&](int f) {
+                if (f < FN) fb[0][f] = read_b(f, st_next, 0);
+                else if (f - FN < 2 * TURN) fa[f - FN] = read_a(f - FN, st_next, 0);
+            };
+            auto turn = [&]() {
+                pin(acc);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+            };
 #pragma unroll
-                        for (int d = g * NLOAD / ALL; d < (g + 1) * NLOAD / ALL; ++d) {
-                            store(d, st_next);
-                            load(d, ahead);
-                        }
-                    const int lo = last ? BAR : 0, n = SLOTS - lo;
-                    if (f >= lo)
+            for (int q = 0; q < PAIRS; ++q) {
+                if (FULL || q == 0 || pairs > q)
+                    pair_of(q, 0, [&](int f) {
+                        if (q == 0 && f < FN) fb[1][f] = read_b(f, st, 1);
+                        renew(q, f, st, 1);
+                    });
+                if (!FULL) stage(q), q == 0 || q == PAIRS - 1 ? stage(q == 0 ? PAIRS : PAIRS + 1) : (void)0;
+            }
 #pragma unroll
-                        for (int r = (f - lo) * READS / n; r < (f - lo + 1) * READS / n; ++r) read(r, nxt, last ? st_next : st, last ? 0 : kk + 1);
+            for (int q = 0; q < TURN; ++q) {
+                if (FULL || q == 0 || pairs > q) pair_of(q, 1, [](int) {});
+                if (!FULL) stage(PAIRS + 2 + q);
+            }
+            turn();
+            if (TURN == PAIRS || !(FULL || pairs > TURN)) {
+#pragma unroll
+                for (int f = 0; f < FN + 2 * TURN; ++f) {
+                    first(f);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
+#pragma unroll
+            for (int q = TURN; q < PAIRS; ++q)
+                if (FULL || pairs > q)
+                    pair_of(q, 1, [&](int f) {
+                        if (q == TURN) first(f);
+                        renew(q, f, st_next, 0);
+                    });
         }
+        if (!AHEAD) settle();
     };
 
     // Scales of the lane's rows and columns (8-bit integers), asked for before the next tile's loads.
     float sa[I8 ? FM : 1];
-    f32x4 sb[I8 ? FN : 1][4];
+    f32x4 sb[I8 ? FN : 1];
     Tile done;
     auto read_scales = [&](const Tile& x) {
         if constexpr (I8) {
             const int64_t group = p.mode == MUON_PRODUCT_ROWS ? x.group * p.stride_sb : 0;
+            const int t = thread(), fr = t & 15, fk = (t >> 4) & 3;
 #pragma unroll
-            for (int i = 0; i < FM; ++i) sa[i] = p.sa[x.m0 + min(64 * i + 32 * wh + fr, x.rows_a - 1)];
+            for (int i = 0; i < FM; ++i) sa[i] = p.sa[x.m0 + min(32 * i + 16 * wh + fr, x.rows_a - 1)];
 #pragma unroll
             for (int j = 0; j < FN; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        sb[j][q][e] = p.sb[GATED ? j : 0][group + x.n0 + min((GATED ? 32 : 64) * wc + (GATED ? 0 : 32) * j + 8 * q + 4 * fk + e, x.rows_b - 1)];
+                for (int e = 0; e < 4; ++e)
+                    sb[j][e] = p.sb[GATED ? j >> 1 : 0][group + x.n0 + min(GATED ? 32 * wc + 16 * (j & 1) + 4 * fk + e : 64 * wc + 16 * j + 4 * fk + e, x.rows_b - 1)];
         }
     };
-    // Row block i of out: 32 rows of the wave through its part of the second stage (which nobody reads between a tile's
-    // last barrier and the next one's first step), then in 16-byte stores along the rows, which leave the caches to the operands.
-    auto write = [&](int i) {
-        // opaque, so that the addresses are worked out per tile instead of being kept through the main loop
-        int ln = lane;
-        asm volatile("" : "+v"(ln));
-        uint8_t* mine = smem + STAGE + wave * 32 * OROW;
-        const int r0 = 64 * i + 32 * wh;
+    // Row blocks WB w on of out: 16 or 32 rows of the wave through its part of the stage of the tile's last step (which is not read any
+    // more after that step's barrier, nor written before the next tile's first step), then in 16-byte stores along the rows, which leave the caches to the operands.
+    auto write = [&](int w2, int st) {  // w2 < FM / WB
+        const int ln = thread() & 63;
+        uint8_t* mine = smem + st * STAGE + wave * 16 * WB * OROW;
+        // byte of column col of row r there
+        auto at = [&](int r, int col) { return r * OROW + (F32 ? ((col >> 2) ^ (r & 15)) << 4 : col * (int)sizeof(OUT)); };
+        const int r0 = 32 * WB * w2 + 16 * wh;             // (the second block's are 32 rows on)
         if (r0 >= done.rows_a) return;
-        auto scaled = [&](int j, int v) {
-            if constexpr (I8) return (float)acc[i][j][v] * sa[i] * sb[j][v >> 2][v & 3];
-            else return acc[i][j][v];
-        };
-        auto put = [&](int col, const f32x4& v) {
-            uint8_t* o = mine + (ln & 31) * OROW + col * (int)sizeof(OUT);
+        auto put = [&](int row, int col, const f32x4& v) {
+            uint8_t* o = mine + at(row, col);
             if constexpr (F32) *reinterpret_cast<f32x4*>(o) = v;
             else *reinterpret_cast<uint2*>(o) = make_uint2(dev::f32x2_to_bf16x2(v[0], v[1]), dev::f32x2_to_bf16x2(v[2], v[3]));
         };
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int c = 8 * q + 4 * (ln >> 5);
-            f32x4 v[2];
+        for (int b = 0; b < WB; ++b) {
+            const int i = WB * w2 + b, row = 16 * b + (ln & 15), c = 4 * (ln >> 4);
+            auto scaled = [&](int j) {
+                f32x4 v;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[j][e] = scaled(j, 4 * q + e);
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (I8) v[e] = (float)acc[i][j][e] * sa[i] * sb[j][e];
+                    else v[e] = acc[i][j][e];
+                }
+                return v;
+            };
             if constexpr (GATED) {
-                f32x4 h;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = gated_value(p.activation, v[0][e], v[1][e]);
-                put(c, h);
-                if (p.out[1]) {
-                    put(32 + c, v[0]);
-                    put(64 + c, v[1]);
+                for (int j = 0; j < FN / 2; ++j) {
+                    const f32x4 g = scaled(j), u = scaled(j + FN / 2);
+                    f32x4 h;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) h[e] = gated_value(p.activation, g[e], u[e]);
+                    put(row, 16 * j + c, h);
+                    if (p.out[1]) {
+                        put(row, 32 + 16 * j + c, g);
+                        put(row, 64 + 16 * j + c, u);
+                    }
                 }
             } else {
-                put(c, v[0]);
-                put(32 + c, v[1]);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) put(row, 16 * j + c, scaled(j));
             }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -484,14 +574,15 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
             const int64_t ld = p.ld_out[GATED && w ? 1 : 0];
             if (p.mode == MUON_PRODUCT_DEPTH) out += done.group * p.out_stride;
 #pragma unroll
-            for (int q = 0; q < 32 / RPS; ++q) {
-                const uint4 u = *reinterpret_cast<const uint4*>(mine + (q * RPS + row) * OROW + (32 * w + col) * (int)sizeof(OUT));
-                int64_t r = done.m0 + r0 + q * RPS + row;
+            for (int q = 0; q < 16 * WB / RPS; ++q) {
+                const uint4 u = *reinterpret_cast<const uint4*>(mine + at(q * RPS + row, 32 * w + col));
+                const int in_tile = r0 + (q * RPS + row) % 16 + (q * RPS + row) / 16 * 32;
+                int64_t r = done.m0 + in_tile;
                 if (ACROSS_A && (r & ~7) + 8 > p.m) {
                     const int64_t place = r & ~7;
                     r += p.m - 8 - place;
                     if (r < place) continue;
-                } else if (r0 + q * RPS + row >= done.rows_a) {
+                } else if (in_tile >= done.rows_a) {
                     continue;
                 }
                 OUT* o = out + r * ld + c0;
@@ -521,37 +612,64 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         __builtin_amdgcn_wave_barrier();
     };
 
-    Tile x = decode<1, pair<FORM>>(p, t, p.tile_rows, COLS, bounds, ends);
-    begin(x);
-    fill();
+    // The tiles.  The next tile's first loads come before this one's stores, behind which loads would wait (a wave's loads and stores
+    // end in order).  Where there is no next tile or no depth they fetch nothing, but are there: past a branch around them the
+    // compiler would hold their registers for loads in flight, and wait in the main loop for all that are.
+    Tile x = decode<1, pair<FORM>>(p, t, ROWS, COLS, bounds, ends), x_next = x;
+    cur = span(x, true, va, vb);
+    begin(-1);
+    auto look = [&]() {
+        t = next_tile(p, my);
+        x_next = decode<1, pair<FORM>>(p, max(t, 0), ROWS, COLS, bounds, ends);
+        nxt = span(x_next, t >= 0, va_next, vb_next);
+        ahead_ok = mask(nxt.steps >= 2 && (I8 || TWO || ACROSS_A || nxt.rest == 0));   // (along, a remainder has to be masked)
+    };
+    if (AHEAD) look();
+    fill(0);
     for (;;) {
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = typename Cores<E>::sums{};
-        if (steps > 0) {
+        if (cur.steps > 0) {
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            const int blocks = (x.rows_a - 32 * wh + 63) / 64;
-            if (blocks >= 4) multiply(ic<4>{});
-            else if (blocks == 3) multiply(ic<3>{});
-            else if (blocks == 2) multiply(ic<2>{});
-            else multiply(ic<1>{});
+            const int pairs = (x.rows_a - 16 * wh + 63) / 64;   // (row block i has rows 16 (2 i + wh) .. + 15)
+            if constexpr (AHEAD) multiply(std::true_type{}, FM / 2);
+            else if (pairs >= FM / 2) multiply(std::true_type{}, FM / 2);
+            else multiply(std::false_type{}, pairs);
         }
         done = x;
         read_scales(done);
-        t = next_tile(p, my);
-        const bool more = t >= 0;
-        // the next tile's first loads run beside this one's stores
-        if (more) {
-            x = decode<1, pair<FORM>>(p, t, p.tile_rows, COLS, bounds, ends);
-            begin(x);
+        const int free = cur.steps > 0 ? (begins + cur.steps - 1) & 1 : begins ^ 1;   // the stage that out may go through
+        const bool loaded = AHEAD && cur.steps > 0 && ahead_ok != 0;                  // the next tile's first steps are under way
+        begins = free ^ 1;
+        if (AHEAD) {
+            x = x_next;
+            cur = nxt;
+            va = va_next;
+            vb = vb_next;
+            if (t < 0) cur.steps = -1;                     // the end
+            else if (!loaded) begin(-1);
+            if (t >= 0) look();
+        } else {
+            t = next_tile(p, my);
+            x = decode<1, pair<FORM>>(p, max(t, 0), ROWS, COLS, bounds, ends);
+            cur = span(x, t >= 0, va, vb);
+            if (t < 0) cur.steps = -1;
+            begin(-1);
         }
-        write(0);
-        write(1);
-        if (more) fill();
-        write(2);
-        write(3);
-        if (!more) break;
+        if constexpr (I8) {                                // (as well: past a row block that is left out)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(sa[i]));
+#pragma unroll
+            for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(sb[j]));
+        }
+#pragma unroll
+        for (int w = 0; w < FM / WB; ++w) {
+            if (w == FM / WB / 2 && (!AHEAD || (!loaded && cur.steps >= 0))) fill(begins);
+            write(w, free);
+        }
+        if (cur.steps < 0) break;
     }
 }
 
@@ -567,7 +685,7 @@ __global__ __launch_bounds__(THREADS) void layer_few_kernel(LayerArgs p) {
     constexpr int ES = (int)sizeof(E), UNIT = STEP / ES;
     constexpr int ROWS = 16 * RB, COLS = 16 * NB, SUMS = COLS + 4;  // of sums; a row of them in LDS
     constexpr int OUT_COLS = GATED ? COLS / 2 : COLS;
-    typedef typename Cores<E>::few_sums sums_t;
+    typedef typename Cores<E>::sums sums_t;
     __shared__ __attribute__((aligned(16))) int sums[WAVES][ROWS * SUMS];
     __shared__ int bounds[MUON_MAX_EXPERTS + 1], ends[MUON_MAX_EXPERTS + 1];
     __shared__ int64_t wave_tot[WAVES];
@@ -684,31 +802,35 @@ bool tile_loads_fit(const LayerArgs& a) {
     return b_across<FORM> ? a.n >= 8 : sizeof(E) == 1 || a.k >= STEP / 2;
 }
 
-// What a launch would take, in us, from what these kernels measured with operands from L2 and the chip partly or fully busy: its
-// rounds of tiles, each a constant and so much a step.  A step of a 256 x 256 tile takes 1.0 us alone on the chip and
-// 1.55 with all CUs busy (clock and caches), with 128 rows 0.73 and 1.0, with 64 0.61 and 0.7 (4096 x 4096 by 1024 gate and up in
-// bfloat16: 79 us in 128 tiles of 256 rows, 71 in 256 of 128, 102 in 512 of 64; 1024 x 4096: 78, 55, 46).
+// What a launch of the big tiles' kernel would take, in us, from what it measured: rounds of tiles, each a constant and so much a
+// step, less where few CUs work (clock and caches).  A step of 256 x 256 takes 1.14 us alone on the chip and 1.47 with all CUs
+// busy, with 128 rows 0.77 and 1.0, with 64 0.57 and 0.72; of 256 rows of which 192, 128 or 64 are there, 1.05, 0.92, 0.73 alone.
+// (Gate and up in bfloat16, 4096 x 4096 by 1024: 93 us in 512 tiles of 64 rows, 70 in 256 of 128, 95 in 128 of 256;
+// 1024 x 4096: 47, 61, 89.  112 rows of 8-bit integers by as many experts, 4096 x 1024: 148, 150, 166.  57344 rows by 128
+// experts, bfloat16: 1677, 1236, 1116.)
 struct Cost {
     int64_t tiles;
     double us;
 };
 template <int FORM>
 Cost big_cost(LayerArgs a, int rows, double steps) {
-    a.tile_rows = rows;
-    const int64_t most = count_tiles<pair<FORM>>(a, rows, FORM == FORM_GATED ? TILE / 2 : TILE);
-    double n = (double)most, used = (double)rows;
+    constexpr bool GATED = FORM == FORM_GATED;
+    const int64_t most = count_tiles<pair<FORM>>(a, rows, GATED ? TILE / 2 : TILE);
+    double n = (double)most, used = rows;
     if (a.mode == MUON_PRODUCT_ROWS) {
         // segments end inside tiles, on average in the middle
         const double segments = (double)std::min<int64_t>(a.m, a.groups);
         n = std::max((double)a.m / rows + 0.5 * segments, segments) * a.tiles_n;
-        used = std::min(used, (double)a.m / segments);
-    } else {
+        if (rows == 256) used = std::min(used, (double)a.m / segments);
+    } else if (!a_across<FORM> && rows == 256) {
         used = std::min(used, (double)a.m);
     }
-    static const double alone[] = {0.61, 0.73, 0.87, 1.0}, busy[] = {0.7, 1.0, 1.3, 1.55}, begin[] = {5.5, 7.0, 8.0, 9.0};
-    const int nb = std::min(std::max((int)std::ceil(used / 64.0), 1), 4) - 1;
-    const double share = std::min(n / CUS, 1.0);
-    return {most, std::ceil(n / CUS) * (begin[nb] + (FORM == FORM_GATED ? 2.0 : 0.0) + steps * (alone[nb] + (busy[nb] - alone[nb]) * share))};
+    static const double small[2][4] = {{0.57, 0.72, 5.7, 2.0}, {0.77, 1.0, 6.8, 3.5}};
+    static const double full[4][4] = {{0.73, 0.85, 7.0, 2.0}, {0.92, 1.15, 8.0, 3.0}, {1.05, 1.35, 9.0, 4.0}, {1.14, 1.47, 9.5, 5.0}};
+    const double(&c)[4] = rows < 256 ? small[rows / 128] : full[std::max((int)std::ceil(used / 64.0), 1) - 1];
+    auto round = [&](double share) { return c[2] + (GATED ? c[3] : 0.0) + steps * (c[0] + (c[1] - c[0]) * share); };
+    const double whole = std::floor(n / CUS), left = n / CUS - whole;
+    return {most, whole * round(1.0) + (left > 0 ? round(left) : 0.0)};
 }
 
 template <class E, int FORM, class OUT>
@@ -736,8 +858,7 @@ hipError_t layer_as(LayerArgs a, hipStream_t s) {
         static const double wait[2][3] = {{0.65, 0.75, 2.4}, {1.2, 1.55, 2.4}}, rate[2][3] = {{1900, 1290, 625}, {1500, 1024, 740}};
         LayerArgs few[3] = {a, a, a};
         for (int i = 0; i < 3; ++i) {
-            few[i].tile_rows = i == 0 ? 16 : 32;
-            const int64_t n = count_tiles<1>(few[i], few[i].tile_rows, i == 2 ? (GATED ? 32 : 64) : 16);
+            const int64_t n = count_tiles<1>(few[i], i == 0 ? 16 : 32, i == 2 ? (GATED ? 32 : 64) : 16);
             const double us = 3.0 + std::max(steps / WAVES * wait[GATED][i], (double)n * (steps + 2.0) / rate[GATED][i]);
             if (n >= 0 && us < best.us) {
                 best = {n, us};
@@ -755,9 +876,10 @@ hipError_t layer_as(LayerArgs a, hipStream_t s) {
             hipLaunchKernelGGL((layer_any_kernel<FORM, OUT>), grid(n, 2 * CUS), dim3(ANY_THREADS), 0, s, a);
             return hipGetLastError();
         }
-    a.tile_rows = pick;
     count_tiles<pair<FORM>>(a, pick, GATED ? TILE / 2 : TILE);
-    hipLaunchKernelGGL((layer_kernel<E, FORM, OUT>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
+    if (pick == 64) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 64>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
+    else if (pick == 128) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 128>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
+    else hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 256>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
     return hipGetLastError();
 }
 

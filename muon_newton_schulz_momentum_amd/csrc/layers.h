@@ -26,7 +26,7 @@ struct LayerArgs {
     int64_t ld_out[2], out_stride;     // in elements; ld_out[1]: of out[1] and out[2] (FORM_GATED)
     int64_t m, n, k;                   // rows and columns of out, depth (of each product that is added up)
     int32_t groups, mode, accumulate, activation;
-    int32_t tile_rows, tiles_m, tiles_n, tiles;  // set by the launch
+    int32_t tiles_m, tiles_n, tiles;   // set by the launch
     int32_t vec;                       // rows of out are 16-byte aligned
 };
 
