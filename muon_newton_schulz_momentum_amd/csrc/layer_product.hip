@@ -242,14 +242,15 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     // Staging: along, load i brings rows 64 i + t / 8, chunk t % 8; across, depth rows KA i + t / CPA, chunk t % CPA (KB, CPB).
     // The permutation of 32-byte pieces does not change from load to load; rows of 128 bytes are two to 256.
     auto swizzle = [](int k, int row_bytes) { return row_bytes == 128 ? ((k >> 1) & 1) | ((k >> 2) & 2) : ((k & 3) << 1) | ((k >> 3) & 1); };
-    int along = 0, across_a = 0, across_b = 0;
-    {
+    // (worked out where it is needed, as are the fragments' places)
+    struct Place {
+        int along, across_a, across_b;
+    };
+    auto stores_at = [&]() {
         const int t = thread();
         auto place = [&](int row, int chunk, int row_bytes) { return row * row_bytes + (((chunk >> 1) ^ swizzle(row, row_bytes)) << 5) + ((chunk & 1) << 4); };
-        if (!ACROSS_A || !ACROSS_B) along = (t >> 7) * BLOCK + (t & 7) * 256 + ((((t >> 3) & 15) ^ (t & 7)) << 4);
-        if (ACROSS_A) across_a = place(t / CPA, t % CPA, KROW_A);
-        if (ACROSS_B) across_b = place(t / CPB, t % CPB, KROW_B);
-    }
+        return Place{(t >> 7) * BLOCK + (t & 7) * 256 + ((((t >> 3) & 15) ^ (t & 7)) << 4), place(t / CPA, t % CPA, KROW_A), place(t / CPB, t % CPB, KROW_B)};
+    };
 
     // A tile's operands: their first rows (along) or depth row 0 (across), sizes of the buffers along; the depth's begin, its
     // values before the whole steps, those of each part, and all steps.
@@ -327,10 +328,10 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, is_a ? r.bytes_a : r.bytes_b, 0x00020000);
         staged[d] = __builtin_amdgcn_raw_buffer_load_b128(buf, (is_a ? r.va : r.vb) + rows_on, across ? 0 : r.along, 0);
     };
-    auto store = [&](int d, int st) {
+    auto store = [&](int d, int st, const Place& p) {
         const bool is_a = d < LA;
         const int i = is_a ? d : d - LA;
-        const int at = !(is_a ? ACROSS_A : ACROSS_B) ? along + 4 * BLOCK * i : is_a ? across_a + KA * KROW_A * i : across_b + KB * KROW_B * i;
+        const int at = !(is_a ? ACROSS_A : ACROSS_B) ? p.along + 4 * BLOCK * i : is_a ? p.across_a + KA * KROW_A * i : p.across_b + KB * KROW_B * i;
         *reinterpret_cast<i32x4*>(smem + st * STAGE + (is_a ? 0 : PANEL_A) + at) = staged[d];
     };
     auto span = [&](const Tile& x, bool there, int& va, int& vb) {
@@ -366,10 +367,11 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 #pragma unroll
         for (int e = 0; e < 4; ++e) inside[e] = have >= 4 * e + 4 ? -1 : have == 4 * e + 2 ? 0xffff : 0;
         const Aim r = aim_on(1);
+        const Place at = stores_at();
 #pragma unroll
         for (int d = 0; d < NLOAD; ++d) {
             if (!I8 && !TWO && !(d < LA ? ACROSS_A : ACROSS_B)) staged[d] &= inside;
-            store(d, st);
+            store(d, st, at);
             load(d, r);
         }
     };
@@ -377,23 +379,27 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     // A fragment, 16 bytes of a row's depth, in sub-step kk: along in one read; across in two, whose lanes take depth rows tk and
     // columns tc.  (Blocks i of a and j of b lie apart by bits of the address that nothing else of it has: 2 i + wh is
     // i << 1 | wh, 4 wc + j is wc << 2 | j.)
-    int ra, rb;
-    {
+    struct Fragments {
+        int a, b;
+    };
+    auto fragments_at = [&]() {
         const int t = thread(), fr = t & 15, fk = (t >> 4) & 3;
         const int tk = 8 * fk + (fr >> 2), tc = 4 * (t & 3);
-        ra = ACROSS_A ? tk * KROW_A + ((wh ^ swizzle(tk, KROW_A)) << 5) + 2 * tc : wh * BLOCK + fk * 256 + ((fr ^ fk) << 4);
-        rb = PANEL_A + (ACROSS_B ? tk * KROW_B + (((4 * wc) ^ swizzle(tk, KROW_B)) << 5) + 2 * tc : (GATED ? 2 : 4) * wc * BLOCK + fk * 256 + ((fr ^ fk) << 4));
-    }
+        Fragments r;
+        r.a = ACROSS_A ? tk * KROW_A + ((wh ^ swizzle(tk, KROW_A)) << 5) + 2 * tc : wh * BLOCK + fk * 256 + ((fr ^ fk) << 4);
+        r.b = PANEL_A + (ACROSS_B ? tk * KROW_B + (((4 * wc) ^ swizzle(tk, KROW_B)) << 5) + 2 * tc : (GATED ? 2 : 4) * wc * BLOCK + fk * 256 + ((fr ^ fk) << 4));
+        return r;
+    };
     static_assert(PANEL_A % 512 == 0 && STAGE % 512 == 0, "stages and panels begin on multiples of all rows");
     auto read_across = [&](int at, int row_bytes) {
         typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
         return __builtin_bit_cast(i32x4, u64x2{read_transposed(smem + at), read_transposed(smem + at + 4 * row_bytes)});
     };
-    auto read_a = [&](int i, int st, int kk) {
+    auto read_a = [&](int ra, int i, int st, int kk) {
         if constexpr (ACROSS_A) return read_across(((ra + st * STAGE) ^ (i << 6)) + 32 * KROW_A * kk, KROW_A);
         else return *reinterpret_cast<const i32x4*>(smem + ((ra + st * STAGE) ^ (kk << 6)) + 2 * BLOCK * i + 1024 * kk);
     };
-    auto read_b = [&](int j, int st, int kk) {
+    auto read_b = [&](int rb, int j, int st, int kk) {
         if constexpr (ACROSS_B) return read_across(((rb + st * STAGE) ^ (j << 5)) + 32 * KROW_B * kk, KROW_B);
         else return *reinterpret_cast<const i32x4*>(smem + ((rb + st * STAGE) ^ (kk << 6)) + (GATED ? (j >> 1) * (TILE / 32) + (j & 1) : j) * BLOCK + 1024 * kk);
     };
@@ -406,33 +412,33 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
     };
 
     typename Cores<E>::sums acc[FM][FN];
-    // The steps of a tile for a wave whose first `pairs` of 4 pairs of row blocks have rows (FULL: all of them).
+    // The steps of a tile for a wave whose first PAIRS pairs of row blocks have rows.
     //
     // A step is two sub-steps; in each a pair's 8 matrix instructions stand together.  Behind them go staging, over the slots before the
     // step's barrier (half way through the second sub-step), and the next sub-step's reads: a's in place, b's to the other
     // registers.
     int begins = 0;                                        // stage of the tile's first step
-    auto multiply = [&](auto full_, int pairs) {
-        constexpr bool FULL = decltype(full_)::value;
-        constexpr int PAIRS = FM / 2, TURN = PAIRS / 2;    // pairs of a sub-step; of the second one before the barrier
-        static_assert(FULL || NLOAD == PAIRS + 2 + TURN, "staging between the pairs");
-        i32x4 fa[FM], fb[2][FN];
+    auto multiply = [&](auto pairs_) {
+        constexpr int PAIRS = decltype(pairs_)::value, TURN = PAIRS / 2;   // pairs of a sub-step; of the second one before the barrier
+        i32x4 fa[2 * PAIRS], fb[2][FN];
+        const Fragments fragments = fragments_at();
+        const Place stores = stores_at();
         // (in the order of the loop's reads, as a wait there covers both)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            fb[0][j] = read_b(j, begins, 0);
+            fb[0][j] = read_b(fragments.b, j, begins, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            fa[i] = read_a(i, begins, 0);
+        for (int i = 0; i < 2 * PAIRS; ++i) {
+            fa[i] = read_a(fragments.a, i, begins, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
         for (int step = 0; step < cur.steps; ++step) {
             const Aim ahead = aim_on(step + 2);
             const int st = (begins + step) & 1, st_next = st ^ 1;
             auto stage = [&](int d) {
-                store(d, st_next);
+                store(d, st_next, stores);
                 load(d, ahead);
             };
             // Pair q in sub-step kk, read(f) behind its instruction f.
@@ -444,55 +450,38 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
                     __builtin_amdgcn_sched_barrier(0);
                     acc[i][j] = Cores<E>::mul(fb[kk][j], fa[i], acc[i][j]);
                     __builtin_amdgcn_sched_barrier(0);
-                    if (FULL && g < ALL && (g + 1) * NLOAD / ALL > g * NLOAD / ALL) stage(g * NLOAD / ALL);
+                    if (g < ALL && (g + 1) * NLOAD / ALL > g * NLOAD / ALL) stage(g * NLOAD / ALL);
                     read(f);
                 }
             };
             // a's of pair q are read for the next sub-step behind their last use
             auto renew = [&](int q, int f, int rst, int kk) {
-                if (f == FN - 1) fa[2 * q] = read_a(2 * q, rst, kk);
-                if (f == 2 * FN - 1) fa[2 * q + 1] = read_a(2 * q + 1, rst, kk);
+                if (f == FN - 1) fa[2 * q] = read_a(fragments.a, 2 * q, rst, kk);
+                if (f == 2 * FN - 1) fa[2 * q + 1] = read_a(fragments.a, 2 * q + 1, rst, kk);
             };
             // the next step's first fragments: b's, and the a's that were used before the barrier
             auto first = [&](int f) {
-                if (f < FN) fb[0][f] = read_b(f, st_next, 0);
-                else if (f - FN < 2 * TURN) fa[f - FN] = read_a(f - FN, st_next, 0);
-            };
-            auto turn = [&]() {
-                pin(acc);
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
+                if (f < FN) fb[0][f] = read_b(fragments.b, f, st_next, 0);
+                else if (f - FN < 2 * TURN) fa[f - FN] = read_a(fragments.a, f - FN, st_next, 0);
             };
 #pragma unroll
-            for (int q = 0; q < PAIRS; ++q) {
-                if (FULL || q == 0 || pairs > q)
-                    pair_of(q, 0, [&](int f) {
-                        if (q == 0 && f < FN) fb[1][f] = read_b(f, st, 1);
-                        renew(q, f, st, 1);
-                    });
-                if (!FULL) stage(q), q == 0 || q == PAIRS - 1 ? stage(q == 0 ? PAIRS : PAIRS + 1) : (void)0;
-            }
+            for (int q = 0; q < PAIRS; ++q)
+                pair_of(q, 0, [&](int f) {
+                    if (q == 0 && f < FN) fb[1][f] = read_b(fragments.b, f, st, 1);
+                    renew(q, f, st, 1);
+                });
 #pragma unroll
-            for (int q = 0; q < TURN; ++q) {
-                if (FULL || q == 0 || pairs > q) pair_of(q, 1, [](int) {});
-                if (!FULL) stage(PAIRS + 2 + q);
-            }
-            turn();
-            if (TURN == PAIRS || !(FULL || pairs > TURN)) {
-#pragma unroll
-                for (int f = 0; f < FN + 2 * TURN; ++f) {
-                    first(f);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
+            for (int q = 0; q < TURN; ++q) pair_of(q, 1, [](int) {});
+            pin(acc);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
 #pragma unroll
             for (int q = TURN; q < PAIRS; ++q)
-                if (FULL || pairs > q)
-                    pair_of(q, 1, [&](int f) {
-                        if (q == TURN) first(f);
-                        renew(q, f, st_next, 0);
-                    });
+                pair_of(q, 1, [&](int f) {
+                    if (q == TURN) first(f);
+                    renew(q, f, st_next, 0);
+                });
         }
         if (!AHEAD) settle();
     };
@@ -634,9 +623,9 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
         if (cur.steps > 0) {
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             const int pairs = (x.rows_a - 16 * wh + 63) / 64;   // (row block i has rows 16 (2 i + wh) .. + 15)
-            if constexpr (AHEAD) multiply(std::true_type{}, FM / 2);
-            else if (pairs >= FM / 2) multiply(std::true_type{}, FM / 2);
-            else multiply(std::false_type{}, pairs);
+            if constexpr (AHEAD) multiply(ic<FM / 2>{});
+            else if (pairs >= 3) multiply(ic<4>{});
+            else multiply(ic<2>{});
         }
         done = x;
         read_scales(done);
