@@ -822,54 +822,90 @@ Cost big_cost(LayerArgs a, int rows, double steps) {
     return {most, whole * round(1.0) + (left > 0 ? round(left) : 0.0)};
 }
 
-template <class E, int FORM, class OUT>
-hipError_t layer_as(LayerArgs a, hipStream_t s) {
+// A launch: the kernel (rows of the big tiles; 0 to 2 for few rows; -1 for any size) and its arguments.
+struct Plan {
+    int pick;
+    Cost cost;
+    LayerArgs args;
+};
+template <class E, int FORM>
+Plan plan(const LayerArgs& a) {
     constexpr bool GATED = FORM == FORM_GATED;
-    auto grid = [](int64_t tiles, int64_t most) { return dim3((unsigned)std::min<int64_t>((tiles + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)); };
-    if (a.m == 0 || a.n == 0) return hipSuccess;
     const double depth = (double)a.k * (double)sizeof(E) / STEP / (a.mode == MUON_PRODUCT_DEPTH ? a.groups : 1);
     const double steps = std::ceil(depth) * parts<FORM>;
-    int pick = -1;
-    Cost best{0, 1e30};
+    Plan best{-1, {0, 1e30}, a};
+    auto offer = [&](int pick, const Cost& cost, const LayerArgs& args) {
+        if (cost.tiles >= 0 && cost.us < best.cost.us) best = {pick, cost, args};
+    };
     if (tile_loads_fit<E, FORM>(a))
         for (int rows : {256, 128, 64}) {
-            const Cost c = big_cost<FORM>(a, rows, steps);
-            if (c.tiles >= 0 && c.us < best.us) {
-                best = c;
-                pick = rows;
-            }
+            LayerArgs big = a;
+            count_tiles<pair<FORM>>(big, rows, GATED ? TILE / 2 : TILE);
+            offer(rows, big_cost<FORM>(a, rows, steps), big);
         }
     if constexpr (GATED || FORM == FORM_SCALED) {
         // 16 rows, 32 rows, 32 rows by 64 columns: bound by a wave's share of the depth where there are few tiles, by the steps of
         // all tiles where there are many (1 row by 5632 x 2048 gate and up in bfloat16: 16, 18, 18 us and 32 in big tiles; 64 rows: 40, 31,
         // 30, 33; 256 rows: 131, 95, 72, 53; 1 row by 2048 x 5632 in 8-bit integers: 7, 8, 15, 32)
-        constexpr int THIN = GATED ? 2 : 1;
         static const double wait[2][3] = {{0.65, 0.75, 2.4}, {1.2, 1.55, 2.4}}, rate[2][3] = {{1900, 1290, 625}, {1500, 1024, 740}};
-        LayerArgs few[3] = {a, a, a};
         for (int i = 0; i < 3; ++i) {
-            const int64_t n = count_tiles<1>(few[i], i == 0 ? 16 : 32, i == 2 ? (GATED ? 32 : 64) : 16);
-            const double us = 3.0 + std::max(steps / WAVES * wait[GATED][i], (double)n * (steps + 2.0) / rate[GATED][i]);
-            if (n >= 0 && us < best.us) {
-                best = {n, us};
-                pick = i;
-            }
+            LayerArgs few = a;
+            const int64_t n = count_tiles<1>(few, i == 0 ? 16 : 32, i == 2 ? (GATED ? 32 : 64) : 16);
+            offer(i, {n, 3.0 + std::max(steps / WAVES * wait[GATED][i], (double)n * (steps + 2.0) / rate[GATED][i])}, few);
         }
-        if (pick == 0) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 1, THIN, 4>), grid(best.tiles, 4 * CUS), dim3(THREADS), 0, s, few[0]);
-        else if (pick == 1) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 2, THIN, 4>), grid(best.tiles, 2 * CUS), dim3(THREADS), 0, s, few[1]);
-        else if (pick == 2) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 2, 4, 2>), grid(best.tiles, 2 * CUS), dim3(THREADS), 0, s, few[2]);
-        if (pick >= 0 && pick <= 2) return hipGetLastError();
     }
+    return best;
+}
+
+template <class E, int FORM, class OUT>
+hipError_t launch(const Plan& p, hipStream_t s) {
+    auto grid = [&](int64_t most) { return dim3((unsigned)std::min<int64_t>((p.cost.tiles + NUM_XCD - 1) / NUM_XCD * NUM_XCD, most)); };
+    if constexpr (FORM == FORM_GATED || FORM == FORM_SCALED) {
+        constexpr int THIN = FORM == FORM_GATED ? 2 : 1;
+        if (p.pick == 0) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 1, THIN, 4>), grid(4 * CUS), dim3(THREADS), 0, s, p.args);
+        else if (p.pick == 1) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 2, THIN, 4>), grid(2 * CUS), dim3(THREADS), 0, s, p.args);
+        else if (p.pick == 2) hipLaunchKernelGGL((layer_few_kernel<E, FORM, OUT, 2, 4, 2>), grid(2 * CUS), dim3(THREADS), 0, s, p.args);
+    }
+    if (p.pick == 64) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 64>), grid(CUS), dim3(THREADS), 0, s, p.args);
+    else if (p.pick == 128) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 128>), grid(CUS), dim3(THREADS), 0, s, p.args);
+    else if (p.pick == 256) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 256>), grid(CUS), dim3(THREADS), 0, s, p.args);
+    return hipGetLastError();
+}
+
+template <class E, int FORM, class OUT>
+hipError_t layer_as(const LayerArgs& a, hipStream_t s) {
+    if (a.m == 0 || a.n == 0) return hipSuccess;
+    const Plan all = plan<E, FORM>(a);
     if constexpr (b_across<FORM>)
-        if (pick < 0) {
-            const int64_t n = count_tiles<pair<FORM>>(a, ANY, ANY);
-            hipLaunchKernelGGL((layer_any_kernel<FORM, OUT>), grid(n, 2 * CUS), dim3(ANY_THREADS), 0, s, a);
+        if (all.pick < 0) {
+            LayerArgs any = a;
+            const int64_t n = count_tiles<pair<FORM>>(any, ANY, ANY);
+            hipLaunchKernelGGL((layer_any_kernel<FORM, OUT>), dim3((unsigned)std::min<int64_t>((n + NUM_XCD - 1) / NUM_XCD * NUM_XCD, 2 * CUS)), dim3(ANY_THREADS), 0, s, any);
             return hipGetLastError();
         }
-    count_tiles<pair<FORM>>(a, pick, GATED ? TILE / 2 : TILE);
-    if (pick == 64) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 64>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
-    else if (pick == 128) hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 128>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
-    else hipLaunchKernelGGL((layer_kernel<E, FORM, OUT, 256>), grid(best.tiles, CUS), dim3(THREADS), 0, s, a);
-    return hipGetLastError();
+    // Without segments the tiles' last round may leave most CUs idle: then the rows of the whole rounds go first, and the others in a
+    // launch of their own, in what suits them (two products of 5632 x 2048 over 8191 in 352 tiles: 417 us in one launch, 379 in 256
+    // tiles and 192 of 128 rows).
+    if (a.mode == MUON_PRODUCT_DENSE && all.cost.tiles > CUS) {
+        LayerArgs first = a, rest = a;
+        const int64_t n = count_tiles<pair<FORM>>(first, TILE, FORM == FORM_GATED ? TILE / 2 : TILE);
+        const int64_t rows = n / CUS * CUS / (pair<FORM> * first.tiles_n) * TILE;
+        if (rows > 0 && rows < a.m) {
+            first.m = rows;
+            rest.m = a.m - rows;
+            for (int i = 0; i < 2; ++i)
+                if (rest.a[i]) rest.a[i] += a_across<FORM> ? rows * 2 : rows * rest.lda;
+            for (int i = 0; i < 3; ++i)
+                if (rest.out[i]) rest.out[i] = static_cast<OUT*>(rest.out[i]) + rows * rest.ld_out[FORM == FORM_GATED && i ? 1 : 0];
+            if (sizeof(E) == 1) rest.sa += rows;
+            const Plan one = plan<E, FORM>(first), two = plan<E, FORM>(rest);
+            if (one.cost.us + two.cost.us + 2.0 < all.cost.us) {
+                const hipError_t error = launch<E, FORM, OUT>(one, s);
+                return error != hipSuccess ? error : launch<E, FORM, OUT>(two, s);
+            }
+        }
+    }
+    return launch<E, FORM, OUT>(all, s);
 }
 
 }  // namespace

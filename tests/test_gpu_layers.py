@@ -95,6 +95,10 @@ SHAPES = [
     (1500, 512, 640, [0, 700, 1500], 0),
     (1100, 1024, 512, None, 0),
     (48, 2048, 1024, None, 0),
+    (16900, 512, 128, None, 0),                            # tiles for little more than all compute units: rows in two launches
+    (16900, 1024, 128, None, 0),
+    (16900, 64, 1030, None, 8),
+    (96, 5003, 2000, None, 3),
     (9, 1000, 2056, [0, 2, 2, 9], 0),
 ]
 
