@@ -112,10 +112,11 @@ def _tensor(name: str, t: torch.Tensor, like: torch.Tensor, dtype, shape=None, c
 
 def _rows(name: str, t: torch.Tensor) -> int:
     """Row stride of a matrix whose rows are contiguous and do not overlap."""
-    cols = t.shape[-1]
-    if cols > 1 and t.stride(-1) != 1:
+    shape, strides = t.shape, t.stride()
+    cols = shape[-1]
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    ld = t.stride(-2) if t.shape[-2] > 1 else cols
+    ld = strides[-2] if shape[-2] > 1 else cols
     if ld < cols:
         raise ValueError(f"{name}'s rows overlap")
     return ld
@@ -419,14 +420,15 @@ class Int8:
         return self.codes[..., :self.cols].float() * self.scales.unsqueeze(-1)
 
 
-def _check_int8(name: str, q: Int8, like: torch.Tensor) -> torch.Size:
-    shape = q.codes.shape
-    if q.cols < 1 or len(shape) < 2 or shape[-1] != _up(q.cols, BLOCK) or q.scales.shape != shape[:-1]:
-        raise ValueError(f"{name}: codes {tuple(shape)} and scales {tuple(q.scales.shape)} are not those of {q.cols} columns")
-    if q.codes.dtype != torch.int8 or q.scales.dtype != torch.float32:
+def _check_int8(name: str, q: Int8, like: torch.Tensor) -> tuple:
+    codes, scales, cols, device = q.codes, q.scales, q.cols, like.device
+    shape = tuple(codes.shape)             # (a torch.Size is slow to slice)
+    if cols < 1 or len(shape) < 2 or shape[-1] != -(-cols // BLOCK) * BLOCK or tuple(scales.shape) != shape[:-1]:
+        raise ValueError(f"{name}: codes {shape} and scales {tuple(scales.shape)} are not those of {cols} columns")
+    if codes.dtype != torch.int8 or scales.dtype != torch.float32:
         raise ValueError(f"{name} must have int8 codes and float32 scales")
-    if q.codes.device != like.device or q.scales.device != like.device:
-        raise ValueError(f"{name} is on {q.codes.device}, expected {like.device}")
+    if (codes is not like and codes.device != device) or scales.device != device:
+        raise ValueError(f"{name} is on {codes.device}, expected {device}")
     return shape
 
 
@@ -473,12 +475,13 @@ def quantize_int8(src: torch.Tensor, *, rows: Optional[torch.Tensor] = None, per
 def _layer_operand(o: L.muon_operand, name: str, t, like: torch.Tensor, stacked: bool):
     """Fills o with a bfloat16 tensor or an Int8, checked; (groups or None, rows, columns)."""
     if isinstance(t, Int8):
-        shape, cols, data = _check_int8(name, t, like), t.cols, t.codes
-        if t.scales.dim() and t.scales.shape[-1] > 1 and t.scales.stride(-1) != 1:
+        shape, cols, data, scales = _check_int8(name, t, like), t.cols, t.codes, t.scales
+        strides = scales.stride()
+        if shape[-2] > 1 and strides[-1] != 1:
             raise ValueError(f"{name}.scales must be contiguous")
-        o.scales = t.scales.data_ptr()
+        o.scales = scales.data_ptr()
         if stacked and shape[0] > 1:
-            o.stride_scales = t.scales.stride(0)
+            o.stride_scales = strides[0]
     else:
         data = _tensor(name, t, like, torch.bfloat16, contiguous=False)
         shape, cols = t.shape, t.shape[-1] if t.dim() else 0

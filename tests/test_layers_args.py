@@ -90,7 +90,7 @@ REFUSED = [
         (dict(operands=2), INVALID), (dict(activation=3), INVALID), (dict(activation=-1), INVALID), (dict(mode=2), INVALID), (dict(groups=0), INVALID),
         (dict(pre_up=None), INVALID), (dict(pre_gate=None), INVALID), (dict(k=-1), SHAPE), (dict(ld_out=19), SHAPE), (dict(ld_pre=19), SHAPE),
         (dict(x__ld=199), SHAPE), (dict(x__ld=1 << 22), SHAPE), (dict(gate__ld=199), SHAPE), (dict(up__stride=19 * 256 + 199), SHAPE),
-        (dict(x__scales=P[1]), INVALID), (dict(up__data=None), INVALID), (dict(up__data=P[4] + 2), ALIGN), (dict(out=P[7] + 8), ALIGN),
+        (dict(up__ld=264), SHAPE), (dict(gate__stride=(1 << 20) + 8), SHAPE), (dict(x__scales=P[1]), INVALID), (dict(up__data=None), INVALID), (dict(up__data=P[4] + 2), ALIGN), (dict(out=P[7] + 8), ALIGN),
         (dict(pre_up=P[9] + 8), ALIGN), (dict(out=P[0]), INVALID), (dict(pre_gate=P[7] + 384), INVALID), (dict(pre_up=P[8]), INVALID),
         (dict(out=P[4] + 6 * (1 << 20)), INVALID), (dict(pre_up=P[6]), INVALID), (dict(offsets=None), INVALID)]],
     *[("gated_backward", kw, st) for kw, st in [
@@ -98,7 +98,7 @@ REFUSED = [
         (dict(accumulate=1, grad_dtype=L.MUON_DTYPE_BF16), INVALID), (dict(grad_up=None), INVALID), (dict(ld_grad=19), SHAPE), (dict(ld_pre=19), SHAPE),
         (dict(ld_grad_pre=0), SHAPE), (dict(ld_grad_pre=96), SHAPE), (dict(ld_grad_pre=1 << 22), SHAPE), (dict(ld_grad_x=199), SHAPE), (dict(ld_grad_w=199), SHAPE),
         (dict(stride_grad_w=3999), SHAPE), (dict(x__ld=199), SHAPE), (dict(gate__ld=199), SHAPE), (dict(x__data=None), INVALID),
-        (dict(up__data=None), INVALID), (dict(grad=None), INVALID), (dict(grad_pre_up=None), INVALID), (dict(pre_gate=P[5] + 2), ALIGN),
+        (dict(up__ld=264), SHAPE), (dict(up__stride=(1 << 20) + 8), SHAPE), (dict(up__data=None), INVALID), (dict(grad=None), INVALID), (dict(grad_pre_up=None), INVALID), (dict(pre_gate=P[5] + 2), ALIGN),
         (dict(offsets=None), INVALID), (dict(grad_x=P[0]), INVALID), (dict(grad_pre_gate=P[4]), INVALID),
         (dict(grad_pre_gate=P[5]), INVALID), (dict(grad_pre_gate=P[6], grad_pre_up=P[5]), INVALID),
         (dict(grad_pre_gate=P[5], grad_pre_up=P[6], ld_grad_pre=128), INVALID), (dict(grad_up=P[10] + 64), INVALID), (dict(grad_x=P[7]), INVALID),
