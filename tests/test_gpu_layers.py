@@ -99,6 +99,9 @@ SHAPES = [
     (16900, 1024, 128, None, 0),
     (16900, 64, 1030, None, 8),
     (96, 5003, 2000, None, 3),
+    # full tiles and ends of all lengths, more tiles than compute units, segments without rows, without full tiles, without ends
+    (24000, 1030, 136, [3, 3, 259, 300, 812, 1000, 1700, 1700, 1701, 3000, 7096, 7100, 9990, 12289, 12350, 15000, 20120, 20120, 23990], 0),
+    (20000, 520, 200, [0] + [17 * i * i // 10 for i in range(4, 108)] + [30000], 8),
     (9, 1000, 2056, [0, 2, 2, 9], 0),
 ]
 
