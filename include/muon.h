@@ -688,7 +688,7 @@ typedef struct muon_gated_backward_config {
     uint16_t* grad_pre_gate;
     uint16_t* grad_pre_up;
     int64_t ld_grad_pre;      /* in elements, a multiple of 64, at least n and below 2^22       */
-    uint16_t* grad_x;         /* nullable: bfloat16, m rows of k                                */
+    uint16_t* grad_x;         /* nullable: bfloat16, m rows of k (with n = 0 refused)           */
     int64_t ld_grad_x;
     void* grad_gate;          /* nullable, both or neither: per group n rows of k               */
     void* grad_up;

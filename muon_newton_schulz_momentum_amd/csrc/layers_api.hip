@@ -226,7 +226,10 @@ muon_status muon_gated_backward(const muon_gated_backward_config* c, void* strea
     if (!is_dtype(c->grad_dtype)) return fail(MUON_ERR_INVALID_ARG, who, "grad_dtype must be F32 or BF16");
     if (c->accumulate != 0 && (c->accumulate != 1 || c->grad_dtype != MUON_DTYPE_F32))
         return fail(MUON_ERR_INVALID_ARG, who, "accumulate must be 0 or, for float32 gradients, 1");
-    if (c->n == 0) return MUON_OK;
+    if (c->n == 0) {
+        if (c->grad_x && c->m > 0 && c->k > 0) return fail(MUON_ERR_SHAPE, who, "n must be at least 1 for grad_x, which would be zeros");
+        return MUON_OK;
+    }
     const bool weights = c->grad_gate && c->k > 0, to_x = c->grad_x && c->m > 0 && c->k > 0, rows = c->mode == MUON_PRODUCT_ROWS;
     if (weights) {
         MUON_RETURN_IF(check_rows(c->grad_gate, c->ld_grad_w, c->k, who, "grad_gate"));

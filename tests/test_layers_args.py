@@ -97,6 +97,7 @@ REFUSED = [
         (dict(activation=3), INVALID), (dict(grad_dtype=2), INVALID), (dict(accumulate=2), INVALID),
         (dict(accumulate=1, grad_dtype=L.MUON_DTYPE_BF16), INVALID), (dict(grad_up=None), INVALID), (dict(ld_grad=19), SHAPE), (dict(ld_pre=19), SHAPE),
         (dict(ld_grad_pre=0), SHAPE), (dict(ld_grad_pre=96), SHAPE), (dict(ld_grad_pre=1 << 22), SHAPE), (dict(ld_grad_x=199), SHAPE), (dict(ld_grad_w=199), SHAPE),
+        (dict(n=0), SHAPE),
         (dict(stride_grad_w=3999), SHAPE), (dict(x__ld=199), SHAPE), (dict(gate__ld=199), SHAPE), (dict(x__data=None), INVALID),
         (dict(up__ld=264), SHAPE), (dict(up__stride=(1 << 20) + 8), SHAPE), (dict(up__data=None), INVALID), (dict(grad=None), INVALID), (dict(grad_pre_up=None), INVALID), (dict(pre_gate=P[5] + 2), ALIGN),
         (dict(offsets=None), INVALID), (dict(grad_x=P[0]), INVALID), (dict(grad_pre_gate=P[4]), INVALID),
@@ -143,7 +144,7 @@ def test_null_and_empty():
     assert L.muon_gated(C.byref(_gated(m=0, out=none, offsets=none, x__data=none)), None) == L.MUON_OK
     assert L.muon_gated(C.byref(_gated(n=0)), None) == L.MUON_OK
     assert L.muon_gated_backward(C.byref(_backward(m=0, grad_gate=none, grad_up=none, offsets=none, grad=none)), None) == L.MUON_OK
-    assert L.muon_gated_backward(C.byref(_backward(n=0)), None) == L.MUON_OK
+    assert L.muon_gated_backward(C.byref(_backward(n=0, grad_x=None)), None) == L.MUON_OK
     assert L.muon_gather_rows(C.byref(_gather(n_rows=0, src_rows=0, src=none, rows=none)), None) == L.MUON_OK
     assert L.muon_combine_rows(C.byref(_combine(tokens=0, out=none)), None) == L.MUON_OK
 
