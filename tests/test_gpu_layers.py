@@ -605,6 +605,51 @@ def test_two_graphs_and_streams():
     assert torch.equal(got, want)
 
 
+def test_rows_in_two_launches_captured_and_side_by_side():
+    """Sizes whose rows go in two launches: added to what is there, captured and replayed, and on two streams at once."""
+    ex = X()
+    x, w, d = _matrix(1, 96, 2000), [_matrix(2 + i, 5003, 2000, std=0.02) for i in range(2)], _matrix(4, 96, 5003)
+    tall, narrow = _matrix(5, 16900, 128), [_matrix(6 + i, 512, 128, std=0.1) for i in range(2)]
+    _, *pre = ex.gated(x, *w, save=True)
+    grads = [torch.zeros(5003, 2000, device="cuda") for _ in range(2)]
+
+    def both():
+        dx, *_ = ex.gated_backward(d, x, *w, *pre, grad_gate=grads[0], grad_up=grads[1], accumulate=True)
+        return dx, ex.gated(tall, *narrow)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for turn in range(3):
+        d.copy_(_matrix(10 + turn, 96, 5003))
+        tall.copy_(_matrix(20 + turn, 16900, 128))
+        for g in grads:
+            g.fill_(float(turn))
+        graph.replay()
+        torch.cuda.synchronize()
+        ours = [g.clone() for g in grads]
+        for g in grads:
+            g.fill_(float(turn))
+        want = both()
+        assert all(torch.equal(a, b) for a, b in zip((*got, *ours), (*want, *grads)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[] for _ in streams]
+    for _ in range(3):
+        for at, st in zip(outs, streams):
+            at.append(ex.gated(tall, *narrow, stream=st))
+            at.append(ex.gated_backward(d, x, *w, *pre, stream=st)[1])
+    torch.cuda.synchronize()
+    for k, (h, g) in enumerate(zip(outs[0], outs[1])):
+        assert torch.equal(h, g) and torch.equal(h, outs[0][k % 2])
+    assert torch.equal(outs[0][0], want[1])
+
+
 def test_wrapper_refuses():
     ex = X()
     x, w = _matrix(1, 4, 64), _matrix(2, 8, 64)
