@@ -162,7 +162,7 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
 // both wave rows half of what there is.  Of a gated block a tile has 128 columns: b's panel holds 128 rows of gate and the
 // same 128 of up, a wave 32 of each, so a lane has both sums of a value of out.
 //
-// Bound by the matrix cores, whose clock falls to what the card's power allows (1.7 to 1.9 GHz): 8192 x 4096 x 4096 gate and up
+// Bound by the matrix cores, whose clock falls to what the card's power allows (1.4 to 2.0 GHz): 8192 x 4096 x 4096 gate and up
 // in bfloat16 takes 427 us (1.29 PFLOP/s), its gradients 894 (1.23), its product in 8-bit integers 117 (2.35 POP/s).  Tried and left out:
 // two workgroups of 128 x 256 per CU (20 to 25 % more time), 32 x 32 instructions (446, 952, 122 us), every second
 // workgroup begun half a tile later, so that not all store at once (nothing).
@@ -195,7 +195,7 @@ __device__ __forceinline__ uint64_t read_transposed(const uint8_t* at) {
 // LDS serves a 16-byte read 16 lanes at a time, which have all 16 rows of a block but not one depth (lanes 0 to 3, 12 to 15, 20 to 23
 // and 24 to 27 for one), and a 16-byte write 8 lanes at a time, here a row's 8 chunks.  So of a panel along its rows, chunk c of
 // row r lies in the r ^ c-th of the 16 slots of its block's c-th 256 bytes: reads fall on different rows' slots, writes on
-// different chunks'.  (Rows of 144 bytes had conflicts in 38 % of LDS's cycles.)  A panel across lies in 64 depth rows of 512 bytes whose 32-byte
+// different chunks'.  (Rows of 144 bytes had conflicts in 38 % of LDS's cycles.)  A panel across lies in 64 depth rows of all its columns, whose 32-byte
 // pieces (16 columns) are permuted by the row, so that the 8 rows that half a wave's transposing read touches fall on 8 different ones.
 //
 // Nothing in the main loop deals with ends:

@@ -399,8 +399,8 @@ def product(a: Fp8, b: Fp8, *, offsets: Optional[torch.Tensor] = None, group: Op
 
 @dataclass
 class Int8:
-    """A matrix of 8-bit integers, or a stack of them: codes (.., rows, cols rounded up to 128) and a float32 scale for
-    each row (.., rows)."""
+    """A matrix of 8-bit integers, or a stack of them: codes (.., rows, cols rounded up to 128, zeros behind cols) and a
+    float32 scale for each row (.., rows)."""
     codes: torch.Tensor
     scales: torch.Tensor
     cols: int
