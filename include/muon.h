@@ -596,7 +596,7 @@ typedef struct muon_operand {
     const void* data;
     const float* scales;   /* 8-bit integers: one per row (4-byte aligned); else NULL            */
     int64_t ld;            /* row stride in elements; of codes a multiple of 16, at least round_up(k, 128);
-                              below 2^22 (codes: 2^23); a row's codes from k to there are zeros */
+                              below 2^22 (codes: 2^23).  Codes from k to round_up(k, 128): zeros   */
     int64_t stride;        /* elements between the groups' matrices (of codes a multiple of 16) */
     int64_t stride_scales; /* and their scales                                                  */
 } muon_operand;
