@@ -572,6 +572,19 @@ def gated(x, gate, up, *, activation: str = "silu", offsets: Optional[torch.Tens
     return (out, pre[0], pre[1]) if save else out
 
 
+def _padded_rows(name: str, t: torch.Tensor) -> int:
+    """Row stride of a matrix (rows, n) that `gated` saved, or of some of its rows, each padded to a multiple of 64.  Where n is none
+    itself the padding is written: every row's has to be its own, the last row's inside the storage as well."""
+    n, ld, first = t.shape[1], t.stride(0), t.storage_offset()
+    own = ld % 64 == 0
+    if n % 64:
+        end = (first + t.shape[0] * ld) * t.element_size() if t.shape[0] else 0
+        own = ld == _up(n, 64) and first % ld == 0 and end <= t.untyped_storage().nbytes()
+    if not own:
+        raise ValueError(f"reuse needs {name} as gated saved it, its rows padded to multiples of 64")
+    return ld
+
+
 def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor, pre_gate: torch.Tensor,
                    pre_up: torch.Tensor, *, activation: str = "silu", offsets: Optional[torch.Tensor] = None,
                    grad_x: Optional[torch.Tensor] = None, grad_gate: Optional[torch.Tensor] = None,
@@ -582,7 +595,8 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
 
     grad_x is bfloat16; grad_gate and grad_up are of `dtype` or go into the given tensors (float32 ones are added to
     with `accumulate`).  Rows outside every segment of offsets are not written in grad_x and have no part in the others.
-    With `reuse` the saved tensors (as `gated` made them) serve as the workspace and do not keep their values.
+    With `reuse` the saved tensors (as `gated` made them, or some of their rows) serve as the workspace and do not keep
+    their values; zeros are written behind each row's n values, to the multiple of 64 that it is padded to.
     """
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(_ACTIVATIONS)}")
@@ -606,10 +620,9 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
         if _rows("pre_up", pre_up) != k.ld_pre:
             raise ValueError("pre_gate and pre_up must have the same row stride")
         if reuse:
-            # rows of `gated`'s are padded, which the stride of one row alone tells as well
-            k.ld_pre = k.ld_grad_pre = pre_gate.stride(0)
-            if k.ld_pre % 64 or pre_up.stride(0) != k.ld_pre:
-                raise ValueError("reuse needs saved tensors whose rows are padded to multiples of 64")
+            k.ld_pre = k.ld_grad_pre = _padded_rows("pre_gate", pre_gate)
+            if _padded_rows("pre_up", pre_up) != k.ld_pre:
+                raise ValueError("pre_gate and pre_up must have the same row stride")
             work = (pre_gate, pre_up)
         else:
             work = torch.empty(2, k.m, _up(k.n, 64), dtype=torch.bfloat16, device=x.device)

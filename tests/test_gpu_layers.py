@@ -692,3 +692,27 @@ def test_wrapper_refuses():
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} is accepted")
+
+
+def test_reuse_writes_no_other_tensor():
+    """Saved values in a wider buffer, of rows apart from others by a column, and in a storage without the last row's padding."""
+    ex, m, n, k = X(), 6, 40, 24
+    x, w, d = _matrix(1, m, k), [_matrix(2 + i, n, k) for i in range(2)], _matrix(4, m, n)
+    _, *saved = ex.gated(x, *w, save=True)
+    for wide, first in ((128, 0), (64, 8)):
+        buf = torch.full((2, m + 1, wide), 7.0, dtype=torch.bfloat16, device="cuda")
+        pre = [b[:m, first:first + n] for b in buf]
+        for p, v in zip(pre, saved):
+            p.copy_(v)
+        kept = buf.clone()
+        with pytest.raises(ValueError):
+            ex.gated_backward(d, x, *w, *pre, reuse=True)
+        assert torch.equal(buf, kept)
+    cut = [torch.empty((m - 1) * 64 + n, dtype=torch.bfloat16, device="cuda").as_strided((m, n), (64, 1)) for _ in range(2)]
+    with pytest.raises(ValueError):
+        ex.gated_backward(d, x, *w, *cut, reuse=True)
+    want = ex.gated_backward(d, x, *w, *saved)
+    some = ex.gated_backward(d[2:], x[2:].clone(), *w, saved[0][2:].contiguous(), saved[1][2:].contiguous())
+    again = ex.gated_backward(d[2:], x[2:].clone(), *w, saved[0][2:], saved[1][2:], reuse=True)
+    assert all(torch.equal(a, b) for a, b in zip(some, again)) and torch.equal(again[0], want[0][2:])
+    assert not saved[0].as_strided((m, 64), (64, 1))[2:, n:].any()

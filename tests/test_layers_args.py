@@ -181,3 +181,26 @@ def test_oracle_combines_what_it_gathers():
     step_y, step_w = rng.normal(size=y.shape), rng.normal(size=w.shape)
     f = lambda s: (d * orc.combine(y + s * step_y, position, w + s * step_w)[0]).sum()  # noqa: E731
     assert abs((f(1e-4) - f(-1e-4)) / 2e-4 - (dy * step_y).sum() - (dw * step_w).sum()) < 1e-8
+
+
+def test_reuse_takes_rows_whose_padding_is_their_own():
+    """Tensors that gated_backward(reuse=True) may write into, up to a multiple of 64 columns in every row, and those where
+    that would be another tensor's memory or none."""
+    import torch
+
+    from muon_newton_schulz_momentum_amd.experts import _padded_rows
+    saved = torch.empty(2, 5, 64, dtype=torch.bfloat16)[:, :, :40]
+    flat = torch.empty(5 * 128, dtype=torch.bfloat16)
+    good = [saved[0], saved[1], saved[1, 2:], saved[1, 4:], saved[0, :0], torch.empty(2, 0, 64)[1, :, :40], flat.view(5, 128), flat.view(10, 64),
+            flat.view(5, 128)[:, :64]]
+    for t in good:
+        assert _padded_rows("t", t) == t.stride(0) and t.stride(0) % 64 == 0
+    bad = [flat.view(5, 128)[:, :40],                      # a wider buffer's columns behind them
+           flat.view(10, 64)[:, 8:48],                     # into the next row
+           flat[:9 * 64 + 40].clone().as_strided((10, 40), (64, 1)),    # the storage ends with the last row's values
+           flat[:40].clone().view(1, 40),
+           torch.empty(5, 40, dtype=torch.bfloat16)]
+    for i, t in enumerate(bad):
+        with pytest.raises(ValueError, match="reuse needs t"):
+            _padded_rows("t", t)
+            pytest.fail(f"tensor {i} is accepted")
