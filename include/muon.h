@@ -642,7 +642,7 @@ typedef struct muon_int8_product_config {
 
 /* out[i][j] = (sum over k of a's codes times b's) * a.scales[i] * b.scales[j]: the sum exact, in 32-bit integers, then
  * float32 products from left to right and one rounding to out's type.  MUON_PRODUCT_ROWS as in muon_fp8_product: rows
- * outside every segment are left as they were.
+ * outside every segment are left as they were.  With k = 0 sums are 0; data and its strides are not looked at then.
  * Errors: INVALID_ARG (NULL, enum, groups, overlap), SHAPE (sizes, strides, 2^31 or more tiles), ALIGNMENT, HIP. */
 MUON_API muon_status muon_int8_product(const muon_int8_product_config* config, void* stream);
 
@@ -665,7 +665,8 @@ typedef struct muon_gated_config {
 
 /* The gated block of a feed-forward layer in one pass: out = act(x gate^T) * (x up^T), each row by its group's
  * matrices.  Sums in float32 (8-bit integers: exact, then scaled as in muon_int8_product); the activation and
- * the product are formed from the unrounded sums and rounded once.  Rows outside every segment are left as they were.
+ * the product are formed from the unrounded sums and rounded once.  Rows outside every segment are left as they were;
+ * k = 0 as in muon_int8_product.
  * Errors: as muon_int8_product; one of pre_gate / pre_up NULL. */
 MUON_API muon_status muon_gated(const muon_gated_config* config, void* stream);
 

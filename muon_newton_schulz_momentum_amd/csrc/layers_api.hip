@@ -24,13 +24,15 @@ muon_status check_rows(const void* p, int64_t ld, int64_t cols, const char* who,
     return MUON_OK;
 }
 
-// An operand of `rows` rows of k values per group.
+// An operand of `rows` rows of k values per group.  Without depth only its scales are read.
 muon_status check_operand(const muon_operand& o, int32_t operands, int64_t rows, int64_t k, int64_t groups, const char* who, const char* name) {
     const bool i8 = operands == MUON_OPERANDS_INT8;
     auto wrong = [&](muon_status s, const char* what) { return fail(s, who, (std::string(name) + what).c_str()); };
-    if (!o.data || (i8 && !o.scales)) return wrong(MUON_ERR_INVALID_ARG, ": data and, of 8-bit integers, scales must be non-NULL");
+    if ((k > 0 && !o.data) || (i8 && !o.scales)) return wrong(MUON_ERR_INVALID_ARG, ": data and, of 8-bit integers, scales must be non-NULL");
     if (!i8 && o.scales) return wrong(MUON_ERR_INVALID_ARG, ": bfloat16 has no scales");
-    if (misaligned(o.data) || ((uintptr_t)o.scales & 3u) != 0) return wrong(MUON_ERR_ALIGNMENT, ": data must be 16-byte aligned (scales 4-byte)");
+    if ((k > 0 && misaligned(o.data)) || ((uintptr_t)o.scales & 3u) != 0) return wrong(MUON_ERR_ALIGNMENT, ": data must be 16-byte aligned (scales 4-byte)");
+    if (i8 && groups > 1 && o.stride_scales < rows) return wrong(MUON_ERR_SHAPE, ": stride_scales must hold one matrix's scales");
+    if (k == 0) return MUON_OK;
     if (i8 ? o.ld % 16 != 0 || o.ld < round_up(k, 128) || o.ld >= MAX_LD_BYTES : o.ld < k || o.ld >= MAX_LD_BYTES / 2)
         return wrong(MUON_ERR_SHAPE, i8 ? ": row stride must be a multiple of 16, at least round_up(k, 128) and below 2^23"
                                         : ": row stride must be at least k and below 2^22");
@@ -38,17 +40,18 @@ muon_status check_operand(const muon_operand& o, int32_t operands, int64_t rows,
         const double need = (double)(rows - 1) * (double)o.ld + (double)(i8 ? round_up(k, 128) : k);
         if ((double)o.stride < need || (i8 && o.stride % 16 != 0))
             return wrong(MUON_ERR_SHAPE, ": stride must hold one matrix (and, of codes, be a multiple of 16)");
-        if (i8 && o.stride_scales < rows) return wrong(MUON_ERR_SHAPE, ": stride_scales must hold one matrix's scales");
     }
     return MUON_OK;
 }
-muon_status check_alike(const muon_operand& gate, const muon_operand& up, int32_t operands, int64_t groups, const char* who) {
-    if (gate.ld != up.ld || (groups > 1 && (gate.stride != up.stride || (operands == MUON_OPERANDS_INT8 && gate.stride_scales != up.stride_scales))))
+muon_status check_alike(const muon_operand& gate, const muon_operand& up, int32_t operands, int64_t k, int64_t groups, const char* who) {
+    if ((k > 0 && (gate.ld != up.ld || (groups > 1 && gate.stride != up.stride))) ||
+        (operands == MUON_OPERANDS_INT8 && groups > 1 && gate.stride_scales != up.stride_scales))
         return fail(MUON_ERR_SHAPE, who, "gate and up must have the same strides");
     return MUON_OK;
 }
 Extent values_of(const muon_operand& o, int32_t operands, int64_t rows, int64_t k, int64_t groups) {
     const bool i8 = operands == MUON_OPERANDS_INT8;
+    if (k == 0) return extent(nullptr, 0.0);
     return extent(o.data, groups, o.stride, rows, o.ld, i8 ? round_up(k, 128) : k, i8 ? 1 : 2);
 }
 Extent scales_of(const muon_operand& o, int64_t rows, int64_t groups) { return extent(o.scales, groups, o.stride_scales, 1, rows, rows, 4); }
@@ -77,16 +80,20 @@ LayerArgs layer_args(int32_t mode, int32_t groups, const int32_t* offsets, int64
     a.k = k;
     return a;
 }
+// (without depth values and their strides were not checked and are not read)
 void set_a(LayerArgs& a, int i, const void* p, const float* scales, int64_t ld, int64_t size) {
-    a.a[i] = static_cast<const uint8_t*>(p);
     a.sa = scales;
+    if (a.k == 0) return;
+    a.a[i] = static_cast<const uint8_t*>(p);
     a.lda = ld * size;
 }
 void set_b(LayerArgs& a, int i, const muon_operand& o, int64_t size) {
-    a.b[i] = static_cast<const uint8_t*>(o.data);
+    if (a.k > 0) {
+        a.b[i] = static_cast<const uint8_t*>(o.data);
+        a.ldb = o.ld * size;
+        a.stride_b = a.groups > 1 ? o.stride * size : 0;
+    }
     a.sb[i] = o.scales;
-    a.ldb = o.ld * size;
-    a.stride_b = a.groups > 1 ? o.stride * size : 0;
     a.stride_sb = a.groups > 1 ? o.stride_scales : 0;
 }
 
@@ -189,7 +196,7 @@ muon_status muon_gated(const muon_gated_config* c, void* stream) try {
     MUON_RETURN_IF(check_operand(c->x, c->operands, c->m, c->k, 1, who, "x"));
     MUON_RETURN_IF(check_operand(c->gate, c->operands, c->n, c->k, c->groups, who, "gate"));
     MUON_RETURN_IF(check_operand(c->up, c->operands, c->n, c->k, c->groups, who, "up"));
-    MUON_RETURN_IF(check_alike(c->gate, c->up, c->operands, c->groups, who));
+    MUON_RETURN_IF(check_alike(c->gate, c->up, c->operands, c->k, c->groups, who));
     const int64_t size = i8 ? 1 : 2;
     LayerArgs a = layer_args(c->mode, c->groups, c->offsets, c->m, c->n, c->k);
     set_a(a, 0, c->x.data, c->x.scales, c->x.ld, size);
@@ -253,7 +260,7 @@ muon_status muon_gated_backward(const muon_gated_backward_config* c, void* strea
         MUON_RETURN_IF(check_rows(c->grad_x, c->ld_grad_x, c->k, who, "grad_x"));
         MUON_RETURN_IF(check_operand(c->gate, bf16, c->n, c->k, c->groups, who, "gate"));
         MUON_RETURN_IF(check_operand(c->up, bf16, c->n, c->k, c->groups, who, "up"));
-        MUON_RETURN_IF(check_alike(c->gate, c->up, bf16, c->groups, who));
+        MUON_RETURN_IF(check_alike(c->gate, c->up, bf16, c->k, c->groups, who));
     }
     LayerArgs x = layer_args(c->mode, c->groups, c->offsets, c->m, c->k, c->n);
     set_a(x, 0, c->grad_pre_gate, nullptr, c->ld_grad_pre, 2);

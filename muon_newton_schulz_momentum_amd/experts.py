@@ -423,7 +423,7 @@ class Int8:
 def _check_int8(name: str, q: Int8, like: torch.Tensor) -> tuple:
     codes, scales, cols, device = q.codes, q.scales, q.cols, like.device
     shape = tuple(codes.shape)             # (a torch.Size is slow to slice)
-    if cols < 1 or len(shape) < 2 or shape[-1] != -(-cols // BLOCK) * BLOCK or tuple(scales.shape) != shape[:-1]:
+    if cols < 0 or len(shape) < 2 or shape[-1] != -(-cols // BLOCK) * BLOCK or tuple(scales.shape) != shape[:-1]:
         raise ValueError(f"{name}: codes {shape} and scales {tuple(scales.shape)} are not those of {cols} columns")
     if codes.dtype != torch.int8 or scales.dtype != torch.float32:
         raise ValueError(f"{name} must have int8 codes and float32 scales")

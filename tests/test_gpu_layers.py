@@ -716,3 +716,26 @@ def test_reuse_writes_no_other_tensor():
     again = ex.gated_backward(d[2:], x[2:].clone(), *w, saved[0][2:], saved[1][2:], reuse=True)
     assert all(torch.equal(a, b) for a, b in zip(some, again)) and torch.equal(again[0], want[0][2:])
     assert not saved[0].as_strided((m, 64), (64, 1))[2:, n:].any()
+
+
+@pytest.mark.parametrize("m,n,ends", [(1, 1, None), (70, 33, None), (5000, 5000, None), (70, 33, [3, 3, 20, 66]), (5000, 1030, [0, 300, 300, 4990])])
+def test_products_without_depth(m, n, ends):
+    """Rows without values: sums of nothing, so zeros, in the rows of the segments."""
+    ex, lead, kinds = X(), () if ends is None else (len(ends) - 1,), (torch.bfloat16, torch.int8)
+    hit = torch.zeros(m, dtype=torch.bool, device="cuda")
+    for _, lo, hi in orc.segments(ends, m):
+        hit[lo:hi] = True
+    for kind in kinds:
+        def operand(*shape):
+            t = torch.empty(*shape, 0, dtype=kind, device="cuda")
+            return t if kind is torch.bfloat16 else ex.Int8(t, torch.ones(shape, device="cuda"), 0)
+        x, w = operand(m), operand(*lead, n)
+        for act in ACTS:
+            out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+            got = ex.gated(x, w, w, activation=act, offsets=_offsets(ends), save=True, out=out)
+            assert not any(bool(t[hit].any()) for t in got) and bool((out[~hit] == 7.0).all())
+        if kind is torch.int8:
+            for dtype in (torch.float32, torch.bfloat16):
+                out = torch.full((m, n), 7.0, dtype=dtype, device="cuda")
+                ex.product_int8(x, w, offsets=_offsets(ends), out=out)
+                assert not out[hit].any() and bool((out[~hit] == 7.0).all())

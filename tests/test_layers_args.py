@@ -204,3 +204,18 @@ def test_reuse_takes_rows_whose_padding_is_their_own():
         with pytest.raises(ValueError, match="reuse needs t"):
             _padded_rows("t", t)
             pytest.fail(f"tensor {i} is accepted")
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("int8_product", dict(a__data=None, b__data=None, a__ld=1, b__ld=7, b__stride=3, out=P[4])),
+    ("gated", dict(x__data=None, gate__data=None, up__data=None, x__ld=1, gate__ld=3, up__ld=5, gate__stride=0, up__stride=1, out=P[6])),
+    ("gated", dict(x__data=P[7], gate__data=P[7] + 2, up__data=P[8], out=P[6]))])
+def test_without_depth_data_is_not_looked_at(name, kw):
+    """Only what is wrong besides is refused: here out, which overlaps offsets."""
+    assert getattr(L, f"muon_{name}")(C.byref(CALLS[name](k=0, **kw)), None) == INVALID and b"overlaps" in L.muon_last_error()
+
+
+def test_without_depth_scales_are():
+    for kw, status in ((dict(a__scales=None), INVALID), (dict(b__scales=P[3] + 2), ALIGN), (dict(b__stride_scales=19), SHAPE)):
+        assert L.muon_int8_product(C.byref(_product(k=0, **kw)), None) == status
+    assert L.muon_gated(C.byref(_gated(True, k=0, up__stride_scales=64)), None) == SHAPE
