@@ -576,7 +576,7 @@ def _padded_rows(name: str, t: torch.Tensor) -> int:
     """Row stride of a matrix (rows, n) that `gated` saved, or of some of its rows, each padded to a multiple of 64.  Where n is none
     itself the padding is written: every row's has to be its own, the last row's inside the storage as well."""
     n, ld, first = t.shape[1], t.stride(0), t.storage_offset()
-    own = ld % 64 == 0
+    own = ld % 64 == 0 or n == 0
     if n % 64:
         end = (first + t.shape[0] * ld) * t.element_size() if t.shape[0] else 0
         own = ld == _up(n, 64) and first % ld == 0 and end <= t.untyped_storage().nbytes()
@@ -595,6 +595,7 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
 
     grad_x is bfloat16; grad_gate and grad_up are of `dtype` or go into the given tensors (float32 ones are added to
     with `accumulate`).  Rows outside every segment of offsets are not written in grad_x and have no part in the others.
+    Without features (n = 0) grad_x is zeros.
     With `reuse` the saved tensors (as `gated` made them, or some of their rows) serve as the workspace and do not keep
     their values; zeros are written behind each row's n values, to the multiple of 64 that it is padded to.
     """
@@ -645,6 +646,10 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
             k.stride_grad_w = grad_gate.stride(0)
         if _rows("grad_up", grad_up) != k.ld_grad_w or (k.groups > 1 and grad_up.stride(0) != k.stride_grad_w):
             raise ValueError("grad_gate and grad_up must have the same strides")
+        if k.n == 0:
+            # sums of nothing: muon_gated_backward refuses this grad_x, muon_gated writes it from rows without values
+            gated(x[:, :0], gate.transpose(-1, -2), up.transpose(-1, -2), offsets=offsets, out=grad_x)
+            k.grad_x = None
         L.check(L.muon_gated_backward(C.byref(k), _stream_ptr(x)), "muon_gated_backward")
     return grad_x, grad_gate, grad_up
 

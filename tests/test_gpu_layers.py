@@ -739,3 +739,18 @@ def test_products_without_depth(m, n, ends):
                 out = torch.full((m, n), 7.0, dtype=dtype, device="cuda")
                 ex.product_int8(x, w, offsets=_offsets(ends), out=out)
                 assert not out[hit].any() and bool((out[~hit] == 7.0).all())
+
+
+@pytest.mark.parametrize("m,k,ends", [(1, 1, None), (70, 200, None), (70, 200, [3, 3, 20, 66]), (0, 24, None)])
+@pytest.mark.parametrize("reuse", [False, True])
+def test_gated_backward_without_features(m, k, ends, reuse):
+    ex, lead = X(), () if ends is None else (len(ends) - 1,)
+    x, w, d = _matrix(1, m, k), [_matrix(2 + i, *lead, 0, k) for i in range(2)], _matrix(4, m, 0)
+    h, *pre = ex.gated(x, *w, offsets=_offsets(ends), save=True)
+    out = torch.full((m, k), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx, dg, du = ex.gated_backward(d, x, *w, *pre, offsets=_offsets(ends), grad_x=out, reuse=reuse, dtype=torch.float32)
+    hit = torch.zeros(m, dtype=torch.bool, device="cuda")
+    for _, lo, hi in orc.segments(ends, m):
+        hit[lo:hi] = True
+    assert h.shape == (m, 0) and dg.shape == du.shape == w[0].shape and dx is out
+    assert not dx[hit].any() and bool((dx[~hit] == 7.0).all())
