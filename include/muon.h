@@ -728,6 +728,7 @@ typedef struct muon_gather_rows_config {
  * where c is outside [0, src_rows * per).  Without weights that is how tokens reach their experts.  With them and
  * src the gradient of muon_combine_rows' out it is the gradient of its rows, and with y those rows grad_weights[c] =
  * sum over columns of src[c / per] * y[r] for r = position[c] (float32; 0 where that is outside [0, n_rows)).
+ * Without rows (n_rows = 0) grad_weights is zeros.
  * Errors: INVALID_ARG (NULL, enum, per, no output, overlap), SHAPE (sizes, strides, src_rows * per of 2^31 or more),
  * ALIGNMENT, HIP. */
 MUON_API muon_status muon_gather_rows(const muon_gather_rows_config* config, void* stream);

@@ -329,14 +329,18 @@ muon_status muon_gather_rows(const muon_gather_rows_config* c, void* stream) try
     if (c->per < 1) return fail(MUON_ERR_INVALID_ARG, who, "per must be at least 1");
     if (c->src_rows < 0 || c->src_rows > MAX_I32 || c->src_rows * c->per > MAX_I32 || c->n_rows < 0 || c->n_rows > (1 << 30) || c->cols < 1 || c->cols > MAX_I32)
         return fail(MUON_ERR_SHAPE, who, "src_rows * per must be below 2^31, n_rows at most 2^30, cols in [1, 2^31)");
-    if (!c->y != !c->grad_weights || !c->y != !c->position) return fail(MUON_ERR_INVALID_ARG, who, "y, position and grad_weights go together");
-    if (!c->out && !c->y) return fail(MUON_ERR_INVALID_ARG, who, "no output");
+    // buffers of 0 elements may be NULL: out and y without rows, position and grad_weights without choices
     const int64_t choices = c->src_rows * c->per, size = size_of(c->dtype);
+    if (choices > 0 && (!c->position != !c->grad_weights || (c->n_rows > 0 && !c->y != !c->grad_weights)))
+        return fail(MUON_ERR_INVALID_ARG, who, "y, position and grad_weights go together");
+    if (c->n_rows > 0 && !c->out && !c->y) return fail(MUON_ERR_INVALID_ARG, who, "no output");
+    const bool gathers = c->n_rows > 0 && c->out, grads = choices > 0 && c->grad_weights;
+    if (!gathers && !grads) return MUON_OK;
     if (c->src_rows > 0) MUON_RETURN_IF(check_rows(c->src, c->ld, c->cols, who, "src"));
     if (c->n_rows > 0) {
         if (!c->rows) return fail(MUON_ERR_INVALID_ARG, who, "rows is NULL");
         if (c->out) MUON_RETURN_IF(check_rows(c->out, c->ld_out, c->cols, who, "out"));
-        if (c->y) MUON_RETURN_IF(check_rows(c->y, c->ld_y, c->cols, who, "y"));
+        if (grads) MUON_RETURN_IF(check_rows(c->y, c->ld_y, c->cols, who, "y"));
     }
     if (misaligned(c->rows) || misaligned(c->weights) || misaligned(c->position) || misaligned(c->grad_weights) || ((uintptr_t)c->limit & 3u) != 0)
         return fail(MUON_ERR_ALIGNMENT, who, "buffers must be 16-byte aligned (limit 4-byte)");
@@ -349,11 +353,11 @@ muon_status muon_gather_rows(const muon_gather_rows_config* c, void* stream) try
     a.src = c->src;
     a.rows = c->rows;
     a.limit = c->limit;
-    a.out = c->out;
+    a.out = gathers ? c->out : nullptr;
     a.weights = c->weights;
-    a.y = c->y;
-    a.position = c->position;
-    a.grad_weights = c->grad_weights;
+    a.y = grads ? c->y : nullptr;
+    a.position = grads ? c->position : nullptr;
+    a.grad_weights = grads ? c->grad_weights : nullptr;
     a.cols = c->cols;
     a.ld = c->ld;
     a.ld_out = c->ld_out;

@@ -754,3 +754,24 @@ def test_gated_backward_without_features(m, k, ends, reuse):
         hit[lo:hi] = True
     assert h.shape == (m, 0) and dg.shape == du.shape == w[0].shape and dx is out
     assert not dx[hit].any() and bool((dx[~hit] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gather_and_combine_without_rows_or_tokens(dtype):
+    ex, cols = X(), 130
+    ints = lambda *shape, value=-1: torch.full(shape, value, dtype=torch.int32, device="cuda")  # noqa: E731
+    # no rows: no gradient of a row, zeros for the weights
+    for T, k in ((1, 1), (70, 3)):
+        d, y = _matrix(1, T, cols, dtype=dtype), _matrix(2, 0, cols, dtype=dtype)
+        for at in (-1, 0):
+            dy, dw = ex.combine_rows_backward(d, y, ints(0), ints(T, k, value=at), torch.ones(T, k, device="cuda"))
+            assert dy.shape == (0, cols) and dw.shape == (T, k) and not dw.any()
+        assert not ex.combine_rows(y, ints(T, k), torch.ones(T, k, device="cuda")).any()
+        assert ex.gather_rows(d, ints(0)).shape == (0, cols)
+    # no tokens: rows that pad segments only
+    d, y = _matrix(1, 0, cols, dtype=dtype), _matrix(2, 40, cols, dtype=dtype)
+    for value in (-1, 0, 5):
+        dy, dw = ex.combine_rows_backward(d, y, ints(40, value=value), ints(0, 3), torch.ones(0, 3, device="cuda"))
+        assert not dy.any() and dw.shape == (0, 3)
+        assert not ex.gather_rows(d, ints(40, value=value), per=3).any()
+    assert ex.combine_rows(y, ints(0, 3), torch.ones(0, 3, device="cuda")).shape == (0, cols)

@@ -219,3 +219,16 @@ def test_without_depth_scales_are():
     for kw, status in ((dict(a__scales=None), INVALID), (dict(b__scales=P[3] + 2), ALIGN), (dict(b__stride_scales=19), SHAPE)):
         assert L.muon_int8_product(C.byref(_product(k=0, **kw)), None) == status
     assert L.muon_gated(C.byref(_gated(True, k=0, up__stride_scales=64)), None) == SHAPE
+
+
+def test_gather_rows_without_rows_or_choices():
+    """Buffers of 0 elements are NULL: only what is wrong besides is refused, here an output over an input."""
+    none = dict.fromkeys(("rows", "out", "y"))
+    for kw in (dict(n_rows=0, grad_weights=P[4], **none), dict(n_rows=0, grad_weights=P[6] + 64, **none),
+               dict(src_rows=0, src=None, weights=None, position=None, grad_weights=None, out=P[1])):
+        assert L.muon_gather_rows(C.byref(_gather(**kw)), None) == INVALID and b"overlaps" in L.muon_last_error(), kw
+    # nothing to write
+    for kw in (dict(n_rows=0, position=None, grad_weights=None, **none), dict(src_rows=0, src=None, position=None, grad_weights=None, out=None)):
+        assert L.muon_gather_rows(C.byref(_gather(**kw)), None) == L.MUON_OK, kw
+    for kw in (dict(n_rows=0, position=None, **none), dict(n_rows=0, grad_weights=None, **none)):
+        assert L.muon_gather_rows(C.byref(_gather(**kw)), None) == INVALID, kw
