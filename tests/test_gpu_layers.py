@@ -775,3 +775,165 @@ def test_gather_and_combine_without_rows_or_tokens(dtype):
         assert not dy.any() and dw.shape == (0, 3)
         assert not ex.gather_rows(d, ints(40, value=value), per=3).any()
     assert ex.combine_rows(y, ints(0, 3), torch.ones(0, 3, device="cuda")).shape == (0, cols)
+
+
+# ---- offsets beyond 32 bits that the kernels form themselves ---------------------------------------
+
+FAR_ROWS, FAR_N, FAR_STRIDE = 266000, 8104, 9 << 18        # rows of FAR_N values; 1024 groups' matrices FAR_STRIDE elements apart
+FAR_BYTES, FAR_ELEMENTS = 2 ** 32, 2 ** 31
+
+
+def _far(t, *index):
+    """t, whose element at index lies beyond 2^31 elements and 2^32 bytes from its first."""
+    away = sum(i * s for i, s in zip(index, t.stride()))
+    assert away >= (FAR_ELEMENTS if t.element_size() > 1 else FAR_BYTES) and away * t.element_size() >= FAR_BYTES
+    return t
+
+
+def _far_stack(n, k, dtype, stride=FAR_STRIDE):
+    return _far(torch.empty(1024 * stride, dtype=dtype, device="cuda").as_strided((1024, n, k), (stride, k, 1)), 1022)
+
+
+def _last_two(m):
+    """Offsets of 1024 groups of which the last two have rows: 25 and 35 before row m."""
+    return [m - 60] * 1023 + [m - 35, m], ((1022, m - 60, m - 35), (1023, m - 35, m))
+
+
+def _check_rows(h, g, u, x, gate, up, act):
+    (gr, gs, _), (ur, us, _) = (orc.rows_product(_np(x), _np(v)) for v in (gate, up))
+    eg, eu, a = sum_tol(x.shape[1]) * gs, sum_tol(x.shape[1]) * us, orc.activation(gr, act)[0]
+    _close(h, a * ur, 1.2 * eg * (np.abs(ur) + eu) + np.abs(a) * eu + (H + 160 * U) * np.abs(a * ur) + TINY, "h")
+    if g is not None:
+        _close(g, gr, eg + H * np.abs(gr) + TINY, "gate")
+        _close(u, ur, eu + H * np.abs(ur) + TINY, "up")
+
+
+@pytest.mark.parametrize("m", [60, FAR_ROWS])
+def test_gated_far_from_the_first_row_and_group(m):
+    """Weights, rows, results, saved values and all gradients; 60 rows in the kernels for few, the others among 256 a tile."""
+    ex, n, k = X(), FAR_N, 64
+    ends, used = _last_two(m)
+    w = [_far_stack(n, k, torch.bfloat16) for _ in range(2)]
+    for i, v in enumerate(w):
+        for g, _, _ in used:
+            v[g] = _matrix(10 * i + g, n, k, std=1.5 / 8)
+    wide = n if m > 60 else k
+    x = torch.empty(m, wide, dtype=torch.bfloat16, device="cuda")[:, :k]
+    x[-60:] = _matrix(1, 60, k)
+    h, g, u = ex.gated(x, *w, offsets=_offsets(ends), save=True)
+    d = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    d[-60:] = _matrix(2, 60, n, std=0.1)
+    if m > 60:
+        for t in (x, h, g, u, d):
+            _far(t, m - 60)
+    for grp, lo, hi in used:
+        _check_rows(h[lo:hi], g[lo:hi], u[lo:hi], x[lo:hi], w[0][grp], w[1][grp], "silu")
+    del h
+    pre = _np(g[-60:]), _np(u[-60:])
+    gx = torch.full((m, wide), 7.0, dtype=torch.bfloat16, device="cuda")[:, :k]
+    grads = [_far_stack(n, k, torch.float32) for _ in range(2)]
+    for v in grads:
+        v[[0, 500, 1022, 1023]] = 7.0
+    ex.gated_backward(d, x, *w, g, u, offsets=_offsets(ends), grad_x=gx, grad_gate=grads[0], grad_up=grads[1], reuse=True)
+    for got, want, size in zip((g, u), orc.gated_pre_grads(_np(d[-60:]), *pre, "silu"),
+                               (_np(d[-60:]) * pre[1] * (1.2 + np.abs(pre[0]) / 4), _np(d[-60:]) * orc.activation(pre[0], "silu")[0])):
+        _close(got[-60:], want, H * np.abs(want) + 160 * U * np.abs(size) + TINY)
+    assert m == 60 or bool((gx[:-60] == 7.0).all())
+    for grp, lo, hi in used:
+        ref, size = orc.gated_grad_x(_np(g[lo:hi]), _np(u[lo:hi]), _np(w[0][grp]), _np(w[1][grp]))
+        _close(gx[lo:hi], ref, sum_tol(2 * n + 32) * size + H * np.abs(ref) + TINY, "grad_x")
+        for got, dd in zip(grads, (g, u)):
+            ref, size = orc.gated_grad_w(_np(dd[lo:hi]), _np(x[lo:hi]))
+            _close(got[grp], ref, sum_tol(hi - lo) * size + U * np.abs(ref) + TINY, "weights")
+    assert not any(bool(v[[0, 500]].any()) for v in grads)
+    del w, x, d, g, u, gx, grads
+    torch.cuda.empty_cache()
+
+
+def test_dense_gated_far_from_the_first_row():
+    """All rows in launches of whole tiles, and weight gradients over a depth whose rows end far away."""
+    ex, m, n, k = X(), FAR_ROWS, FAR_N, 64
+    w = [_matrix(2 + i, n, k, std=1.5 / 8) for i in range(2)]
+    x = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")[:, :k]
+    some = torch.tensor([0, 1, 255, 256, m // 2, *range(m - 60, m)], device="cuda")
+    x[some] = _matrix(1, len(some), k)
+    h, g, u = ex.gated(x, *w, activation="gelu", save=True)
+    _check_rows(h[some], g[some], u[some], x[some], *w, "gelu")
+    assert not h[1000:1100].any()
+    d = h.zero_()
+    d[some] = _matrix(4, len(some), n, std=0.1)
+    for t in (x, g, u, d):
+        _far(t, m - 60)
+    gx, gg, gu = ex.gated_backward(d, x, *w, g, u, activation="gelu", grad_x=torch.empty_like(d)[:, :k], dtype=torch.float32, reuse=True)
+    dg, du = _np(g[some]), _np(u[some])
+    ref, size = orc.gated_grad_x(dg, du, *map(_np, w))
+    _close(_far(gx, m - 60)[some], ref, sum_tol(2 * n + 32) * size + H * np.abs(ref) + TINY, "grad_x")
+    for got, dd in ((gg, dg), (gu, du)):
+        ref, size = orc.gated_grad_w(dd, _np(x[some]))
+        # (the other rows add zeros, which round nothing)
+        _close(got, ref, sum_tol(len(some) * 16) * size + U * np.abs(ref) + TINY, "weights")
+    del x, h, g, u, d, gx
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m", [60, FAR_ROWS])
+def test_int8_far_from_the_first_row_and_group(m):
+    ex, n, k = X(), FAR_N, 100
+    ends, used = _last_two(m)
+    wide = 2 * FAR_N if m > 60 else 128                    # (a multiple of 16)
+    a = ex.Int8(torch.empty(m, wide, dtype=torch.int8, device="cuda")[:, :128], torch.empty(m, device="cuda"), k)
+    some = _int8(1, 60, k)
+    a.codes[-60:], a.scales[-60:] = some.codes, some.scales
+    codes = _far_stack(n, 128, torch.int8, 2 * FAR_STRIDE)
+    b = ex.Int8(codes, _far(torch.empty(1024 * FAR_STRIDE, device="cuda").as_strided((1024, n), (FAR_STRIDE, 1)), 1022), k)
+    for i, (grp, _, _) in enumerate(used):
+        q = _int8(2 + i, n, k)
+        b.codes[grp], b.scales[grp] = q.codes, q.scales
+    y = ex.product_int8(a, b, offsets=_offsets(ends), dtype=torch.float32)
+    h = ex.gated(a, b, b, activation="relu", offsets=_offsets(ends))
+    if m > 60:
+        for t in (a.codes, y, h):
+            _far(t, m - 60)
+    for grp, lo, hi in used:
+        want, _ = _scaled(ex.Int8(a.codes[lo:hi], a.scales[lo:hi], k), ex.Int8(b.codes[grp], b.scales[grp], k), None)
+        _close(y[lo:hi], want, 4 * U * np.abs(want) + TINY, "product")
+        want = np.maximum(want, 0) * want
+        _close(h[lo:hi], want, (H + 10 * U) * np.abs(want) + TINY, "gated")
+    del a, b, codes, y, h
+    torch.cuda.empty_cache()
+
+
+def test_rows_written_far_from_the_first():
+    """Gathered, combined and quantised rows, a residual, and rows whose weights' gradients are formed."""
+    ex, T, cols = X(), 40, FAR_N
+    src = _matrix(1, T, cols)
+    rows = torch.full((FAR_ROWS,), -1, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 1000, FAR_ROWS // 2, *range(FAR_ROWS - 37, FAR_ROWS)], device="cuda")
+    rows[at] = torch.arange(T, dtype=torch.int32, device="cuda")
+    out = _far(ex.gather_rows(src, rows), FAR_ROWS - 37)
+    assert torch.equal(out[at], src) and not out[2000:2100].any() and not out[-100:-37].any()
+    # the gradients of a sum of single rows, each far away
+    position, w = at.to(torch.int32).view(T, 1), torch.rand(T, 1, device="cuda", generator=_gen(3))
+    d = _matrix(4, T, cols)
+    dy, dw = ex.combine_rows_backward(d, out, rows, position, w)
+    ref = _np(w) * _np(d)
+    _close(_far(dy, FAR_ROWS - 37)[at], ref, H * np.abs(ref) + TINY, "rows")
+    _close(dw[:, 0], (_np(d) * _np(src)).sum(-1), (-(-cols // 512) * 8 + 7) * 2 * U * np.abs(_np(d) * _np(src)).sum(-1) + TINY, "weights")
+    del dy
+    # single rows to tokens far away, in place of their residual
+    position = rows.view(-1, 1).clone()
+    out.fill_(1.0)
+    assert ex.combine_rows(src, position, residual=out, out=out) is out
+    ref = 1.0 + _np(src)
+    _close(out[at], ref, 4 * U * (1 + np.abs(_np(src))) + H * np.abs(ref) + TINY, "combined")
+    assert bool((out[2000:2100] == 1.0).all())
+    del out
+    n = 2 * FAR_ROWS                                       # (codes of one byte)
+    rows = torch.cat([rows[:FAR_ROWS // 2], torch.full((FAR_ROWS,), -1, dtype=torch.int32, device="cuda"), rows[FAR_ROWS // 2:]])
+    q = ex.quantize_int8(src, rows=rows)
+    at = torch.nonzero(rows >= 0)[:, 0]
+    codes, scales = orc.quantize_int8(_np(src))
+    assert q.codes.shape[0] == n and np.array_equal(_far(q.codes, n - 37)[at, :cols].cpu().numpy(), codes)
+    assert np.array_equal(q.scales[at].cpu().numpy(), scales) and not q.codes[n - 100:n - 37].any() and not q.codes[at, cols:].any()
+    del q
+    torch.cuda.empty_cache()
