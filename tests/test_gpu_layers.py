@@ -937,3 +937,79 @@ def test_rows_written_far_from_the_first():
     assert np.array_equal(q.scales[at].cpu().numpy(), scales) and not q.codes[n - 100:n - 37].any() and not q.codes[at, cols:].any()
     del q
     torch.cuda.empty_cache()
+
+
+# ---- outputs left out, and the deepest sums ------------------------------------------------------
+
+@pytest.mark.parametrize("m,n,k,ends", [(70, 40, 96, None), (300, 136, 264, [0, 1, 2, 130, 130, 280, 290]), (16900, 512, 128, None), (9, 5, 7, [2, 2, 8]), (70, 40, 0, None)])
+def test_gated_backward_of_some_outputs(m, n, k, ends):
+    """Each subset of the nullable outputs holds what the whole call writes, and what a subset does not read may be NULL."""
+    import ctypes as C
+
+    from muon_newton_schulz_momentum_amd import binding as L
+    ex, lead = X(), () if ends is None else (len(ends) - 1,)
+    x, w = _matrix(1, m, k), [_matrix(2 + i, *lead, n, k, std=0.1) for i in range(2)]
+    d, *pre = (_matrix(8 + i, m, n, std=0.5) for i in range(3))
+    hit = torch.from_numpy(orc.rows_product(_np(x), _np(w[0]), ends)[2]).cuda()
+    offsets, width = _offsets(ends), -(-n // 64) * 64
+    want = ex.gated_backward(d, x, *w, *pre, offsets=offsets, dtype=torch.float32)
+    for rows, weights in itertools.product((False, True), repeat=2):
+        work = torch.full((2, m, width), 5.0, dtype=torch.bfloat16, device="cuda")
+        gx = torch.full((m, k), 7.0, dtype=torch.bfloat16, device="cuda")
+        gw = [torch.full(w[0].shape, 7.0, device="cuda") for _ in range(2)]
+        operand = lambda t: L.muon_operand(t.data_ptr(), None, k, n * k, 0)  # noqa: E731
+        c = L.muon_gated_backward_config(
+            L.MUON_PRODUCT_DENSE if ends is None else L.MUON_PRODUCT_ROWS, lead[0] if lead else 1, L.MUON_ACT_SILU, L.MUON_DTYPE_F32, 0, 0, m, n, k,
+            operand(x) if weights else L.muon_operand(), operand(w[0]) if rows else L.muon_operand(), operand(w[1]) if rows else L.muon_operand(),
+            None if ends is None else offsets.data_ptr(), d.data_ptr(), n, pre[0].data_ptr(), pre[1].data_ptr(), n,
+            work[0].data_ptr(), work[1].data_ptr(), width, gx.data_ptr() if rows else None, k,
+            gw[0].data_ptr() if weights else None, gw[1].data_ptr() if weights else None, k, n * k)
+        L.check(L.muon_gated_backward(C.byref(c), torch.cuda.current_stream().cuda_stream), "muon_gated_backward")
+        ref, there = [_np(v) for v in (d, *pre)], hit.cpu().numpy()
+        slack = np.abs(ref[0] * ref[2]) * (1.2 + np.abs(ref[1]) / 4), np.abs(ref[0] * orc.activation(ref[1], "silu")[0])
+        for got, v, size in zip(work, orc.gated_pre_grads(*ref, "silu"), slack):
+            _close(got[hit][:, :n], v[there], (H * np.abs(v) + 160 * U * size + TINY)[there])
+            assert not got[hit][:, n:].any() and bool((got[~hit] == 5.0).all())
+        assert torch.equal(gx[hit], want[0][hit]) if rows else bool((gx == 7.0).all())
+        assert bool((gx[~hit] == 7.0).all())
+        assert all(torch.equal(a, b) if weights else bool((a == 7.0).all()) for a, b in zip(gw, want[1:]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("tokens,top_k,experts,align,cols", [(1, 1, 1, 1, 3), (64, 7, 32, 16, 200), (300, 3, 16, 128, 513)])
+def test_gather_rows_of_the_weights_gradients_alone(dtype, tokens, top_k, experts, align, cols):
+    import ctypes as C
+
+    from muon_newton_schulz_momentum_amd import binding as L
+    ex, g = X(), _grouped(tokens, top_k, experts, align, 5, 2)
+    n, kind = g.rows.numel(), L.MUON_DTYPE_F32 if dtype is torch.float32 else L.MUON_DTYPE_BF16
+    d, y = _matrix(1, tokens, cols, dtype=dtype), _matrix(2, n, cols, dtype=dtype)
+    w = torch.rand(tokens, top_k, device="cuda", generator=_gen(3))
+    _, want = ex.combine_rows_backward(d, y, g.rows, g.position, w, limit=g.limit)
+    got = torch.full_like(w, 7.0)
+    c = L.muon_gather_rows_config(d.data_ptr(), tokens, cols, cols, kind, top_k, g.rows.data_ptr(), n, g.limit.data_ptr(), None, 0, None,
+                                  y.data_ptr(), cols, g.position.data_ptr(), got.data_ptr())
+    L.check(L.muon_gather_rows(C.byref(c), torch.cuda.current_stream().cuda_stream), "muon_gather_rows")
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("m,n,ends", [(1, 33, None), (300, 520, None), (300, 136, [0, 100, 100, 290])])
+def test_deepest_sums_of_8_bit_integers(m, n, ends):
+    """131071 products of 16384 each, the largest sum that 32 bits hold, and of -128 by 127."""
+    ex, k, lead = X(), 131071, () if ends is None else (len(ends) - 1,)
+    a, b = ex.Int8.empty(m, k), ex.Int8.empty(n, k, stack=lead[0] if lead else None)
+    for q in (a, b):
+        q.codes.fill_(-128)
+        q.codes[..., k:] = 0
+        q.scales.fill_(1.0)
+    b.codes[..., 1::2, :k] = 127
+    got = ex.product_int8(a, b, offsets=_offsets(ends), dtype=torch.float32)
+    want = np.where(np.arange(n) % 2, -128.0 * 127 * k, 128.0 * 128 * k)
+    for _, lo, hi in orc.segments(ends, m):
+        _close(got[lo:hi], np.broadcast_to(want, (hi - lo, n)), U * np.abs(want))
+    # (relu(g) u with g = u: 0 where the sum is negative; a scale keeps the square within the type)
+    a.scales.fill_(2.0 ** -20)
+    got = ex.gated(a, b, b, activation="relu", offsets=_offsets(ends))
+    want = np.maximum(want, 0) * want * 2.0 ** -40
+    for _, lo, hi in orc.segments(ends, m):
+        _close(got[lo:hi], np.broadcast_to(want, (hi - lo, n)), (H + 4 * U) * np.abs(want))
