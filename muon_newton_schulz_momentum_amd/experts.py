@@ -595,6 +595,7 @@ def gated_backward(grad: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, up: 
 
     grad_x is bfloat16; grad_gate and grad_up are of `dtype` or go into the given tensors (float32 ones are added to
     with `accumulate`).  Rows outside every segment of offsets are not written in grad_x and have no part in the others.
+    The products' terms are the pre-activations' gradients rounded to bfloat16, float32 results are sums of those too.
     Without features (n = 0) grad_x is zeros.
     With `reuse` the saved tensors (as `gated` made them, or some of their rows) serve as the workspace and do not keep
     their values; zeros are written behind each row's n values, to the multiple of 64 that it is padded to.

@@ -1013,3 +1013,30 @@ def test_deepest_sums_of_8_bit_integers(m, n, ends):
     want = np.maximum(want, 0) * want * 2.0 ** -40
     for _, lo, hi in orc.segments(ends, m):
         _close(got[lo:hi], np.broadcast_to(want, (hi - lo, n)), (H + 4 * U) * np.abs(want))
+
+
+@pytest.mark.parametrize("m,n,k,ends", [(1, 130, 72, None), (2, 40, 96, [0, 2, 2]), (448, 200, 264, None), (900, 128, 192, [0, 10, 520, 890]), (8191, 64, 40, None)])
+@pytest.mark.parametrize("act", ACTS)
+def test_gated_backward_end_to_end(m, n, k, ends, act):
+    """The whole call against the definition of unrounded terms: each term is off by dg's or du's rounding, h of itself, and by what
+    these were off before it (as above); float32 results by no more than that and their sums."""
+    lead = () if ends is None else (len(ends) - 1,)
+    x, w = _matrix(1, m, k), [_matrix(2 + i, *lead, n, k, std=1.5 / math.sqrt(k)) for i in range(2)]
+    d, g, u = (_matrix(8 + i, m, n, std=s) for i, s in enumerate((0.1, 1.5, 1.0)))
+    hit = orc.rows_product(_np(x), _np(w[0]), ends)[2]
+    pick = torch.from_numpy(hit).cuda()
+    dg, du = orc.gated_pre_grads(_np(d), _np(g), _np(u), act)
+    off = (H * np.abs(dg) + 160 * U * np.abs(_np(d) * _np(u)) * (1.2 + np.abs(_np(g)) / 4) + TINY,
+           H * np.abs(du) + 160 * U * np.abs(_np(d) * orc.activation(_np(g), act)[0]) + TINY)
+    ref_x, size = orc.gated_grad_x(dg, du, _np(w[0]), _np(w[1]), ends)
+    off_x = orc.gated_grad_x(*off, *(np.abs(_np(v)) for v in w), ends)[0]
+    tol_x = off_x + sum_tol(2 * n + 32) * (size + off_x)
+    longest = max([hi - lo for _, lo, hi in orc.segments(ends, m)], default=1)
+    for dtype in (torch.float32, torch.bfloat16):
+        gx, *gw = X().gated_backward(d, x, *w, g, u, activation=act, offsets=_offsets(ends), dtype=dtype)
+        _close(gx[pick], ref_x[hit], (tol_x + H * (np.abs(ref_x) + tol_x) + TINY)[hit], "grad_x")
+        for got, dd, o, name in zip(gw, (dg, du), off, ("gate", "up")):
+            ref, size = orc.gated_grad_w(dd, _np(x), ends)
+            tol = orc.gated_grad_w(o, np.abs(_np(x)), ends)[0]
+            tol = tol + sum_tol(longest) * (size + tol)
+            _close(got, ref, tol + HALF[dtype] * (np.abs(ref) + tol) + TINY, name)
