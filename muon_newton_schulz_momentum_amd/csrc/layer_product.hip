@@ -163,8 +163,8 @@ __global__ __launch_bounds__(ANY_THREADS) void layer_any_kernel(LayerArgs p) {
 // same 128 of up, a wave 32 of each, so a lane has both sums of a value of out.
 //
 // Bound by the matrix cores, whose clock falls to what the card's power allows (1.4 to 2.0 GHz): 8192 x 4096 x 4096 gate and up
-// in bfloat16 takes 427 us (1.29 PFLOP/s), its gradients 894 (1.23), its product in 8-bit integers 117 (2.35 POP/s).  Tried and left out:
-// two workgroups of 128 x 256 per CU (20 to 25 % more time), 32 x 32 instructions (446, 952, 122 us), every second
+// in bfloat16 takes 423 to 440 us (1.25 to 1.30 PFLOP/s), its gradients 895 (1.23), its product in 8-bit integers 115 (2.39 POP/s).  Tried
+// and left out: two workgroups of 128 x 256 per CU (20 to 25 % more time), 32 x 32 instructions (4 to 7 % more), every second
 // workgroup begun half a tile later, so that not all store at once (nothing).
 constexpr int TILE = 256, WAVES = 8, THREADS = 64 * WAVES;
 constexpr int FN = 4;                                      // 16 x 16 blocks of a wave along b; along a: FM
@@ -675,7 +675,8 @@ __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // depth of a tile of 16 RB rows of a by 16 NB rows of b (of a gated block NB / 2 blocks of gate and as many of up), its fragments
 // straight from memory into registers, AHEAD steps at a time, so that a tile's loads are under way together; the
 // waves' sums are added up through LDS in the order of the waves.  Bound by memory, and for a single call by its latency
-// (1 row by 5632 x 2048 gate and up in bfloat16: 12.9 us, 46 MB; 1 row by 2048 x 5632 in 8-bit integers: 7.0 us, 11.5 MB).
+// (1 row by 5632 x 2048 gate and up in bfloat16: 13.1 us for 46 MB that the last-level cache keeps from call to call, 16.2 from memory; 1 row
+// by 2048 x 5632 in 8-bit integers: 7.0 us, 11.5 MB).
 template <class E, int FORM, class OUT, int RB, int NB, int AHEAD>
 __global__ __launch_bounds__(THREADS) void layer_few_kernel(LayerArgs p) {
     constexpr bool GATED = FORM == FORM_GATED, I8 = sizeof(E) == 1, F32 = sizeof(OUT) == 4;
@@ -800,11 +801,12 @@ bool tile_loads_fit(const LayerArgs& a) {
 }
 
 // What a launch of the big tiles' kernel would take, in us, from what it measured: rounds of tiles, each a constant and so much a
-// step, less where few CUs work (clock and caches).  A step of 256 x 256 takes 1.14 us alone on the chip and 1.47 with all CUs
-// busy, with 128 rows 0.77 and 1.0, with 64 0.57 and 0.72; of 256 rows of which 192, 128 or 64 are there, 1.05, 0.92, 0.73 alone.
-// (Gate and up in bfloat16, 4096 x 4096 by 1024: 93 us in 512 tiles of 64 rows, 70 in 256 of 128, 95 in 128 of 256;
-// 1024 x 4096: 47, 61, 89.  112 rows of 8-bit integers by as many experts, 4096 x 1024: 148, 150, 166.  57344 rows by 128
-// experts, bfloat16: 1677, 1236, 1116.)
+// step, less where few CUs work (clock and caches).  A step of 256 x 256 takes 1.11 us alone on the chip and 1.43 with all CUs
+// busy, with 128 rows 0.77 and 1.04, with 64 0.57 and 0.69; of 256 rows of which 192, 128 or 64 are there, 1.11, 0.79, 0.80 alone.  (The
+// constants are from before the loops of 4 and 2 pairs and lie within 17 % of that.)
+// Gate and up in bfloat16, 4096 x 4096 by 1024: 103 us in 512 tiles of 64 rows, 74 in 256 of 128, 96 in 128 of 256;
+// 1024 x 4096: 46, 60, 87.  112 rows of 8-bit integers by as many experts, 4096 x 1024: 88, 94, 99.  57344 rows by 128
+// experts, bfloat16: 1656, 1230, 1063.
 struct Cost {
     int64_t tiles;
     double us;
@@ -853,8 +855,8 @@ Plan plan(const LayerArgs& a) {
         }
     if constexpr (GATED || FORM == FORM_SCALED) {
         // 16 rows, 32 rows, 32 rows by 64 columns: bound by a wave's share of the depth where there are few tiles, by the steps of
-        // all tiles where there are many (1 row by 5632 x 2048 gate and up in bfloat16: 16, 18, 18 us and 32 in big tiles; 64 rows: 40, 31,
-        // 30, 33; 256 rows: 131, 95, 72, 53; 1 row by 2048 x 5632 in 8-bit integers: 7, 8, 15, 32)
+        // all tiles where there are many (1 row by 5632 x 2048 gate and up in bfloat16, weights from memory: 16, 18, 16 us and 28 in
+        // tiles of 64 rows; 64 rows: 40, 32, 30, 32; 256 rows: 130, 94, 76, 31; 1 row by 2048 x 5632 in 8-bit integers: 7, 8, 15, 30)
         static const double wait[2][3] = {{0.65, 0.75, 2.4}, {1.2, 1.55, 2.4}}, rate[2][3] = {{1900, 1290, 625}, {1500, 1024, 740}};
         for (int i = 0; i < 3; ++i) {
             LayerArgs few = a;

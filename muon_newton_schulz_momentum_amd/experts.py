@@ -19,11 +19,11 @@ The same layer in bfloat16 between its ends, and back:
 
     x = gather_rows(tokens, g.rows, per=top_k, limit=g.limit)
     h, pre_gate, pre_up = gated(x, W_gate, W_up, offsets=g.offsets, save=True)
-    ...                                                              # y: h through the experts' third matrices
+    ...                                                              # y: h through the experts' third matrices, by the caller
     out = combine_rows(y, g.position, weights, residual=tokens)
     ...
     dy, dweights = combine_rows_backward(dout, y, g.rows, g.position, weights, limit=g.limit)
-    ...                                                              # dh: dy through the third matrices
+    ...                                                              # dh: dy through the third matrices, and their gradient
     dx, *_ = gated_backward(dh, x, W_gate, W_up, pre_gate, pre_up, offsets=g.offsets, grad_gate=G_gate, grad_up=G_up)
     dtokens = combine_rows(dx, g.position)
     dlogits = route_backward(logits, chosen, dweights, score="sigmoid")
